@@ -19,6 +19,9 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libagmm.so")
 
 AGMM_BF16, AGMM_FP16, AGMM_FP32 = 0, 1, 2
+AGMM_E4M3, AGMM_E5M2 = 0, 1
+FORMATS = {"e4m3": AGMM_E4M3, "e5m2": AGMM_E5M2}
+SCALE_BLOCK = 128   # elements of k that share one scale
 AGMM_OK, AGMM_ERR_INVALID_ARG, AGMM_ERR_UNSUPPORTED, AGMM_ERR_OOM, AGMM_ERR_HIP = 0, 1, 2, 3, 4
 (AGMM_VARIANT_AUTO, AGMM_VARIANT_FUSED, AGMM_VARIANT_STAGED, AGMM_VARIANT_UNFUSED,
  AGMM_VARIANT_SKINNY) = 0, 1, 2, 3, 4
@@ -55,6 +58,7 @@ EXPORTS = [
     ("agmm_plan_timing_end", _ci, [_vp]),
     ("agmm_plan_destroy", None, [_vp]),
     ("agmm_run_noalloc", _ci, [_ci, _i64, _i64, _i64, _ci, _ci, ctypes.POINTER(_vp), _vp, _vp, _vp]),
+    ("agmm_quantize", _ci, [_vp, _ci, _i64, _i64, _i64, _ci, _ci, _vp, _i64, _vp, _vp, _i64, _vp, _vp]),
     ("agmm_last_status", _ci, []),
     ("agmm_last_error", _cc, []),
     ("agmm_version", _cc, []),
@@ -230,6 +234,11 @@ def run_noalloc(shards, B, C, rhs_transpose: bool, stream=None):
     agmm_run_noalloc(len(shards), m_s, k, n, dtype, rhs_transpose, [s.data_ptr() for s in shards],
                      B.data_ptr(), C.data_ptr(), _stream_handle(stream, device.index))
     return C
+
+
+def agmm_quantize(x, dtype, rows, cols, ldx, fmt, block_rows, q, ldq, scale, qt, ldqt, scale_t, stream) -> int:
+    return _check(load_library().agmm_quantize(x, dtype, rows, cols, ldx, fmt, block_rows, q, ldq, scale, qt, ldqt,
+                                               scale_t, stream))
 
 
 def agmm_last_status() -> int:
@@ -429,6 +438,98 @@ class Plan:
 
     def __exit__(self, *exc):
         self.close()
+
+
+# ------------------------------------------------ block-scaled 8-bit operands
+class Scaled:
+    """A block-scaled 8-bit matrix [rows, k]: `values` (float8, [rows, k
+    rounded up to 16], zeros past k), `scales` (fp32, [ceil(k / 128),
+    ceil(rows / block_rows)]), the true row length `k` and `block_rows` (1 or
+    128).  Element (r, c) stands for values[r, c] * scales[c // 128, r //
+    block_rows]."""
+
+    __slots__ = ("values", "scales", "k", "block_rows")
+
+    def __init__(self, values, scales, k: int, block_rows: int = 1):
+        self.values, self.scales, self.k, self.block_rows = values, scales, int(k), int(block_rows)
+
+    @property
+    def rows(self) -> int:
+        return self.values.shape[0]
+
+    def dequantize(self):
+        """The fp32 matrix [rows, k] this one stands for (torch operations; for
+        checks, not for speed)."""
+        s = self.scales.t().repeat_interleave(SCALE_BLOCK, dim=1)[:, :self.k]
+        if self.block_rows > 1:
+            s = s.repeat_interleave(self.block_rows, dim=0)[:self.rows]
+        return self.values[:, :self.k].float() * s
+
+
+def _device_and_stream(device, stream):
+    """Context in which outputs are allocated and kernels launched: the
+    tensors' device, and the caller's torch stream if one was passed (so that
+    the allocator hands out memory in that stream's order)."""
+    import contextlib
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)   # sets the stream's device too
+    if device.index is not None and device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _format(fmt) -> int:
+    if isinstance(fmt, str):
+        if fmt not in FORMATS:
+            raise ValueError(f"unknown 8-bit format {fmt!r} (one of {sorted(FORMATS)})")
+        return FORMATS[fmt]
+    return int(fmt)
+
+
+def _format_dtype(fmt: int):
+    import torch
+    return {AGMM_E4M3: torch.float8_e4m3fn, AGMM_E5M2: torch.float8_e5m2}[fmt]
+
+
+def quantize(x, fmt="e4m3", block_rows: int = 1, out: str = "rows", stream=None):
+    """Block-scaled 8-bit copies of x [rows, cols] (bf16, fp16 or fp32, unit
+    column stride): agmm_quantize.  `out` is "rows" (x, for a product that
+    contracts its columns), "cols" (x transposed, for one that contracts its
+    rows) or "both"; returns a Scaled, or the pair for "both"."""
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if out not in ("rows", "cols", "both"):
+        raise ValueError(f"out must be 'rows', 'cols' or 'both' (got {out!r})")
+    code = {torch.bfloat16: AGMM_BF16, torch.float16: AGMM_FP16, torch.float32: AGMM_FP32}.get(x.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if x.device.type != "cuda":
+        raise ValueError("x must be on the GPU")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be a row-major matrix (unit column stride)")
+    rows, cols = x.shape
+    fmt = _format(fmt)
+    if block_rows not in (1, SCALE_BLOCK):
+        raise ValueError(f"block_rows must be 1 or {SCALE_BLOCK}")
+    fmt_dtype = _format_dtype(fmt)
+
+    def new(r, c):
+        return (torch.empty((r, -(-c // 16) * 16), dtype=fmt_dtype, device=x.device),
+                torch.empty((-(-c // SCALE_BLOCK), -(-r // block_rows)), dtype=torch.float32, device=x.device))
+
+    with _device_and_stream(x.device, stream):
+        q, s = new(rows, cols) if out != "cols" else (None, None)
+        qt, st = new(cols, rows) if out != "rows" else (None, None)
+        agmm_quantize(x.data_ptr(), code, rows, cols, x.stride(0) if rows > 1 else max(cols, 1), fmt, block_rows,
+                      q.data_ptr() if q is not None else None, q.stride(0) if q is not None else 0,
+                      s.data_ptr() if s is not None else None,
+                      qt.data_ptr() if qt is not None else None, qt.stride(0) if qt is not None else 0,
+                      st.data_ptr() if st is not None else None, _stream_handle(stream, x.device.index))
+    a = Scaled(q, s, cols, block_rows) if q is not None else None
+    b = Scaled(qt, st, rows, block_rows) if qt is not None else None
+    return (a, b) if out == "both" else a if out == "rows" else b
 
 
 # ------------------------------------------------ one call, cached plans

@@ -36,6 +36,8 @@ SOURCES = {
     "gemm_mfma.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
     "skinny.hip": [],
     "noalloc.hip": [],
+    "agmm_ops.cpp": [],
+    "quantize.hip": [],
 }
 
 

@@ -37,33 +37,16 @@
 #include <vector>
 
 #include "agmm.h"
+#include "agmm_host.h"
 #include "agmm_kernels.h"
 
 namespace {
 
-thread_local int g_status = AGMM_OK;
-thread_local std::string g_msg;
-
-int set_err(int status, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  g_status = status;
-  g_msg = buf;
-  return status;
-}
-
-int ok() {
-  g_status = AGMM_OK;
-  g_msg.clear();
-  return AGMM_OK;
-}
-
-int hip_err(hipError_t e, const char* what) {
-  return set_err(AGMM_ERR_HIP, "%s failed: %s", what, hipGetErrorString(e));
-}
+using agmm::g_msg;
+using agmm::g_status;
+using agmm::hip_err;
+using agmm::ok;
+using agmm::set_err;
 
 constexpr int64_t kDimLimit = int64_t(1) << 30;
 // automatic transposed copy of B (stored k x n) from this many rows of m

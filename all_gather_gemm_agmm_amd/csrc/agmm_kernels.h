@@ -152,6 +152,32 @@ hipError_t launch_pad_copy(const PadCopyProblem& p, hipStream_t stream);
 hipError_t launch_transpose16(const void* in, int64_t ld_in, int64_t rows, int64_t cols, void* out,
                               hipStream_t stream);
 
+// 8-bit formats (OCP: e4m3 without infinities, e5m2 with them).
+constexpr int kFmtE4M3 = 0;
+constexpr int kFmtE5M2 = 1;
+
+// Elements of k that share one scale of the block-scaled 8-bit operands.
+constexpr int kScaleBlock = 128;
+
+// Block-scaled 8-bit copies of x [rows][cols]: q [rows][ldq] with
+// scale[block of columns][row block] and, of x transposed, qt [cols][ldqt]
+// with scale_t[block of rows][column block].  Either pair may be null.
+// Columns cols .. cols16 of q (rows .. rows16 of qt) are written as zeros.
+struct QuantProblem {
+  const void* x;
+  int64_t rows, cols, ldx;
+  int32_t dtype, format;
+  int32_t block_rows;      // 1: a scale per row and 128 columns; 128: per 128 x 128 tile
+  void* q;
+  int64_t ldq;
+  float* scale;
+  void* qt;
+  int64_t ldqt;
+  float* scale_t;
+  int64_t cols16, rows16;  // cols and rows rounded up to 16
+};
+hipError_t launch_quantize(const QuantProblem& p, hipStream_t stream);
+
 // Size of the device scratch of the no-allocation entry point (one per GPU,
 // held for the life of the process; equal to AGMM_NOALLOC_SCRATCH_BYTES).
 constexpr size_t kNoallocScratchBytes = size_t(32) << 20;

@@ -59,6 +59,12 @@ typedef enum {
   AGMM_FP32 = 2
 } agmm_dtype;
 
+/* 8-bit floating-point formats (OCP). */
+typedef enum {
+  AGMM_E4M3 = 0, /* largest value 448, no infinities */
+  AGMM_E5M2 = 1  /* largest value 57344 */
+} agmm_format;
+
 typedef enum {
   AGMM_OK = 0,
   AGMM_ERR_INVALID_ARG = 1, /* NULL pointer, size < 1, unknown key or dtype */
@@ -404,6 +410,40 @@ void agmm_plan_destroy(agmm_plan_t plan);
 int agmm_run_noalloc(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_local, int dtype,
                      int rhs_transpose, const void *const *shard_ptrs, const void *B, void *C,
                      void *stream);
+
+/*
+ * Block-scaled 8-bit copies of a matrix: the operands of agmm_scaled_run.
+ *
+ *     s = max(max |x| of the block / F, 2^-126)     F: the format's largest value
+ *     q = x / s, rounded to nearest even
+ *
+ * A block is 128 consecutive elements of a row (block_rows 1) or a 128 x 128
+ * tile (block_rows 128), ending where the matrix ends.  s is the fp32
+ * quotient, q the rounding of the fp32 product x * (1 / s).  Infinities and
+ * NaN do not enter the maximum; they become NaN in e4m3 and stay what they
+ * are in e5m2.  A block of zeros has s = 2^-126.
+ *   x        device, [rows, cols] of `dtype`, rows ldx elements apart (any
+ *            alignment of whole elements; rows of whole 16-byte vectors are
+ *            read faster)
+ *   format   agmm_format
+ *   q, scale     x: q[r * ldq + c], ldq >= cols rounded up to 16 (columns
+ *            past cols up to there are written as zeros), and
+ *            scale[(c / 128) * row_blocks + r / block_rows], row_blocks =
+ *            ceil(rows / block_rows)
+ *   qt, scale_t  x transposed, laid out by the same rule: qt[c * ldqt + r],
+ *            ldqt >= rows rounded up to 16, and
+ *            scale_t[(r / 128) * col_blocks + c / block_rows], col_blocks =
+ *            ceil(cols / block_rows).  Its blocks are those of the transposed
+ *            matrix (128 consecutive rows of one column for block_rows 1).
+ * Either pair may be NULL, not both; x is read once for both.  q and qt are
+ * 16-byte aligned with rows of whole 16-byte vectors.  rows, cols >= 1 and
+ * < 2^28, rows * cols < 2^37.  Needs no plan and no workspace; outputs must
+ * not overlap x.  Returns AGMM_OK, AGMM_ERR_INVALID_ARG,
+ * AGMM_ERR_UNSUPPORTED (alignment, size) or AGMM_ERR_HIP.
+ */
+int agmm_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ldx, int format,
+                  int block_rows, void *q, int64_t ldq, float *scale, void *qt, int64_t ldqt,
+                  float *scale_t, void *stream);
 
 /* Thread-local status / message of this thread's most recent call into the
  * library (AGMM_OK and "" after a call that succeeded; calls on other threads
