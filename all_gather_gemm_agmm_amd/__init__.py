@@ -59,6 +59,13 @@ EXPORTS = [
     ("agmm_plan_destroy", None, [_vp]),
     ("agmm_run_noalloc", _ci, [_ci, _i64, _i64, _i64, _ci, _ci, ctypes.POINTER(_vp), _vp, _vp, _vp]),
     ("agmm_quantize", _ci, [_vp, _ci, _i64, _i64, _i64, _ci, _ci, _vp, _i64, _vp, _vp, _i64, _vp, _vp]),
+    ("agmm_scaled_plan_validate", _ci, [_ci, _i64, _i64, _i64, _ci, _ci, _ci]),
+    ("agmm_scaled_plan_create", _vp, [_ci, _i64, _i64, _i64, _ci, _ci, _ci]),
+    ("agmm_scaled_run", _ci, [_vp, ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp, _vp, _vp, _vp]),
+    ("agmm_scaled_plan_set_int", _ci, [_vp, _cc, _i64]),
+    ("agmm_scaled_plan_get_int", _ci, [_vp, _cc, ctypes.POINTER(_i64)]),
+    ("agmm_scaled_plan_workspace_bytes", ctypes.c_size_t, [_vp]),
+    ("agmm_scaled_plan_destroy", None, [_vp]),
     ("agmm_last_status", _ci, []),
     ("agmm_last_error", _cc, []),
     ("agmm_version", _cc, []),
@@ -530,6 +537,133 @@ def quantize(x, fmt="e4m3", block_rows: int = 1, out: str = "rows", stream=None)
     a = Scaled(q, s, cols, block_rows) if q is not None else None
     b = Scaled(qt, st, rows, block_rows) if qt is not None else None
     return (a, b) if out == "both" else a if out == "rows" else b
+
+
+class _OpPlan:
+    """What the plans of the operators share: their handle, its settings and
+    its end.  `_create`, `_set`, `_get`, `_bytes`, `_destroy` name the C
+    functions."""
+
+    def _make(self, *args):
+        import torch
+        lib = load_library()
+        self.handle = None
+        self.device = torch.cuda.current_device()
+        self.handle = getattr(lib, self._prefix + "_create")(*args)
+        if not self.handle:
+            raise AgmmError(lib.agmm_last_status(), lib.agmm_last_error().decode())
+
+    def set(self, key: str, value: int) -> None:
+        _check(getattr(load_library(), self._prefix + "_set_int")(self.handle, key.encode(), int(value)))
+        self._read_strides()
+
+    def get(self, key: str) -> int:
+        v = ctypes.c_int64(0)
+        _check(getattr(load_library(), self._prefix + "_get_int")(self.handle, key.encode(), ctypes.byref(v)))
+        return int(v.value)
+
+    def workspace_bytes(self) -> int:
+        return int(getattr(load_library(), self._prefix + "_workspace_bytes")(self.handle))
+
+    def _read_strides(self):
+        self._ld = {k: self.get(k) for k in self._strides}
+
+    def _on(self, t, shape, dtype, name, ld=None):
+        """A tensor of this shape and dtype on the plan's device, its rows `ld`
+        elements apart (None: dense)."""
+        import torch
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be on the GPU")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} is on {t.device}; the plan was created on cuda:{self.device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, plan expects {dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if len(shape) == 1:
+            if shape[0] > 1 and t.stride(0) != 1:
+                raise ValueError(f"{name} must be dense")
+            return t.data_ptr()
+        ld = shape[1] if ld is None else ld
+        if (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) != ld):
+            raise ValueError(f"{name} must be row-major with rows {ld} elements apart (stride {tuple(t.stride())})")
+        return t.data_ptr()
+
+    def _new(self, rows, cols, ld, dtype, device):
+        import torch
+        return torch.empty((rows, ld), dtype=dtype, device=device)[:, :cols]
+
+    @property
+    def m(self) -> int:
+        return self.num_shards * self.m_per_shard
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            getattr(load_library(), self._prefix + "_destroy")(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+class ScaledPlan(_OpPlan):
+    """C = concat_r(shards[r]) @ B^T for block-scaled 8-bit operands
+    (agmm_scaled_run): shards are Scaled [m_per_shard, k] with block_rows 1 in
+    `a_format`, B a Scaled [n_local, k] in e4m3 with `b_block_rows`, C of
+    `c_dtype` (AGMM_BF16, AGMM_FP16 or AGMM_FP32)."""
+
+    _prefix = "agmm_scaled_plan"
+    _strides = ("lda", "ldb", "ldc")
+
+    def __init__(self, num_shards: int, m_per_shard: int, k: int, n_local: int, a_format="e4m3",
+                 b_block_rows: int = SCALE_BLOCK, c_dtype: int = AGMM_BF16, **settings):
+        a_format = _format(a_format)
+        self._make(num_shards, m_per_shard, k, n_local, a_format, b_block_rows, c_dtype)
+        import torch
+        self.num_shards, self.m_per_shard, self.k, self.n_local = num_shards, m_per_shard, k, n_local
+        self.b_block_rows = b_block_rows
+        self._k16 = -(-k // 16) * 16
+        self._kb = -(-k // SCALE_BLOCK)
+        self._a_dtype, self._b_dtype = _format_dtype(a_format), torch.float8_e4m3fn
+        self._c_dtype, self._f32 = _torch_dtype(c_dtype), torch.float32
+        self._a, self._s = (ctypes.c_void_p * num_shards)(), (ctypes.c_void_p * num_shards)()
+        self._read_strides()
+        for key, val in settings.items():
+            if val is not None:
+                self.set(key, val)
+
+    def _operand(self, x, rows, dtype, block_rows, ld, name):
+        if not isinstance(x, Scaled):
+            raise TypeError(f"{name} must be a Scaled")
+        if x.k != self.k or x.block_rows != block_rows:
+            raise ValueError(f"{name} has k {x.k} and block_rows {x.block_rows}, expected {self.k} and {block_rows}")
+        return (self._on(x.values, (rows, self._k16), dtype, f"{name}.values", ld),
+                self._on(x.scales, (self._kb, -(-rows // block_rows)), self._f32, f"{name}.scales"))
+
+    def run(self, shards, B, C=None, stream=None):
+        if len(shards) != self.num_shards:
+            raise ValueError(f"expected {self.num_shards} shards, got {len(shards)}")
+        for r, s in enumerate(shards):
+            self._a[r], self._s[r] = self._operand(s, self.m_per_shard, self._a_dtype, 1, self._ld["lda"], f"shards[{r}]")
+        b, bs = self._operand(B, self.n_local, self._b_dtype, self.b_block_rows, self._ld["ldb"], "B")
+        with _device_and_stream(B.values.device, stream):
+            if C is None:
+                C = self._new(self.m, self.n_local, self._ld["ldc"], self._c_dtype, B.values.device)
+            c = self._on(C, (self.m, self.n_local), self._c_dtype, "C", self._ld["ldc"])
+            _check(load_library().agmm_scaled_run(self.handle, self._a, self._s, b, bs, c,
+                                                  _stream_handle(stream, self.device)))
+        return C
 
 
 # ------------------------------------------------ one call, cached plans

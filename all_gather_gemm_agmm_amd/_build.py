@@ -38,6 +38,7 @@ SOURCES = {
     "noalloc.hip": [],
     "agmm_ops.cpp": [],
     "quantize.hip": [],
+    "scaled.hip": [],
 }
 
 

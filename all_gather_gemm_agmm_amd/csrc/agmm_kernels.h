@@ -178,6 +178,44 @@ struct QuantProblem {
 };
 hipError_t launch_quantize(const QuantProblem& p, hipStream_t stream);
 
+// Block-scaled 8-bit product: logical row i is row i % rows_per_group of
+// group i / rows_per_group, and row i of C.  Scales are [k block][row] for A
+// (per group) and [k block][nb] for B.
+struct ScaledProblem {
+  const void* a_group[kMaxGroups];
+  const float* a_scale[kMaxGroups];
+  int64_t a_ld;            // bytes between rows of a group
+  int32_t rows_per_group, num_groups;
+  int32_t m, n, k16;       // k16: row length rounded up to 16 (zeros past k)
+  int32_t kb;              // blocks of 128 of k
+  const void* b;
+  int64_t ldb;
+  const float* b_scale;
+  int32_t nb;              // row blocks of B (n for b_block_rows 1)
+  int32_t b_block_rows;
+  int32_t a_format;        // B is e4m3
+  void* c;
+  int64_t ldc;             // elements
+  int32_t c_dtype;
+  int32_t wide;            // kScaled128: sums of 128 by bf16 MFMAs on the widened values
+  TileOrder order;         // tiles kScaled256 and kScaled128
+  int32_t splits;          // k ranges of kb_per_split blocks, into partials [splits][m][n]
+  int32_t kb_per_split;
+  float* partials;
+};
+enum ScaledTile : int {
+  kScaled256 = 0,          // 256 x 256, 8 waves, 8-bit MFMAs
+  kScaled128 = 1,          // 128 x 128, 4 waves, two workgroups per CU; 8-bit or bf16 MFMAs (wide)
+  kScaledSkinny16 = 2,     // 16 x 32, k-tiles shared out over 4 waves, bf16 MFMAs
+  kScaledSkinny32 = 3,     // 32 x 32
+  kScaledTiles = 4,
+};
+constexpr int scaled_tile_rows(int t) {
+  return t == kScaled256 ? 256 : t == kScaled128 ? 128 : t == kScaledSkinny16 ? 16 : t == kScaledSkinny32 ? 32 : 0;
+}
+constexpr int scaled_tile_cols(int t) { return t == kScaled256 ? 256 : t == kScaled128 ? 128 : 32; }
+hipError_t launch_scaled(const ScaledProblem& p, int tile, hipStream_t stream);
+
 // Size of the device scratch of the no-allocation entry point (one per GPU,
 // held for the life of the process; equal to AGMM_NOALLOC_SCRATCH_BYTES).
 constexpr size_t kNoallocScratchBytes = size_t(32) << 20;

@@ -1,6 +1,18 @@
 // C ABI of the operators around the all-gather matmul (host side): the
-// block-scaled 8-bit quantiser.
+// block-scaled 8-bit quantiser and product.
+//
+// Their plans are used as the all-gather matmul's are: a plan validates its
+// problem, owns a workspace when a call needs one, and orders its calls: every
+// call records the plan's completion event on its stream and the next call's
+// stream waits for it, so that calls on different streams or threads never
+// share the workspace at one time.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdlib>
+#include <mutex>
+#include <new>
+#include <string>
 
 #include "agmm.h"
 #include "agmm_host.h"
@@ -19,9 +31,259 @@ constexpr int64_t kQuantElems = int64_t(1) << 37;
 
 int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+constexpr int64_t kDimLimit = int64_t(1) << 30;
+constexpr int64_t kElemLimit = int64_t(1) << 40;
+
+// Shard counts and sizes every plan here accepts (the all-gather matmul's
+// rules).
+int check_sizes(int N, int64_t m_s, int64_t k, int64_t n) {
+  if (N < 1) return set_err(AGMM_ERR_INVALID_ARG, "num_shards must be >= 1 (got %d)", N);
+  if (N > agmm::kMaxGroups)
+    return set_err(AGMM_ERR_UNSUPPORTED, "num_shards %d exceeds the supported maximum %d", N, agmm::kMaxGroups);
+  if (m_s < 1 || k < 1 || n < 1)
+    return set_err(AGMM_ERR_INVALID_ARG, "sizes must be >= 1 (m_per_shard=%lld, k=%lld, n_local=%lld)",
+                   (long long)m_s, (long long)k, (long long)n);
+  const int64_t m = N * m_s;
+  if (m >= kDimLimit || k >= kDimLimit || n >= kDimLimit || m * k >= kElemLimit || k * n >= kElemLimit ||
+      m * n >= kElemLimit)
+    return set_err(AGMM_ERR_UNSUPPORTED, "problem too large (m=%lld, k=%lld, n=%lld)", (long long)m, (long long)k,
+                   (long long)n);
+  return AGMM_OK;
+}
+
+// What every plan here owns: its device, a workspace, and the event that
+// orders its calls.
+struct PlanBase {
+  int device = 0;
+  int cu_count = 256;
+  char* ws = nullptr;
+  size_t ws_bytes = 0;
+  hipEvent_t ev_done = nullptr;
+  enum { kNone, kEager, kCaptured } done = kNone;
+  unsigned long long done_capture = 0;
+  hipStream_t done_stream = nullptr;
+  bool captured = false;
+  std::mutex mu;
+
+  int init() {
+    hipError_t err = hipGetDevice(&device);
+    if (err != hipSuccess) return hip_err(err, "hipGetDevice");
+    int cus = 0;
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) == hipSuccess && cus > 0)
+      cu_count = cus;
+    err = hipEventCreateWithFlags(&ev_done, hipEventDisableTiming);
+    return err == hipSuccess ? AGMM_OK : hip_err(err, "hipEventCreate");
+  }
+
+  // Replace the workspace by one of at least `bytes` (kept when it is large
+  // enough).  On failure the plan keeps the one it has.
+  int reserve(size_t bytes) {
+    if (bytes <= ws_bytes) return AGMM_OK;
+    // test hook: AGMM_TEST_FAIL_ALLOC=<n> makes every workspace allocation of
+    // more than n bytes fail (n = 0 or 1: all of them)
+    if (const char* hook = std::getenv("AGMM_TEST_FAIL_ALLOC")) {
+      const long long limit = std::atoll(hook);
+      if (limit <= 1 || (long long)bytes > limit)
+        return set_err(AGMM_ERR_OOM, "workspace allocation of %zu bytes failed (forced by test hook)", bytes);
+    }
+    void* q = nullptr;
+    const hipError_t err = hipMalloc(&q, bytes);
+    if (err != hipSuccess) {
+      (void)hipGetLastError();
+      return set_err(AGMM_ERR_OOM, "workspace allocation of %zu bytes failed: %s", bytes, hipGetErrorString(err));
+    }
+    const int rc = idle();   // the previous call may still use the old one
+    if (rc != AGMM_OK) {
+      hipFree(q);
+      return rc;
+    }
+    if (ws) hipFree(ws);
+    ws = static_cast<char*>(q);
+    ws_bytes = bytes;
+    return AGMM_OK;
+  }
+
+  int idle() {
+    if (done != kEager) return AGMM_OK;
+    const hipError_t err = hipEventSynchronize(ev_done);
+    return err == hipSuccess ? AGMM_OK : hip_err(err, "hipEventSynchronize(done)");
+  }
+
+  // Order a call on `s` after the plan's previous one.  Across a graph-capture
+  // boundary no event links calls: the caller's streams order replays.
+  int enter(hipStream_t s, bool& capturing, unsigned long long& id) {
+    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+    id = 0;
+    hipError_t err = hipStreamGetCaptureInfo(s, &st, &id);
+    if (err != hipSuccess) return hip_err(err, "hipStreamGetCaptureInfo");
+    if (st == hipStreamCaptureStatusInvalidated)
+      return set_err(AGMM_ERR_HIP, "the stream's graph capture has been invalidated");
+    capturing = st == hipStreamCaptureStatusActive;
+    if (capturing) captured = true;
+    const bool linked = done == kEager ? !capturing : done == kCaptured && capturing && done_capture == id;
+    if (linked && done_stream != s) {
+      err = hipStreamWaitEvent(s, ev_done, 0);
+      if (err != hipSuccess) return hip_err(err, "hipStreamWaitEvent(done)");
+    }
+    return AGMM_OK;
+  }
+
+  int leave(hipStream_t s, bool capturing, unsigned long long id) {
+    const hipError_t err = hipEventRecord(ev_done, s);
+    if (err != hipSuccess) return hip_err(err, "hipEventRecord(done)");
+    done = capturing ? kCaptured : kEager;
+    done_capture = capturing ? id : 0;
+    done_stream = s;
+    return AGMM_OK;
+  }
+
+  // A call that enqueues work.  One that uses no workspace needs no ordering.
+  template <class F>
+  int run(hipStream_t s, bool ordered, F&& body) {
+    if (!ordered) {
+      const int rc = body();
+      return rc == AGMM_OK ? ok() : rc;
+    }
+    bool capturing = false;
+    unsigned long long id = 0;
+    int rc = enter(s, capturing, id);
+    if (rc != AGMM_OK) return rc;
+    rc = body();
+    if (rc != AGMM_OK) {
+      // whatever was enqueued before the failure still counts
+      const int st = agmm::g_status;
+      const std::string msg = agmm::g_msg;
+      leave(s, capturing, id);
+      return set_err(st, "%s", msg.c_str());
+    }
+    rc = leave(s, capturing, id);
+    return rc == AGMM_OK ? ok() : rc;
+  }
+
+  ~PlanBase() {
+    if (done == kEager && ev_done) hipEventSynchronize(ev_done);
+    (void)hipGetLastError();
+    if (ws) hipFree(ws);
+    if (ev_done) hipEventDestroy(ev_done);
+  }
+};
+
+// The shard and other pointers of a call: none NULL, all aligned.
+int check_ptr(const void* p, const char* name, int index, uintptr_t to) {
+  char label[64];
+  if (index >= 0) snprintf(label, sizeof label, "%s[%d]", name, index);
+  else snprintf(label, sizeof label, "%s", name);
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "%s is NULL", label);
+  if (!aligned(p, to)) return set_err(AGMM_ERR_UNSUPPORTED, "%s is not %d-byte aligned", label, (int)to);
+  return AGMM_OK;
+}
+
+// Row blocks of `rows` x `cols` tiles walked together: the grouping whose
+// first XCD range touches the fewest row and column blocks (tiles of one XCD
+// share its L2).
+int group_rows(int64_t nrb, int64_t ncb) {
+  const int64_t per = cdiv(nrb * ncb, 8);
+  int best = 4;
+  int64_t best_cost = INT64_MAX;
+  for (int g : {4, 8, 2, 16, 1}) {
+    int64_t t = 0, rows = 0, cols = 0;
+    for (int64_t grp = 0; t < per; ++grp) {
+      const int64_t rh = std::min<int64_t>(nrb - grp * g, g), take = std::min(rh * ncb, per - t);
+      rows += std::min(take, rh);
+      cols = std::max(cols, cdiv(take, rh));
+      t += take;
+    }
+    if (rows + cols < best_cost) best_cost = rows + cols, best = g;
+  }
+  return best;
+}
+
+// Rows and columns of a scaled product's C: with m * n below 2^36 the 128 x 128
+// tiles then stay below the launch limit.
+constexpr int64_t kScaledDim = int64_t(1) << 27;
+constexpr int64_t kMaxGrid = int64_t(1) << 23;
+
+int validate_scaled(int N, int64_t m_s, int64_t k, int64_t n, int a_format, int b_block_rows, int c_dtype) {
+  const int rc = check_sizes(N, m_s, k, n);
+  if (rc != AGMM_OK) return rc;
+  if (a_format != AGMM_E4M3 && a_format != AGMM_E5M2)
+    return set_err(AGMM_ERR_INVALID_ARG, "unknown 8-bit format %d", a_format);
+  if (b_block_rows != 1 && b_block_rows != agmm::kScaleBlock)
+    return set_err(AGMM_ERR_INVALID_ARG, "b_block_rows must be 1 or %d (got %d)", agmm::kScaleBlock, b_block_rows);
+  if (c_dtype != AGMM_BF16 && c_dtype != AGMM_FP16 && c_dtype != AGMM_FP32)
+    return set_err(AGMM_ERR_INVALID_ARG, "unknown dtype %d", c_dtype);
+  if (N * m_s >= kScaledDim || n >= kScaledDim || N * m_s * n >= (int64_t(1) << 36))
+    return set_err(AGMM_ERR_UNSUPPORTED, "problem too large (m=%lld, n_local=%lld)", (long long)(N * m_s), (long long)n);
+  return ok();
+}
+
 }  // namespace
+
+struct agmm_scaled_plan : PlanBase {
+  int N = 0;
+  int64_t m_s = 0, k = 0, n = 0, m = 0, k16 = 0;
+  int a_format = 0, b_block_rows = 0, c_dtype = 0;
+  int64_t lda = 0, ldb = 0, ldc = 0;   // 0: dense
+  int tile_key = -1, splits_key = 0;
+  int tile = 0, splits = 1, kb_per_split = 0;
+
+  // Sums of 128 by bf16 MFMAs.  The 8-bit ones lose up to about 3700 units of
+  // 2^-24 of a block's sum of sizes (scaled.hip): below the rounding of a
+  // 16-bit C, and below what fp32 additions over the whole of k may lose from
+  // k = 1024 on, so they are used there and where C is 16 bits.
+  bool wide() const { return c_dtype == AGMM_FP32 || k < 1024; }
+
+  int64_t kb() const { return cdiv(k, agmm::kScaleBlock); }
+
+  // Tile and k ranges for a pair of keys; host only.
+  void derive(int tile_k, int splits_k, int& t, int& sp, int& per) const {
+    const auto tiles = [&](int c) {
+      return cdiv(m, agmm::scaled_tile_rows(c)) * cdiv(n, agmm::scaled_tile_cols(c));
+    };
+    if (tile_k >= 0) t = tile_k;
+    else if (m <= 16 && tiles(agmm::kScaledSkinny16) < kMaxGrid) t = agmm::kScaledSkinny16;
+    else if (m <= 128 && tiles(agmm::kScaledSkinny32) < kMaxGrid) t = agmm::kScaledSkinny32;
+    else {
+      // rounds of workgroups over the CUs times the work of a tile; the large
+      // tile reads half the LDS bytes per product
+      const double big = (double)cdiv(tiles(agmm::kScaled256), cu_count) * 4.0;
+      const double small = (double)cdiv(tiles(agmm::kScaled128), 2 * (int64_t)cu_count) * 2.0 * 1.3;
+      t = !wide() && big <= small ? agmm::kScaled256 : agmm::kScaled128;
+    }
+    int64_t want = splits_k;
+    if (want <= 0) {
+      want = 1;
+      const bool skinny = agmm::scaled_tile_rows(t) < 128;
+      const int64_t slots = cu_count * (t == agmm::kScaled128 ? 2 : 1);
+      const int64_t shortest = skinny ? 4 : 8;   // k blocks of a range
+      while (want * 2 * tiles(t) <= slots && kb() / (want * 2) >= shortest) want *= 2;
+    }
+    want = std::max<int64_t>(1, std::min(want, kb()));
+    per = (int)cdiv(kb(), want);
+    sp = (int)cdiv(kb(), per);
+  }
+
+  size_t need(int sp) const { return sp > 1 ? (size_t)sp * m * n * sizeof(float) : 0; }
+
+  int apply(int tile_k, int splits_k) {
+    int t, sp, per;
+    derive(tile_k, splits_k, t, sp, per);
+    if (cdiv(m, agmm::scaled_tile_rows(t)) * cdiv(n, agmm::scaled_tile_cols(t)) * sp >= kMaxGrid)
+      return set_err(AGMM_ERR_UNSUPPORTED, "too many workgroups for tile %d with %d k ranges", t, sp);
+    const int rc = reserve(need(sp));
+    if (rc != AGMM_OK) return rc;
+    tile_key = tile_k;
+    splits_key = splits_k;
+    tile = t;
+    splits = sp;
+    kb_per_split = per;
+    return ok();
+  }
+};
 
 extern "C" {
 
@@ -72,5 +334,135 @@ int agmm_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t 
   const hipError_t err = agmm::launch_quantize(p, static_cast<hipStream_t>(stream));
   return err == hipSuccess ? ok() : hip_err(err, "quantiser launch");
 }
+
+int agmm_scaled_plan_validate(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_local, int a_format,
+                              int b_block_rows, int c_dtype) {
+  return validate_scaled(num_shards, m_per_shard, k, n_local, a_format, b_block_rows, c_dtype);
+}
+
+agmm_scaled_plan_t agmm_scaled_plan_create(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_local,
+                                           int a_format, int b_block_rows, int c_dtype) {
+  if (validate_scaled(num_shards, m_per_shard, k, n_local, a_format, b_block_rows, c_dtype) != AGMM_OK)
+    return nullptr;
+  agmm_scaled_plan* p = new (std::nothrow) agmm_scaled_plan();
+  if (!p) {
+    set_err(AGMM_ERR_OOM, "out of host memory");
+    return nullptr;
+  }
+  p->N = num_shards;
+  p->m_s = m_per_shard;
+  p->k = k;
+  p->k16 = round_up(k, 16);
+  p->n = n_local;
+  p->m = num_shards * m_per_shard;
+  p->a_format = a_format;
+  p->b_block_rows = b_block_rows;
+  p->c_dtype = c_dtype;
+  if (p->init() != AGMM_OK || p->apply(-1, 0) != AGMM_OK) {
+    const int st = agmm::g_status;
+    const std::string msg = agmm::g_msg;
+    delete p;
+    set_err(st, "%s", msg.c_str());
+    return nullptr;
+  }
+  return p;
+}
+
+int agmm_scaled_plan_set_int(agmm_scaled_plan_t p, const char* key, int64_t v) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!key) return set_err(AGMM_ERR_INVALID_ARG, "key is NULL");
+  std::lock_guard<std::mutex> lk(p->mu);
+  if (p->captured)
+    return set_err(AGMM_ERR_UNSUPPORTED,
+                   "the plan has been captured into a graph; its settings are fixed (create a new plan)");
+  const std::string k(key);
+  const auto bad = [&]() {
+    return set_err(AGMM_ERR_INVALID_ARG, "value %lld out of range for key '%s'", (long long)v, key);
+  };
+  if (k == "tile") {
+    if (v < -1 || v >= agmm::kScaledTiles) return bad();
+    return p->apply((int)v, p->splits_key);
+  }
+  if (k == "splits") {
+    if (v < 0 || v > 4096) return bad();
+    return p->apply(p->tile_key, (int)v);
+  }
+  if (k == "lda" || k == "ldb" || k == "ldc") {
+    const int64_t row = k == "ldc" ? p->n : p->k16;
+    if (v != 0 && (v < row || v >= kDimLimit || (k != "ldc" && v % 16 != 0))) return bad();
+    (k == "lda" ? p->lda : k == "ldb" ? p->ldb : p->ldc) = v;
+    return ok();
+  }
+  return set_err(AGMM_ERR_INVALID_ARG, "unknown key '%s'", key);
+}
+
+int agmm_scaled_plan_get_int(agmm_scaled_plan_t p, const char* key, int64_t* value) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!key || !value) return set_err(AGMM_ERR_INVALID_ARG, "key or value is NULL");
+  std::lock_guard<std::mutex> lk(p->mu);
+  const std::string k(key);
+  if (k == "tile") *value = p->tile;
+  else if (k == "splits") *value = p->splits;
+  else if (k == "lda") *value = p->lda ? p->lda : p->k16;
+  else if (k == "ldb") *value = p->ldb ? p->ldb : p->k16;
+  else if (k == "ldc") *value = p->ldc ? p->ldc : p->n;
+  else if (k == "captured") *value = p->captured;
+  else return set_err(AGMM_ERR_INVALID_ARG, "unknown key '%s'", key);
+  return ok();
+}
+
+size_t agmm_scaled_plan_workspace_bytes(agmm_scaled_plan_t p) { return p ? p->ws_bytes : 0; }
+
+int agmm_scaled_run(agmm_scaled_plan_t p, const void* const* shard_ptrs, const float* const* scale_ptrs,
+                    const void* B, const float* B_scales, void* C, void* stream) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!shard_ptrs || !scale_ptrs) return set_err(AGMM_ERR_INVALID_ARG, "shard_ptrs or scale_ptrs is NULL");
+  int rc = AGMM_OK;
+  for (int r = 0; r < p->N && rc == AGMM_OK; ++r) {
+    rc = check_ptr(shard_ptrs[r], "shard_ptrs", r, 16);
+    if (rc == AGMM_OK) rc = check_ptr(scale_ptrs[r], "scale_ptrs", r, 4);
+  }
+  if (rc == AGMM_OK) rc = check_ptr(B, "B", -1, 16);
+  if (rc == AGMM_OK) rc = check_ptr(B_scales, "B_scales", -1, 4);
+  if (rc == AGMM_OK) rc = check_ptr(C, "C", -1, 16);
+  if (rc != AGMM_OK) return rc;
+  std::lock_guard<std::mutex> lk(p->mu);
+  agmm::ScaledProblem g{};
+  for (int r = 0; r < p->N; ++r) {
+    g.a_group[r] = shard_ptrs[r];
+    g.a_scale[r] = scale_ptrs[r];
+  }
+  g.a_ld = p->lda ? p->lda : p->k16;
+  g.rows_per_group = (int32_t)p->m_s;
+  g.num_groups = p->N;
+  g.m = (int32_t)p->m;
+  g.n = (int32_t)p->n;
+  g.k16 = (int32_t)p->k16;
+  g.kb = (int32_t)p->kb();
+  g.b = B;
+  g.ldb = p->ldb ? p->ldb : p->k16;
+  g.b_scale = B_scales;
+  g.nb = (int32_t)cdiv(p->n, p->b_block_rows);
+  g.b_block_rows = p->b_block_rows;
+  g.a_format = p->a_format;
+  g.c = C;
+  g.ldc = p->ldc ? p->ldc : p->n;
+  g.c_dtype = p->c_dtype;
+  g.wide = p->wide();
+  g.order.num_rb = (int32_t)cdiv(p->m, agmm::scaled_tile_rows(p->tile));
+  g.order.num_cb = (int32_t)cdiv(p->n, agmm::scaled_tile_cols(p->tile));
+  g.order.group_m = group_rows(g.order.num_rb, g.order.num_cb);
+  g.order.xcd_remap = 1;
+  g.splits = p->splits;
+  g.kb_per_split = p->kb_per_split;
+  g.partials = reinterpret_cast<float*>(p->ws);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return p->run(s, p->splits > 1, [&]() -> int {
+    const hipError_t err = agmm::launch_scaled(g, p->tile, s);
+    return err == hipSuccess ? AGMM_OK : hip_err(err, "scaled product launch");
+  });
+}
+
+void agmm_scaled_plan_destroy(agmm_scaled_plan_t p) { delete p; }
 
 }  // extern "C"

@@ -445,6 +445,80 @@ int agmm_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t 
                   int block_rows, void *q, int64_t ldq, float *scale, void *qt, int64_t ldqt,
                   float *scale_t, void *stream);
 
+/*
+ * Block-scaled 8-bit product over the shards' rows:
+ *
+ *     C[m, n_local] = concat_r(A_r) @ B^T
+ *
+ * with A_r and B as agmm_quantize lays them out (B stored [n_local, k]) and
+ * every element standing for its 8-bit value times its block's scale.  The
+ * products of one block of 128 of k are summed by the matrix cores, scaled in
+ * fp32 and added in fp32; C is rounded once.  With a 16-bit C and k >= 1024
+ * the sums of 128 are those of the 8-bit matrix instruction, whose adder may
+ * lose up to 2^-12 of the sum of a block's |terms|; otherwise (and for
+ * m <= 128) they are fp32 sums of exact products.
+ * A linear layer y = x W^T trains with three such products: y from x and W;
+ * dx from dy and W transposed (the weight's blocks are square, so W and its
+ * transpose hold the same values); dW from dy transposed and x transposed,
+ * with b_block_rows 1.
+ */
+typedef struct agmm_scaled_plan agmm_scaled_plan;
+typedef agmm_scaled_plan *agmm_scaled_plan_t;
+
+/* Check a problem without touching the GPU: agmm_plan_validate's rules for
+ * the sizes, m and n_local < 2^27, m * n_local < 2^36, and
+ *   a_format      agmm_format of the shards (B is AGMM_E4M3)
+ *   b_block_rows  1 or 128: rows of B that share a scale (A: 1)
+ *   c_dtype       agmm_dtype of C
+ * Any k >= 1: rows are read up to k rounded up to 16, where they hold zeros. */
+int agmm_scaled_plan_validate(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_local,
+                              int a_format, int b_block_rows, int c_dtype);
+
+/* Create a plan on the current HIP device (NULL on failure).  It allocates
+ * what a run needs (fp32 partial sums where few output tiles make it split
+ * k), so agmm_scaled_run never allocates. */
+agmm_scaled_plan_t agmm_scaled_plan_create(int num_shards, int64_t m_per_shard, int64_t k,
+                                           int64_t n_local, int a_format, int b_block_rows,
+                                           int c_dtype);
+
+/*
+ * Enqueue C on `stream`.
+ *   shard_ptrs  host array of num_shards device pointers: [m_per_shard, k] 8-bit values, rows
+ *               "lda" bytes apart (default: k rounded up to 16), zeros past k up to there
+ *   scale_ptrs  host array of num_shards device pointers: fp32 [ceil(k / 128), m_per_shard]
+ *   B           device, [n_local, k] e4m3 values, rows "ldb" bytes apart (same default and rule)
+ *   B_scales    device, fp32 [ceil(k / 128), ceil(n_local / b_block_rows)]
+ *   C           device, [m, n_local] of c_dtype, rows "ldc" elements apart; must not overlap an
+ *               input
+ * Values and C are 16-byte aligned, scales 4-byte.  A NaN or infinity in a
+ * row of A or B reaches that row's or column's results only.  Stream,
+ * capture and ordering rules are agmm_run's (a plan that does not split k
+ * shares nothing between calls and orders none).  Returns AGMM_OK,
+ * AGMM_ERR_INVALID_ARG, AGMM_ERR_UNSUPPORTED (alignment) or AGMM_ERR_HIP.
+ */
+int agmm_scaled_run(agmm_scaled_plan_t plan, const void *const *shard_ptrs,
+                    const float *const *scale_ptrs, const void *B, const float *B_scales, void *C,
+                    void *stream);
+
+/*
+ * Tune a plan.  Keys:
+ *   "lda", "ldb"  bytes between rows of the shards and of B: 0 (dense) or a multiple of 16, at
+ *                 least k rounded up to 16
+ *   "ldc"         elements between rows of C: 0 (dense) or at least n_local
+ *   "tile"        -1 automatic, 0 256 x 256 (always on the 8-bit matrix instruction), 1 128 x 128,
+ *                 2 16 x 32, 3 32 x 32 (rows x columns; 2 and 3 share k out over the waves of a
+ *                 workgroup; automatic for m <= 16 and m <= 128)
+ *   "splits"      0 automatic, else k ranges summed in a fixed order
+ * Settings are fixed once a call was captured into a graph.  get reads the
+ * values in use, and "captured".
+ */
+int agmm_scaled_plan_set_int(agmm_scaled_plan_t plan, const char *key, int64_t value);
+int agmm_scaled_plan_get_int(agmm_scaled_plan_t plan, const char *key, int64_t *value);
+size_t agmm_scaled_plan_workspace_bytes(agmm_scaled_plan_t plan);
+
+/* Wait for the plan's last call, then free it.  NULL is a no-op. */
+void agmm_scaled_plan_destroy(agmm_scaled_plan_t plan);
+
 /* Thread-local status / message of this thread's most recent call into the
  * library (AGMM_OK and "" after a call that succeeded; calls on other threads
  * never change them). */

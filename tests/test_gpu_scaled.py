@@ -167,3 +167,230 @@ def test_quantize_refusals():
         agmm.quantize(x.double())
     with pytest.raises(ValueError, match="GPU"):
         agmm.quantize(x.cpu())
+
+
+# ---------------------------------------------------------------- product
+#
+# Tolerance.  The 8-bit products are exact in fp32; the sum of n of them with
+# any order of fp32 additions is off by at most (n - 1) u sum |terms|, u =
+# 2^-24, and a truncating adder at most twice that.  Each scaling adds u per
+# block, C's rounding half a unit of its type.  So
+#   |C - ref| <= (2 k + 8) u * sum |a b|  +  half ulp(ref) (+ its spacing at 0).
+HALF_ULP = {agmm.AGMM_BF16: 2.0 ** -8, agmm.AGMM_FP16: 2.0 ** -11, agmm.AGMM_FP32: 2.0 ** -24}
+FLOOR = {agmm.AGMM_BF16: 0.0, agmm.AGMM_FP16: 2.0 ** -25, agmm.AGMM_FP32: 0.0}
+
+
+def operand(rows, k, fmt, block, seed, device="cuda"):
+    """A Scaled made on the CPU with scales of its own (not from a quantiser):
+    random 8-bit values and fp32 scales, zeros past k."""
+    g = torch.Generator().manual_seed(seed)
+    values = torch.zeros((rows, -(-k // 16) * 16))
+    values[:, :k] = torch.randn((rows, k), generator=g) * 8
+    scales = torch.exp2(torch.rand((-(-k // 128), -(-rows // block)), generator=g) * 12 - 9)
+    return agmm.Scaled(values.to(F8[fmt]).to(device), scales.to(device), k, block)
+
+
+def spread64(x):
+    v = x.values[:, :x.k].cpu().float().double()
+    s = x.scales.cpu().double().t().repeat_interleave(128, dim=1)[:, :x.k]
+    return v * s.repeat_interleave(x.block_rows, dim=0)[:x.rows]
+
+
+def check_product(got, a, b, c_dtype):
+    ref = a @ b.t()
+    size = a.abs() @ b.abs().t()
+    k = a.shape[1]
+    bound = (2 * k + 8) * 2.0 ** -24 * size + HALF_ULP[c_dtype] * ref.abs() * (1 + 2.0 ** -7) + FLOOR[c_dtype]
+    got = got.cpu().double()
+    if c_dtype == agmm.AGMM_FP16:   # beyond fp16's range: an infinity of the right sign, within the bound of its edge
+        over = torch.isinf(got)
+        assert (ref[over].abs() + bound[over] >= 65520).all() and torch.equal(got[over].sign(), ref[over].sign())
+        assert (over | (ref.abs() - bound < 65520)).all()
+        got, ref, bound = got[~over], ref[~over], bound[~over]
+    assert torch.isfinite(got).all()
+    err = (got - ref).abs()
+    worst = (err - bound).max().item()
+    assert worst <= 0, (worst, err.max().item())
+
+
+def run_product(N, ms, k, n, fmt="e4m3", block=128, c_dtype=agmm.AGMM_BF16, seed=0, **settings):
+    shards = [operand(ms, k, fmt, 1, seed * 100 + r) for r in range(N)]
+    B = operand(n, k, "e4m3", block, seed * 100 + 99)
+    with agmm.ScaledPlan(N, ms, k, n, fmt, block, c_dtype, **settings) as plan:
+        C = plan.run(shards, B)
+        torch.cuda.synchronize()
+        used = plan.get("tile"), plan.get("splits")
+    check_product(C, torch.cat([spread64(s) for s in shards]), spread64(B), c_dtype)
+    return C, shards, B, used
+
+
+@pytest.mark.parametrize("N,ms,k,n", [
+    (1, 1, 1, 1), (1, 1, 128, 16), (8, 1, 512, 48), (3, 5, 130, 33), (2, 8, 1000, 100), (1, 16, 2048, 64),
+    (4, 16, 272, 96), (1, 129, 128, 128), (2, 100, 256, 200), (3, 337, 404, 261), (1, 256, 640, 256),
+    (2, 256, 128, 512), (5, 103, 1160, 515), (64, 5, 144, 140), (2, 512, 4096, 256)])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("block", [1, 128])
+def test_product(N, ms, k, n, fmt, block):
+    run_product(N, ms, k, n, fmt, block, agmm.AGMM_BF16, seed=ms + k)
+
+
+@pytest.mark.parametrize("tile", [0, 1, 2, 3])
+@pytest.mark.parametrize("c_dtype", [agmm.AGMM_BF16, agmm.AGMM_FP16, agmm.AGMM_FP32])
+@pytest.mark.parametrize("N,ms,k,n", [(2, 20, 700, 70), (1, 300, 1300, 301), (2, 256, 512, 512)])
+def test_product_every_tile(tile, c_dtype, N, ms, k, n):
+    for splits in (1, 2, 3):
+        _, _, _, used = run_product(N, ms, k, n, c_dtype=c_dtype, tile=tile, splits=splits, seed=7)
+        kb = -(-k // 128)
+        assert used == (tile, -(-kb // -(-kb // splits)))   # ranges of equal whole blocks
+
+
+def test_product_strides():
+    """Operands and C as views with row strides; bytes between C's rows stay."""
+    N, ms, k, n = 2, 70, 300, 90
+    shards = [operand(ms, k, "e4m3", 1, r) for r in range(N)]
+    B = operand(n, k, "e4m3", 128, 9)
+
+    def wide(x, ld):
+        buf = torch.full((x.rows, ld), 127, dtype=torch.uint8, device="cuda").view(x.values.dtype)   # NaN
+        buf[:, :x.values.shape[1]] = x.values
+        return agmm.Scaled(buf[:, :x.values.shape[1]], x.scales, x.k, x.block_rows)
+
+    buf = torch.full((N * ms, 101), -7.0, dtype=torch.bfloat16, device="cuda")
+    with agmm.ScaledPlan(N, ms, k, n, "e4m3", 128, agmm.AGMM_BF16, lda=336, ldb=320, ldc=101) as plan:
+        C = plan.run([wide(s, 336) for s in shards], wide(B, 320), buf[:, :n])
+    torch.cuda.synchronize()
+    check_product(C, torch.cat([spread64(s) for s in shards]), spread64(B), agmm.AGMM_BF16)
+    assert (buf[:, n:] == -7).all()
+
+
+def test_product_keeps_rows_and_columns_apart():
+    """NaN in one row of A and one row of B reaches that row and column only."""
+    N, ms, k, n = 2, 150, 256, 140
+    shards = [operand(ms, k, "e4m3", 1, r) for r in range(N)]
+    B = operand(n, k, "e4m3", 128, 9)
+    with agmm.ScaledPlan(N, ms, k, n) as plan:
+        want = plan.run(shards, B)
+        shards[1].values.view(torch.uint8)[7, 200] = 0x7F
+        B.values.view(torch.uint8)[33, 3] = 0x7F
+        got = plan.run(shards, B)
+    torch.cuda.synchronize()
+    bad = torch.isnan(got)
+    assert bad[ms + 7].all() and bad[:, 33].all()
+    bad[ms + 7] = False
+    bad[:, 33] = False
+    assert not bad.any()
+    keep = torch.ones_like(bad)
+    keep[ms + 7] = False
+    keep[:, 33] = False
+    assert torch.equal(got[keep], want[keep])
+
+
+def test_product_calls_share_a_plan_across_streams():
+    """A plan that splits k (its partial sums are shared), called on two
+    streams with other inputs each: every result is that of its inputs."""
+    N, ms, k, n = 1, 16, 8192, 64
+    with agmm.ScaledPlan(N, ms, k, n, splits=8) as plan:
+        sets = [([operand(ms, k, "e4m3", 1, 10 + i)], operand(n, k, "e4m3", 128, 20 + i)) for i in range(2)]
+        want = [plan.run(*s) for s in sets]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        got = [[], []]
+        for _ in range(20):
+            for i in range(2):
+                got[i].append(plan.run(*sets[i], stream=streams[i]))
+        torch.cuda.synchronize()
+    for i in range(2):
+        check_product(want[i], spread64(sets[i][0][0]), spread64(sets[i][1]), agmm.AGMM_BF16)
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+def test_product_in_a_graph():
+    N, ms, k, n = 2, 8, 2048, 96
+    shards = [operand(ms, k, "e4m3", 1, r) for r in range(N)]
+    B = operand(n, k, "e4m3", 128, 5)
+    with agmm.ScaledPlan(N, ms, k, n) as plan:
+        C = torch.empty((N * ms, n), dtype=torch.bfloat16, device="cuda")
+        want = plan.run(shards, B).clone()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            plan.run(shards, B, C)
+        for _ in range(4):
+            C.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(C, want)
+        with pytest.raises(agmm.AgmmError) as ei:
+            plan.set("splits", 1)
+        assert ei.value.status == agmm.AGMM_ERR_UNSUPPORTED
+        del graph
+
+
+def test_product_of_quantised_operands():
+    """Quantise and multiply: against the product of the unquantised matrices,
+    within the formats' half spacing (2^-4 relative for e4m3) per factor."""
+    g = torch.Generator().manual_seed(0)
+    x, w = torch.randn((200, 1000), generator=g), torch.randn((150, 1000), generator=g) / 30
+    shards = [agmm.quantize(s.bfloat16().cuda()) for s in x.split(100)]
+    W = agmm.quantize(w.cuda(), block_rows=128)
+    with agmm.ScaledPlan(2, 100, 1000, 150, c_dtype=agmm.AGMM_FP32) as plan:
+        C = plan.run(shards, W)
+    torch.cuda.synchronize()
+    ref = x.double() @ w.double().t()
+    rel = (C.cpu().double() - ref).norm() / ref.norm()
+    assert rel < 2.0 ** -4
+    check_product(C, torch.cat([spread64(s) for s in shards]), spread64(W), agmm.AGMM_FP32)
+
+
+def test_product_training_identities():
+    """dx and dW of y = x W^T through the same product on transposed
+    operands, against their formulas on the quantised values."""
+    g = torch.Generator().manual_seed(1)
+    m, k, n = 260, 300, 200
+    x, dy, w = (torch.randn(s, generator=g).cuda() for s in ((m, k), (m, n), (n, k)))
+    xq, xt = agmm.quantize(x, out="both")
+    dq, dt = agmm.quantize(dy, "e5m2", out="both")
+    wq, wt = agmm.quantize(w, block_rows=128, out="both")
+    assert torch.equal(wq.dequantize(), wt.dequantize().t())
+    with agmm.ScaledPlan(1, m, n, k, "e5m2", 128, agmm.AGMM_FP32) as plan:
+        dx = plan.run([dq], wt)
+    with agmm.ScaledPlan(1, n, m, k, "e5m2", 1, agmm.AGMM_FP32) as plan:
+        dw = plan.run([dt], xt)
+    torch.cuda.synchronize()
+    check_product(dx, spread64(dq), spread64(wt), agmm.AGMM_FP32)
+    check_product(dw, spread64(dt), spread64(xt), agmm.AGMM_FP32)
+
+
+def test_product_refusals():
+    a, b = operand(8, 64, "e4m3", 1, 0), operand(16, 64, "e4m3", 128, 1)
+    with agmm.ScaledPlan(1, 8, 64, 16) as plan:
+        with pytest.raises(ValueError, match="shards"):
+            plan.run([a, a], b)
+        with pytest.raises(TypeError, match="Scaled"):
+            plan.run([a.values], b)
+        with pytest.raises(ValueError, match="block_rows"):
+            plan.run([a], operand(16, 64, "e4m3", 1, 1))
+        with pytest.raises(TypeError, match="dtype"):
+            plan.run([operand(8, 64, "e5m2", 1, 0)], b)
+        with pytest.raises(ValueError, match="shape"):
+            plan.run([operand(9, 64, "e4m3", 1, 0)], b)
+        with pytest.raises(ValueError, match="GPU"):
+            plan.run([operand(8, 64, "e4m3", 1, 0, "cpu")], b)
+        with pytest.raises(ValueError, match="row-major"):
+            plan.run([a], b, torch.empty((16, 8), dtype=torch.bfloat16, device="cuda").t())
+        for key, val in (("lda", 48), ("lda", 72), ("ldc", 8), ("tile", 4), ("splits", -1), ("nothing", 1)):
+            with pytest.raises(agmm.AgmmError) as ei:
+                plan.set(key, val)
+            assert ei.value.status == agmm.AGMM_ERR_INVALID_ARG
+        with pytest.raises(ValueError, match="row-major"):
+            plan.set("lda", 80)
+            plan.run([a], b)
+
+
+def test_product_out_of_memory_is_an_error(monkeypatch):
+    monkeypatch.setenv("AGMM_TEST_FAIL_ALLOC", "1")
+    with pytest.raises(agmm.AgmmError) as ei:
+        agmm.ScaledPlan(1, 16, 8192, 64)
+    assert ei.value.status == agmm.AGMM_ERR_OOM
+    with agmm.ScaledPlan(1, 512, 512, 65536) as plan:
+        assert plan.workspace_bytes() == 0      # no k split: nothing to allocate
