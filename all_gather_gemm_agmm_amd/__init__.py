@@ -66,6 +66,14 @@ EXPORTS = [
     ("agmm_scaled_plan_get_int", _ci, [_vp, _cc, ctypes.POINTER(_i64)]),
     ("agmm_scaled_plan_workspace_bytes", ctypes.c_size_t, [_vp]),
     ("agmm_scaled_plan_destroy", None, [_vp]),
+    ("agmm_loss_plan_validate", _ci, [_ci, _i64, _i64, _i64, _ci, _i64, _i64]),
+    ("agmm_loss_plan_create", _vp, [_ci, _i64, _i64, _i64, _ci, _i64, _i64, _ci]),
+    ("agmm_loss_forward", _ci, [_vp, ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("agmm_loss_backward", _ci, [_vp, ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("agmm_loss_plan_set_int", _ci, [_vp, _cc, _i64]),
+    ("agmm_loss_plan_get_int", _ci, [_vp, _cc, ctypes.POINTER(_i64)]),
+    ("agmm_loss_plan_workspace_bytes", ctypes.c_size_t, [_vp]),
+    ("agmm_loss_plan_destroy", None, [_vp]),
     ("agmm_last_status", _ci, []),
     ("agmm_last_error", _cc, []),
     ("agmm_version", _cc, []),
@@ -664,6 +672,80 @@ class ScaledPlan(_OpPlan):
             _check(load_library().agmm_scaled_run(self.handle, self._a, self._s, b, bs, c,
                                                   _stream_handle(stream, self.device)))
         return C
+
+
+class LossPlan(_OpPlan):
+    """Softmax cross entropy of the vocabulary projection concat_r(shards[r])
+    @ W^T without its logits, and its gradient (agmm_loss_forward,
+    agmm_loss_backward).  W [n_local, k] holds columns [vocab_start,
+    vocab_start + n_local) of a vocabulary of `vocab_size` (default: all of
+    it); `merge_vocab_slices` joins the results of several devices."""
+
+    _prefix = "agmm_loss_plan"
+    _strides = ("lda", "ldw", "ldda", "lddw")
+
+    def __init__(self, num_shards: int, m_per_shard: int, k: int, n_local: int, dtype: int = AGMM_BF16,
+                 vocab_start: int = 0, vocab_size: Optional[int] = None, with_gradient: bool = True, **settings):
+        self._make(num_shards, m_per_shard, k, n_local, dtype, vocab_start,
+                   vocab_start + n_local if vocab_size is None else vocab_size, int(bool(with_gradient)))
+        import torch
+        self.num_shards, self.m_per_shard, self.k, self.n_local = num_shards, m_per_shard, k, n_local
+        self._tdt, self._f32, self._i64 = _torch_dtype(dtype), torch.float32, torch.int64
+        self._a = (ctypes.c_void_p * num_shards)()
+        self._read_strides()
+        for key, val in settings.items():
+            if val is not None:
+                self.set(key, val)
+
+    def _operands(self, shards, W, labels):
+        if len(shards) != self.num_shards:
+            raise ValueError(f"expected {self.num_shards} shards, got {len(shards)}")
+        for r, s in enumerate(shards):
+            self._a[r] = self._on(s, (self.m_per_shard, self.k), self._tdt, f"shards[{r}]", self._ld["lda"])
+        return (self._on(W, (self.n_local, self.k), self._tdt, "W", self._ld["ldw"]),
+                self._on(labels, (self.m,), self._i64, "labels"))
+
+    def forward(self, shards, W, labels, stream=None):
+        """(loss, lse, target), fp32 [m] each."""
+        import torch
+        w, lab = self._operands(shards, W, labels)
+        with _device_and_stream(W.device, stream):
+            loss, lse, target = (torch.empty(self.m, dtype=self._f32, device=W.device) for _ in range(3))
+            _check(load_library().agmm_loss_forward(self.handle, self._a, w, lab, loss.data_ptr(), lse.data_ptr(),
+                                                    target.data_ptr(), _stream_handle(stream, self.device)))
+        return loss, lse, target
+
+    def backward(self, shards, W, labels, lse, grad_loss, grad_lse=None, dA=None, dW=None, need_dA: bool = True,
+                 need_dW: bool = True, stream=None):
+        """(dA [m, k], dW [n_local, k]) for upstream gradients of loss and,
+        optionally, lse; None in the place of one that is not needed."""
+        w, lab = self._operands(shards, W, labels)
+        m = (self.m,)
+        ls, gl = self._on(lse, m, self._f32, "lse"), self._on(grad_loss, m, self._f32, "grad_loss")
+        gz = None if grad_lse is None else self._on(grad_lse, m, self._f32, "grad_lse")
+        with _device_and_stream(W.device, stream):
+            if dA is None and need_dA:
+                dA = self._new(self.m, self.k, self._ld["ldda"], self._tdt, W.device)
+            if dW is None and need_dW:
+                dW = self._new(self.n_local, self.k, self._ld["lddw"], self._tdt, W.device)
+            da = None if dA is None else self._on(dA, (self.m, self.k), self._tdt, "dA", self._ld["ldda"])
+            dw = None if dW is None else self._on(dW, (self.n_local, self.k), self._tdt, "dW", self._ld["lddw"])
+            _check(load_library().agmm_loss_backward(self.handle, self._a, w, lab, ls, gl, gz, da, dw,
+                                                     _stream_handle(stream, self.device)))
+        return dA, dW
+
+
+def merge_vocab_slices(lse, target, labels, vocab_size: int, ignore_index: int = -100):
+    """(loss, lse) over a whole vocabulary from the devices' `lse` and
+    `target`, [slices, m] each (torch operations on [slices, m] values): the
+    log-sum-exp of the slices' and the sum of their targets.  As in LossPlan,
+    ignored rows have loss 0, labels outside the vocabulary NaN."""
+    import torch
+    whole = torch.logsumexp(lse, dim=0)
+    loss = whole - target.sum(dim=0)
+    bad = (labels < 0) | (labels >= vocab_size)
+    loss = torch.where(bad, torch.full_like(loss, float("nan")), loss)
+    return torch.where(labels == ignore_index, torch.zeros_like(loss), loss), whole
 
 
 # ------------------------------------------------ one call, cached plans

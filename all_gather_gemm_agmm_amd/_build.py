@@ -27,7 +27,7 @@ COMMON = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
-# Per-source extra flags.  The MFMA GEMM asks the machine scheduler to favour
+# Per-source extra flags.  The kernels around the MFMA GEMM's main loop ask the machine scheduler to favour
 # latency hiding (it keeps several LDS fragment loads in flight ahead of the
 # MFMAs instead of minimising register pressure).
 SOURCES = {
@@ -39,6 +39,8 @@ SOURCES = {
     "agmm_ops.cpp": [],
     "quantize.hip": [],
     "scaled.hip": [],
+    "loss_logits.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
+    "loss_grads.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
 }
 
 

@@ -216,6 +216,65 @@ constexpr int scaled_tile_rows(int t) {
 constexpr int scaled_tile_cols(int t) { return t == kScaled256 ? 256 : t == kScaled128 ? 128 : 32; }
 hipError_t launch_scaled(const ScaledProblem& p, int tile, hipStream_t stream);
 
+// Vocabulary loss over one piece of the vocabulary: gemm describes the logits
+// of the piece (A rows through the row map, B the piece's rows of W, n x k;
+// rows of whole 16-byte vectors), label0 is the label of its column 0.
+struct LossProblem {
+  GemmProblem gemm;
+  int32_t tile;            // 256 or 128
+  const int64_t* labels;   // [m]
+  int64_t label0;
+  // statistics: (maximum, sum of exp) pairs [2 * column block + half][m]
+  float* stats;
+  float* target;           // [m], written where the piece holds the label
+  // gradient: rows {lse, a, b, s} [m]; d [m][ldd] and dt [n][ldt], the
+  // columns past n (m) up to ldd (ldt) within the last tile as zeros
+  const float* rows;
+  const float* scale_all;
+  void* d;
+  int64_t ldd;
+  void* dt;
+  int64_t ldt;
+};
+hipError_t launch_loss_logits(const LossProblem& p, int dtype, bool grad, hipStream_t stream);
+
+struct LossCombine {
+  const float* stats;
+  int32_t parts;
+  int64_t m;
+  float* running;          // (maximum, sum) [m] between pieces
+  int32_t first, last;
+  const int64_t* labels;
+  int64_t start, n, total, ignore;
+  float *loss, *lse, *target;
+};
+hipError_t launch_loss_combine(const LossCombine& c, hipStream_t stream);
+
+struct LossRows {
+  int64_t m;
+  const int64_t* labels;
+  int64_t total, ignore;
+  const float *lse, *grad_loss, *grad_lse;   // grad_lse may be null
+  float* rows;
+  float* scale_all;
+};
+hipError_t launch_loss_rows(const LossRows& c, hipStream_t stream);
+
+// fp32 sums of d W: A = d [m][ldd], B = W k x n; into p.partials [splits][m][n].
+hipError_t launch_loss_da(const GemmProblem& p, int tile, int dtype, bool add, hipStream_t stream);
+// C = scale[0] * dt A.
+hipError_t launch_loss_dw(const GemmProblem& p, int tile, int dtype, const float* scale, hipStream_t stream);
+struct LossFinish {
+  const float* sums;       // [ranges][m][k]
+  int32_t ranges;
+  int64_t m;
+  int32_t k;
+  const float* rows;
+  void* da;
+  int64_t ldda;
+};
+hipError_t launch_loss_da_finish(const LossFinish& c, int dtype, hipStream_t stream);
+
 // Size of the device scratch of the no-allocation entry point (one per GPU,
 // held for the life of the process; equal to AGMM_NOALLOC_SCRATCH_BYTES).
 constexpr size_t kNoallocScratchBytes = size_t(32) << 20;

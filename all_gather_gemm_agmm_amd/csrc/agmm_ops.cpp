@@ -1,5 +1,5 @@
 // C ABI of the operators around the all-gather matmul (host side): the
-// block-scaled 8-bit quantiser and product.
+// block-scaled 8-bit quantiser and product, and the vocabulary loss.
 //
 // Their plans are used as the all-gather matmul's are: a plan validates its
 // problem, owns a workspace when a call needs one, and orders its calls: every
@@ -285,6 +285,341 @@ struct agmm_scaled_plan : PlanBase {
   }
 };
 
+namespace {
+
+int validate_loss(int N, int64_t m_s, int64_t k, int64_t n, int dtype, int64_t start, int64_t total) {
+  const int rc = check_sizes(N, m_s, k, n);
+  if (rc != AGMM_OK) return rc;
+  if (dtype == AGMM_FP32)
+    return set_err(AGMM_ERR_UNSUPPORTED, "the vocabulary loss takes bf16 or fp16 operands");
+  if (dtype != AGMM_BF16 && dtype != AGMM_FP16) return set_err(AGMM_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (start < 0 || total < 1 || total >= kElemLimit || start + n > total)
+    return set_err(AGMM_ERR_INVALID_ARG, "columns [%lld, %lld) do not lie in a vocabulary of %lld", (long long)start,
+                   (long long)(start + n), (long long)total);
+  if (N * m_s >= (int64_t(1) << 27) || n >= (int64_t(1) << 27))
+    return set_err(AGMM_ERR_UNSUPPORTED, "problem too large (m=%lld, n_local=%lld)", (long long)(N * m_s), (long long)n);
+  return ok();
+}
+
+// A workspace cut into 256-byte aligned pieces.  With base NULL it only adds
+// up sizes.
+struct Cut {
+  char* base;
+  size_t at = 0;
+  char* take(size_t bytes) {
+    char* p = base ? base + at : nullptr;
+    at += (bytes + 255) & ~size_t(255);
+    return p;
+  }
+};
+
+}  // namespace
+
+struct agmm_loss_plan : PlanBase {
+  int N = 0;
+  int64_t m_s = 0, k = 0, n = 0, m = 0;
+  int dtype = 0;
+  int64_t start = 0, total = 0, ignore = -100;
+  bool with_gradient = true;
+  int64_t lda = 0, ldw = 0, ldda = 0, lddw = 0;   // 0: dense
+  int64_t piece_key = 0;                          // columns per piece; 0: automatic
+
+  // What a call of a pass uses, derived from the settings.
+  struct Layout {
+    bool pad_a = false, pad_w = false;   // rows that are not whole 16-byte vectors: zero-padded copies
+    int64_t kp = 0;                      // k rounded up to 8
+    int64_t piece = 0;                   // columns of the vocabulary per piece
+    int tile = 256, tile_da = 256, tile_dw = 256;
+    int ranges = 1;                      // k ranges of the dA product
+    int64_t per_range = 0;
+    char *a = nullptr, *w = nullptr, *d = nullptr, *dt = nullptr;
+    float *stats = nullptr, *running = nullptr, *rows = nullptr, *scale_all = nullptr, *sums = nullptr;
+    size_t bytes = 0;
+  };
+
+  int64_t ld_a() const { return lda ? lda : k; }
+  int64_t ld_w() const { return ldw ? ldw : k; }
+  int64_t m8() const { return round_up(m, 8); }
+
+  // 256 x 256 tiles unless 128 x 128 ones (two per CU, 0.8 of the rate) need
+  // fewer rounds of the CUs.
+  int pick_tile(int64_t rows, int64_t cols) const {
+    const double big = (double)cdiv(cdiv(rows, 256) * cdiv(cols, 256), cu_count) * 4.0;
+    const double small = (double)cdiv(cdiv(rows, 128) * cdiv(cols, 128), cu_count) / 0.8;
+    return big <= small ? 256 : 128;
+  }
+
+  Layout layout(bool grad, char* base) const {
+    Layout L;
+    L.kp = round_up(k, 8);
+    L.pad_a = k % 8 != 0 || ld_a() % 8 != 0;
+    L.pad_w = k % 8 != 0 || ld_w() % 8 != 0;
+    // Piece: the gradient keeps d twice (16 bits) for a piece, the forward
+    // pass 8 bytes per row and 64 columns; 512 MiB of either by default, which
+    // at 8192 rows is 16384 columns, long enough for the three products.
+    const int64_t budget = int64_t(512) << 20;
+    int64_t piece = piece_key;
+    if (!piece) piece = grad ? budget / (4 * m8()) : budget / (m * 8) * 64;
+    if (!piece_key && L.pad_w) piece = std::min(piece, budget / (2 * L.kp));
+    piece = std::max<int64_t>(256, piece / 256 * 256);
+    L.piece = std::min(piece, n);
+    L.tile = pick_tile(m, L.piece);
+    Cut c{base};
+    if (L.pad_w) L.w = c.take((size_t)L.piece * L.kp * 2);
+    if (!grad) {
+      if (L.pad_a) L.a = c.take((size_t)m * L.kp * 2);
+      L.stats = reinterpret_cast<float*>(c.take((size_t)cdiv(L.piece, L.tile) * 2 * m * 8));
+      L.running = reinterpret_cast<float*>(c.take((size_t)m * 8));
+    } else {
+      if (L.pad_a || N > 1) L.a = c.take((size_t)m * L.kp * 2);
+      L.rows = reinterpret_cast<float*>(c.take((size_t)m * 16));
+      L.scale_all = reinterpret_cast<float*>(c.take(4));
+      L.d = c.take((size_t)m * round_up(L.piece, 8) * 2);
+      L.dt = c.take((size_t)L.piece * m8() * 2);
+      L.tile_da = pick_tile(m, k);
+      L.tile_dw = pick_tile(L.piece, k);
+      // ranges of a piece's columns where dA has too few output tiles
+      const int64_t tiles = cdiv(m, L.tile_da) * cdiv(k, L.tile_da);
+      const int64_t slots = (int64_t)cu_count * (L.tile_da == 128 ? 2 : 1);
+      int64_t want = 1;
+      while (want * 2 * tiles <= slots && L.piece / (want * 2) >= 512) want *= 2;
+      L.per_range = round_up(cdiv(L.piece, want), 64);
+      L.ranges = (int)cdiv(L.piece, L.per_range);
+      L.sums = reinterpret_cast<float*>(c.take((size_t)L.ranges * m * k * 4));
+    }
+    L.bytes = c.at;
+    return L;
+  }
+
+  int apply() {
+    const size_t fwd = layout(false, nullptr).bytes;
+    return reserve(with_gradient ? std::max(fwd, layout(true, nullptr).bytes) : fwd);
+  }
+
+  agmm::TileOrder order(int64_t rows, int64_t cols, int tile) const {
+    agmm::TileOrder o{};
+    o.num_rb = (int32_t)cdiv(rows, tile);
+    o.num_cb = (int32_t)cdiv(cols, tile);
+    o.group_m = group_rows(o.num_rb, o.num_cb);
+    o.xcd_remap = 1;
+    return o;
+  }
+
+  static agmm::RowMap dense(const void* a, int64_t rows, int64_t ld) {
+    agmm::RowMap r{};
+    r.a_group[0] = a;
+    r.a_ld = ld;
+    r.rows_per_group = (int32_t)rows;
+    r.num_groups = 1;
+    return r;
+  }
+
+  // The gathered, zero-padded rows of A into L.a.
+  int copy_a(const Layout& L, const void* const* shards, hipStream_t s) const {
+    hipError_t err;
+    if (!L.pad_a) {
+      agmm::GatherProblem g{};
+      for (int r = 0; r < N; ++r) g.src_group[r] = shards[r];
+      g.num_groups = N;
+      g.rows = m_s;
+      g.row_bytes = k * 2;
+      g.src_ld_bytes = ld_a() * 2;
+      g.dst = L.a;
+      g.dst_group_rows = m_s;
+      err = agmm::launch_gather(g, 0, s);
+    } else {
+      agmm::PadCopyProblem g{};
+      for (int r = 0; r < N; ++r) g.src_group[r] = shards[r];
+      g.num_groups = N;
+      g.elem_bytes = 2;
+      g.src_rows = m_s;
+      g.src_ld = ld_a();
+      g.cols = k;
+      g.rows = m_s;
+      g.dst = L.a;
+      g.dst_group_rows = m_s;
+      g.dst_ld = L.kp;
+      g.dst_cols = L.kp;
+      err = agmm::launch_pad_copy(g, s);
+    }
+    return err == hipSuccess ? AGMM_OK : hip_err(err, "gather launch");
+  }
+
+  // Rows [v0, v0 + vn) of W as whole 16-byte vectors: in place, or copied.
+  int piece_w(const Layout& L, const void* W, int64_t v0, int64_t vn, hipStream_t s, const void** w, int64_t* ld) const {
+    const char* src = static_cast<const char*>(W) + v0 * ld_w() * 2;
+    if (!L.pad_w) {
+      *w = src;
+      *ld = ld_w();
+      return AGMM_OK;
+    }
+    agmm::PadCopyProblem g{};
+    g.src_group[0] = src;
+    g.num_groups = 1;
+    g.elem_bytes = 2;
+    g.src_rows = vn;
+    g.src_ld = ld_w();
+    g.cols = k;
+    g.rows = vn;
+    g.dst = L.w;
+    g.dst_group_rows = vn;
+    g.dst_ld = L.kp;
+    g.dst_cols = L.kp;
+    const hipError_t err = agmm::launch_pad_copy(g, s);
+    *w = L.w;
+    *ld = L.kp;
+    return err == hipSuccess ? AGMM_OK : hip_err(err, "pad copy launch");
+  }
+
+  agmm::RowMap rows_of_a(const Layout& L, const void* const* shards) const {
+    if (L.a) return dense(L.a, m, L.kp);
+    agmm::RowMap r{};
+    for (int g = 0; g < N; ++g) r.a_group[g] = shards[g];
+    r.a_ld = ld_a();
+    r.rows_per_group = (int32_t)m_s;
+    r.num_groups = N;
+    r.c_group_rows = m_s;
+    return r;
+  }
+
+  agmm::LossProblem logits(const Layout& L, const agmm::RowMap& rows, const void* w, int64_t ldb, int64_t v0,
+                           int64_t vn, const int64_t* labels) const {
+    agmm::LossProblem p{};
+    p.gemm.rows = rows;
+    p.gemm.order = order(m, vn, L.tile);
+    p.gemm.m = (int32_t)m;
+    p.gemm.n = (int32_t)vn;
+    p.gemm.k = (int32_t)L.kp;
+    p.gemm.b = w;
+    p.gemm.ldb = ldb;
+    p.gemm.splits = 1;
+    p.gemm.k_per_split = (int32_t)L.kp;
+    p.tile = L.tile;
+    p.labels = labels;
+    p.label0 = start + v0;
+    return p;
+  }
+
+  int forward(const void* const* shards, const void* W, const int64_t* labels, float* loss, float* lse, float* target,
+              hipStream_t s) {
+    const Layout L = layout(false, ws);
+    int rc = L.a ? copy_a(L, shards, s) : AGMM_OK;
+    const agmm::RowMap rows = rows_of_a(L, shards);
+    for (int64_t v0 = 0; v0 < n && rc == AGMM_OK; v0 += L.piece) {
+      const int64_t vn = std::min(L.piece, n - v0);
+      const void* w;
+      int64_t ldb;
+      rc = piece_w(L, W, v0, vn, s, &w, &ldb);
+      if (rc != AGMM_OK) break;
+      agmm::LossProblem p = logits(L, rows, w, ldb, v0, vn, labels);
+      p.stats = L.stats;
+      p.target = target;
+      hipError_t err = agmm::launch_loss_logits(p, dtype, false, s);
+      if (err != hipSuccess) return hip_err(err, "loss logits launch");
+      agmm::LossCombine c{};
+      c.stats = L.stats;
+      c.parts = 2 * p.gemm.order.num_cb;
+      c.m = m;
+      c.running = L.running;
+      c.first = v0 == 0;
+      c.last = v0 + vn == n;
+      c.labels = labels;
+      c.start = start;
+      c.n = n;
+      c.total = total;
+      c.ignore = ignore;
+      c.loss = loss;
+      c.lse = lse;
+      c.target = target;
+      err = agmm::launch_loss_combine(c, s);
+      if (err != hipSuccess) return hip_err(err, "loss combine launch");
+    }
+    return rc;
+  }
+
+  int backward(const void* const* shards, const void* W, const int64_t* labels, const float* lse,
+               const float* grad_loss, const float* grad_lse, void* dA, void* dW, hipStream_t s) {
+    const Layout L = layout(true, ws);
+    int rc = L.a ? copy_a(L, shards, s) : AGMM_OK;
+    if (rc != AGMM_OK) return rc;
+    const agmm::RowMap rows = rows_of_a(L, shards);
+    agmm::LossRows lr{};
+    lr.m = m;
+    lr.labels = labels;
+    lr.total = total;
+    lr.ignore = ignore;
+    lr.lse = lse;
+    lr.grad_loss = grad_loss;
+    lr.grad_lse = grad_lse;
+    lr.rows = L.rows;
+    lr.scale_all = L.scale_all;
+    hipError_t err = agmm::launch_loss_rows(lr, s);
+    if (err != hipSuccess) return hip_err(err, "loss rows launch");
+    for (int64_t v0 = 0; v0 < n; v0 += L.piece) {
+      const int64_t vn = std::min(L.piece, n - v0);
+      const void* w;
+      int64_t ldb;
+      rc = piece_w(L, W, v0, vn, s, &w, &ldb);
+      if (rc != AGMM_OK) return rc;
+      agmm::LossProblem p = logits(L, rows, w, ldb, v0, vn, labels);
+      p.rows = L.rows;
+      p.scale_all = L.scale_all;
+      p.d = dA ? L.d : nullptr;
+      p.ldd = round_up(vn, 8);
+      p.dt = dW ? L.dt : nullptr;
+      p.ldt = m8();
+      err = agmm::launch_loss_logits(p, dtype, true, s);
+      if (err != hipSuccess) return hip_err(err, "loss gradient launch");
+      if (dA) {
+        agmm::GemmProblem g{};
+        g.rows = dense(L.d, m, round_up(vn, 8));
+        g.order = order(m, k, L.tile_da);
+        g.m = (int32_t)m;
+        g.n = (int32_t)k;
+        g.k = (int32_t)vn;
+        g.b = w;
+        g.ldb = ldb;
+        // the last piece may have fewer ranges: the rest keep their sums
+        g.k_per_split = (int32_t)L.per_range;
+        g.splits = (int32_t)cdiv(vn, L.per_range);
+        g.partials = L.sums;
+        err = agmm::launch_loss_da(g, L.tile_da, dtype, v0 > 0, s);
+        if (err != hipSuccess) return hip_err(err, "dA launch");
+      }
+      if (dW) {
+        agmm::GemmProblem g{};
+        g.rows = dense(L.dt, vn, m8());
+        g.order = order(vn, k, L.tile_dw);
+        g.m = (int32_t)vn;
+        g.n = (int32_t)k;
+        g.k = (int32_t)m;
+        g.b = L.a ? L.a : shards[0];
+        g.ldb = L.a ? L.kp : ld_a();
+        g.splits = 1;
+        g.k_per_split = (int32_t)round_up(m, 64);
+        const int64_t ldc = lddw ? lddw : k;
+        g.c = static_cast<char*>(dW) + v0 * ldc * 2;
+        g.ldc = ldc;
+        err = agmm::launch_loss_dw(g, L.tile_dw, dtype, L.scale_all, s);
+        if (err != hipSuccess) return hip_err(err, "dW launch");
+      }
+    }
+    if (dA) {
+      agmm::LossFinish f{};
+      f.sums = L.sums;
+      f.ranges = L.ranges;
+      f.m = m;
+      f.k = (int32_t)k;
+      f.rows = L.rows;
+      f.da = dA;
+      f.ldda = ldda ? ldda : k;
+      err = agmm::launch_loss_da_finish(f, dtype, s);
+      if (err != hipSuccess) return hip_err(err, "dA cast launch");
+    }
+    return AGMM_OK;
+  }
+};
+
 extern "C" {
 
 int agmm_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, int format,
@@ -464,5 +799,131 @@ int agmm_scaled_run(agmm_scaled_plan_t p, const void* const* shard_ptrs, const f
 }
 
 void agmm_scaled_plan_destroy(agmm_scaled_plan_t p) { delete p; }
+
+int agmm_loss_plan_validate(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_local, int dtype,
+                            int64_t vocab_start, int64_t vocab_size) {
+  return validate_loss(num_shards, m_per_shard, k, n_local, dtype, vocab_start, vocab_size);
+}
+
+agmm_loss_plan_t agmm_loss_plan_create(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_local, int dtype,
+                                       int64_t vocab_start, int64_t vocab_size, int with_gradient) {
+  if (validate_loss(num_shards, m_per_shard, k, n_local, dtype, vocab_start, vocab_size) != AGMM_OK) return nullptr;
+  agmm_loss_plan* p = new (std::nothrow) agmm_loss_plan();
+  if (!p) {
+    set_err(AGMM_ERR_OOM, "out of host memory");
+    return nullptr;
+  }
+  p->N = num_shards;
+  p->m_s = m_per_shard;
+  p->k = k;
+  p->n = n_local;
+  p->m = num_shards * m_per_shard;
+  p->dtype = dtype;
+  p->start = vocab_start;
+  p->total = vocab_size;
+  p->with_gradient = with_gradient != 0;
+  if (p->init() != AGMM_OK || p->apply() != AGMM_OK) {
+    const int st = agmm::g_status;
+    const std::string msg = agmm::g_msg;
+    delete p;
+    set_err(st, "%s", msg.c_str());
+    return nullptr;
+  }
+  ok();
+  return p;
+}
+
+int agmm_loss_plan_set_int(agmm_loss_plan_t p, const char* key, int64_t v) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!key) return set_err(AGMM_ERR_INVALID_ARG, "key is NULL");
+  std::lock_guard<std::mutex> lk(p->mu);
+  if (p->captured)
+    return set_err(AGMM_ERR_UNSUPPORTED,
+                   "the plan has been captured into a graph; its settings are fixed (create a new plan)");
+  const std::string k(key);
+  const auto bad = [&]() {
+    return set_err(AGMM_ERR_INVALID_ARG, "value %lld out of range for key '%s'", (long long)v, key);
+  };
+  int64_t* field = nullptr;
+  if (k == "lda" || k == "ldw" || k == "ldda" || k == "lddw") {
+    if (v != 0 && (v < p->k || v >= kDimLimit)) return bad();
+    field = k == "lda" ? &p->lda : k == "ldw" ? &p->ldw : k == "ldda" ? &p->ldda : &p->lddw;
+  } else if (k == "piece") {
+    if (v < 0 || v >= kDimLimit) return bad();
+    field = &p->piece_key;
+  } else if (k == "ignore_index") {
+    p->ignore = v;
+    return ok();
+  } else {
+    return set_err(AGMM_ERR_INVALID_ARG, "unknown key '%s'", key);
+  }
+  const int64_t old = *field;
+  *field = v;
+  if (p->apply() != AGMM_OK) {   // the plan keeps its settings and workspace
+    *field = old;
+    return agmm::g_status;
+  }
+  return ok();
+}
+
+int agmm_loss_plan_get_int(agmm_loss_plan_t p, const char* key, int64_t* value) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!key || !value) return set_err(AGMM_ERR_INVALID_ARG, "key or value is NULL");
+  std::lock_guard<std::mutex> lk(p->mu);
+  const std::string k(key);
+  if (k == "lda") *value = p->ld_a();
+  else if (k == "ldw") *value = p->ld_w();
+  else if (k == "ldda") *value = p->ldda ? p->ldda : p->k;
+  else if (k == "lddw") *value = p->lddw ? p->lddw : p->k;
+  else if (k == "piece") *value = p->layout(p->with_gradient, nullptr).piece;
+  else if (k == "tile") *value = p->layout(false, nullptr).tile;
+  else if (k == "ignore_index") *value = p->ignore;
+  else if (k == "captured") *value = p->captured;
+  else return set_err(AGMM_ERR_INVALID_ARG, "unknown key '%s'", key);
+  return ok();
+}
+
+size_t agmm_loss_plan_workspace_bytes(agmm_loss_plan_t p) { return p ? p->ws_bytes : 0; }
+
+int agmm_loss_forward(agmm_loss_plan_t p, const void* const* shard_ptrs, const void* W, const int64_t* labels,
+                      float* loss, float* lse, float* target, void* stream) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!shard_ptrs) return set_err(AGMM_ERR_INVALID_ARG, "shard_ptrs is NULL");
+  int rc = AGMM_OK;
+  for (int r = 0; r < p->N && rc == AGMM_OK; ++r) rc = check_ptr(shard_ptrs[r], "shard_ptrs", r, 16);
+  if (rc == AGMM_OK) rc = check_ptr(W, "W", -1, 16);
+  if (rc == AGMM_OK) rc = check_ptr(labels, "labels", -1, 8);
+  if (rc == AGMM_OK) rc = check_ptr(loss, "loss", -1, 4);
+  if (rc == AGMM_OK) rc = check_ptr(lse, "lse", -1, 4);
+  if (rc == AGMM_OK) rc = check_ptr(target, "target", -1, 4);
+  if (rc != AGMM_OK) return rc;
+  std::lock_guard<std::mutex> lk(p->mu);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return p->run(s, true, [&] { return p->forward(shard_ptrs, W, labels, loss, lse, target, s); });
+}
+
+int agmm_loss_backward(agmm_loss_plan_t p, const void* const* shard_ptrs, const void* W, const int64_t* labels,
+                       const float* lse, const float* grad_loss, const float* grad_lse, void* dA, void* dW,
+                       void* stream) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!p->with_gradient) return set_err(AGMM_ERR_UNSUPPORTED, "the plan was created without the gradient's workspace");
+  if (!shard_ptrs) return set_err(AGMM_ERR_INVALID_ARG, "shard_ptrs is NULL");
+  if (!dA && !dW) return set_err(AGMM_ERR_INVALID_ARG, "dA and dW are both NULL");
+  int rc = AGMM_OK;
+  for (int r = 0; r < p->N && rc == AGMM_OK; ++r) rc = check_ptr(shard_ptrs[r], "shard_ptrs", r, 16);
+  if (rc == AGMM_OK) rc = check_ptr(W, "W", -1, 16);
+  if (rc == AGMM_OK) rc = check_ptr(labels, "labels", -1, 8);
+  if (rc == AGMM_OK) rc = check_ptr(lse, "lse", -1, 4);
+  if (rc == AGMM_OK) rc = check_ptr(grad_loss, "grad_loss", -1, 4);
+  if (rc == AGMM_OK && grad_lse) rc = check_ptr(grad_lse, "grad_lse", -1, 4);
+  if (rc == AGMM_OK && dA) rc = check_ptr(dA, "dA", -1, 16);
+  if (rc == AGMM_OK && dW) rc = check_ptr(dW, "dW", -1, 16);
+  if (rc != AGMM_OK) return rc;
+  std::lock_guard<std::mutex> lk(p->mu);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return p->run(s, true, [&] { return p->backward(shard_ptrs, W, labels, lse, grad_loss, grad_lse, dA, dW, s); });
+}
+
+void agmm_loss_plan_destroy(agmm_loss_plan_t p) { delete p; }
 
 }  // extern "C"

@@ -519,6 +519,92 @@ size_t agmm_scaled_plan_workspace_bytes(agmm_scaled_plan_t plan);
 /* Wait for the plan's last call, then free it.  NULL is a no-op. */
 void agmm_scaled_plan_destroy(agmm_scaled_plan_t plan);
 
+/*
+ * Softmax cross entropy of a vocabulary projection, without the logits.
+ *
+ *     x[i, v] = sum_k A[i, k] * W[v, k]      rows i of the shards, v of this device's columns
+ *     lse_i   = log sum_v exp(x[i, v])       over this device's columns
+ *     target_i = x[i, label_i]               0 where the label is another device's
+ *     loss_i  = lse_i - target_i             0 where label_i is "ignore_index"
+ *
+ * W is [n_local, k], this device's columns [vocab_start, vocab_start +
+ * n_local) of a vocabulary of vocab_size.  Where that is the whole
+ * vocabulary, `loss` is the loss.  Otherwise the devices merge: the
+ * vocabulary's lse is the log-sum-exp of theirs, its target their sum, and the
+ * backward pass takes the merged lse.  The logits are computed in pieces of
+ * the vocabulary, fp32, and are never written; the backward pass computes them
+ * again, and its work is three products of the forward pass's size:
+ *
+ *     d[i, v] = (gl_i + gz_i) exp(x[i, v] - lse_i) - gl_i [v = label_i]
+ *     dA = d W,  dW = d^T A
+ *
+ * gl: gradient of loss (taken as 0 in ignored rows), gz: of lse (a z-loss
+ * c lse^2 has 2 c lse; NULL: none).  d is rounded to the operands' type, as
+ * their products need (scaled by powers of two so that fp16 keeps its small
+ * values); sums, maxima and the exponentials are fp32; dA and dW are rounded
+ * once.  dA is this device's part of the gathered rows' gradient [m, k], to be
+ * reduce-scattered over the devices.
+ * A label that is neither ignore_index nor in [0, vocab_size) gives a NaN loss
+ * and NaN gradients.  A row of logits with a NaN gives NaN.
+ */
+typedef struct agmm_loss_plan agmm_loss_plan;
+typedef agmm_loss_plan *agmm_loss_plan_t;
+
+/* Check a problem without touching the GPU: agmm_plan_validate's rules for the
+ * sizes, m and n_local < 2^27, dtype AGMM_BF16 or AGMM_FP16 (AGMM_FP32 is not
+ * supported), 0 <= vocab_start, vocab_start + n_local <= vocab_size < 2^40.
+ * Rows that are not whole 16-byte vectors (k or a stride not a multiple of 8)
+ * run on zero-padded copies of A and of each piece of W. */
+int agmm_loss_plan_validate(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_local,
+                            int dtype, int64_t vocab_start, int64_t vocab_size);
+
+/* Create a plan on the current HIP device (NULL on failure), with everything
+ * its calls need; with_gradient 0 leaves out the backward pass and its
+ * workspace. */
+agmm_loss_plan_t agmm_loss_plan_create(int num_shards, int64_t m_per_shard, int64_t k,
+                                       int64_t n_local, int dtype, int64_t vocab_start,
+                                       int64_t vocab_size, int with_gradient);
+
+/*
+ * Enqueue the forward pass on `stream`.
+ *   shard_ptrs  host array of num_shards device pointers [m_per_shard, k], rows "lda" apart
+ *   W           device [n_local, k], rows "ldw" apart
+ *   labels      device int64 [m], in the order of the gathered rows
+ *   loss, lse, target  device fp32 [m], written
+ * Operands are 16-byte aligned.  Stream, capture and ordering rules are
+ * agmm_run's; agmm_loss_backward is ordered with it.
+ */
+int agmm_loss_forward(agmm_loss_plan_t plan, const void *const *shard_ptrs, const void *W,
+                      const int64_t *labels, float *loss, float *lse, float *target, void *stream);
+
+/*
+ * Enqueue the backward pass.
+ *   lse         device fp32 [m]: the forward pass's, or the merged one
+ *   grad_loss   device fp32 [m];  grad_lse: the same or NULL
+ *   dA          device [m, k] of the plan's dtype, rows "ldda" apart, or NULL
+ *   dW          device [n_local, k], rows "lddw" apart, or NULL (not both)
+ */
+int agmm_loss_backward(agmm_loss_plan_t plan, const void *const *shard_ptrs, const void *W,
+                       const int64_t *labels, const float *lse, const float *grad_loss,
+                       const float *grad_lse, void *dA, void *dW, void *stream);
+
+/*
+ * Tune a plan.  Keys:
+ *   "lda", "ldw", "ldda", "lddw"  elements between rows: 0 (dense) or at least k
+ *   "piece"         columns of the vocabulary computed at a time: 0 automatic (512 MiB of
+ *                   intermediate values), rounded down to a multiple of 256, at least 256
+ *   "ignore_index"  the label of rows without a loss (default -100)
+ * A change that needs more workspace reallocates it; the plan keeps its
+ * previous settings when that fails.  Settings are fixed once a call was
+ * captured into a graph.  get also reads "tile" and "captured".
+ */
+int agmm_loss_plan_set_int(agmm_loss_plan_t plan, const char *key, int64_t value);
+int agmm_loss_plan_get_int(agmm_loss_plan_t plan, const char *key, int64_t *value);
+size_t agmm_loss_plan_workspace_bytes(agmm_loss_plan_t plan);
+
+/* Wait for the plan's last call, then free it.  NULL is a no-op. */
+void agmm_loss_plan_destroy(agmm_loss_plan_t plan);
+
 /* Thread-local status / message of this thread's most recent call into the
  * library (AGMM_OK and "" after a call that succeeded; calls on other threads
  * never change them). */

@@ -208,3 +208,20 @@ def test_gemm_kernels_write_m0_only_in_inline_asm(gemm_asm):
         checked += n
     assert checked > 0, "no LDS-DMA load found: the check would be vacuous"
 
+
+
+@pytest.mark.parametrize("source", ["loss_logits.hip", "loss_grads.hip", "scaled.hip"])
+def test_operator_kernels_keep_the_inline_asm_rules(source):
+    """The kernels built around the same main loop and loads: the tied MFMAs'
+    rules and the M0 rule on each of them."""
+    mfmas = loads = 0
+    for sym, lines in asm_rules.functions(_device_asm(source)):
+        n, bad = asm_rules.check_function(lines)
+        assert bad == [], f"{sym}: {bad[:5]}"
+        mfmas += n
+        n, bad = asm_rules.check_m0(lines)
+        assert bad == [], f"{sym}: {bad[:5]}"
+        loads += n
+    assert loads > 0, "no LDS-DMA load found: the check would be vacuous"
+    if source != "scaled.hip":
+        assert mfmas > 0, "no inline-asm MFMA found: the check would be vacuous"
