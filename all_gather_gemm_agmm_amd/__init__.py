@@ -11,6 +11,7 @@ stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -481,17 +482,19 @@ class Scaled:
         return self.values[:, :self.k].float() * s
 
 
-def _device_and_stream(device, stream):
-    """Context in which outputs are allocated and kernels launched: the
-    tensors' device, and the caller's torch stream if one was passed (so that
-    the allocator hands out memory in that stream's order)."""
-    import contextlib
+_HERE = contextlib.nullcontext()
+
+
+def _device_and_stream(index: int, stream):
+    """Context in which outputs are allocated and kernels launched: GPU
+    `index`, and the caller's torch stream if one was passed (so that the
+    allocator hands out memory in that stream's order)."""
     import torch
     if isinstance(stream, torch.cuda.Stream):
         return torch.cuda.stream(stream)   # sets the stream's device too
-    if device.index is not None and device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    if index != torch.cuda.current_device():
+        return torch.cuda.device(index)
+    return _HERE
 
 
 def _format(fmt) -> int:
@@ -534,7 +537,7 @@ def quantize(x, fmt="e4m3", block_rows: int = 1, out: str = "rows", stream=None)
         return (torch.empty((r, -(-c // 16) * 16), dtype=fmt_dtype, device=x.device),
                 torch.empty((-(-c // SCALE_BLOCK), -(-r // block_rows)), dtype=torch.float32, device=x.device))
 
-    with _device_and_stream(x.device, stream):
+    with _device_and_stream(x.device.index, stream):
         q, s = new(rows, cols) if out != "cols" else (None, None)
         qt, st = new(cols, rows) if out != "rows" else (None, None)
         agmm_quantize(x.data_ptr(), code, rows, cols, x.stride(0) if rows > 1 else max(cols, 1), fmt, block_rows,
@@ -549,8 +552,8 @@ def quantize(x, fmt="e4m3", block_rows: int = 1, out: str = "rows", stream=None)
 
 class _OpPlan:
     """What the plans of the operators share: their handle, its settings and
-    its end.  `_create`, `_set`, `_get`, `_bytes`, `_destroy` name the C
-    functions."""
+    its end.  `_prefix` is that of their C functions; `_expect` says what the
+    tensors of a call look like."""
 
     def _make(self, *args):
         import torch
@@ -563,7 +566,7 @@ class _OpPlan:
 
     def set(self, key: str, value: int) -> None:
         _check(getattr(load_library(), self._prefix + "_set_int")(self.handle, key.encode(), int(value)))
-        self._read_strides()
+        self._expect()
 
     def get(self, key: str) -> int:
         v = ctypes.c_int64(0)
@@ -573,13 +576,22 @@ class _OpPlan:
     def workspace_bytes(self) -> int:
         return int(getattr(load_library(), self._prefix + "_workspace_bytes")(self.handle))
 
-    def _read_strides(self):
-        self._ld = {k: self.get(k) for k in self._strides}
-
-    def _on(self, t, shape, dtype, name, ld=None):
-        """A tensor of this shape and dtype on the plan's device, its rows `ld`
-        elements apart (None: dense)."""
+    def _like(self, shape, dtype, ld=None):
+        """What `_on` expects of a tensor, for its one-comparison case."""
         import torch
+        stride = (1,) if len(shape) == 1 else (shape[1] if ld is None else ld, 1)
+        return (dtype, torch.device("cuda", self.device), torch.Size(shape), stride)
+
+    def _on(self, t, like, name):
+        """The address of a tensor of this dtype, device and shape, dense or with
+        the row stride of `like`."""
+        try:
+            if (t.dtype, t.device, t.shape, t.stride()) == like:
+                return t.data_ptr()
+        except AttributeError:
+            pass
+        import torch
+        dtype, _, shape, stride = like
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.device.type != "cuda":
@@ -590,18 +602,18 @@ class _OpPlan:
             raise TypeError(f"{name} has dtype {t.dtype}, plan expects {dtype}")
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if len(shape) == 1:
-            if shape[0] > 1 and t.stride(0) != 1:
-                raise ValueError(f"{name} must be dense")
-            return t.data_ptr()
-        ld = shape[1] if ld is None else ld
-        if (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) != ld):
-            raise ValueError(f"{name} must be row-major with rows {ld} elements apart (stride {tuple(t.stride())})")
+        # a dimension of one element may have any stride
+        if any(n > 1 and got != want for n, got, want in zip(shape, t.stride(), stride)):
+            raise ValueError(f"{name} must be row-major with rows {stride[0]} elements apart (stride {tuple(t.stride())})")
         return t.data_ptr()
 
-    def _new(self, rows, cols, ld, dtype, device):
+    def _new(self, like):
+        """A new tensor as `like` describes it."""
         import torch
-        return torch.empty((rows, ld), dtype=dtype, device=device)[:, :cols]
+        dtype, device, shape, stride = like
+        if len(shape) == 1 or stride[0] == shape[1]:
+            return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty((shape[0], stride[0]), dtype=dtype, device=device)[:, :shape[1]]
 
     @property
     def m(self) -> int:
@@ -632,45 +644,50 @@ class ScaledPlan(_OpPlan):
     `c_dtype` (AGMM_BF16, AGMM_FP16 or AGMM_FP32)."""
 
     _prefix = "agmm_scaled_plan"
-    _strides = ("lda", "ldb", "ldc")
 
     def __init__(self, num_shards: int, m_per_shard: int, k: int, n_local: int, a_format="e4m3",
                  b_block_rows: int = SCALE_BLOCK, c_dtype: int = AGMM_BF16, **settings):
         a_format = _format(a_format)
         self._make(num_shards, m_per_shard, k, n_local, a_format, b_block_rows, c_dtype)
-        import torch
         self.num_shards, self.m_per_shard, self.k, self.n_local = num_shards, m_per_shard, k, n_local
-        self.b_block_rows = b_block_rows
-        self._k16 = -(-k // 16) * 16
-        self._kb = -(-k // SCALE_BLOCK)
-        self._a_dtype, self._b_dtype = _format_dtype(a_format), torch.float8_e4m3fn
-        self._c_dtype, self._f32 = _torch_dtype(c_dtype), torch.float32
+        self.a_format, self.b_block_rows, self.c_dtype = a_format, b_block_rows, c_dtype
         self._a, self._s = (ctypes.c_void_p * num_shards)(), (ctypes.c_void_p * num_shards)()
-        self._read_strides()
+        self._run = load_library().agmm_scaled_run
+        self._expect()
         for key, val in settings.items():
             if val is not None:
                 self.set(key, val)
 
-    def _operand(self, x, rows, dtype, block_rows, ld, name):
+    def _expect(self):
+        import torch
+        k16, kb, f32 = -(-self.k // 16) * 16, -(-self.k // SCALE_BLOCK), torch.float32
+        self._la = self._like((self.m_per_shard, k16), _format_dtype(self.a_format), self.get("lda"))
+        self._ls = self._like((kb, self.m_per_shard), f32)
+        self._lb = self._like((self.n_local, k16), torch.float8_e4m3fn, self.get("ldb"))
+        self._lbs = self._like((kb, -(-self.n_local // self.b_block_rows)), f32)
+        self._lc = self._like((self.m, self.n_local), _torch_dtype(self.c_dtype), self.get("ldc"))
+
+    def _operand(self, x, block_rows, name):
         if not isinstance(x, Scaled):
             raise TypeError(f"{name} must be a Scaled")
         if x.k != self.k or x.block_rows != block_rows:
             raise ValueError(f"{name} has k {x.k} and block_rows {x.block_rows}, expected {self.k} and {block_rows}")
-        return (self._on(x.values, (rows, self._k16), dtype, f"{name}.values", ld),
-                self._on(x.scales, (self._kb, -(-rows // block_rows)), self._f32, f"{name}.scales"))
+        return x
 
     def run(self, shards, B, C=None, stream=None):
         if len(shards) != self.num_shards:
             raise ValueError(f"expected {self.num_shards} shards, got {len(shards)}")
-        for r, s in enumerate(shards):
-            self._a[r], self._s[r] = self._operand(s, self.m_per_shard, self._a_dtype, 1, self._ld["lda"], f"shards[{r}]")
-        b, bs = self._operand(B, self.n_local, self._b_dtype, self.b_block_rows, self._ld["ldb"], "B")
-        with _device_and_stream(B.values.device, stream):
+        la, ls, on, pa, ps = self._la, self._ls, self._on, self._a, self._s
+        for r, x in enumerate(shards):
+            x = self._operand(x, 1, "shards")
+            pa[r] = on(x.values, la, "shards.values")
+            ps[r] = on(x.scales, ls, "shards.scales")
+        self._operand(B, self.b_block_rows, "B")
+        b, bs = on(B.values, self._lb, "B.values"), on(B.scales, self._lbs, "B.scales")
+        with _device_and_stream(self.device, stream):
             if C is None:
-                C = self._new(self.m, self.n_local, self._ld["ldc"], self._c_dtype, B.values.device)
-            c = self._on(C, (self.m, self.n_local), self._c_dtype, "C", self._ld["ldc"])
-            _check(load_library().agmm_scaled_run(self.handle, self._a, self._s, b, bs, c,
-                                                  _stream_handle(stream, self.device)))
+                C = self._new(self._lc)
+            _check(self._run(self.handle, pa, ps, b, bs, on(C, self._lc, "C"), _stream_handle(stream, self.device)))
         return C
 
 
@@ -682,37 +699,45 @@ class LossPlan(_OpPlan):
     it); `merge_vocab_slices` joins the results of several devices."""
 
     _prefix = "agmm_loss_plan"
-    _strides = ("lda", "ldw", "ldda", "lddw")
 
     def __init__(self, num_shards: int, m_per_shard: int, k: int, n_local: int, dtype: int = AGMM_BF16,
                  vocab_start: int = 0, vocab_size: Optional[int] = None, with_gradient: bool = True, **settings):
         self._make(num_shards, m_per_shard, k, n_local, dtype, vocab_start,
                    vocab_start + n_local if vocab_size is None else vocab_size, int(bool(with_gradient)))
-        import torch
-        self.num_shards, self.m_per_shard, self.k, self.n_local = num_shards, m_per_shard, k, n_local
-        self._tdt, self._f32, self._i64 = _torch_dtype(dtype), torch.float32, torch.int64
+        self.num_shards, self.m_per_shard, self.k, self.n_local, self.dtype = num_shards, m_per_shard, k, n_local, dtype
         self._a = (ctypes.c_void_p * num_shards)()
-        self._read_strides()
+        self._fwd, self._bwd = load_library().agmm_loss_forward, load_library().agmm_loss_backward
+        self._expect()
         for key, val in settings.items():
             if val is not None:
                 self.set(key, val)
 
+    def _expect(self):
+        import torch
+        t = _torch_dtype(self.dtype)
+        self._la = self._like((self.m_per_shard, self.k), t, self.get("lda"))
+        self._lw = self._like((self.n_local, self.k), t, self.get("ldw"))
+        self._lda = self._like((self.m, self.k), t, self.get("ldda"))
+        self._ldw = self._like((self.n_local, self.k), t, self.get("lddw"))
+        self._llab = self._like((self.m,), torch.int64)
+        self._lrow = self._like((self.m,), torch.float32)
+
     def _operands(self, shards, W, labels):
         if len(shards) != self.num_shards:
             raise ValueError(f"expected {self.num_shards} shards, got {len(shards)}")
+        la, on, pa = self._la, self._on, self._a
         for r, s in enumerate(shards):
-            self._a[r] = self._on(s, (self.m_per_shard, self.k), self._tdt, f"shards[{r}]", self._ld["lda"])
-        return (self._on(W, (self.n_local, self.k), self._tdt, "W", self._ld["ldw"]),
-                self._on(labels, (self.m,), self._i64, "labels"))
+            pa[r] = on(s, la, "shards")
+        return on(W, self._lw, "W"), on(labels, self._llab, "labels")
 
     def forward(self, shards, W, labels, stream=None):
         """(loss, lse, target), fp32 [m] each."""
-        import torch
         w, lab = self._operands(shards, W, labels)
-        with _device_and_stream(W.device, stream):
-            loss, lse, target = (torch.empty(self.m, dtype=self._f32, device=W.device) for _ in range(3))
-            _check(load_library().agmm_loss_forward(self.handle, self._a, w, lab, loss.data_ptr(), lse.data_ptr(),
-                                                    target.data_ptr(), _stream_handle(stream, self.device)))
+        with _device_and_stream(self.device, stream):
+            new = self._new
+            loss, lse, target = new(self._lrow), new(self._lrow), new(self._lrow)
+            _check(self._fwd(self.handle, self._a, w, lab, loss.data_ptr(), lse.data_ptr(), target.data_ptr(),
+                             _stream_handle(stream, self.device)))
         return loss, lse, target
 
     def backward(self, shards, W, labels, lse, grad_loss, grad_lse=None, dA=None, dW=None, need_dA: bool = True,
@@ -720,18 +745,16 @@ class LossPlan(_OpPlan):
         """(dA [m, k], dW [n_local, k]) for upstream gradients of loss and,
         optionally, lse; None in the place of one that is not needed."""
         w, lab = self._operands(shards, W, labels)
-        m = (self.m,)
-        ls, gl = self._on(lse, m, self._f32, "lse"), self._on(grad_loss, m, self._f32, "grad_loss")
-        gz = None if grad_lse is None else self._on(grad_lse, m, self._f32, "grad_lse")
-        with _device_and_stream(W.device, stream):
+        on = self._on
+        ls, gl = on(lse, self._lrow, "lse"), on(grad_loss, self._lrow, "grad_loss")
+        gz = None if grad_lse is None else on(grad_lse, self._lrow, "grad_lse")
+        with _device_and_stream(self.device, stream):
             if dA is None and need_dA:
-                dA = self._new(self.m, self.k, self._ld["ldda"], self._tdt, W.device)
+                dA = self._new(self._lda)
             if dW is None and need_dW:
-                dW = self._new(self.n_local, self.k, self._ld["lddw"], self._tdt, W.device)
-            da = None if dA is None else self._on(dA, (self.m, self.k), self._tdt, "dA", self._ld["ldda"])
-            dw = None if dW is None else self._on(dW, (self.n_local, self.k), self._tdt, "dW", self._ld["lddw"])
-            _check(load_library().agmm_loss_backward(self.handle, self._a, w, lab, ls, gl, gz, da, dw,
-                                                     _stream_handle(stream, self.device)))
+                dW = self._new(self._ldw)
+            _check(self._bwd(self.handle, self._a, w, lab, ls, gl, gz, None if dA is None else on(dA, self._lda, "dA"),
+                             None if dW is None else on(dW, self._ldw, "dW"), _stream_handle(stream, self.device)))
         return dA, dW
 
 

@@ -178,6 +178,18 @@ struct QuantProblem {
 };
 hipError_t launch_quantize(const QuantProblem& p, hipStream_t stream);
 
+// Division of 0 <= n < 2^31 by a divisor known on the host: the high half of
+// n * floor(2^32 / d) is the quotient or one less.
+struct FastDiv {
+  uint32_t d, m;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t by) : d(by), m(by == 1 ? 0xFFFFFFFFu : (uint32_t)((uint64_t(1) << 32) / by)) {}
+  __device__ __forceinline__ int quotient(int n) const {
+    const uint32_t q = (uint32_t)(((uint64_t)(uint32_t)n * m) >> 32);
+    return (int)((uint32_t)n - q * d >= d ? q + 1 : q);
+  }
+};
+
 // Block-scaled 8-bit product: logical row i is row i % rows_per_group of
 // group i / rows_per_group, and row i of C.  Scales are [k block][row] for A
 // (per group) and [k block][nb] for B.
@@ -197,23 +209,31 @@ struct ScaledProblem {
   void* c;
   int64_t ldc;             // elements
   int32_t c_dtype;
+  int32_t deep;            // kScaled128: four k-tiles in LDS, one workgroup per CU
   int32_t wide;            // kScaled128: sums of 128 by bf16 MFMAs on the widened values
   TileOrder order;         // tiles kScaled256 and kScaled128
-  int32_t splits;          // k ranges of kb_per_split blocks, into partials [splits][m][n]
+  int32_t splits;          // k ranges of kb_per_split blocks, into partials [splits][m][part_ld]
   int32_t kb_per_split;
   float* partials;
+  int64_t part_ld;         // a multiple of 4
+  FastDiv by_rows, by_tiles, by_group, by_full, by_last;   // set by launch_scaled
 };
 enum ScaledTile : int {
   kScaled256 = 0,          // 256 x 256, 8 waves, 8-bit MFMAs
   kScaled128 = 1,          // 128 x 128, 4 waves, two workgroups per CU; 8-bit or bf16 MFMAs (wide)
   kScaledSkinny16 = 2,     // 16 x 32, k-tiles shared out over 4 waves, bf16 MFMAs
   kScaledSkinny32 = 3,     // 32 x 32
-  kScaledTiles = 4,
+  kScaledSkinny16n = 4,    // 16 x 16, 8 waves
+  kScaledSkinny64 = 5,     // 64 x 64
+  kScaledTiles = 6,
 };
 constexpr int scaled_tile_rows(int t) {
-  return t == kScaled256 ? 256 : t == kScaled128 ? 128 : t == kScaledSkinny16 ? 16 : t == kScaledSkinny32 ? 32 : 0;
+  return t == kScaled256 ? 256 : t == kScaled128 ? 128 : t == kScaledSkinny16 || t == kScaledSkinny16n ? 16
+       : t == kScaledSkinny32 ? 32 : t == kScaledSkinny64 ? 64 : 0;
 }
-constexpr int scaled_tile_cols(int t) { return t == kScaled256 ? 256 : t == kScaled128 ? 128 : 32; }
+constexpr int scaled_tile_cols(int t) {
+  return t == kScaledSkinny16n ? 16 : t == kScaledSkinny16 || t == kScaledSkinny32 ? 32 : scaled_tile_rows(t);
+}
 hipError_t launch_scaled(const ScaledProblem& p, int tile, hipStream_t stream);
 
 // Vocabulary loss over one piece of the vocabulary: gemm describes the logits

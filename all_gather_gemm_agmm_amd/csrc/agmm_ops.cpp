@@ -107,34 +107,59 @@ struct PlanBase {
     return AGMM_OK;
   }
 
+  // The default stream needs no event of its own per call: it never ends, so
+  // what orders a later call after it (and what the plan's end waits for) is
+  // recorded, or waited for, when that time comes.
+  int on_device(hipError_t (*f)(PlanBase*), const char* what) {
+    int dev = device;
+    hipError_t err = hipGetDevice(&dev);
+    if (err == hipSuccess && dev != device) err = hipSetDevice(device);
+    if (err == hipSuccess) err = f(this);
+    if (dev != device) (void)hipSetDevice(dev);
+    return err == hipSuccess ? AGMM_OK : hip_err(err, what);
+  }
+
   int idle() {
     if (done != kEager) return AGMM_OK;
+    if (!done_stream) return on_device([](PlanBase*) { return hipStreamSynchronize(nullptr); }, "hipStreamSynchronize");
     const hipError_t err = hipEventSynchronize(ev_done);
     return err == hipSuccess ? AGMM_OK : hip_err(err, "hipEventSynchronize(done)");
   }
 
-  // Order a call on `s` after the plan's previous one.  Across a graph-capture
-  // boundary no event links calls: the caller's streams order replays.
-  int enter(hipStream_t s, bool& capturing, unsigned long long& id) {
-    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  // Find out whether `s` is being captured into a graph (the default stream
+  // cannot be).
+  int look(hipStream_t s, bool& capturing, unsigned long long& id) {
+    capturing = false;
     id = 0;
-    hipError_t err = hipStreamGetCaptureInfo(s, &st, &id);
+    if (!s) return AGMM_OK;
+    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+    const hipError_t err = hipStreamGetCaptureInfo(s, &st, &id);
     if (err != hipSuccess) return hip_err(err, "hipStreamGetCaptureInfo");
     if (st == hipStreamCaptureStatusInvalidated)
       return set_err(AGMM_ERR_HIP, "the stream's graph capture has been invalidated");
     capturing = st == hipStreamCaptureStatusActive;
     if (capturing) captured = true;
-    const bool linked = done == kEager ? !capturing : done == kCaptured && capturing && done_capture == id;
-    if (linked && done_stream != s) {
-      err = hipStreamWaitEvent(s, ev_done, 0);
-      if (err != hipSuccess) return hip_err(err, "hipStreamWaitEvent(done)");
-    }
     return AGMM_OK;
   }
 
+  // Order a call on `s` after the plan's previous one.  Across a graph-capture
+  // boundary no event links calls: the caller's streams order replays.
+  int enter(hipStream_t s, bool capturing, unsigned long long id) {
+    const bool linked = done == kEager ? !capturing : done == kCaptured && capturing && done_capture == id;
+    if (!linked || done_stream == s) return AGMM_OK;
+    if (!done_stream) {
+      const int rc = on_device([](PlanBase* p) { return hipEventRecord(p->ev_done, nullptr); }, "hipEventRecord(done)");
+      if (rc != AGMM_OK) return rc;
+    }
+    const hipError_t err = hipStreamWaitEvent(s, ev_done, 0);
+    return err == hipSuccess ? AGMM_OK : hip_err(err, "hipStreamWaitEvent(done)");
+  }
+
   int leave(hipStream_t s, bool capturing, unsigned long long id) {
-    const hipError_t err = hipEventRecord(ev_done, s);
-    if (err != hipSuccess) return hip_err(err, "hipEventRecord(done)");
+    if (s) {
+      const hipError_t err = hipEventRecord(ev_done, s);
+      if (err != hipSuccess) return hip_err(err, "hipEventRecord(done)");
+    }
     done = capturing ? kCaptured : kEager;
     done_capture = capturing ? id : 0;
     done_stream = s;
@@ -144,15 +169,13 @@ struct PlanBase {
   // A call that enqueues work.  One that uses no workspace needs no ordering.
   template <class F>
   int run(hipStream_t s, bool ordered, F&& body) {
-    if (!ordered) {
-      const int rc = body();
-      return rc == AGMM_OK ? ok() : rc;
-    }
-    bool capturing = false;
-    unsigned long long id = 0;
-    int rc = enter(s, capturing, id);
+    bool capturing;
+    unsigned long long id;
+    int rc = look(s, capturing, id);
+    if (rc == AGMM_OK && ordered) rc = enter(s, capturing, id);
     if (rc != AGMM_OK) return rc;
     rc = body();
+    if (!ordered) return rc == AGMM_OK ? ok() : rc;
     if (rc != AGMM_OK) {
       // whatever was enqueued before the failure still counts
       const int st = agmm::g_status;
@@ -165,7 +188,7 @@ struct PlanBase {
   }
 
   ~PlanBase() {
-    if (done == kEager && ev_done) hipEventSynchronize(ev_done);
+    (void)idle();
     (void)hipGetLastError();
     if (ws) hipFree(ws);
     if (ev_done) hipEventDestroy(ev_done);
@@ -229,7 +252,8 @@ struct agmm_scaled_plan : PlanBase {
   int a_format = 0, b_block_rows = 0, c_dtype = 0;
   int64_t lda = 0, ldb = 0, ldc = 0;   // 0: dense
   int tile_key = -1, splits_key = 0;
-  int tile = 0, splits = 1, kb_per_split = 0;
+  int tile = 0, splits = 1, kb_per_split = 0, group_m = 1;
+  bool deep = false;
 
   // Sums of 128 by bf16 MFMAs.  The 8-bit ones lose up to about 3700 units of
   // 2^-24 of a block's sum of sizes (scaled.hip): below the rounding of a
@@ -239,35 +263,70 @@ struct agmm_scaled_plan : PlanBase {
 
   int64_t kb() const { return cdiv(k, agmm::kScaleBlock); }
 
+  // Cycles a launch of a tile with `sp` k ranges takes, from measurements on
+  // MI355X (8-bit operands, cycles of about 2.1 GHz):
+  //  * a CU streams its operands at about 26 bytes per cycle from one
+  //    workgroup, 38 from two; every workgroup reads (rows + columns) * 128
+  //    bytes per k block, which is what bounds all but the bf16-MFMA form of
+  //    the 128 x 128 tile and the 256 x 256 tile (MFMA);
+  //  * setup, first loads and epilogue: 8 thousand cycles for the skinny tiles,
+  //    12 for 128 x 128, 20 for 256 x 256;
+  //  * a second launch that adds k ranges: 6 thousand, and 8 bytes per partial
+  //    sum at about 1900 bytes per cycle.
+  // E.g. (us, measured): 192 x 2048 x 2048: 32 x 32 tiles 9.3, 64 x 64 10.5,
+  // 128 x 128 15.2; 512 x 4096 -> 2048: 128 x 128 with 4 ranges 18.8, one 22.7,
+  // 256 x 256 26.8; 4096 x 4096 -> 4096: 256 x 256 60, 128 x 128 73; 8 x 4096 ->
+  // 1792: 16 x 16 tiles 5.1, 16 x 32 7.3.
+  double cycles(int t, int64_t sp) const {
+    const int64_t rows = agmm::scaled_tile_rows(t), cols = agmm::scaled_tile_cols(t);
+    const int64_t wgs = cdiv(m, rows) * cdiv(n, cols) * sp, blocks = cdiv(kb(), sp);
+    double base, step;
+    int64_t rounds = cdiv(wgs, cu_count);
+    if (t == agmm::kScaled256) {
+      base = 20e3;
+      step = 2300;
+    } else if (t == agmm::kScaled128) {
+      base = 12e3;
+      rounds = cdiv(wgs, 2 * (int64_t)cu_count);
+      step = wgs <= cu_count ? (wide() ? 2100 : 1300) : wide() ? 3700 : 1700;
+    } else {
+      base = 8e3;
+      step = (double)(rows + cols) * 128 / 26;
+    }
+    return base + rounds * blocks * step + (sp > 1 ? 6e3 + (double)sp * m * n * 8 / 1900 : 0);
+  }
+
   // Tile and k ranges for a pair of keys; host only.
   void derive(int tile_k, int splits_k, int& t, int& sp, int& per) const {
-    const auto tiles = [&](int c) {
-      return cdiv(m, agmm::scaled_tile_rows(c)) * cdiv(n, agmm::scaled_tile_cols(c));
-    };
-    if (tile_k >= 0) t = tile_k;
-    else if (m <= 16 && tiles(agmm::kScaledSkinny16) < kMaxGrid) t = agmm::kScaledSkinny16;
-    else if (m <= 128 && tiles(agmm::kScaledSkinny32) < kMaxGrid) t = agmm::kScaledSkinny32;
-    else {
-      // rounds of workgroups over the CUs times the work of a tile; the large
-      // tile reads half the LDS bytes per product
-      const double big = (double)cdiv(tiles(agmm::kScaled256), cu_count) * 4.0;
-      const double small = (double)cdiv(tiles(agmm::kScaled128), 2 * (int64_t)cu_count) * 2.0 * 1.3;
-      t = !wide() && big <= small ? agmm::kScaled256 : agmm::kScaled128;
+    // the tiles of each value of the key "tile"
+    static const int of_key[4][2] = {{agmm::kScaled256, agmm::kScaled256},
+                                     {agmm::kScaled128, agmm::kScaled128},
+                                     {agmm::kScaledSkinny16, agmm::kScaledSkinny16n},
+                                     {agmm::kScaledSkinny32, agmm::kScaledSkinny64}};
+    double best = -1;
+    t = agmm::kScaled128;
+    int64_t want = 1;
+    for (int key = 0; key < 4; ++key) {
+      if (tile_k >= 0 ? key != tile_k : key == 0 && wide()) continue;
+      for (int c : of_key[key]) {
+        const int64_t tiles = cdiv(m, agmm::scaled_tile_rows(c)) * cdiv(n, agmm::scaled_tile_cols(c));
+        for (int64_t w : {1, 2, 3, 4, 6, 8, 12, 16}) {
+          if (splits_k > 0) w = splits_k;
+          w = std::max<int64_t>(1, std::min(w, kb()));
+          if (tile_k < 0 && tiles * w >= kMaxGrid) continue;
+          const double cost = cycles(c, w);
+          if (best < 0 || cost < best) best = cost, t = c, want = w;
+        }
+      }
     }
-    int64_t want = splits_k;
-    if (want <= 0) {
-      want = 1;
-      const bool skinny = agmm::scaled_tile_rows(t) < 128;
-      const int64_t slots = cu_count * (t == agmm::kScaled128 ? 2 : 1);
-      const int64_t shortest = skinny ? 4 : 8;   // k blocks of a range
-      while (want * 2 * tiles(t) <= slots && kb() / (want * 2) >= shortest) want *= 2;
-    }
-    want = std::max<int64_t>(1, std::min(want, kb()));
     per = (int)cdiv(kb(), want);
     sp = (int)cdiv(kb(), per);
   }
 
-  size_t need(int sp) const { return sp > 1 ? (size_t)sp * m * n * sizeof(float) : 0; }
+  // Row length of the partial sums: whole 16-byte vectors.
+  int64_t part_ld() const { return round_up(n, 4); }
+
+  size_t need(int sp) const { return sp > 1 ? (size_t)sp * m * part_ld() * sizeof(float) : 0; }
 
   int apply(int tile_k, int splits_k) {
     int t, sp, per;
@@ -281,6 +340,8 @@ struct agmm_scaled_plan : PlanBase {
     tile = t;
     splits = sp;
     kb_per_split = per;
+    deep = t == agmm::kScaled128 && cdiv(m, 128) * cdiv(n, 128) * sp <= cu_count;
+    group_m = group_rows(cdiv(m, agmm::scaled_tile_rows(t)), cdiv(n, agmm::scaled_tile_cols(t)));
     return ok();
   }
 };
@@ -715,7 +776,7 @@ int agmm_scaled_plan_set_int(agmm_scaled_plan_t p, const char* key, int64_t v) {
     return set_err(AGMM_ERR_INVALID_ARG, "value %lld out of range for key '%s'", (long long)v, key);
   };
   if (k == "tile") {
-    if (v < -1 || v >= agmm::kScaledTiles) return bad();
+    if (v < -1 || v > 3) return bad();
     return p->apply((int)v, p->splits_key);
   }
   if (k == "splits") {
@@ -736,7 +797,7 @@ int agmm_scaled_plan_get_int(agmm_scaled_plan_t p, const char* key, int64_t* val
   if (!key || !value) return set_err(AGMM_ERR_INVALID_ARG, "key or value is NULL");
   std::lock_guard<std::mutex> lk(p->mu);
   const std::string k(key);
-  if (k == "tile") *value = p->tile;
+  if (k == "tile") *value = p->tile == agmm::kScaledSkinny16n ? 2 : p->tile == agmm::kScaledSkinny64 ? 3 : p->tile;
   else if (k == "splits") *value = p->splits;
   else if (k == "lda") *value = p->lda ? p->lda : p->k16;
   else if (k == "ldb") *value = p->ldb ? p->ldb : p->k16;
@@ -784,13 +845,15 @@ int agmm_scaled_run(agmm_scaled_plan_t p, const void* const* shard_ptrs, const f
   g.ldc = p->ldc ? p->ldc : p->n;
   g.c_dtype = p->c_dtype;
   g.wide = p->wide();
+  g.deep = p->deep;
   g.order.num_rb = (int32_t)cdiv(p->m, agmm::scaled_tile_rows(p->tile));
   g.order.num_cb = (int32_t)cdiv(p->n, agmm::scaled_tile_cols(p->tile));
-  g.order.group_m = group_rows(g.order.num_rb, g.order.num_cb);
+  g.order.group_m = p->group_m;
   g.order.xcd_remap = 1;
   g.splits = p->splits;
   g.kb_per_split = p->kb_per_split;
   g.partials = reinterpret_cast<float*>(p->ws);
+  g.part_ld = p->part_ld();
   hipStream_t s = static_cast<hipStream_t>(stream);
   return p->run(s, p->splits > 1, [&]() -> int {
     const hipError_t err = agmm::launch_scaled(g, p->tile, s);

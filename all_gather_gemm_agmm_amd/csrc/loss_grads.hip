@@ -112,8 +112,16 @@ __global__ __launch_bounds__(256) void loss_da_finish_kernel(LossFinish c) {
     const float f = c.rows[4 * row + 3] * (DT == kDtypeFp16 ? 1.0f / 16384.0f : 1.0f);
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
     if (c.k % 4 == 0) {
-      v = *reinterpret_cast<const f32x4_t*>(src);
-      for (int q = 1; q < c.ranges; ++q) v += *reinterpret_cast<const f32x4_t*>(src + q * plane);
+      // eight ranges are on their way at a time, added in order
+      for (int q0 = 0; q0 < c.ranges; q0 += 8) {
+        f32x4_t w[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q0 + q < c.ranges) w[q] = *reinterpret_cast<const f32x4_t*>(src + (q0 + q) * plane);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q0 + q < c.ranges) v += w[q];
+      }
     } else {
       for (int q = 0; q < c.ranges; ++q)
 #pragma unroll

@@ -32,6 +32,8 @@ namespace agmm {
 
 namespace {
 
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -107,15 +109,22 @@ __device__ __forceinline__ void loss_body(const LossProblem& lp, char* smem) {
   } else {
     const float top = DT == kDtypeFp16 ? 16384.0f : 1.0f;
     const float inv_all = top / lp.scale_all[0];
+    // the rows' values, all on their way at once
+    f32x4_t rv[FM];
+    int at[FM];       // the label's column within the wave's, or anything outside
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int row = m0 + wm * T::TM + 16 * i + i16;
-      const float lse = row < M ? lp.rows[4 * (int64_t)row] : 0.0f;
+      rv[i] = row < M ? *reinterpret_cast<const f32x4_t*>(lp.rows + 4 * (int64_t)row) : f32x4_t{0.f, 0.f, 0.f, 1.f};
+      const int64_t rel = row < M ? lp.labels[row] - lp.label0 - wcol : -1;
+      at[i] = rel >= 0 && rel < T::TN ? (int)rel : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = exp_of(acc[i][j][e] - lse);
-    }
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = exp_of(acc[i][j][e] - rv[i][0]);
     __syncthreads();   // the LDS now holds the output tiles
     // Row by row: chunk c (16 bytes) of tile row r at c ^ (r mod 8), as 4
     // columns of a row are 8 bytes; transposed: columns are rows of BM elements.
@@ -129,11 +138,9 @@ __device__ __forceinline__ void loss_body(const LossProblem& lp, char* smem) {
         const int r = wm * T::TM + 16 * i + i16;
         const int row = m0 + r;
         const bool in = row < M;
-        const float a = in ? lp.rows[4 * (int64_t)row + 1] : 0.0f, b = in ? lp.rows[4 * (int64_t)row + 2] : 0.0f;
-        const float f = pass ? inv_all : top / (in ? lp.rows[4 * (int64_t)row + 3] : 1.0f);
-        const float af = a * f, bf = b * f;
-        const int64_t at = in ? lp.labels[row] - lp.label0 - wcol : -1;
-        const bool hit = __any(at >= 0 && at < T::TN);
+        const float f = pass ? inv_all : top / rv[i][3];
+        const float af = rv[i][1] * f, bf = rv[i][2] * f;
+        const bool hit = __any(at[i] >= 0);
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
           float d[4];
@@ -142,7 +149,7 @@ __device__ __forceinline__ void loss_body(const LossProblem& lp, char* smem) {
           if (hit)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (at == 16 * j + 4 * g4 + e) d[e] -= bf;
+              if (at[i] == 16 * j + 4 * g4 + e) d[e] -= bf;
           if (!whole)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -211,10 +218,24 @@ __global__ __launch_bounds__(256) void loss_combine_kernel(LossCombine c) {
     s = s * exp_of(m - off) + ps * exp_of(pm - off);
     m = top;
   };
+  // eight partials are on their way at a time
   if (row < c.m)
-    for (int q = l; q < c.parts; q += LANES) {
-      const float* d = c.stats + ((int64_t)q * c.m + row) * 2;
-      merge(d[0], d[1]);
+    for (int q0 = l; q0 < c.parts; q0 += 8 * LANES) {
+      f32x2_t v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int q = q0 + e * LANES;
+        v[e] = q < c.parts ? *reinterpret_cast<const f32x2_t*>(c.stats + ((int64_t)q * c.m + row) * 2)
+                           : f32x2_t{-__builtin_inff(), 0.0f};
+      }
+      float top = v[0][0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) top = fmaxf(top, v[e][0]);
+      const float off = finite_or_zero(top);
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += v[e][1] * exp_of(v[e][0] - off);
+      merge(top, sum);
     }
   sm[l][r] = m;
   ss[l][r] = s;

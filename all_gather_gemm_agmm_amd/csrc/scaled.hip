@@ -14,8 +14,8 @@
 // row, the chunks the bf16 kernel's 64-deep rows are read in, so the same XOR
 // swizzle keeps the reads free of LDS bank conflicts.
 //
-//  * scaled_gemm_kernel: two 128-deep k-tiles in LDS, refilled by global ->
-//    LDS loads; the row and column scales of a k-tile ride along as one
+//  * scaled_gemm_kernel: two 128-deep k-tiles in LDS (four where a CU has one
+//    workgroup of the small tile to itself), refilled by global -> LDS loads; the row and column scales of a k-tile ride along as one
 //    4-byte-per-lane load per wave.  B fragments of a k-tile stay in
 //    registers, A fragments pass through; the FMAs of row block i run beside
 //    the MFMAs of row block i + 1.  The workgroup synchronises before the last
@@ -110,43 +110,65 @@ __device__ __forceinline__ void load_lds4_buf(const u32x4_t& rsrc, uint32_t voff
                : "m0");
 }
 
-// Four consecutive columns of one row to C in its own type.
+// One element, and four consecutive ones (aligned to four), of an output type.
+template <int CT>
+struct OutOf {
+  typedef uint16_t type;
+};
+template <>
+struct OutOf<kDtypeFp32> {
+  typedef float type;
+};
+template <int CT, class P>
+__device__ __forceinline__ void put1(P* c, float v) {
+  if constexpr (CT == kDtypeFp32) *c = v;
+  else *c = cvt1<CT>(v);
+}
+template <int CT, class P>
+__device__ __forceinline__ void put4(P* c, const f32x4_t& v) {
+  if constexpr (CT == kDtypeFp32) *reinterpret_cast<f32x4_t*>(c) = v;
+  else *reinterpret_cast<u32x2_t*>(c) = u32x2_t{pack2<CT>(v[0], v[1]), pack2<CT>(v[2], v[3])};
+}
+
+// Four consecutive columns (col % 4 == 0) of one row to C in its own type.
 __device__ __forceinline__ void store4(const ScaledProblem& p, int row, int col, const f32x4_t& v) {
   const int64_t at = (int64_t)row * p.ldc + col;
   const bool whole = col + 3 < p.n && (p.ldc % 4) == 0;
-  if (p.c_dtype == kDtypeFp32) {
-    float* c = static_cast<float*>(p.c) + at;
+  const auto put = [&](auto type) {
+    constexpr int CT = decltype(type)::value;
+    typename OutOf<CT>::type* c = static_cast<typename OutOf<CT>::type*>(p.c) + at;
     if (whole) {
-      *reinterpret_cast<f32x4_t*>(c) = v;
+      put4<CT>(c, v);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (col + e < p.n) c[e] = v[e];
+        if (col + e < p.n) put1<CT>(c + e, v[e]);
     }
-  } else {
-    uint16_t* c = static_cast<uint16_t*>(p.c) + at;
-    uint32_t lo, hi;
-    if (p.c_dtype == kDtypeBf16) {
-      lo = pack2<kDtypeBf16>(v[0], v[1]);
-      hi = pack2<kDtypeBf16>(v[2], v[3]);
-    } else {
-      lo = pack2<kDtypeFp16>(v[0], v[1]);
-      hi = pack2<kDtypeFp16>(v[2], v[3]);
-    }
-    if (whole) {
-      *reinterpret_cast<u32x2_t*>(c) = u32x2_t{lo, hi};
-    } else {
-      if (col + 0 < p.n) c[0] = (uint16_t)lo;
-      if (col + 1 < p.n) c[1] = (uint16_t)(lo >> 16);
-      if (col + 2 < p.n) c[2] = (uint16_t)hi;
-      if (col + 3 < p.n) c[3] = (uint16_t)(hi >> 16);
-    }
-  }
+  };
+  if (p.c_dtype == kDtypeFp32) put(IntTag<kDtypeFp32>{});
+  else if (p.c_dtype == kDtypeBf16) put(IntTag<kDtypeBf16>{});
+  else put(IntTag<kDtypeFp16>{});
 }
 
-// BM x BN output tile, WM x WN waves.  WIDE: bf16 MFMAs.
-template <int FMTA, bool BROW, bool WIDE, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
+// Tile and k range of a workgroup: k ranges outermost; of a range, XCD x
+// (workgroup id mod 8) takes consecutive tiles, in groups of group_m row
+// blocks walked column by column.
+__device__ __forceinline__ void tile_of(const ScaledProblem& p, int wg, int& rb, int& cb, int& split) {
+  const int ntiles = p.order.num_rb * p.order.num_cb;
+  split = p.by_tiles.quotient(wg);
+  wg -= split * ntiles;
+  const int xcd = wg & 7, per = ntiles >> 3, rem = ntiles & 7;
+  wg = xcd * per + min(xcd, rem) + (wg >> 3);
+  const int grp = p.by_group.quotient(wg);
+  const int first = grp * p.order.group_m, rows = min(p.order.num_rb - first, p.order.group_m);
+  const int in = wg - grp * p.order.group_m * p.order.num_cb;
+  cb = (rows == p.order.group_m ? p.by_full : p.by_last).quotient(in);
+  rb = first + in - cb * rows;
+}
+
+// BM x BN output tile, WM x WN waves, NST k-tiles in LDS.  WIDE: bf16 MFMAs.
+template <int FMTA, bool BROW, bool WIDE, int BM, int BN, int WM, int WN, int NST, int OCC>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 void scaled_gemm_kernel(ScaledProblem p) {
   constexpr int WAVES = WM * WN;
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
@@ -154,121 +176,47 @@ void scaled_gemm_kernel(ScaledProblem p) {
   constexpr int AL = A_BYTES / 1024 / WAVES, BL = B_BYTES / 1024 / WAVES;   // 1 KiB loads per wave and k-tile
   static_assert(BM + BN == 64 * WAVES, "one scale per lane of the workgroup");
   static_assert(AL >= 1 && BL >= 1 && BM % 64 == 0, "tile too small for the load split");
+  static_assert(NST * (AL + BL + 1) < 64, "vmcnt range");
   // [stage][A tile, B tile], then [stage][row scales, column scales]
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE + 2 * (BM + BN) * 4];
-  char* const sc = smem + 2 * STAGE;
+  __shared__ __attribute__((aligned(1024))) char smem[NST * (STAGE + (BM + BN) * 4)];
+  char* const sc = smem + NST * STAGE;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int g4 = lane >> 4, i16 = lane & 15;
-  const int ntiles = p.order.num_rb * p.order.num_cb;
-  int wg = blockIdx.x, split = 0;
-  if (p.splits > 1) {
-    split = wg / ntiles;
-    wg -= split * ntiles;
-  }
-  int rb, cb;
-  tile_coords(p.order, wg, ntiles, rb, cb);
+  int rb, cb, split;
+  tile_of(p, blockIdx.x, rb, cb, split);
   const int m0 = rb * BM, n0 = cb * BN;
   const int t0 = split * p.kb_per_split;
   const int nk = min(p.kb, t0 + p.kb_per_split) - t0;
   const int rpg = p.rows_per_group;
   const char* zero = reinterpret_cast<const char*>(g_zero_chunk);
 
-  // ---- sources of this lane's loads ------------------------------------------
+  // ---- this lane's loads -----------------------------------------------------
   // Instruction j of this wave fills rows 8 (wave * AL + j) + lane / 8 of its
-  // tile; position lane % 8 holds chunk (lane % 8) ^ swz_k16(row).
-  const char* a_src[AL];
-  const char* b_src[BL];
-  uint32_t ok_bits = 0;
+  // tile; position lane % 8 holds chunk (lane % 8) ^ swz_k16(row).  The scales
+  // of a k-tile are LDS words [BM + BN], one per thread; row scales sit in the
+  // order a lane reads them: word wm*TM + i16*FM + i is row wm*TM + 16i + i16.
   const int pos = lane & 7;
-  // chunk of the row: the same for every instruction up to row bits 0-3
-  int a_kc[AL], b_kc[BL];
-#pragma unroll
-  for (int j = 0; j < AL; ++j) {
-    const int r = (wave * AL + j) * 8 + (lane >> 3);
-    const int c = pos ^ swz_k16(r);
-    a_kc[j] = c * 16;
-    a_src[j] = zero;
-    const int gi = m0 + r;
-    if (gi < p.m) {
-      const int g = gi / rpg, t = gi - g * rpg;
-      a_src[j] = static_cast<const char*>(p.a_group[g]) + (int64_t)t * p.a_ld + (int64_t)t0 * 128 + c * 16;
-      ok_bits |= 1u << j;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < BL; ++j) {
-    const int r = (wave * BL + j) * 8 + (lane >> 3);
-    const int c = pos ^ swz_k16(r);
-    b_kc[j] = c * 16;
-    b_src[j] = zero;
-    const int gn = n0 + r;
-    if (gn < p.n) {
-      b_src[j] = static_cast<const char*>(p.b) + (int64_t)gn * p.ldb + (int64_t)t0 * 128 + c * 16;
-      ok_bits |= 1u << (AL + j);
-    }
-  }
-  // Scale of this thread: LDS word tid of a k-tile's [BM + BN].  Row scales
-  // sit in the order a lane reads them: word wm*TM + i16*FM + i is row
-  // wm*TM + 16i + i16.
-  const char* s_src = zero;
-  int64_t s_step = 0;
-  if (tid < BM) {
-    const int in = tid % TM;
-    const int gi = m0 + (tid / TM) * TM + 16 * (in % FM) + in / FM;
-    if (gi < p.m) {
-      const int g = gi / rpg;
-      s_src = reinterpret_cast<const char*>(p.a_scale[g] + (int64_t)t0 * rpg + (gi - g * rpg));
-      s_step = (int64_t)rpg * 4;
-    }
-  } else {
-    const int gn = n0 + tid - BM;
-    if (gn < p.n) {
-      s_src = reinterpret_cast<const char*>(p.b_scale + (int64_t)t0 * p.nb + (BROW ? gn : gn >> 7));
-      s_step = (int64_t)p.nb * 4;
-    }
-  }
-
-  // Tiles wholly inside one shard, n and k: buffer descriptors over the tile's
-  // rows (scalar base and k offset, 32-bit lane offsets), offsets shifted for
-  // load_lds16_buf_j.  `s_` is the wave's scale array: its rows or columns.
-  const int g0 = m0 / rpg, in0 = m0 - g0 * rpg;
-  const int kend = p.k16 - t0 * 128;               // bytes of a row from k-tile t0 on
-  const int64_t a_span = (int64_t)(BM - 1) * p.a_ld + nk * 128, b_span = (int64_t)(BN - 1) * p.ldb + nk * 128;
-  const int s_ld = wave * 64 < BM ? rpg : p.nb;
-  const int64_t s_span = ((int64_t)(nk - 1) * s_ld + 256) * 4;
-  const bool fast = m0 + BM <= p.m && n0 + BN <= p.n && in0 + BM <= rpg && nk * 128 <= kend && p.a_ld >= 128 &&
-                    p.ldb >= 128 && a_span < (1ll << 32) && b_span < (1ll << 32) && s_span < (1ll << 32);
-  u32x4_t rsrc_a{}, rsrc_b{}, rsrc_s{};
-  uint32_t a_voff[AL], b_voff[BL], s_voff = 0;
-  if (fast) {
-    rsrc_a = buffer_rsrc(static_cast<const char*>(p.a_group[g0]) + (int64_t)in0 * p.a_ld + (int64_t)t0 * 128, a_span);
-    rsrc_b = buffer_rsrc(static_cast<const char*>(p.b) + (int64_t)n0 * p.ldb + (int64_t)t0 * 128, b_span);
-    if (wave * 64 < BM) {
-      const int in = tid % TM;
-      rsrc_s = buffer_rsrc(p.a_scale[g0] + (int64_t)t0 * rpg + in0, s_span);
-      s_voff = ((tid / TM) * TM + 16 * (in % FM) + in / FM) * 4;
-    } else {
-      rsrc_s = buffer_rsrc(p.b_scale + (int64_t)t0 * p.nb + (BROW ? n0 : n0 >> 7), s_span);
-      s_voff = (BROW ? tid - BM : (tid - BM) >> 7) * 4;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < AL; ++j) {
-    const int r = (wave * AL + j) * 8 + (lane >> 3);
-    a_voff[j] = (uint32_t)((int64_t)r * p.a_ld + a_kc[j] - (j & 3) * 1024);
-  }
-#pragma unroll
-  for (int j = 0; j < BL; ++j) {
-    const int r = (wave * BL + j) * 8 + (lane >> 3);
-    b_voff[j] = (uint32_t)((int64_t)r * p.ldb + b_kc[j] - (j & 3) * 1024);
-  }
+  auto a_row = [&](int j) { return (wave * AL + j) * 8 + (lane >> 3); };
+  auto b_row = [&](int j) { return (wave * BL + j) * 8 + (lane >> 3); };
+  auto chunk = [&](int r) { return (pos ^ swz_k16(r)) * 16; };
+  const int s_row = (tid / TM) * TM + 16 * ((tid % TM) % FM) + (tid % TM) / FM;   // waves of row scales
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char_t*)smem;
   const uint32_t lds_a = lds0 + wave * (AL * 1024), lds_b = lds0 + A_BYTES + wave * (BL * 1024);
-  const uint32_t lds_s = lds0 + 2 * STAGE + wave * 256;
+  const uint32_t lds_s = lds0 + NST * STAGE + wave * 256;
+  const int kend = p.k16 - t0 * 128;               // bytes of a row from k-tile t0 on
+
+  // Tiles wholly inside one shard, n and k load through buffer descriptors
+  // over the tile's rows (scalar base and k offset, 32-bit lane offsets).
+  const int g0 = p.by_rows.quotient(m0), in0 = m0 - g0 * rpg;
+  const int64_t a_span = (int64_t)(BM - 1) * p.a_ld + nk * 128, b_span = (int64_t)(BN - 1) * p.ldb + nk * 128;
+  const int s_ld = wave * 64 < BM ? rpg : p.nb;    // this wave's scales: rows or columns
+  const int64_t s_span = ((int64_t)(nk - 1) * s_ld + 256) * 4;
+  const bool fast = m0 + BM <= p.m && n0 + BN <= p.n && in0 + BM <= rpg && nk * 128 <= kend && p.a_ld >= 128 &&
+                    p.ldb >= 128 && a_span < (1ll << 32) && b_span < (1ll << 32) && s_span < (1ll << 32);
 
   // ---- LDS fragment offsets ----------------------------------------------------
   // rows of consecutive 16-row blocks have the same swizzle (it depends on
@@ -285,29 +233,83 @@ void scaled_gemm_kernel(ScaledProblem p) {
 
   auto body = [&](auto tag) {
     constexpr bool FAST = decltype(tag)::value;
-    // loads of k-tile t (relative) into stage st; k-tiles past the end read
-    // the last one again into a stage nobody reads
-    auto issue = [&](int st, int t) {
-      const int tc = t < nk ? t : nk - 1;
-      if constexpr (FAST) {
-#pragma unroll
-        for (int j = 0; j < AL; ++j) load_lds16_buf_j(j, rsrc_a, a_voff[j], tc * 128, lds_a + st * STAGE);
-#pragma unroll
-        for (int j = 0; j < BL; ++j) load_lds16_buf_j(j, rsrc_b, b_voff[j], tc * 128, lds_b + st * STAGE);
-        load_lds4_buf(rsrc_s, s_voff, (uint32_t)((int64_t)tc * s_ld * 4), lds_s + st * (BM + BN) * 4);
+    constexpr int LOADS = AL + BL + 1;
+    u32x4_t rsrc_a{}, rsrc_b{}, rsrc_s{};
+    uint32_t a_voff[AL], b_voff[BL], s_voff = 0;
+    const char *a_src[AL], *b_src[BL], *s_src = zero;
+    uint32_t ok_bits = 0;
+    int64_t s_step = 0;
+    if constexpr (FAST) {
+      // offsets shifted for load_lds16_buf_j
+      rsrc_a = buffer_rsrc(static_cast<const char*>(p.a_group[g0]) + (int64_t)in0 * p.a_ld + (int64_t)t0 * 128, a_span);
+      rsrc_b = buffer_rsrc(static_cast<const char*>(p.b) + (int64_t)n0 * p.ldb + (int64_t)t0 * 128, b_span);
+      if (wave * 64 < BM) {
+        rsrc_s = buffer_rsrc(p.a_scale[g0] + (int64_t)t0 * rpg + in0, s_span);
+        s_voff = s_row * 4;
       } else {
-        const int64_t off = (int64_t)tc * 128;
+        rsrc_s = buffer_rsrc(p.b_scale + (int64_t)t0 * p.nb + (BROW ? n0 : n0 >> 7), s_span);
+        s_voff = (BROW ? tid - BM : (tid - BM) >> 7) * 4;
+      }
 #pragma unroll
-        for (int j = 0; j < AL; ++j) {
-          const bool ok = ((ok_bits >> j) & 1) && tc * 128 + a_kc[j] < kend;
-          load_lds16_at(ok ? a_src[j] + off : zero, lds_a + st * STAGE + j * 1024);
-        }
+      for (int j = 0; j < AL; ++j)
+        a_voff[j] = (uint32_t)((int64_t)a_row(j) * p.a_ld + chunk(a_row(j)) - (j & 3) * 1024);
 #pragma unroll
-        for (int j = 0; j < BL; ++j) {
-          const bool ok = ((ok_bits >> (AL + j)) & 1) && tc * 128 + b_kc[j] < kend;
-          load_lds16_at(ok ? b_src[j] + off : zero, lds_b + st * STAGE + j * 1024);
+      for (int j = 0; j < BL; ++j)
+        b_voff[j] = (uint32_t)((int64_t)b_row(j) * p.ldb + chunk(b_row(j)) - (j & 3) * 1024);
+    } else {
+      // rows past the end keep the last row's address and are never read; all
+      // pointer loads of a lane are on their way at once
+#pragma unroll
+      for (int j = 0; j < AL; ++j) {
+        const int gi = m0 + a_row(j), gc = min(gi, p.m - 1), g = p.by_rows.quotient(gc);
+        a_src[j] = static_cast<const char*>(p.a_group[g]) + (int64_t)(gc - g * rpg) * p.a_ld + (int64_t)t0 * 128 +
+                   chunk(a_row(j));
+        ok_bits |= (uint32_t)(gi < p.m) << j;
+      }
+#pragma unroll
+      for (int j = 0; j < BL; ++j) {
+        const int gn = n0 + b_row(j);
+        b_src[j] = static_cast<const char*>(p.b) + (int64_t)min(gn, p.n - 1) * p.ldb + (int64_t)t0 * 128 +
+                   chunk(b_row(j));
+        ok_bits |= (uint32_t)(gn < p.n) << (AL + j);
+      }
+      if (wave * 64 < BM) {
+        const int gi = m0 + s_row, gc = min(gi, p.m - 1), g = p.by_rows.quotient(gc);
+        const float* src = p.a_scale[g] + (int64_t)t0 * rpg + (gc - g * rpg);
+        s_src = gi < p.m ? reinterpret_cast<const char*>(src) : zero;
+        s_step = gi < p.m ? (int64_t)rpg * 4 : 0;
+      } else {
+        const int gn = n0 + tid - BM;
+        const float* src = p.b_scale + (int64_t)t0 * p.nb + (BROW ? min(gn, p.n - 1) : min(gn, p.n - 1) >> 7);
+        s_src = gn < p.n ? reinterpret_cast<const char*>(src) : zero;
+        s_step = gn < p.n ? (int64_t)p.nb * 4 : 0;
+      }
+    }
+    // load number d of k-tile t (relative) into stage st: A, B, then scales;
+    // k-tiles past the end read the last one again into a stage nobody reads
+    auto issue = [&](int d, int st, int t) {
+      const int tc = t < nk ? t : nk - 1;
+      if (d < AL) {
+        if constexpr (FAST) {
+          load_lds16_buf_j(d, rsrc_a, a_voff[d < AL ? d : 0], tc * 128, lds_a + st * STAGE);
+        } else {
+          const int j = d < AL ? d : 0;
+          const bool ok = (((ok_bits >> j) & 1) != 0) & (tc * 128 + chunk(a_row(j)) < kend);
+          load_lds16_at(ok ? a_src[j] + (int64_t)tc * 128 : zero, lds_a + st * STAGE + j * 1024);
         }
-        load_lds4_at(s_src + tc * s_step, lds_s + st * (BM + BN) * 4);
+      } else if (d < AL + BL) {
+        const int j = d >= AL && d < AL + BL ? d - AL : 0;
+        if constexpr (FAST) {
+          load_lds16_buf_j(j, rsrc_b, b_voff[j], tc * 128, lds_b + st * STAGE);
+        } else {
+          const bool ok = (((ok_bits >> (AL + j)) & 1) != 0) & (tc * 128 + chunk(b_row(j)) < kend);
+          load_lds16_at(ok ? b_src[j] + (int64_t)tc * 128 : zero, lds_b + st * STAGE + j * 1024);
+        }
+      } else {
+        if constexpr (FAST)
+          load_lds4_buf(rsrc_s, s_voff, (uint32_t)((int64_t)tc * s_ld * 4), lds_s + st * (BM + BN) * 4);
+        else
+          load_lds4_at(s_src + tc * s_step, lds_s + st * (BM + BN) * 4);
       }
     };
     auto read_frag = [&](const char* base, u32x4_t (&f)[2]) {
@@ -317,109 +319,145 @@ void scaled_gemm_kernel(ScaledProblem p) {
     u32x4_t bf[FN][2], af[2][2];
     bf16x8_t bw[WIDE ? FN : 1][4], aw[4];
     f32x4_t part[FN];
-    float sa[FM];
+    float sa[FM], sa_last = 0.0f;
     f32x4_t sb[BROW ? FN : 1];
-    auto read_scales = [&](int st) {
-      const float* s = reinterpret_cast<const float*>(sc + st * (BM + BN) * 4);
-#pragma unroll
-      for (int i = 0; i < FM; i += 4) {
-        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(s + wm * TM + i16 * FM + i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sa[i + e] = v[e];
-      }
-      if constexpr (BROW) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j) sb[j] = *reinterpret_cast<const f32x4_t*>(s + BM + wn * TN + 16 * j + 4 * g4);
-      } else {
-        const float b = s[BM + wn * TN];           // one scale per 128 columns
-#pragma unroll
-        for (int i = 0; i < FM; ++i) sa[i] *= b;
-      }
-    };
-    auto product = [&](int i, int j) {
-      if constexpr (WIDE) part[j] = mfma128_wide(bw[j], aw);
-      else part[j] = mfma128<FMTA>(bf[j], af[i & 1]);
-    };
-    // acc of block (i, j) += its scaled product
-    auto add = [&](int i, int j) {
+    // block (i, j)'s accumulators += its scaled product
+    auto add = [&](int i, int j, float f) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        acc[i][j][e] += sa[i] * (BROW ? part[j][e] * sb[BROW ? j : 0][e] : part[j][e]);
+        acc[i][j][e] += f * (BROW ? part[j][e] * sb[BROW ? j : 0][e] : part[j][e]);
     };
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      part[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (BROW) sb[BROW ? j : 0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
 
-    issue(0, 0);
-    issue(1, 1);
-    wait_vmcnt<AL + BL + 1>();
+    // Schedule.  One slot per product: the FMAs of the product FN slots ago,
+    // the product, then the slot's memory operation, fenced so that it stays
+    // there.  Slots of block row i < FM - 1 read A fragment i + 1 (first slot);
+    // before the last block row the workgroup synchronises (all reads of
+    // k-tile t are done, the loads of t + 1 have landed), and its slots read
+    // the first fragments of k-tile t + 1 and begin to refill t's stage; the
+    // other loads of that refill ride on the first slots of t + 1, where the
+    // scales are read too.
+    constexpr int EARLY = FN - 1;   // refill loads in the last block row
+    static_assert(EARLY + (FM - 1) * FN >= LOADS, "every refill is issued before the next synchronisation");
+    for (int t = 0; t < NST - 1; ++t)
+#pragma unroll
+      for (int d = 0; d < LOADS; ++d) issue(d, t, t);
+#pragma unroll
+    for (int d = 0; d < EARLY; ++d) issue(d, NST - 1, NST - 1);
+    wait_vmcnt<(NST - 2) * LOADS + EARLY>();
     block_barrier();
-    read_scales(0);
+    read_frag(smem + a_base, af[0]);
 #pragma unroll
     for (int j = 0; j < FN; ++j) read_frag(smem + b_base + j * 2048, bf[j]);
-    read_frag(smem + a_base, af[0]);
+    int st = 0, prev = NST - 1;                    // stages of k-tiles t and t - 1
     for (int t = 0; t < nk; ++t) {
-      const char* cur = smem + (t & 1) * STAGE;
-      const char* nxt = smem + ((t + 1) & 1) * STAGE;
-      if constexpr (WIDE)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) widen<kFmtE4M3>(bf[j], bw[j]);
+      const int sn = st + 1 == NST ? 0 : st + 1;
+      const char* cur = smem + st * STAGE;
+      const char* nxt = smem + sn * STAGE;
+      const float* s = reinterpret_cast<const float*>(sc + st * (BM + BN) * 4);
+      float b128 = 0.0f;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        if constexpr (WIDE) widen<FMTA>(af[i & 1], aw);
-        if (i + 1 < FM) {
-          read_frag(cur + a_base + (i + 1) * 2048, af[(i + 1) & 1]);
-#pragma unroll
-          for (int j = 0; j < FN; ++j) {
-            if (i > 0) add(i - 1, j);
-            product(i, j);
-          }
-        } else {
-          // every fragment of k-tile t is in registers: refill its stage, and
-          // read the first fragments of k-tile t + 1 beside the last MFMAs
-          wait_vmcnt<0>();
+        if (i == FM - 1) {
+          wait_vmcnt<(NST - 2) * LOADS>();
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
           block_barrier();
-          issue(t & 1, t + 2);
-          read_frag(nxt + a_base, af[(i + 1) & 1]);
+        }
+        if constexpr (WIDE) {
+          // the four MFMAs of a block depend on each other: block by block in
+          // turn, scheduled by the compiler within the block row
+          widen<FMTA>(af[i & 1], aw);
 #pragma unroll
           for (int j = 0; j < FN; ++j) {
-            add(i - 1, j);
-            product(i, j);
-            read_frag(nxt + b_base + j * 2048, bf[j]);
+            if (i == 0) widen<kFmtE4M3>(bf[j], bw[j]);
+            add(i > 0 ? i - 1 : FM - 1, j, i > 0 ? sa[i > 0 ? i - 1 : 0] : sa_last);
+            part[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
           }
 #pragma unroll
-          for (int j = 0; j < FN; ++j) add(i, j);
-          read_scales((t + 1) & 1);
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+              part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[j][q], aw[q], part[j], 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if constexpr (!WIDE) {
+            if (i > 0) add(i - 1, j, sa[i - 1]);
+            else add(FM - 1, j, sa_last);          // of the previous k-tile
+            part[j] = mfma128<FMTA>(bf[j], af[i & 1]);
+          }
+          if (i < FM - 1) {
+            if (j == 0) read_frag(cur + a_base + (i + 1) * 2048, af[(i + 1) & 1]);
+            const int d = EARLY + i * FN + j;
+            if (d < LOADS) issue(d < LOADS ? d : 0, prev, t - 1 + NST);
+            if (i == 0) {
+              if (j == 1) {
+#pragma unroll
+                for (int q = 0; q < FM; q += 4) {
+                  const f32x4_t v = *reinterpret_cast<const f32x4_t*>(s + wm * TM + i16 * FM + q);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) sa[q + e] = v[e];
+                }
+                if constexpr (!BROW) b128 = s[BM + wn * TN];   // one scale per 128 columns
+              }
+              if constexpr (BROW) sb[j] = *reinterpret_cast<const f32x4_t*>(s + BM + wn * TN + 16 * j + 4 * g4);
+              if constexpr (!BROW)
+                if (j == FN - 1)
+#pragma unroll
+                  for (int q = 0; q < FM; ++q) sa[q] *= b128;
+            }
+          } else {
+            if (j == 0) read_frag(nxt + a_base, af[FM & 1]);
+            read_frag(nxt + b_base + j * 2048, bf[j]);
+            if (j > 0) issue(j > 0 ? j - 1 : 0, st, t + NST);
+          }
+          if (!WIDE || j == FN - 1) __builtin_amdgcn_sched_barrier(0);
         }
       }
-      static_assert(FM % 2 == 0, "two sets of A fragments alternate by row block");
+      sa_last = sa[FM - 1];
+      prev = st;
+      st = sn;
+      static_assert(FM % 4 == 0, "two sets of A fragments alternate by row block; scales are read by fours");
     }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) add(FM - 1, j, sa_last);
     wait_vmcnt<0>();
   };
   if (fast) body(BoolTag<true>{});
   else body(BoolTag<false>{});
 
   // ---- epilogue: acc[i][j][e] = C[m0 + wm*TM + 16i + i16][n0 + wn*TN + 16j + 4*g4 + e]
+  const int row0 = m0 + wm * TM + i16, col0 = n0 + wn * TN + 4 * g4;
+  const bool split_k = p.splits > 1;
+  const int64_t ld = split_k ? p.part_ld : p.ldc;
+  const int ncols = split_k ? (int)p.part_ld : p.n;   // padding columns of the sums are never read as results
+  const bool inside = m0 + BM <= p.m && n0 + BN <= ncols && ld % 4 == 0;
+  const auto store = [&](auto type) {
+    constexpr int CT = decltype(type)::value;
+    typedef typename OutOf<CT>::type out_t;
+    out_t* base = static_cast<out_t*>(split_k ? p.partials + (int64_t)split * p.m * ld : p.c) + (int64_t)row0 * ld + col0;
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int row = m0 + wm * TM + 16 * i + i16;
-    if (row >= p.m) continue;
+    for (int i = 0; i < FM; ++i, base += 16 * ld)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int col = n0 + wn * TN + 16 * j + 4 * g4;
-      if (col >= p.n) continue;
-      if (p.splits > 1) {
-        float* d = p.partials + ((int64_t)split * p.m + row) * p.n + col;
-        if (col + 3 < p.n && (p.n % 4) == 0) {
-          *reinterpret_cast<f32x4_t*>(d) = acc[i][j];
-        } else {
+      for (int j = 0; j < FN; ++j) {
+        if (inside) {
+          put4<CT>(base + 16 * j, acc[i][j]);
+        } else if (row0 + 16 * i < p.m && ld % 4 == 0 && col0 + 16 * j + 4 <= ncols) {
+          put4<CT>(base + 16 * j, acc[i][j]);
+        } else if (row0 + 16 * i < p.m) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (col + e < p.n) d[e] = acc[i][j][e];
+            if (col0 + 16 * j + e < p.n) put1<CT>(base + 16 * j + e, acc[i][j][e]);
         }
-      } else {
-        store4(p, row, col, acc[i][j]);
       }
-    }
-  }
+  };
+  if (split_k || p.c_dtype == kDtypeFp32) store(IntTag<kDtypeFp32>{});
+  else if (p.c_dtype == kDtypeBf16) store(IntTag<kDtypeBf16>{});
+  else store(IntTag<kDtypeFp16>{});
 }
 
 // Few rows: ROWS x COLS outputs per workgroup, over all of k or one of
@@ -429,70 +467,64 @@ void scaled_gemm_kernel(ScaledProblem p) {
 template <int FMTA, int ROWS, int COLS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES / 4)))
 void scaled_skinny_kernel(ScaledProblem p) {
-  constexpr int AL = ROWS / 8, BL = COLS / 8, LOADS = AL + BL + 1;
-  constexpr int SLOT = (ROWS + COLS) * 128 + 256;
+  constexpr int SL = (ROWS + COLS + 63) / 64;                 // loads of scales
+  constexpr int AL = ROWS / 8, BL = COLS / 8, LOADS = AL + BL + SL;
+  constexpr int SLOT = (ROWS + COLS) * 128 + SL * 256;
   constexpr int FIT = 160 * 1024 / WAVES / SLOT, SLOTS = FIT < 6 ? FIT : 6;
   constexpr int WAVE_LDS = SLOTS * SLOT;
   constexpr int FM = ROWS / 16, FN = COLS / 16;
-  static_assert(ROWS + COLS <= 64, "one scale per lane");
   static_assert(SLOTS >= 2 && SLOTS * LOADS < 64, "ring");
   __shared__ __attribute__((aligned(1024))) char smem[WAVES * WAVE_LDS];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int RB = (p.m + ROWS - 1) / ROWS, CB = (p.n + COLS - 1) / COLS;
   int tile, split;
   {
     // XCD x (workgroup id mod 8) takes a contiguous range, row blocks
     // fastest: the row blocks of one column block share its L2
-    const int T = RB * CB * p.splits, wg = blockIdx.x;
+    const int ntiles = p.order.num_rb * p.order.num_cb;
+    const int T = ntiles * p.splits, wg = blockIdx.x;
     const int xcd = wg & 7, local = wg >> 3, per = T >> 3, rem = T & 7;
-    const int u = xcd * per + (xcd < rem ? xcd : rem) + local;
-    tile = u % (RB * CB);
-    split = u / (RB * CB);
+    const int u = xcd * per + min(xcd, rem) + local;
+    split = p.by_tiles.quotient(u);
+    tile = u - split * ntiles;
   }
-  const int row0 = (tile % RB) * ROWS, n0 = (tile / RB) * COLS;
+  const int cb = p.by_group.quotient(tile);
+  const int row0 = (tile - cb * p.order.num_rb) * ROWS, n0 = cb * COLS;
   const int t0 = split * p.kb_per_split, t1 = min(p.kb, t0 + p.kb_per_split);
   const int rpg = p.rows_per_group;
   const char* zero = reinterpret_cast<const char*>(g_zero_chunk);
 
+  // rows and columns past the end keep the last one's address and are never
+  // read; all pointer loads of a lane are on their way at once
   const char* a_src[AL];
   const char* b_src[BL];
   uint32_t ok_bits = 0;
 #pragma unroll
   for (int q = 0; q < AL; ++q) {
-    const int r = 8 * q + (lane >> 3), gr = row0 + r;
-    a_src[q] = zero;
-    if (gr < p.m) {
-      const int g = gr / rpg, t = gr - g * rpg;
-      a_src[q] = static_cast<const char*>(p.a_group[g]) + (int64_t)t * p.a_ld + ((lane & 7) ^ swz_k16(r)) * 16;
-      ok_bits |= 1u << q;
-    }
+    const int r = 8 * q + (lane >> 3), gr = row0 + r, gc = min(gr, p.m - 1), g = p.by_rows.quotient(gc);
+    a_src[q] = static_cast<const char*>(p.a_group[g]) + (int64_t)(gc - g * rpg) * p.a_ld + ((lane & 7) ^ swz_k16(r)) * 16;
+    ok_bits |= (uint32_t)(gr < p.m) << q;
   }
 #pragma unroll
   for (int q = 0; q < BL; ++q) {
     const int r = 8 * q + (lane >> 3), gn = n0 + r;
-    b_src[q] = zero;
-    if (gn < p.n) {
-      b_src[q] = static_cast<const char*>(p.b) + (int64_t)gn * p.ldb + ((lane & 7) ^ swz_k16(r)) * 16;
-      ok_bits |= 1u << (AL + q);
-    }
+    b_src[q] = static_cast<const char*>(p.b) + (int64_t)min(gn, p.n - 1) * p.ldb + ((lane & 7) ^ swz_k16(r)) * 16;
+    ok_bits |= (uint32_t)(gn < p.n) << (AL + q);
   }
-  const char* s_src = zero;
-  int64_t s_step = 0;
-  if (lane < ROWS) {
-    const int gr = row0 + lane;
-    if (gr < p.m) {
-      const int g = gr / rpg;
-      s_src = reinterpret_cast<const char*>(p.a_scale[g] + (gr - g * rpg));
-      s_step = (int64_t)rpg * 4;
-    }
-  } else if (lane < ROWS + COLS) {
-    const int gn = n0 + lane - ROWS;
-    if (gn < p.n) {
-      s_src = reinterpret_cast<const char*>(p.b_scale + gn / p.b_block_rows);
-      s_step = (int64_t)p.nb * 4;
-    }
+  const char* s_src[SL];
+  int64_t s_step[SL];
+#pragma unroll
+  for (int q = 0; q < SL; ++q) {
+    const int l = 64 * q + lane;
+    const int gr = row0 + l, gn = n0 + l - ROWS;
+    const int gc = min(gr, p.m - 1), g = p.by_rows.quotient(gc);
+    const int cn = min(max(gn, 0), p.n - 1);
+    const float* as = p.a_scale[g] + (gc - g * rpg);
+    const float* bs = p.b_scale + (p.b_block_rows == 1 ? cn : cn >> 7);
+    const bool is_a = l < ROWS, ok = is_a ? gr < p.m : l < ROWS + COLS && gn < p.n;
+    s_src[q] = ok ? reinterpret_cast<const char*>(is_a ? as : bs) : zero;
+    s_step[q] = ok ? (int64_t)(is_a ? rpg : p.nb) * 4 : 0;
   }
 
   char* const ring = smem + wave * WAVE_LDS;
@@ -505,10 +537,11 @@ void scaled_skinny_kernel(ScaledProblem p) {
 #pragma unroll
     for (int q = 0; q < AL + BL; ++q) {
       const int r = 8 * (q < AL ? q : q - AL) + (lane >> 3);
-      const bool ok = ((ok_bits >> q) & 1) && t * 128 + ((lane & 7) ^ swz_k16(r)) * 16 < p.k16;
+      const bool ok = (((ok_bits >> q) & 1) != 0) & (t * 128 + ((lane & 7) ^ swz_k16(r)) * 16 < p.k16);
       load_lds16_at(ok ? (q < AL ? a_src[q < AL ? q : 0] : b_src[q < AL ? 0 : q - AL]) + off : zero, dst + q * 1024);
     }
-    load_lds4_at(s_src + (int64_t)t * s_step, dst + (ROWS + COLS) * 128);
+#pragma unroll
+    for (int q = 0; q < SL; ++q) load_lds4_at(s_src[q] + (int64_t)t * s_step[q], dst + (ROWS + COLS) * 128 + q * 256);
   };
 
   const int g4 = lane >> 4, i16 = lane & 15;
@@ -595,10 +628,7 @@ void scaled_skinny_kernel(ScaledProblem p) {
     const int row = row0 + r, col = n0 + c;
     if (row >= p.m || col >= p.n) continue;
     if (p.splits > 1) {
-      float* d = p.partials + ((int64_t)split * p.m + row) * p.n + col;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (col + e < p.n) d[e] = v[e];
+      *reinterpret_cast<f32x4_t*>(p.partials + ((int64_t)split * p.m + row) * p.part_ld + col) = v;
     } else {
       store4(p, row, col, v);
     }
@@ -607,20 +637,21 @@ void scaled_skinny_kernel(ScaledProblem p) {
 
 // Sum of the k ranges in order, four columns per thread.
 __global__ __launch_bounds__(256) void scaled_reduce_kernel(ScaledProblem p) {
-  const int n4 = (p.n + 3) / 4;
-  const int64_t plane = (int64_t)p.m * p.n;
+  const int n4 = (int)(p.part_ld / 4);
+  const int64_t plane = (int64_t)p.m * p.part_ld;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < (int64_t)p.m * n4; u += (int64_t)gridDim.x * 256) {
     const int row = (int)(u / n4), col = (int)(u % n4) * 4;
-    const float* src = p.partials + (int64_t)row * p.n + col;
-    f32x4_t v = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if ((p.n % 4) == 0) {
-      v = *reinterpret_cast<const f32x4_t*>(src);
-      for (int s = 1; s < p.splits; ++s) v += *reinterpret_cast<const f32x4_t*>(src + s * plane);
-    } else {
-      for (int s = 0; s < p.splits; ++s)
+    const float* src = p.partials + (int64_t)row * p.part_ld + col;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    // eight ranges are on their way at a time, added in order
+    for (int s0 = 0; s0 < p.splits; s0 += 8) {
+      f32x4_t w[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < p.n) v[e] += src[s * plane + e];
+      for (int s = 0; s < 8; ++s)
+        if (s0 + s < p.splits) w[s] = *reinterpret_cast<const f32x4_t*>(src + (s0 + s) * plane);
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s0 + s < p.splits) v += w[s];
     }
     store4(p, row, col, v);
   }
@@ -629,12 +660,15 @@ __global__ __launch_bounds__(256) void scaled_reduce_kernel(ScaledProblem p) {
 template <int FMTA, bool BROW>
 hipError_t launch_tile(const ScaledProblem& p, int tile, hipStream_t stream) {
   const int64_t grid = (int64_t)p.order.num_rb * p.order.num_cb * p.splits;
-  if (tile == kScaled256)
-    hipLaunchKernelGGL((scaled_gemm_kernel<FMTA, BROW, false, 256, 256, 2, 4>), dim3((unsigned)grid), dim3(512), 0, stream, p);
-  else if (p.wide)
-    hipLaunchKernelGGL((scaled_gemm_kernel<FMTA, BROW, true, 128, 128, 2, 2>), dim3((unsigned)grid), dim3(256), 0, stream, p);
-  else
-    hipLaunchKernelGGL((scaled_gemm_kernel<FMTA, BROW, false, 128, 128, 2, 2>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+#define AGMM_SCALED(WIDE, BM, BN, WM, WN, NST, OCC)                                                             \
+  hipLaunchKernelGGL((scaled_gemm_kernel<FMTA, BROW, WIDE, BM, BN, WM, WN, NST, OCC>), dim3((unsigned)grid),   \
+                     dim3(64 * WM * WN), 0, stream, p)
+  if (tile == kScaled256) AGMM_SCALED(false, 256, 256, 2, 4, 2, 2);
+  else if (p.wide && p.deep) AGMM_SCALED(true, 128, 128, 2, 2, 4, 2);
+  else if (p.wide) AGMM_SCALED(true, 128, 128, 2, 2, 2, 2);
+  else if (p.deep) AGMM_SCALED(false, 128, 128, 2, 2, 4, 2);
+  else AGMM_SCALED(false, 128, 128, 2, 2, 2, 2);
+#undef AGMM_SCALED
   return hipGetLastError();
 }
 
@@ -642,26 +676,44 @@ template <int FMTA>
 hipError_t launch_skinny(const ScaledProblem& p, int tile, hipStream_t stream) {
   const int rows = scaled_tile_rows(tile), cols = scaled_tile_cols(tile);
   const int64_t grid = (int64_t)((p.m + rows - 1) / rows) * ((p.n + cols - 1) / cols) * p.splits;
-  if (tile == kScaledSkinny16)
+  if (tile == kScaledSkinny16n)
+    hipLaunchKernelGGL((scaled_skinny_kernel<FMTA, 16, 16, 8>), dim3((unsigned)grid), dim3(512), 0, stream, p);
+  else if (tile == kScaledSkinny16)
     hipLaunchKernelGGL((scaled_skinny_kernel<FMTA, 16, 32, 4>), dim3((unsigned)grid), dim3(256), 0, stream, p);
-  else
+  else if (tile == kScaledSkinny32)
     hipLaunchKernelGGL((scaled_skinny_kernel<FMTA, 32, 32, 4>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+  else
+    hipLaunchKernelGGL((scaled_skinny_kernel<FMTA, 64, 64, 4>), dim3((unsigned)grid), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_scaled(const ScaledProblem& p, int tile, hipStream_t stream) {
+hipError_t launch_scaled(const ScaledProblem& problem, int tile, hipStream_t stream) {
+  ScaledProblem p = problem;
   const int rows = scaled_tile_rows(tile), cols = scaled_tile_cols(tile);
   const int64_t grid = (int64_t)((p.m + rows - 1) / rows) * ((p.n + cols - 1) / cols) * p.splits;
   if (rows == 0 || grid < 1 || grid >= (int64_t(1) << 23) || p.splits < 1 ||
-      (p.splits > 1 && !p.partials) || (int64_t)p.splits * p.kb_per_split < p.kb ||
+      (p.splits > 1 && (!p.partials || p.part_ld % 4 != 0 || p.part_ld < p.n)) || (int64_t)p.splits * p.kb_per_split < p.kb ||
       (int64_t)(p.splits - 1) * p.kb_per_split >= p.kb || p.k16 % 16 != 0 || p.kb != (p.k16 + 127) / 128 ||
-      p.num_groups < 1 || p.num_groups > kMaxGroups || (int64_t)p.num_groups * p.rows_per_group != p.m)
+      p.num_groups < 1 || p.num_groups > kMaxGroups || p.order.num_rb != (p.m + rows - 1) / rows ||
+      p.order.num_cb != (p.n + cols - 1) / cols || (int64_t)p.num_groups * p.rows_per_group != p.m)
     return hipErrorInvalidValue;
+  const int group_m = p.order.group_m;
+  if (tile < kScaledSkinny16 && group_m < 1) return hipErrorInvalidValue;
+  p.by_rows = FastDiv(p.rows_per_group);
+  p.by_tiles = FastDiv(p.order.num_rb * p.order.num_cb);
+  if (tile >= kScaledSkinny16) {
+    p.by_group = FastDiv(p.order.num_rb);
+  } else {
+    const int last = p.order.num_rb % group_m;
+    p.by_group = FastDiv(group_m * p.order.num_cb);
+    p.by_full = FastDiv(group_m);
+    p.by_last = FastDiv(last ? last : group_m);
+  }
   hipError_t err;
   const bool e5m2 = p.a_format == kFmtE5M2;
-  if (tile == kScaledSkinny16 || tile == kScaledSkinny32)
+  if (tile >= kScaledSkinny16)
     err = e5m2 ? launch_skinny<kFmtE5M2>(p, tile, stream) : launch_skinny<kFmtE4M3>(p, tile, stream);
   else if (p.b_block_rows == 1)
     err = e5m2 ? launch_tile<kFmtE5M2, true>(p, tile, stream) : launch_tile<kFmtE4M3, true>(p, tile, stream);
