@@ -247,10 +247,10 @@ struct LossProblem {
   // statistics: (maximum, sum of exp) pairs [2 * column block + half][m]
   float* stats;
   float* target;           // [m], written where the piece holds the label
-  // gradient: rows {lse, a, b, s} [m]; d [m][ldd] and dt [n][ldt], the
-  // columns past n (m) up to ldd (ldt) within the last tile as zeros
+  // gradient: rows {lse, a, b, s} [m]; d [m][ldd] and dt [n][ldt] (either
+  // may be null), the columns past n (m) up to ldd (ldt) as zeros; both
+  // strides are multiples of 8
   const float* rows;
-  const float* scale_all;
   void* d;
   int64_t ldd;
   void* dt;
@@ -278,14 +278,25 @@ struct LossRows {
   float* rows;
   float* scale_all;
 };
-hipError_t launch_loss_rows(const LossRows& c, hipStream_t stream);
+hipError_t launch_loss_rows(const LossRows& c, int dtype, hipStream_t stream);
 
-// fp32 sums of d W: A = d [m][ldd], B = W k x n; into p.partials [splits][m][n].
-hipError_t launch_loss_da(const GemmProblem& p, int tile, int dtype, bool add, hipStream_t stream);
-// C = scale[0] * dt A.
-hipError_t launch_loss_dw(const GemmProblem& p, int tile, int dtype, const float* scale, hipStream_t stream);
+// out [m][8 * chunks] = fp16 rows of A times rows[i][3] / scale_all[0] (at most 1).
+struct LossScaleRows {
+  const void* group[kMaxGroups];
+  int64_t rows_per_group, ld, m, chunks;
+  const float* rows;
+  const float* scale_all;
+  void* out;
+};
+hipError_t launch_loss_scale_rows(const LossScaleRows& c, hipStream_t stream);
+
+// The two gradient products, B k x n, in one launch: fp32 sums of d W (A = d
+// [m][ldd]) into a->partials [splits][m][n rounded up to 4], added to what is there
+// when `add`, and C = scale[0] * dt A (scale null: 1).  Either may be null.
+hipError_t launch_loss_grads(const GemmProblem* a, bool add, const GemmProblem* w, const float* scale, int tile, int dtype,
+                             hipStream_t stream);
 struct LossFinish {
-  const float* sums;       // [ranges][m][k]
+  const float* sums;       // [ranges][m][k rounded up to 4]
   int32_t ranges;
   int64_t m;
   int32_t k;

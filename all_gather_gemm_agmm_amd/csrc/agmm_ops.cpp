@@ -390,10 +390,11 @@ struct agmm_loss_plan : PlanBase {
     bool pad_a = false, pad_w = false;   // rows that are not whole 16-byte vectors: zero-padded copies
     int64_t kp = 0;                      // k rounded up to 8
     int64_t piece = 0;                   // columns of the vocabulary per piece
-    int tile = 256, tile_da = 256, tile_dw = 256;
+    int tile = 256, tile_grads = 256;
     int ranges = 1;                      // k ranges of the dA product
     int64_t per_range = 0;
-    char *a = nullptr, *w = nullptr, *d = nullptr, *dt = nullptr;
+    // a: gathered or padded copy of A; as: fp16, its rows scaled for dW's product
+    char *a = nullptr, *as = nullptr, *w = nullptr, *d = nullptr, *dt = nullptr;
     float *stats = nullptr, *running = nullptr, *rows = nullptr, *scale_all = nullptr, *sums = nullptr;
     size_t bytes = 0;
   };
@@ -432,21 +433,25 @@ struct agmm_loss_plan : PlanBase {
       L.stats = reinterpret_cast<float*>(c.take((size_t)cdiv(L.piece, L.tile) * 2 * m * 8));
       L.running = reinterpret_cast<float*>(c.take((size_t)m * 8));
     } else {
-      if (L.pad_a || N > 1) L.a = c.take((size_t)m * L.kp * 2);
+      const bool half = dtype == AGMM_FP16;
+      if (L.pad_a || (N > 1 && !half)) L.a = c.take((size_t)m * L.kp * 2);
+      if (half) L.as = c.take((size_t)m * L.kp * 2);
       L.rows = reinterpret_cast<float*>(c.take((size_t)m * 16));
       L.scale_all = reinterpret_cast<float*>(c.take(4));
       L.d = c.take((size_t)m * round_up(L.piece, 8) * 2);
       L.dt = c.take((size_t)L.piece * m8() * 2);
-      L.tile_da = pick_tile(m, k);
-      L.tile_dw = pick_tile(L.piece, k);
+      // one launch computes both products, in tiles that suit their sum
+      const double big = (double)cdiv(cdiv(m, 256) * cdiv(k, 256) + cdiv(L.piece, 256) * cdiv(k, 256), cu_count) * 4.0;
+      const double small = (double)cdiv(cdiv(m, 128) * cdiv(k, 128) + cdiv(L.piece, 128) * cdiv(k, 128), cu_count) / 0.8;
+      L.tile_grads = big <= small ? 256 : 128;
       // ranges of a piece's columns where dA has too few output tiles
-      const int64_t tiles = cdiv(m, L.tile_da) * cdiv(k, L.tile_da);
-      const int64_t slots = (int64_t)cu_count * (L.tile_da == 128 ? 2 : 1);
+      const int64_t tiles = cdiv(m, L.tile_grads) * cdiv(k, L.tile_grads);
+      const int64_t slots = (int64_t)cu_count * (L.tile_grads == 128 ? 2 : 1);
       int64_t want = 1;
       while (want * 2 * tiles <= slots && L.piece / (want * 2) >= 512) want *= 2;
       L.per_range = round_up(cdiv(L.piece, want), 64);
       L.ranges = (int)cdiv(L.piece, L.per_range);
-      L.sums = reinterpret_cast<float*>(c.take((size_t)L.ranges * m * k * 4));
+      L.sums = reinterpret_cast<float*>(c.take((size_t)L.ranges * m * round_up(k, 4) * 4));
     }
     L.bytes = c.at;
     return L;
@@ -614,8 +619,21 @@ struct agmm_loss_plan : PlanBase {
     lr.grad_lse = grad_lse;
     lr.rows = L.rows;
     lr.scale_all = L.scale_all;
-    hipError_t err = agmm::launch_loss_rows(lr, s);
+    hipError_t err = agmm::launch_loss_rows(lr, dtype, s);
     if (err != hipSuccess) return hip_err(err, "loss rows launch");
+    if (L.as && dW) {
+      agmm::LossScaleRows r{};
+      for (int g = 0; g < rows.num_groups; ++g) r.group[g] = rows.a_group[g];
+      r.rows_per_group = rows.rows_per_group;
+      r.ld = rows.a_ld;
+      r.m = m;
+      r.chunks = L.kp / 8;
+      r.rows = L.rows;
+      r.scale_all = L.scale_all;
+      r.out = L.as;
+      err = agmm::launch_loss_scale_rows(r, s);
+      if (err != hipSuccess) return hip_err(err, "row scaling launch");
+    }
     for (int64_t v0 = 0; v0 < n; v0 += L.piece) {
       const int64_t vn = std::min(L.piece, n - v0);
       const void* w;
@@ -624,46 +642,38 @@ struct agmm_loss_plan : PlanBase {
       if (rc != AGMM_OK) return rc;
       agmm::LossProblem p = logits(L, rows, w, ldb, v0, vn, labels);
       p.rows = L.rows;
-      p.scale_all = L.scale_all;
       p.d = dA ? L.d : nullptr;
       p.ldd = round_up(vn, 8);
       p.dt = dW ? L.dt : nullptr;
       p.ldt = m8();
       err = agmm::launch_loss_logits(p, dtype, true, s);
       if (err != hipSuccess) return hip_err(err, "loss gradient launch");
-      if (dA) {
-        agmm::GemmProblem g{};
-        g.rows = dense(L.d, m, round_up(vn, 8));
-        g.order = order(m, k, L.tile_da);
-        g.m = (int32_t)m;
-        g.n = (int32_t)k;
-        g.k = (int32_t)vn;
-        g.b = w;
-        g.ldb = ldb;
-        // the last piece may have fewer ranges: the rest keep their sums
-        g.k_per_split = (int32_t)L.per_range;
-        g.splits = (int32_t)cdiv(vn, L.per_range);
-        g.partials = L.sums;
-        err = agmm::launch_loss_da(g, L.tile_da, dtype, v0 > 0, s);
-        if (err != hipSuccess) return hip_err(err, "dA launch");
-      }
-      if (dW) {
-        agmm::GemmProblem g{};
-        g.rows = dense(L.dt, vn, m8());
-        g.order = order(vn, k, L.tile_dw);
-        g.m = (int32_t)vn;
-        g.n = (int32_t)k;
-        g.k = (int32_t)m;
-        g.b = L.a ? L.a : shards[0];
-        g.ldb = L.a ? L.kp : ld_a();
-        g.splits = 1;
-        g.k_per_split = (int32_t)round_up(m, 64);
-        const int64_t ldc = lddw ? lddw : k;
-        g.c = static_cast<char*>(dW) + v0 * ldc * 2;
-        g.ldc = ldc;
-        err = agmm::launch_loss_dw(g, L.tile_dw, dtype, L.scale_all, s);
-        if (err != hipSuccess) return hip_err(err, "dW launch");
-      }
+      agmm::GemmProblem ga{}, gw{};
+      ga.rows = dense(L.d, m, round_up(vn, 8));
+      ga.order = order(m, k, L.tile_grads);
+      ga.m = (int32_t)m;
+      ga.n = (int32_t)k;
+      ga.k = (int32_t)vn;
+      ga.b = w;
+      ga.ldb = ldb;
+      // the last piece may have fewer ranges: the rest keep their sums
+      ga.k_per_split = (int32_t)L.per_range;
+      ga.splits = (int32_t)cdiv(vn, L.per_range);
+      ga.partials = L.sums;
+      gw.rows = dense(L.dt, vn, m8());
+      gw.order = order(vn, k, L.tile_grads);
+      gw.m = (int32_t)vn;
+      gw.n = (int32_t)k;
+      gw.k = (int32_t)m;
+      gw.b = L.as ? L.as : L.a ? L.a : shards[0];
+      gw.ldb = L.as || L.a ? L.kp : ld_a();
+      gw.splits = 1;
+      gw.k_per_split = (int32_t)round_up(m, 64);
+      gw.ldc = lddw ? lddw : k;
+      gw.c = static_cast<char*>(dW) + v0 * gw.ldc * 2;
+      err = agmm::launch_loss_grads(dA ? &ga : nullptr, v0 > 0, dW ? &gw : nullptr, L.as ? L.scale_all : nullptr,
+                                    L.tile_grads, dtype, s);
+      if (err != hipSuccess) return hip_err(err, "gradient products launch");
     }
     if (dA) {
       agmm::LossFinish f{};

@@ -4,11 +4,12 @@
 //     dA[i, :] = s_i * sum_v d[i, v] * W[v, :]         (rows of d, W k x n as stored)
 //     dW[v, :] = S   * sum_i dt[v, i] * A[i, :]        (d transposed, A k x n as gathered)
 //
-// Both are the part-ring GEMM (gemm_m16_loop.inc) with B stored k x n.  dA is
-// summed over the pieces of the vocabulary (and over ranges of a piece where
-// few output tiles would leave CUs idle) in fp32 sums [range][m][k] that
-// each piece adds to in place, in order; one last pass adds the ranges, scales
-// and casts.  dW of a piece is complete at once.  Bound: MFMA.
+// Both are the part-ring GEMM (gemm_m16_loop.inc) with B stored k x n, and
+// share a launch: with few rows neither fills the CUs alone.  dA is summed
+// over the pieces of the vocabulary (and over ranges of a piece where few
+// output tiles would leave CUs idle) in fp32 sums [range][m][k] that each
+// piece adds to in place, in order; one last pass adds the ranges, scales and
+// casts.  dW of a piece is complete at once.  Bound: MFMA.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -19,114 +20,111 @@ namespace agmm {
 
 namespace {
 
-// SPLIT: fp32 sums of range `split` into p.partials, added to what is there
-// when `add`; else C = scale * sums.
-template <int BM, int BN, int BK, int DT, bool SPLIT, int WAVES, int OCC>
-__device__ __forceinline__ void grad_body(const GemmProblem& p, bool add, const float* scale, char* smem) {
-  constexpr bool BT = false;
+struct GradPair {
+  GemmProblem a, w;        // dA and dW
+  int32_t a_tiles;         // workgroups of dA: the first ones
+  int32_t add;             // dA: add to the sums that are there
+  const float* scale;      // dW: its factor, or null
+};
+
+template <int BM, int BN, int DT, int OCC>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
+void loss_grads_kernel(GradPair gp) {
+  constexpr bool BT = false, SPLIT = true;
+  constexpr int BK = 64, WAVES = 4;
   using T = GemmTile<BM, BN, BK, DT, BT, 5, WAVES, kLoopParts>;
   constexpr int kBK = BK;
   constexpr int FM = T::TM / 16, FN = T::TN / 16;
   constexpr int STEPS = BK / 32;
+  __shared__ __attribute__((aligned(1024))) char smem[T::LDS_BYTES];
+  const bool is_a = (int)blockIdx.x < gp.a_tiles;
+  const GemmProblem& p = is_a ? gp.a : gp.w;
 
+#define AGMM_TILE_ID (is_a ? (int)blockIdx.x : (int)blockIdx.x - gp.a_tiles)
 #include "gemm_m16_loop.inc"
 
-  if constexpr (SPLIT) {
+  if (is_a) {
+    // rows of the sums are whole 16-byte vectors; what lies past k in the last
+    // one is never used
+    const int row0 = m0 + wm * T::TM + i16, col0 = n0 + wn * T::TN + 4 * g4;
+    const int64_t ld = (N + 3) & ~3;
+    float* base = p.partials + ((int64_t)split * M + row0) * ld + col0;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int row = m0 + wm * T::TM + 16 * i + i16;
-      if (row >= M) continue;
-      float* d = p.partials + ((int64_t)split * M + row) * N;
+    for (int i = 0; i < FM; ++i, base += 16 * ld) {
+      if (row0 + 16 * i < M) {
+        if (gp.add) {
+          f32x4_t was[FN];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int col = n0 + wn * T::TN + 16 * j + 4 * g4;
-        if (col + 3 < N && N % 4 == 0) {
-          f32x4_t* q = reinterpret_cast<f32x4_t*>(d + col);
-          *q = add ? *q + acc[i][j] : acc[i][j];
+          for (int j = 0; j < FN; ++j)
+            if (col0 + 16 * j < N) was[j] = *reinterpret_cast<const f32x4_t*>(base + 16 * j);
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            if (col0 + 16 * j < N) *reinterpret_cast<f32x4_t*>(base + 16 * j) = was[j] + acc[i][j];
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col + e < N) d[col + e] = add ? d[col + e] + acc[i][j][e] : acc[i][j][e];
+          for (int j = 0; j < FN; ++j)
+            if (col0 + 16 * j < N) *reinterpret_cast<f32x4_t*>(base + 16 * j) = acc[i][j];
         }
       }
+      __builtin_amdgcn_sched_barrier(0);   // one block row's values at a time
     }
   } else {
-    const float f = scale[0] * (DT == kDtypeFp16 ? 1.0f / 16384.0f : 1.0f);
-    // whole rows through LDS, as in gemm_m16_kernel
-    constexpr int kRowB = BN * 2, kChunks = kRowB / 16;
-    const bool staged = m0 + BM <= M && n0 + BN <= N && p.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0;
-    if (staged) __syncthreads();
+    const float f = (gp.scale ? gp.scale[0] : 1.0f) * (DT == kDtypeFp16 ? 1.0f / 16384.0f : 1.0f);
+    // whole rows through LDS
+    constexpr int RB = BN * 2, CH = RB / 16;
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const int r = wm * T::TM + 16 * i + i16;
+      const int r = wm * T::TM + i * 16 + i16;
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const int c = wn * T::TN + 16 * j + 4 * g4;
+        const int c = wn * T::TN + j * 16 + 4 * g4;
         const f32x4_t v = acc[i][j] * f;
-        if (staged) {
-          *reinterpret_cast<u32x2_t*>(smem + r * kRowB + (((c >> 3) ^ (r & (kChunks - 1))) << 4) + (c & 4) * 2) =
-              u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
-        } else if (m0 + r < M) {
-          uint16_t* d = static_cast<uint16_t*>(p.c) + (int64_t)(m0 + r) * p.ldc + n0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n0 + c + e < N) d[c + e] = cvt1<DT>(v[e]);
-        }
+        *reinterpret_cast<u32x2_t*>(smem + r * RB + (((c >> 3) ^ (r & (CH - 1))) << 4) + (c & 4) * 2) =
+            u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
       }
     }
-    if (staged) {
-      __syncthreads();
-      for (int u = tid; u < BM * kChunks; u += T::THREADS) {
-        const int r = u / kChunks, c = u % kChunks;
-        __builtin_nontemporal_store(
-            *reinterpret_cast<const u32x4_t*>(smem + r * kRowB + ((c ^ (r & (kChunks - 1))) << 4)),
-            reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p.c) + (int64_t)(m0 + r) * p.ldc + n0 + c * 8));
+    __syncthreads();
+    constexpr int ROWS = T::THREADS / CH;
+    const int c = tid % CH, left = N - (n0 + c * 8);   // columns from this lane's chunk on
+    uint16_t* out = static_cast<uint16_t*>(p.c) + (int64_t)m0 * p.ldc + n0 + c * 8;
+    const bool vec = left >= 8 && p.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0;
+#pragma unroll 8
+    for (int r = tid / CH; r < BM; r += ROWS) {
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(smem + r * RB + ((c ^ (r & (CH - 1))) << 4));
+      uint16_t* d = out + (int64_t)r * p.ldc;
+      if (m0 + r >= M) continue;
+      if (vec) {
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(d));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < left) d[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
       }
     }
   }
-}
-
-template <int BM, int BN, int DT, int OCC>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
-void loss_da_kernel(GemmProblem p, int add) {
-  __shared__ __attribute__((aligned(1024))) char smem[GemmTile<BM, BN, 64, DT, false, 5, 4, kLoopParts>::LDS_BYTES];
-  grad_body<BM, BN, 64, DT, true, 4, OCC>(p, add != 0, nullptr, smem);
-}
-
-template <int BM, int BN, int DT, int OCC>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
-void loss_dw_kernel(GemmProblem p, const float* scale) {
-  __shared__ __attribute__((aligned(1024))) char smem[GemmTile<BM, BN, 64, DT, false, 5, 4, kLoopParts>::LDS_BYTES];
-  grad_body<BM, BN, 64, DT, false, 4, OCC>(p, false, scale, smem);
 }
 
 // dA = s_i * (sum of the ranges in order), cast.  Four columns per thread.
 template <int DT>
 __global__ __launch_bounds__(256) void loss_da_finish_kernel(LossFinish c) {
   const int n4 = (c.k + 3) / 4;
-  const int64_t plane = c.m * (int64_t)c.k;
+  const int64_t plane = c.m * (int64_t)n4 * 4;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < c.m * n4; u += (int64_t)gridDim.x * 256) {
     const int64_t row = u / n4;
-    const int col = (int)(u % n4) * 4;
-    const float* src = c.sums + row * c.k + col;
+    const int col = (int)(u - row * n4) * 4;
+    const float* src = c.sums + u * 4;
     const float f = c.rows[4 * row + 3] * (DT == kDtypeFp16 ? 1.0f / 16384.0f : 1.0f);
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-    if (c.k % 4 == 0) {
-      // eight ranges are on their way at a time, added in order
-      for (int q0 = 0; q0 < c.ranges; q0 += 8) {
-        f32x4_t w[8];
+    // eight ranges are on their way at a time, added in order
+    for (int q0 = 0; q0 < c.ranges; q0 += 8) {
+      f32x4_t w[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q0 + q < c.ranges) w[q] = *reinterpret_cast<const f32x4_t*>(src + (q0 + q) * plane);
+      for (int q = 0; q < 8; ++q)
+        if (q0 + q < c.ranges) w[q] = *reinterpret_cast<const f32x4_t*>(src + (q0 + q) * plane);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q0 + q < c.ranges) v += w[q];
-      }
-    } else {
-      for (int q = 0; q < c.ranges; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < c.k) v[e] += src[q * plane + e];
+      for (int q = 0; q < 8; ++q)
+        if (q0 + q < c.ranges) v += w[q];
     }
     v *= f;
     uint16_t* d = static_cast<uint16_t*>(c.da) + row * c.ldda + col;
@@ -149,28 +147,30 @@ bool fits(const GemmProblem& p, int tile) {
 
 }  // namespace
 
-hipError_t launch_loss_da(const GemmProblem& p, int tile, int dtype, bool add, hipStream_t s) {
-  if (!fits(p, tile) || !p.partials) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)(p.order.num_rb * p.order.num_cb * p.splits));
-  if (tile == 256) {
-    if (dtype == kDtypeBf16) hipLaunchKernelGGL((loss_da_kernel<256, 256, kDtypeBf16, 1>), grid, dim3(256), 0, s, p, (int)add);
-    else hipLaunchKernelGGL((loss_da_kernel<256, 256, kDtypeFp16, 1>), grid, dim3(256), 0, s, p, (int)add);
-  } else {
-    if (dtype == kDtypeBf16) hipLaunchKernelGGL((loss_da_kernel<128, 128, kDtypeBf16, 2>), grid, dim3(256), 0, s, p, (int)add);
-    else hipLaunchKernelGGL((loss_da_kernel<128, 128, kDtypeFp16, 2>), grid, dim3(256), 0, s, p, (int)add);
+hipError_t launch_loss_grads(const GemmProblem* a, bool add, const GemmProblem* w, const float* scale, int tile, int dtype,
+                             hipStream_t s) {
+  if ((!a && !w) || (a && (!fits(*a, tile) || !a->partials)) || (w && (!fits(*w, tile) || w->splits != 1)))
+    return hipErrorInvalidValue;
+  GradPair gp{};
+  int64_t grid = 0;
+  if (a) {
+    gp.a = *a;
+    grid += (int64_t)a->order.num_rb * a->order.num_cb * a->splits;
   }
-  return hipGetLastError();
-}
-
-hipError_t launch_loss_dw(const GemmProblem& p, int tile, int dtype, const float* scale, hipStream_t s) {
-  if (!fits(p, tile) || p.splits != 1 || !scale) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)(p.order.num_rb * p.order.num_cb));
+  gp.a_tiles = (int32_t)grid;
+  gp.add = add;
+  if (w) {
+    gp.w = *w;
+    grid += (int64_t)w->order.num_rb * w->order.num_cb;
+  }
+  gp.scale = scale;
+  if (grid >= (int64_t(1) << 24)) return hipErrorInvalidValue;
   if (tile == 256) {
-    if (dtype == kDtypeBf16) hipLaunchKernelGGL((loss_dw_kernel<256, 256, kDtypeBf16, 1>), grid, dim3(256), 0, s, p, scale);
-    else hipLaunchKernelGGL((loss_dw_kernel<256, 256, kDtypeFp16, 1>), grid, dim3(256), 0, s, p, scale);
+    if (dtype == kDtypeBf16) hipLaunchKernelGGL((loss_grads_kernel<256, 256, kDtypeBf16, 1>), dim3((unsigned)grid), dim3(256), 0, s, gp);
+    else hipLaunchKernelGGL((loss_grads_kernel<256, 256, kDtypeFp16, 1>), dim3((unsigned)grid), dim3(256), 0, s, gp);
   } else {
-    if (dtype == kDtypeBf16) hipLaunchKernelGGL((loss_dw_kernel<128, 128, kDtypeBf16, 2>), grid, dim3(256), 0, s, p, scale);
-    else hipLaunchKernelGGL((loss_dw_kernel<128, 128, kDtypeFp16, 2>), grid, dim3(256), 0, s, p, scale);
+    if (dtype == kDtypeBf16) hipLaunchKernelGGL((loss_grads_kernel<128, 128, kDtypeBf16, 2>), dim3((unsigned)grid), dim3(256), 0, s, gp);
+    else hipLaunchKernelGGL((loss_grads_kernel<128, 128, kDtypeFp16, 2>), dim3((unsigned)grid), dim3(256), 0, s, gp);
   }
   return hipGetLastError();
 }

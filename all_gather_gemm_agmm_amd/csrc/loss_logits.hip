@@ -9,12 +9,15 @@
 //    lse = M + log(sum_p s_p exp(m_p - M)), loss = lse - target.
 //  * loss_grad_kernel: d[i, v] = a_i exp(x - lse_i) - b_i [v = label_i] as
 //    16-bit operands of the two gradient products, by rows [i][v] for
-//    dA = d W and transposed [v][i] for dW = d^T A.  a_i and b_i are scaled by
-//    powers of two (exact): by rows to [1, 2), undone on dA's fp32 sums;
-//    transposed to the largest row's, undone on dW's.  fp16 also carries 2^14,
-//    so that a probability of 2^-28 is still a normal number.  Rounding d
-//    to 16 bits (the operands' own precision) is what lets the matrix cores
-//    compute both gradients; the sums are fp32.
+//    dA = d W and transposed [v][i] for dW = d^T A: one tile in LDS, stored
+//    row by row, then once more through transposing reads.  Rounding d to 16
+//    bits (the operands' own precision) is what lets the matrix cores compute
+//    both gradients; the sums are fp32.  bf16 has the range of fp32.  fp16 has
+//    not: its rows of d are scaled by powers of two (exact) so that the larger
+//    of |a_i| and |b_i| lies in [1, 2), times 2^14, which keeps a probability
+//    of 2^-28 a normal number; dA's rows are scaled back in fp32, and
+//    the copy of A that dW's product reads carries each row's scale relative
+//    to the largest one (loss_scale_rows_kernel).
 //
 // Bound: MFMA.  The exponentials cost 256 (256 x 256 tile) per lane once per
 // tile, 3-5% beside the k loop of a 4096-deep product.
@@ -107,82 +110,76 @@ __device__ __forceinline__ void loss_body(const LossProblem& lp, char* smem) {
       }
     }
   } else {
-    const float top = DT == kDtypeFp16 ? 16384.0f : 1.0f;
-    const float inv_all = top / lp.scale_all[0];
     // the rows' values, all on their way at once
     f32x4_t rv[FM];
-    int at[FM];       // the label's column within the wave's, or anything outside
+    int at[FM];       // the label's column within the wave's, or -1
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const int row = m0 + wm * T::TM + 16 * i + i16;
-      rv[i] = row < M ? *reinterpret_cast<const f32x4_t*>(lp.rows + 4 * (int64_t)row) : f32x4_t{0.f, 0.f, 0.f, 1.f};
-      const int64_t rel = row < M ? lp.labels[row] - lp.label0 - wcol : -1;
+      const int row = min(m0 + wm * T::TM + 16 * i + i16, M - 1);
+      rv[i] = *reinterpret_cast<const f32x4_t*>(lp.rows + 4 * (int64_t)row);
+      const int64_t rel = lp.labels[row] - lp.label0 - wcol;
       at[i] = rel >= 0 && rel < T::TN ? (int)rel : -1;
     }
+    __syncthreads();   // the LDS now holds d: chunk c (8 columns) of tile row r at c ^ (r mod 16)
+    constexpr int RB = BN * 2, CH = RB / 16;
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i) {
+      const int r = wm * T::TM + 16 * i + i16;
+      const bool in = m0 + r < M;
+      const float f = (DT == kDtypeFp16 ? 16384.0f : 1.0f) / rv[i][3];   // powers of two: exact
+      const float lse = rv[i][0], a = rv[i][1] * f, b = rv[i][2] * f;
+      const bool hit = __any(at[i] >= 0);
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
+      for (int j = 0; j < FN; ++j) {
+        float d[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = exp_of(acc[i][j][e] - rv[i][0]);
-    __syncthreads();   // the LDS now holds the output tiles
-    // Row by row: chunk c (16 bytes) of tile row r at c ^ (r mod 8), as 4
-    // columns of a row are 8 bytes; transposed: columns are rows of BM elements.
-    constexpr int RB = BN * 2, TB = BM * 2;
+        for (int e = 0; e < 4; ++e) d[e] = a * exp_of(acc[i][j][e] - lse);
+        if (hit)
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-      if (!(pass ? lp.dt : lp.d)) continue;
-      if (pass) __syncthreads();   // the row-major tile has been read
+          for (int e = 0; e < 4; ++e)
+            if (at[i] == 16 * j + 4 * g4 + e) d[e] -= b;
+        if (!whole)
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int r = wm * T::TM + 16 * i + i16;
-        const int row = m0 + r;
-        const bool in = row < M;
-        const float f = pass ? inv_all : top / rv[i][3];
-        const float af = rv[i][1] * f, bf = rv[i][2] * f;
-        const bool hit = __any(at[i] >= 0);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          float d[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) d[e] = af * acc[i][j][e];
-          if (hit)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (at[i] == 16 * j + 4 * g4 + e) d[e] -= bf;
-          if (!whole)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!in || wcol + 16 * j + 4 * g4 + e >= N) d[e] = 0.0f;
-          const int c = wn * T::TN + 16 * j + 4 * g4;
-          if (pass == 0) {
-            *reinterpret_cast<u32x2_t*>(smem + r * RB + (((c >> 3) ^ (r & 7)) << 4) + (c & 4) * 2) =
-                u32x2_t{pack2<DT>(d[0], d[1]), pack2<DT>(d[2], d[3])};
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint16_t*>(smem + (c + e) * TB + (((r >> 3) ^ (((c >> 2) & 3) * 2)) << 4) + (r & 7) * 2) =
-                  cvt1<DT>(d[e]);
-          }
-        }
+          for (int e = 0; e < 4; ++e)
+            if (!in || wcol + 16 * j + 4 * g4 + e >= N) d[e] = 0.0f;
+        const int c = wn * T::TN + 16 * j + 4 * g4;
+        *reinterpret_cast<u32x2_t*>(smem + r * RB + (((c >> 3) ^ (r & 15)) << 4) + (c & 4) * 2) =
+            u32x2_t{pack2<DT>(d[0], d[1]), pack2<DT>(d[2], d[3])};
       }
-      __syncthreads();
-      if (pass == 0) {
-        constexpr int CH = RB / 16;
-        for (int u = tid; u < BM * CH; u += T::THREADS) {
-          const int r = u / CH, c = u % CH;
-          if (m0 + r < M && n0 + c * 8 < lp.ldd)
-            *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(lp.d) + (int64_t)(m0 + r) * lp.ldd + n0 + c * 8) =
-                *reinterpret_cast<const u32x4_t*>(smem + r * RB + ((c ^ (r & 7)) << 4));
+    }
+    __syncthreads();
+    if (lp.d) {
+      // whole rows, 16 bytes per lane, eight on their way at a time
+      constexpr int ROWS = T::THREADS / CH;          // rows per pass
+      const int c = tid % CH;
+      const bool cin = n0 + c * 8 < lp.ldd;
+      uint16_t* out = static_cast<uint16_t*>(lp.d) + (int64_t)m0 * lp.ldd + n0 + c * 8;
+#pragma unroll 8
+      for (int r = tid / CH; r < BM; r += ROWS) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(smem + r * RB + ((c ^ (r & 15)) << 4));
+        if (cin && m0 + r < M) *reinterpret_cast<u32x4_t*>(out + (int64_t)r * lp.ldd) = v;
+      }
+    }
+    if (lp.dt) {
+      // Transposing reads: a wave takes 16 columns x 32 rows at a time, lane
+      // (g4, i16) the rows 8 g4 .. 8 g4 + 7 of column i16 (two reads of four
+      // rows, each lane of a group giving the address of row i16 / 4, columns
+      // 4 (i16 % 4) .. + 3 of the 4 x 16 block), 16 bytes of the column's row.
+      constexpr int PASSES = (BM / 32) * (BN / 16) / (T::THREADS / 64);
+      uint16_t* out = static_cast<uint16_t*>(lp.dt) + (int64_t)n0 * lp.ldt + m0;
+#pragma unroll 8
+      for (int q = 0; q < PASSES; ++q) {
+        const int u = q * (T::THREADS / 64) + wave;
+        const int nb = (u / (BM / 32)) * 16, mb = (u % (BM / 32)) * 32 + 8 * g4;
+        u32x2_t half[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = mb + 4 * h + (i16 >> 2), c = nb + 4 * (i16 & 3);
+          half[h] = read_tr(smem + r * RB + (((c >> 3) ^ (r & 15)) << 4) + (c & 4) * 2);
         }
-      } else {
-        constexpr int CH = TB / 16;
-        for (int u = tid; u < BN * CH; u += T::THREADS) {
-          const int v = u / CH, c = u % CH;
-          if (n0 + v < N && m0 + c * 8 < lp.ldt)
-            *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(lp.dt) + (int64_t)(n0 + v) * lp.ldt + m0 + c * 8) =
-                *reinterpret_cast<const u32x4_t*>(smem + v * TB + ((c ^ (((v >> 2) & 3) * 2)) << 4));
-        }
+        if (n0 + nb + i16 < N && m0 + mb < lp.ldt)
+          *reinterpret_cast<u32x4_t*>(out + (int64_t)(nb + i16) * lp.ldt + mb) =
+              u32x4_t{half[0][0], half[0][1], half[1][0], half[1][1]};
       }
     }
   }
@@ -257,41 +254,64 @@ __global__ __launch_bounds__(256) void loss_combine_kernel(LossCombine c) {
   c.loss[row] = label == c.ignore ? 0.0f : label < 0 || label >= c.total ? __builtin_nanf("") : lse - target;
 }
 
-// Per row {lse, a, b, s}: a = grad_loss + grad_lse (0 and grad_lse for ignored
-// rows), b = grad_loss, s the power of two that brings the larger of them to
-// [1, 2); scale_all = max s.  A label outside the vocabulary makes a and b NaN.
-// One workgroup: the maximum is over all rows.
+// a and b of a row and the power of two s of its scale: a = grad_loss +
+// grad_lse (grad_lse alone for ignored rows), b = grad_loss, s = 2^exponent of
+// the larger of them (1 where both are 0 or one is not finite).  A label
+// outside the vocabulary makes a and b NaN.
+__device__ __forceinline__ void row_weights(const LossRows& c, int64_t row, float& a, float& b, float& s) {
+  const int64_t label = c.labels[row];
+  b = label == c.ignore ? 0.0f : c.grad_loss[row];
+  a = b + (c.grad_lse ? c.grad_lse[row] : 0.0f);
+  if (label != c.ignore && (label < 0 || label >= c.total)) a = b = __builtin_nanf("");
+  const float big = fmaxf(__builtin_fabsf(a), __builtin_fabsf(b));
+  // within [2^-100, 2^100], so that s and its inverse are normal
+  const uint32_t e = __builtin_bit_cast(uint32_t, big) & 0x7F800000u;
+  s = big > 0.0f && e < 0x7F800000u ? __builtin_bit_cast(float, min(max(e, 27u << 23), 227u << 23)) : 0.0f;
+}
+
+// rows[m] = {lse, a, b, s} (s = 1 for bf16, whose d needs no scale) and, for
+// fp16, scale_all = max s.  One workgroup: the maximum is over all rows.
+template <int DT>
 __global__ __launch_bounds__(1024) void loss_rows_kernel(LossRows c) {
   __shared__ float top[16];
   float most = 0.0f;
   for (int64_t row = threadIdx.x; row < c.m; row += 1024) {
-    const int64_t label = c.labels[row];
-    float b = label == c.ignore ? 0.0f : c.grad_loss[row];
-    float a = b + (c.grad_lse ? c.grad_lse[row] : 0.0f);
-    if (label != c.ignore && (label < 0 || label >= c.total)) a = b = __builtin_nanf("");
-    const float big = fmaxf(__builtin_fabsf(a), __builtin_fabsf(b));
-    // 2^exponent, kept within [2^-100, 2^100] so that it and its inverse are normal
-    uint32_t e = __builtin_bit_cast(uint32_t, big) & 0x7F800000u;
-    float s = 1.0f;
-    if (big > 0.0f && e < 0x7F800000u) {
-      e = min(max(e, 27u << 23), 227u << 23);
-      s = __builtin_bit_cast(float, e);
-      most = fmaxf(most, s);
-    }
-    float* d = c.rows + 4 * row;
-    d[0] = c.lse[row];
-    d[1] = a;
-    d[2] = b;
-    d[3] = s;
+    float a, b, s;
+    row_weights(c, row, a, b, s);
+    most = fmaxf(most, s);
+    *reinterpret_cast<f32x4_t*>(c.rows + 4 * row) = f32x4_t{c.lse[row], a, b, DT == kDtypeFp16 && s > 0.0f ? s : 1.0f};
   }
+  if constexpr (DT == kDtypeFp16) {
 #pragma unroll
-  for (int o = 1; o < 64; o *= 2) most = fmaxf(most, __shfl_xor(most, o));
-  if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = most;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 16; ++w) most = fmaxf(most, top[w]);
-    c.scale_all[0] = most > 0.0f ? most : 1.0f;
+    for (int o = 1; o < 64; o *= 2) most = fmaxf(most, __shfl_xor(most, o));
+    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < 16; ++w) most = fmaxf(most, top[w]);
+      c.scale_all[0] = most > 0.0f ? most : 1.0f;
+    }
   }
+}
+
+// The fp16 copy of A that dW's product reads: row i times s_i / scale_all, a
+// power of two (at most 1: a row without a gradient has s = 1 whatever the
+// others have).  16 bytes per thread.
+__global__ __launch_bounds__(256) void loss_scale_rows_kernel(LossScaleRows c) {
+  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = u / c.chunks;
+  if (row >= c.m) return;
+  const int64_t at = row * c.chunks * 8 + (u - row * c.chunks) * 8;
+  const int64_t g = row / c.rows_per_group;
+  const uint16_t* src = static_cast<const uint16_t*>(c.group[g]) + (row - g * c.rows_per_group) * c.ld + (u - row * c.chunks) * 8;
+  u32x4_t v = *reinterpret_cast<const u32x4_t*>(src);
+  const float f = fminf(c.rows[4 * row + 3] / c.scale_all[0], 1.0f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t w = v[e];
+    v[e] = pack2<kDtypeFp16>((float)__builtin_bit_cast(_Float16, (uint16_t)w) * f,
+                             (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16)) * f);
+  }
+  *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(c.out) + at) = v;
 }
 
 template <int DT>
@@ -326,8 +346,16 @@ hipError_t launch_loss_combine(const LossCombine& c, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_loss_rows(const LossRows& c, hipStream_t stream) {
-  hipLaunchKernelGGL(loss_rows_kernel, dim3(1), dim3(1024), 0, stream, c);
+hipError_t launch_loss_rows(const LossRows& c, int dtype, hipStream_t stream) {
+  if (dtype == kDtypeBf16) hipLaunchKernelGGL((loss_rows_kernel<kDtypeBf16>), dim3(1), dim3(1024), 0, stream, c);
+  else hipLaunchKernelGGL((loss_rows_kernel<kDtypeFp16>), dim3(1), dim3(1024), 0, stream, c);
+  return hipGetLastError();
+}
+
+hipError_t launch_loss_scale_rows(const LossScaleRows& c, hipStream_t stream) {
+  const int64_t blocks = (c.m * c.chunks + 255) / 256;
+  if (blocks < 1 || blocks >= (int64_t(1) << 24) || c.ld % 8 != 0) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(loss_scale_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, c);
   return hipGetLastError();
 }
 
