@@ -413,3 +413,25 @@ def test_refusals(monkeypatch):
         with pytest.raises(agmm.AgmmError) as ei:
             c.plan()
         assert ei.value.status == agmm.AGMM_ERR_OOM
+
+
+def test_example_trains():
+    """examples/vocab_head_step.py: the 8-bit projection, the loss and both
+    ways back, run together; the loss falls, dx matches the formula on the
+    dequantised operands."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "vocab_head_step.py")
+    spec = importlib.util.spec_from_file_location("vocab_head_step", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for rows in (64, 128):
+        head = mod.Head(rows=rows)
+        first, dx = head.step()
+        assert dx.shape == (head.m, 256) and torch.isfinite(dx).all() and dx.float().norm() > 0
+        assert (dx[::16] == 0).all()                       # rows without a target
+        for _ in range(14):
+            last, _ = head.step()
+        head.close()
+        assert abs(first.item() - math.log(head.vocab)) < 1.0
+        assert last.item() < 0.7 * first.item()
