@@ -497,12 +497,14 @@ def _device_and_stream(index: int, stream):
     return _HERE
 
 
+_QUANT_TYPES: dict = {}   # torch's types and this library's codes, filled on first use
+
+
 def _format(fmt) -> int:
-    if isinstance(fmt, str):
-        if fmt not in FORMATS:
-            raise ValueError(f"unknown 8-bit format {fmt!r} (one of {sorted(FORMATS)})")
-        return FORMATS[fmt]
-    return int(fmt)
+    code = FORMATS.get(fmt, fmt)
+    if code != AGMM_E4M3 and code != AGMM_E5M2:
+        raise ValueError(f"unknown 8-bit format {fmt!r} (one of {sorted(FORMATS)})")
+    return code
 
 
 def _format_dtype(fmt: int):
@@ -518,36 +520,45 @@ def quantize(x, fmt="e4m3", block_rows: int = 1, out: str = "rows", stream=None)
     import torch
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    if out not in ("rows", "cols", "both"):
+    if not _QUANT_TYPES:
+        _QUANT_TYPES.update({torch.bfloat16: AGMM_BF16, torch.float16: AGMM_FP16, torch.float32: AGMM_FP32,
+                             AGMM_E4M3: torch.float8_e4m3fn, AGMM_E5M2: torch.float8_e5m2, None: torch.float32})
+    if out != "rows" and out != "cols" and out != "both":
         raise ValueError(f"out must be 'rows', 'cols' or 'both' (got {out!r})")
-    code = {torch.bfloat16: AGMM_BF16, torch.float16: AGMM_FP16, torch.float32: AGMM_FP32}.get(x.dtype)
+    code = _QUANT_TYPES.get(x.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {x.dtype}")
-    if x.device.type != "cuda":
+    device = x.device
+    if device.type != "cuda":
         raise ValueError("x must be on the GPU")
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    (rows, cols), (ldx, unit) = x.shape, x.stride()
+    if unit != 1 and cols > 1:
         raise ValueError("x must be a row-major matrix (unit column stride)")
-    rows, cols = x.shape
     fmt = _format(fmt)
-    if block_rows not in (1, SCALE_BLOCK):
+    if block_rows != 1 and block_rows != SCALE_BLOCK:
         raise ValueError(f"block_rows must be 1 or {SCALE_BLOCK}")
-    fmt_dtype = _format_dtype(fmt)
-
-    def new(r, c):
-        return (torch.empty((r, -(-c // 16) * 16), dtype=fmt_dtype, device=x.device),
-                torch.empty((-(-c // SCALE_BLOCK), -(-r // block_rows)), dtype=torch.float32, device=x.device))
-
-    with _device_and_stream(x.device.index, stream):
-        q, s = new(rows, cols) if out != "cols" else (None, None)
-        qt, st = new(cols, rows) if out != "rows" else (None, None)
-        agmm_quantize(x.data_ptr(), code, rows, cols, x.stride(0) if rows > 1 else max(cols, 1), fmt, block_rows,
-                      q.data_ptr() if q is not None else None, q.stride(0) if q is not None else 0,
-                      s.data_ptr() if s is not None else None,
-                      qt.data_ptr() if qt is not None else None, qt.stride(0) if qt is not None else 0,
-                      st.data_ptr() if st is not None else None, _stream_handle(stream, x.device.index))
-    a = Scaled(q, s, cols, block_rows) if q is not None else None
-    b = Scaled(qt, st, rows, block_rows) if qt is not None else None
-    return (a, b) if out == "both" else a if out == "rows" else b
+    f8, f32, empty = _QUANT_TYPES[fmt], _QUANT_TYPES[None], torch.empty
+    q = s = qt = st = None
+    q_ptr = s_ptr = qt_ptr = st_ptr = None
+    ldq, ldqt = (cols + 15) // 16 * 16, (rows + 15) // 16 * 16
+    with _device_and_stream(device.index, stream):
+        if out != "cols":
+            q = empty((rows, ldq), dtype=f8, device=device)
+            s = empty(((cols + 127) // 128, -(-rows // block_rows)), dtype=f32, device=device)
+            q_ptr, s_ptr = q.data_ptr(), s.data_ptr()
+        if out != "rows":
+            qt = empty((cols, ldqt), dtype=f8, device=device)
+            st = empty(((rows + 127) // 128, -(-cols // block_rows)), dtype=f32, device=device)
+            qt_ptr, st_ptr = qt.data_ptr(), st.data_ptr()
+        _check(load_library().agmm_quantize(x.data_ptr(), code, rows, cols, ldx if rows > 1 else max(cols, 1), fmt, block_rows,
+                                            q_ptr, ldq, s_ptr, qt_ptr, ldqt, st_ptr, _stream_handle(stream, device.index)))
+    if out == "rows":
+        return Scaled(q, s, cols, block_rows)
+    if out == "cols":
+        return Scaled(qt, st, rows, block_rows)
+    return Scaled(q, s, cols, block_rows), Scaled(qt, st, rows, block_rows)
 
 
 class _OpPlan:
@@ -585,13 +596,17 @@ class _OpPlan:
     def _on(self, t, like, name):
         """The address of a tensor of this dtype, device and shape, dense or with
         the row stride of `like`."""
+        dtype, device, shape, stride = like
         try:
-            if (t.dtype, t.device, t.shape, t.stride()) == like:
-                return t.data_ptr()
+            if t.dtype == dtype and t.device == device and t.shape == shape:
+                got = t.stride()
+                # a dimension of one element may have any stride
+                if (got == stride or (shape[0] <= 1 or got[0] == stride[0]) and
+                        (len(shape) == 1 or shape[1] <= 1 or got[1] == stride[1])):
+                    return t.data_ptr()
         except AttributeError:
             pass
         import torch
-        dtype, _, shape, stride = like
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.device.type != "cuda":
@@ -602,10 +617,7 @@ class _OpPlan:
             raise TypeError(f"{name} has dtype {t.dtype}, plan expects {dtype}")
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        # a dimension of one element may have any stride
-        if any(n > 1 and got != want for n, got, want in zip(shape, t.stride(), stride)):
-            raise ValueError(f"{name} must be row-major with rows {stride[0]} elements apart (stride {tuple(t.stride())})")
-        return t.data_ptr()
+        raise ValueError(f"{name} must be row-major with rows {stride[0]} elements apart (stride {tuple(t.stride())})")
 
     def _new(self, like):
         """A new tensor as `like` describes it."""
@@ -672,16 +684,20 @@ class ScaledPlan(_OpPlan):
             raise TypeError(f"{name} must be a Scaled")
         if x.k != self.k or x.block_rows != block_rows:
             raise ValueError(f"{name} has k {x.k} and block_rows {x.block_rows}, expected {self.k} and {block_rows}")
-        return x
 
     def run(self, shards, B, C=None, stream=None):
         if len(shards) != self.num_shards:
             raise ValueError(f"expected {self.num_shards} shards, got {len(shards)}")
-        la, ls, on, pa, ps = self._la, self._ls, self._on, self._a, self._s
-        for r, x in enumerate(shards):
-            x = self._operand(x, 1, "shards")
-            pa[r] = on(x.values, la, "shards.values")
-            ps[r] = on(x.scales, ls, "shards.scales")
+        k, la, ls, on, pa, ps = self.k, self._la, self._ls, self._on, self._a, self._s
+        r = 0
+        for x in shards:
+            if x.__class__ is not Scaled or x.k != k or x.block_rows != 1:
+                self._operand(x, 1, "shards")
+            v, s = x.values, x.scales
+            # the common case in one comparison each
+            pa[r] = v.data_ptr() if (v.dtype, v.device, v.shape, v.stride()) == la else on(v, la, "shards.values")
+            ps[r] = s.data_ptr() if (s.dtype, s.device, s.shape, s.stride()) == ls else on(s, ls, "shards.scales")
+            r += 1
         self._operand(B, self.b_block_rows, "B")
         b, bs = on(B.values, self._lb, "B.values"), on(B.scales, self._lbs, "B.scales")
         with _device_and_stream(self.device, stream):
