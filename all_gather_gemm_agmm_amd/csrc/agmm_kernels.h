@@ -280,7 +280,7 @@ struct LossRows {
 };
 hipError_t launch_loss_rows(const LossRows& c, int dtype, hipStream_t stream);
 
-// out [m][8 * chunks] = fp16 rows of A times rows[i][3] / scale_all[0] (at most 1).
+// out [m][8 * chunks] = fp16 rows of A times rows[i][3] / scale_all[0], powers of two of at most 1.
 struct LossScaleRows {
   const void* group[kMaxGroups];
   int64_t rows_per_group, ld, m, chunks;
@@ -292,7 +292,7 @@ hipError_t launch_loss_scale_rows(const LossScaleRows& c, hipStream_t stream);
 
 // The two gradient products, B k x n, in one launch: fp32 sums of d W (A = d
 // [m][ldd]) into a->partials [splits][m][n rounded up to 4], added to what is there
-// when `add`, and C = scale[0] * dt A (scale null: 1).  Either may be null.
+// when `add`, and C = scale[0] * dt A.  Either may be null.
 hipError_t launch_loss_grads(const GemmProblem* a, bool add, const GemmProblem* w, const float* scale, int tile, int dtype,
                              hipStream_t stream);
 struct LossFinish {

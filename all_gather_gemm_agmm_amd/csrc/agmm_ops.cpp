@@ -671,8 +671,7 @@ struct agmm_loss_plan : PlanBase {
       gw.k_per_split = (int32_t)round_up(m, 64);
       gw.ldc = lddw ? lddw : k;
       gw.c = static_cast<char*>(dW) + v0 * gw.ldc * 2;
-      err = agmm::launch_loss_grads(dA ? &ga : nullptr, v0 > 0, dW ? &gw : nullptr, L.as ? L.scale_all : nullptr,
-                                    L.tile_grads, dtype, s);
+      err = agmm::launch_loss_grads(dA ? &ga : nullptr, v0 > 0, dW ? &gw : nullptr, L.scale_all, L.tile_grads, dtype, s);
       if (err != hipSuccess) return hip_err(err, "gradient products launch");
     }
     if (dA) {

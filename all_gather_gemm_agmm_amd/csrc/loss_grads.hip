@@ -24,7 +24,7 @@ struct GradPair {
   GemmProblem a, w;        // dA and dW
   int32_t a_tiles;         // workgroups of dA: the first ones
   int32_t add;             // dA: add to the sums that are there
-  const float* scale;      // dW: its factor, or null
+  const float* scale;      // dW: its factor
 };
 
 template <int BM, int BN, int DT, int OCC>
@@ -69,7 +69,7 @@ void loss_grads_kernel(GradPair gp) {
       __builtin_amdgcn_sched_barrier(0);   // one block row's values at a time
     }
   } else {
-    const float f = (gp.scale ? gp.scale[0] : 1.0f) * (DT == kDtypeFp16 ? 1.0f / 16384.0f : 1.0f);
+    const float f = gp.scale[0] * (DT == kDtypeFp16 ? 1.0f / 16384.0f : 1.0f);
     // whole rows through LDS
     constexpr int RB = BN * 2, CH = RB / 16;
     __syncthreads();
@@ -149,7 +149,7 @@ bool fits(const GemmProblem& p, int tile) {
 
 hipError_t launch_loss_grads(const GemmProblem* a, bool add, const GemmProblem* w, const float* scale, int tile, int dtype,
                              hipStream_t s) {
-  if ((!a && !w) || (a && (!fits(*a, tile) || !a->partials)) || (w && (!fits(*w, tile) || w->splits != 1)))
+  if ((!a && !w) || (a && (!fits(*a, tile) || !a->partials)) || (w && (!fits(*w, tile) || w->splits != 1 || !scale)))
     return hipErrorInvalidValue;
   GradPair gp{};
   int64_t grid = 0;

@@ -12,12 +12,12 @@
 //    dA = d W and transposed [v][i] for dW = d^T A: one tile in LDS, stored
 //    row by row, then once more through transposing reads.  Rounding d to 16
 //    bits (the operands' own precision) is what lets the matrix cores compute
-//    both gradients; the sums are fp32.  bf16 has the range of fp32.  fp16 has
-//    not: its rows of d are scaled by powers of two (exact) so that the larger
-//    of |a_i| and |b_i| lies in [1, 2), times 2^14, which keeps a probability
-//    of 2^-28 a normal number; dA's rows are scaled back in fp32, and
-//    the copy of A that dW's product reads carries each row's scale relative
-//    to the largest one (loss_scale_rows_kernel).
+//    both gradients; the sums are fp32.  d is scaled by 1 / S, S the rows'
+//    largest weight (loss_rows_kernel).  bf16 has the range of fp32.  fp16 has
+//    not: each row of d is scaled by a further power of two (exact) that brings
+//    its weight near 1, and by 2^14, which keeps a probability of 2^-28 a
+//    normal number; dA's rows are scaled back in fp32, and the copy of A that
+//    dW's product reads carries each row's power of two (loss_scale_rows_kernel).
 //
 // Bound: MFMA.  The exponentials cost 256 (256 x 256 tile) per lane once per
 // tile, 3-5% beside the k loop of a 4096-deep product.
@@ -126,7 +126,7 @@ __device__ __forceinline__ void loss_body(const LossProblem& lp, char* smem) {
     for (int i = 0; i < FM; ++i) {
       const int r = wm * T::TM + 16 * i + i16;
       const bool in = m0 + r < M;
-      const float f = (DT == kDtypeFp16 ? 16384.0f : 1.0f) / rv[i][3];   // powers of two: exact
+      const float f = (DT == kDtypeFp16 ? 16384.0f : 1.0f) / rv[i][3];
       const float lse = rv[i][0], a = rv[i][1] * f, b = rv[i][2] * f;
       const bool hit = __any(at[i] >= 0);
 #pragma unroll
@@ -254,48 +254,72 @@ __global__ __launch_bounds__(256) void loss_combine_kernel(LossCombine c) {
   c.loss[row] = label == c.ignore ? 0.0f : label < 0 || label >= c.total ? __builtin_nanf("") : lse - target;
 }
 
-// a and b of a row and the power of two s of its scale: a = grad_loss +
-// grad_lse (grad_lse alone for ignored rows), b = grad_loss, s = 2^exponent of
-// the larger of them (1 where both are 0 or one is not finite).  A label
-// outside the vocabulary makes a and b NaN.
-__device__ __forceinline__ void row_weights(const LossRows& c, int64_t row, float& a, float& b, float& s) {
+// a and b of a row: a = grad_loss + grad_lse (grad_lse alone for ignored rows),
+// b = grad_loss.  A label outside the vocabulary makes both NaN.
+__device__ __forceinline__ void row_weights(const LossRows& c, int64_t row, float& a, float& b) {
   const int64_t label = c.labels[row];
   b = label == c.ignore ? 0.0f : c.grad_loss[row];
   a = b + (c.grad_lse ? c.grad_lse[row] : 0.0f);
   if (label != c.ignore && (label < 0 || label >= c.total)) a = b = __builtin_nanf("");
-  const float big = fmaxf(__builtin_fabsf(a), __builtin_fabsf(b));
-  // within [2^-100, 2^100], so that s and its inverse are normal
-  const uint32_t e = __builtin_bit_cast(uint32_t, big) & 0x7F800000u;
-  s = big > 0.0f && e < 0x7F800000u ? __builtin_bit_cast(float, min(max(e, 27u << 23), 227u << 23)) : 0.0f;
 }
 
-// rows[m] = {lse, a, b, s} (s = 1 for bf16, whose d needs no scale) and, for
-// fp16, scale_all = max s.  One workgroup: the maximum is over all rows.
+__device__ __forceinline__ float finite_size(float x) {
+  x = __builtin_fabsf(x);
+  return x < __builtin_inff() ? x : 0.0f;
+}
+
+// 2^exponent of a positive normal number.
+__device__ __forceinline__ float power_below(float x) {
+  return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0x7F800000u);
+}
+
+// rows[m] = {lse, a, b, s} and scale_all = S, the scales of d: s_i d_i are the
+// gradients' rows.  S is the largest |b| times the power of two that keeps
+// |a| <= 2 S: where all rows weigh the same (a mean over tokens) the label's
+// entry of d is exactly -1 plus its probability, instead of every row being
+// off by the rounding of one and the same weight.  bf16: s_i = S.  fp16: S
+// times the power of two, at most 1, that brings the larger of |a_i| and |b_i|
+// near 1.  One workgroup: the maxima are over all rows.
 template <int DT>
 __global__ __launch_bounds__(1024) void loss_rows_kernel(LossRows c) {
-  __shared__ float top[16];
-  float most = 0.0f;
+  __shared__ float top[2][16];
+  float most[2] = {0.0f, 0.0f};
   for (int64_t row = threadIdx.x; row < c.m; row += 1024) {
-    float a, b, s;
-    row_weights(c, row, a, b, s);
-    most = fmaxf(most, s);
-    *reinterpret_cast<f32x4_t*>(c.rows + 4 * row) = f32x4_t{c.lse[row], a, b, DT == kDtypeFp16 && s > 0.0f ? s : 1.0f};
+    float a, b;
+    row_weights(c, row, a, b);
+    most[0] = fmaxf(most[0], finite_size(a));
+    most[1] = fmaxf(most[1], finite_size(b));
   }
-  if constexpr (DT == kDtypeFp16) {
 #pragma unroll
-    for (int o = 1; o < 64; o *= 2) most = fmaxf(most, __shfl_xor(most, o));
-    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = most;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < 16; ++w) most = fmaxf(most, top[w]);
-      c.scale_all[0] = most > 0.0f ? most : 1.0f;
+  for (int q = 0; q < 2; ++q) {
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) most[q] = fmaxf(most[q], __shfl_xor(most[q], o));
+    if ((threadIdx.x & 63) == 0) top[q][threadIdx.x >> 6] = most[q];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    for (int w = 0; w < 16; ++w) most[q] = fmaxf(most[q], top[q][w]);
+  constexpr float kLow = 7.888609052210118e-31f, kHigh = 1.2676506002282294e30f;   // 2^-100, 2^100: inverses are normal
+  float all = most[1] > 0.0f ? most[1] : most[0] > 0.0f ? most[0] : 1.0f;
+  all = fminf(fmaxf(all, kLow), kHigh);
+  const float over = most[0] / all;
+  if (over > 2.0f) all = fminf(all * power_below(over), kHigh);
+  if (threadIdx.x == 0) c.scale_all[0] = all;
+  for (int64_t row = threadIdx.x; row < c.m; row += 1024) {
+    float a, b;
+    row_weights(c, row, a, b);
+    float s = all;
+    if constexpr (DT == kDtypeFp16) {
+      const float part = fmaxf(finite_size(a), finite_size(b)) / all;
+      if (part > 0.0f) s = all * fminf(fmaxf(power_below(fmaxf(part, kLow)), kLow / all), 1.0f);
     }
+    *reinterpret_cast<f32x4_t*>(c.rows + 4 * row) = f32x4_t{c.lse[row], a, b, s};
   }
 }
 
-// The fp16 copy of A that dW's product reads: row i times s_i / scale_all, a
-// power of two (at most 1: a row without a gradient has s = 1 whatever the
-// others have).  16 bytes per thread.
+// The fp16 copy of A that dW's product reads: row i times s_i / S, a power of
+// two of at most 1.  16 bytes per thread.
 __global__ __launch_bounds__(256) void loss_scale_rows_kernel(LossScaleRows c) {
   const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = u / c.chunks;
@@ -304,7 +328,7 @@ __global__ __launch_bounds__(256) void loss_scale_rows_kernel(LossScaleRows c) {
   const int64_t g = row / c.rows_per_group;
   const uint16_t* src = static_cast<const uint16_t*>(c.group[g]) + (row - g * c.rows_per_group) * c.ld + (u - row * c.chunks) * 8;
   u32x4_t v = *reinterpret_cast<const u32x4_t*>(src);
-  const float f = fminf(c.rows[4 * row + 3] / c.scale_all[0], 1.0f);
+  const float f = c.rows[4 * row + 3] / c.scale_all[0];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint32_t w = v[e];

@@ -2,15 +2,26 @@
 // product from bf16, fp16 or fp32 matrices.
 //
 //     s = max(max_{block} |x| / F, 2^-126)      (finite elements only)
-//     q = rne8(x * (1 / s))                     F = 448 (e4m3), 57344 (e5m2)
+//     q = rne8(x / s)                           F = 448 (e4m3), 57344 (e5m2)
 //
 // with one block per 128 consecutive elements of a row (block_rows 1) or per
 // 128 x 128 tile (block_rows 128), of x, of x transposed, or of both from one
-// read of x.  s and 1 / s are correctly rounded fp32 quotients and the product
-// is rounded once to fp32 before its rounding to 8 bits, so the result is
-// the same on every path.  |x * (1 / s)| <= F (1 + 2^-22), which rounds to at
-// most F; non-finite elements do not enter a maximum and come out as NaN
-// (e4m3) or as themselves (e5m2), never as a finite number.
+// read of x.  s is the correctly rounded fp32 quotient, q the format's value
+// nearest to the real quotient x / s (the even one of two).  t = x * (1 / s) in
+// fp32 is within 2 units of that, so only near the midpoint of two values can
+// rounding t to 8 bits go wrong:
+//  * 16-bit x (quotient16): F x / max is a ratio of short integers, so either
+//    it is a midpoint or it lies 2^-20 or more (relative) from one.  Where it is
+//    one, x / s lies on the side that the rounding of s took it to, for the
+//    whole block, and 1 / s moved two units that way puts every such t on that
+//    side and changes no other.  Where s is exact, one Newton step makes t
+//    exact wherever x / s is an fp32 number, midpoints among them.  (Without
+//    this about one bf16 element in 300 went to the wrong side.)
+//  * fp32 x (exact8): a t within 4 units of a midpoint, about one in a
+//    million, is decided by the sign of the exact remainder x - midpoint * s.
+// |t| <= F (1 + 2^-20) rounds to at most F; non-finite elements do not enter
+// a maximum and come out as NaN (e4m3) or as themselves (e5m2), never as a
+// finite number.
 //
 // Bound: HBM.  Each element is read once and written once (twice for
 // "both").
@@ -165,10 +176,92 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   return (uint32_t)w;
 }
 
+// What dividing a block by its scale takes: the scale, its inverse (16-bit x:
+// moved two units where s is not exact), and the factor of the Newton step (the
+// inverse where s is exact, else 0).
+struct Divisor {
+  float s, inv, step;
+};
+
 template <int FMT, int DT>
-__device__ __forceinline__ u32x2_t pack8(const Eight<DT>& v, float inv) {
-  return u32x2_t{pack4<FMT>(v.value(0) * inv, v.value(1) * inv, v.value(2) * inv, v.value(3) * inv),
-                 pack4<FMT>(v.value(4) * inv, v.value(5) * inv, v.value(6) * inv, v.value(7) * inv)};
+__device__ __forceinline__ Divisor divisor(float size) {
+  Divisor d;
+  d.s = scale_of<FMT>(size);
+  d.inv = 1.0f / d.s;
+  d.step = 0.0f;
+  if constexpr (DT != kDtypeFp32) {
+    // the sign of s * F - max, exact; at the smallest scale the product with
+    // its inverse, a power of two, is exact already
+    const float off = __builtin_fmaf(d.s, top_value<FMT>(), -size);
+    const int32_t move = d.s > kTinyScale ? (off > 0.0f ? -2 : off < 0.0f ? 2 : 0) : 0;
+    d.step = move ? 0.0f : d.inv;
+    d.inv = __builtin_bit_cast(float, __builtin_bit_cast(int32_t, d.inv) + move);
+  }
+  return d;
+}
+
+template <int FMT>
+__device__ __forceinline__ float quotient16(float x, const Divisor& d) {
+  const float t = x * d.inv, r = __builtin_fmaf(__builtin_fmaf(-t, d.s, x), d.step, t);
+  // the step makes NaN of an infinity, which e5m2 keeps
+  return FMT == kFmtE5M2 && !(__builtin_fabsf(t) < __builtin_inff()) ? t : r;
+}
+
+// How far the bits of t are from 4 units below a midpoint, in the upper bits.
+template <int FMT>
+__device__ __forceinline__ uint32_t beyond_midpoint(float t) {
+  constexpr int kShift = FMT == kFmtE4M3 ? 12 : 11;   // the bits below the format's mantissa to the top
+  return (__builtin_bit_cast(uint32_t, t) << kShift) + ((4u << kShift) - 0x80000000u);
+}
+
+// The same of the binade above the smallest normal value, whose spacing is
+// that of everything below it.
+template <int FMT>
+__device__ __forceinline__ float low_binade(float size) {
+  return size + (FMT == kFmtE4M3 ? 0.015625f : 6.103515625e-05f);
+}
+
+// Eight quotients by one divisor.  fp32: `near` tells whether one of them may
+// be on the wrong side of a midpoint (then exact8 does it over).
+template <int FMT, int DT, class X>
+__device__ __forceinline__ u32x2_t pack8(X&& x, const Divisor& d, bool& near) {
+  float t[8];
+  if constexpr (DT != kDtypeFp32) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = quotient16<FMT>(x(e), d);
+  } else {
+    uint32_t least = 0xFFFFFFFFu;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      t[e] = x(e) * d.inv;
+      least = min(least, min(beyond_midpoint<FMT>(t[e]), beyond_midpoint<FMT>(low_binade<FMT>(__builtin_fabsf(t[e])))));
+    }
+    near = least <= (8u << (FMT == kFmtE4M3 ? 12 : 11));
+  }
+  return u32x2_t{pack4<FMT>(t[0], t[1], t[2], t[3]), pack4<FMT>(t[4], t[5], t[6], t[7])};
+}
+
+// fp32: up to eight elements `step` apart once more, each a byte, `out_step` apart.  Rare
+// (about one group of eight in 10^5), so it reads them again and is not
+// unrolled.
+template <int FMT>
+__device__ __forceinline__ void exact8(const float* x, int64_t step, int count, const Divisor& d, uint8_t* out, int out_step) {
+  constexpr uint32_t kBelow = FMT == kFmtE4M3 ? 0xFFFFFu : 0x1FFFFFu;
+#pragma unroll 1
+  for (int e = 0; e < count; ++e) {
+    const float v = x[e * step], t = v * d.inv, size = __builtin_fabsf(t);
+    const bool low = size < low_binade<FMT>(0.0f);
+    const float w = low ? low_binade<FMT>(size) : size;
+    float r = t;
+    if (beyond_midpoint<FMT>(w) <= (8u << (FMT == kFmtE4M3 ? 12 : 11)) && size < __builtin_inff()) {
+      const float mid = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, w) & ~kBelow) | ((kBelow + 1) / 2)) -
+                        (low ? low_binade<FMT>(0.0f) : 0.0f);
+      const float rest = __builtin_fmaf(-mid, d.s, __builtin_fabsf(v));
+      const uint32_t m = __builtin_bit_cast(uint32_t, mid);   // just above or below the midpoint, or on it
+      r = __builtin_copysignf(rest == 0.0f ? mid : __builtin_bit_cast(float, rest > 0.0f ? m + 1 : m - 1), v);
+    }
+    out[e * out_step] = (uint8_t)pack4<FMT>(r, r, r, r);
+  }
 }
 
 template <int DT, int FMT, bool VEC, int RPW>
@@ -195,12 +288,16 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantProblem p) {
 #pragma unroll
       for (int e = 0; e < E::W; ++e) b = larger<DT>(b, finite_sizes<DT>(sizes<DT>(v[i].w[e])));
     }
-    const float s = scale_of<FMT>(size_value<DT>(one_size<DT>(max16<DT>(b))));
-    const float inv = 1.0f / s;
+    const Divisor d = divisor<FMT, DT>(size_value<DT>(one_size<DT>(max16<DT>(b))));
     if (r0 + i >= p.rows) break;
-    if (c < p.cols16)
-      *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(p.q) + (r0 + i) * p.ldq + c) = pack8<FMT>(v[i], inv);
-    if ((lane & 15) == 0 && left > 0) p.scale[(c >> 7) * p.rows + r0 + i] = s;
+    if (c < p.cols16) {
+      uint8_t* out = static_cast<uint8_t*>(p.q) + (r0 + i) * p.ldq + c;
+      bool near = false;
+      *reinterpret_cast<u32x2_t*>(out) = pack8<FMT, DT>([&](int e) { return v[i].value(e); }, d, near);
+      if (DT == kDtypeFp32 && near && left > 0)
+        exact8<FMT>(static_cast<const float*>(p.x) + (r0 + i) * p.ldx + c, 1, (int)min(left, (int64_t)8), d, out, 1);
+    }
+    if ((lane & 15) == 0 && left > 0) p.scale[(c >> 7) * p.rows + r0 + i] = d.s;
   }
 }
 
@@ -214,7 +311,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantProblem p) {
   using E = Eight<DT>;
   __shared__ __attribute__((aligned(16))) uint8_t tile[128 * 128];
   __shared__ __attribute__((aligned(16))) uint32_t cmax[4][16][E::W];   // column sizes: wave, 8-column piece, word
-  __shared__ __attribute__((aligned(16))) float cinv[128];
+  __shared__ __attribute__((aligned(16))) float cs[128], cinv[128], cstep[128];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t kb = (p.cols + 127) / 128, rb = (p.rows + 127) / 128;
   const int64_t tb = blockIdx.x % (uint32_t)kb, tr = blockIdx.x / (uint32_t)kb;
@@ -250,7 +347,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantProblem p) {
       }
   }
 
-  float inv_all = 0.0f;        // SQUARE: of the tile
+  Divisor all{};               // SQUARE: of the tile
   if constexpr (SQUARE) {
     uint32_t b = row[0];
 #pragma unroll
@@ -261,11 +358,10 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantProblem p) {
     if (lane == 0) cmax[wave][0][0] = b;
     __syncthreads();
     b = larger<DT>(larger<DT>(cmax[0][0][0], cmax[1][0][0]), larger<DT>(cmax[2][0][0], cmax[3][0][0]));
-    const float s = scale_of<FMT>(size_value<DT>(one_size<DT>(b)));
-    inv_all = 1.0f / s;
+    all = divisor<FMT, DT>(size_value<DT>(one_size<DT>(b)));
     if (tid == 0) {
-      if (p.q) p.scale[tb * rb + tr] = s;
-      if (p.qt) p.scale_t[tr * kb + tb] = s;
+      if (p.q) p.scale[tb * rb + tr] = all.s;
+      if (p.qt) p.scale_t[tr * kb + tb] = all.s;
     }
   } else if (p.qt) {
 #pragma unroll
@@ -280,62 +376,118 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantProblem p) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) b = larger<DT>(b, cmax[w][tid >> 3][E::kWide ? tid & 7 : (tid & 7) >> 1]);
       if (!E::kWide) b = tid & 1 ? b >> 16 : b & 0xFFFFu;
-      const float s = scale_of<FMT>(size_value<DT>(b));
-      cinv[tid] = 1.0f / s;
-      if (tb * 128 + tid < p.cols) p.scale_t[tr * p.cols + tb * 128 + tid] = s;
+      const Divisor d = divisor<FMT, DT>(size_value<DT>(b));
+      cs[tid] = d.s;
+      cinv[tid] = d.inv;
+      cstep[tid] = d.step;
+      if (tb * 128 + tid < p.cols) p.scale_t[tr * p.cols + tb * 128 + tid] = d.s;
     }
     __syncthreads();
   }
 
-  if (p.q) {
-    float inv = inv_all;
-    if constexpr (!SQUARE) {
-      // lane cl of 16 takes row cl % 8: its size, scale and inverse
-      uint32_t mine = 0;
+  // 8 rows of one column are 8 consecutive bytes of the transposed tile:
+  // 8-byte piece rl of tile row c sits at piece rl ^ (c / 8).
+  const auto piece = [&](int e) { return tile + (cl * 8 + e) * 128 + (rl ^ cl) * 8; };
+  const auto row_out = [&](int i) { return static_cast<uint8_t*>(p.q) + (r0 + i) * p.ldq + c0; };
+  const auto row_in = [&](int i) { return static_cast<const float*>(p.x) + (r0 + i) * p.ldx + c0; };
+  const int count = (int)max((int64_t)0, min(left, (int64_t)8));   // columns of x in this piece
+  if constexpr (SQUARE) {
+    // one divisor, so one set of bytes, turned for the transposed output
+    u32x2_t q[8];
+    uint32_t near_rows = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      bool near = false;
+      q[i] = pack8<FMT, DT>([&](int e) { return v[i].value(e); }, all, near);
+      near_rows |= (uint32_t)(near && r0 + i < p.rows) << i;
+    }
+    if (p.q && c0 < p.cols16)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (r0 + i < p.rows) *reinterpret_cast<u32x2_t*>(row_out(i)) = q[i];
+    if (p.qt)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t col[2][4];   // of rows 0-3 and 4-7: 4 x 4 bytes turned by eight permutes
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a = q[4 * h][w], b = q[4 * h + 1][w], c = q[4 * h + 2][w], d = q[4 * h + 3][w];
+          const uint32_t ab0 = __builtin_amdgcn_perm(b, a, 0x05010400), ab1 = __builtin_amdgcn_perm(b, a, 0x07030602);
+          const uint32_t cd0 = __builtin_amdgcn_perm(d, c, 0x05010400), cd1 = __builtin_amdgcn_perm(d, c, 0x07030602);
+          col[h][0] = __builtin_amdgcn_perm(cd0, ab0, 0x05040100);
+          col[h][1] = __builtin_amdgcn_perm(cd0, ab0, 0x07060302);
+          col[h][2] = __builtin_amdgcn_perm(cd1, ab1, 0x05040100);
+          col[h][3] = __builtin_amdgcn_perm(cd1, ab1, 0x07060302);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<u32x2_t*>(piece(4 * w + e)) = u32x2_t{col[0][e], col[1][e]};
+      }
+    if constexpr (DT == kDtypeFp32)
+      if (near_rows && count > 0)
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          if (!(near_rows >> i & 1)) continue;
+          if (p.q) exact8<FMT>(row_in(i), 1, count, all, row_out(i), 1);
+          if (p.qt) exact8<FMT>(row_in(i), 1, count, all, piece(0) + i, 128);
+        }
+  } else {
+    if (p.q) {
+      // lane cl of 16 takes row cl % 8: its size and divisor
+      uint32_t size = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t b = one_size<DT>(max16<DT>(row[i]));
-        mine = (cl & 7) == i ? b : mine;
+        size = (cl & 7) == i ? b : size;
       }
-      const float s = scale_of<FMT>(size_value<DT>(mine));
-      inv = 1.0f / s;
-      if (cl < 8 && r0 + cl < p.rows) p.scale[tb * p.rows + r0 + cl] = s;
+      const Divisor mine = divisor<FMT, DT>(size_value<DT>(size));
+      if (cl < 8 && r0 + cl < p.rows) p.scale[tb * p.rows + r0 + cl] = mine.s;
+      uint32_t near_rows = 0;
+      const auto put = [&](auto row_tag) {
+        constexpr int I = decltype(row_tag)::value;
+        const Divisor d{row_lane<I>(mine.s), row_lane<I>(mine.inv), row_lane<I>(mine.step)};
+        if (r0 + I < p.rows && c0 < p.cols16) {
+          bool near = false;
+          *reinterpret_cast<u32x2_t*>(row_out(I)) = pack8<FMT, DT>([&](int e) { return v[I].value(e); }, d, near);
+          near_rows |= (uint32_t)near << I;
+        }
+      };
+      put(Row<0>{});
+      put(Row<1>{});
+      put(Row<2>{});
+      put(Row<3>{});
+      put(Row<4>{});
+      put(Row<5>{});
+      put(Row<6>{});
+      put(Row<7>{});
+      if constexpr (DT == kDtypeFp32)
+        if (__any(near_rows != 0 && count > 0))
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const int src = (lane & 48) + i;                   // the lane that holds row i's divisor
+            const Divisor d{__shfl(mine.s, src), __shfl(mine.inv, src), 0.0f};
+            if ((near_rows >> i & 1) && count > 0) exact8<FMT>(row_in(i), 1, count, d, row_out(i), 1);
+          }
     }
-    const auto put = [&](auto row_tag) {
-      constexpr int I = decltype(row_tag)::value;
-      const float f = SQUARE ? inv_all : row_lane<I>(inv);
-      if (r0 + I < p.rows && c0 < p.cols16)
-        *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(p.q) + (r0 + I) * p.ldq + c0) = pack8<FMT>(v[I], f);
-    };
-    put(Row<0>{});
-    put(Row<1>{});
-    put(Row<2>{});
-    put(Row<3>{});
-    put(Row<4>{});
-    put(Row<5>{});
-    put(Row<6>{});
-    put(Row<7>{});
+    if (p.qt) {
+      uint32_t near_cols = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const Divisor d{cs[cl * 8 + e], cinv[cl * 8 + e], cstep[cl * 8 + e]};
+        bool near = false;
+        *reinterpret_cast<u32x2_t*>(piece(e)) = pack8<FMT, DT>([&](int i) { return v[i].value(e); }, d, near);
+        near_cols |= (uint32_t)near << e;
+      }
+      if constexpr (DT == kDtypeFp32)
+        if (near_cols && r0 < p.rows)
+#pragma unroll 1
+          for (int e = 0; e < count; ++e) {
+            if (!(near_cols >> e & 1)) continue;
+            const Divisor d{cs[cl * 8 + e], cinv[cl * 8 + e], 0.0f};
+            exact8<FMT>(row_in(0) + e, p.ldx, (int)min(p.rows - r0, (int64_t)8), d, piece(e), 1);
+          }
+    }
   }
   if (p.qt) {
-    // 8 rows of one column are 8 consecutive bytes of the transposed tile:
-    // 8-byte piece rl of tile row c sits at piece rl ^ (c / 8).
-    float ci[8];
-    if constexpr (SQUARE) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ci[e] = inv_all;
-    } else {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const f32x4_t c4 = *reinterpret_cast<const f32x4_t*>(cinv + cl * 8 + 4 * q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ci[4 * q + e] = c4[e];
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      *reinterpret_cast<u32x2_t*>(tile + (cl * 8 + e) * 128 + (rl ^ cl) * 8) =
-          u32x2_t{pack4<FMT>(v[0].value(e) * ci[e], v[1].value(e) * ci[e], v[2].value(e) * ci[e], v[3].value(e) * ci[e]),
-                  pack4<FMT>(v[4].value(e) * ci[e], v[5].value(e) * ci[e], v[6].value(e) * ci[e], v[7].value(e) * ci[e])};
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -415,13 +415,13 @@ int agmm_run_noalloc(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_l
  * Block-scaled 8-bit copies of a matrix: the operands of agmm_scaled_run.
  *
  *     s = max(max |x| of the block / F, 2^-126)     F: the format's largest value
- *     q = x / s, rounded to nearest even
+ *     q = x / s, rounded once to nearest even
  *
  * A block is 128 consecutive elements of a row (block_rows 1) or a 128 x 128
  * tile (block_rows 128), ending where the matrix ends.  s is the fp32
- * quotient, q the rounding of the fp32 product x * (1 / s).  Infinities and
- * NaN do not enter the maximum; they become NaN in e4m3 and stay what they
- * are in e5m2.  A block of zeros has s = 2^-126.
+ * quotient, q the format's value nearest to the real quotient of x and that
+ * s.  Infinities and NaN do not enter the maximum; they become NaN in e4m3 and
+ * stay what they are in e5m2.  A block of zeros has s = 2^-126.
  *   x        device, [rows, cols] of `dtype`, rows ldx elements apart (any
  *            alignment of whole elements; rows of whole 16-byte vectors are
  *            read faster)

@@ -1,8 +1,8 @@
 """Block-scaled 8-bit quantiser and product on the GPU.
 
-The quantiser's definition fixes every rounding (fp32 quotients, one fp32
-product, one rounding to 8 bits), so its outputs are compared bit for bit with
-the same steps on the CPU.
+The quantiser's definition fixes every rounding (fp32 scales, the nearest
+8-bit value of the real quotient), so its outputs are compared bit for bit with
+the same steps on the CPU, the quotient in 64 bits.
 """
 import numpy as np
 import pytest
@@ -52,7 +52,7 @@ def quantize_ref(x, fmt, block):
                 s = max(np.float32(size) / np.float32(TOP[fmt]), np.float32(2.0 ** -126))
                 scales[b, r] = s
                 values[r * block:(r + 1) * block, b * 128:b * 128 + part.shape[1]] = \
-                    to8(part * (np.float32(1) / s), fmt)
+                    to8(part.astype(np.float64) / np.float64(s), fmt)
     return values, scales
 
 
@@ -104,6 +104,49 @@ def test_quantize_special_values(fmt, block):
     x[13, :128] = 3.0e38                     # the largest scale
     x[14, :] = -0.0
     x[128:, 256:] = 0.0                      # a tile of zeros
+    for got, want in zip(agmm.quantize(x.cuda(), fmt, block, out="both"), (x, x.t())):
+        check_quantized(got, want, fmt, block)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("block", [1, 128])
+def test_quantize_special_values_of_16_bits(fmt, dtype, block):
+    x = draw(140, 300, dtype, 4)
+    x[3, 5], x[3, 6], x[4, 200] = float("inf"), -float("inf"), float("nan")
+    x[10, :] = 0.0
+    x[11, :] = float("nan")
+    x[12, 128:256] = 6e-8 if dtype == "fp16" else 1e-39
+    x[13, :128] = 6.5e4
+    for got, want in zip(agmm.quantize(x.cuda(), fmt, block, out="both"), (x, x.t())):
+        check_quantized(got, want, fmt, block)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("block", [1, 128])
+def test_quantize_midpoints(fmt, dtype, block):
+    """Every pair of a maximum and an element whose quotient is a midpoint or
+    next to one: multiples of the maximum by midpoints of the format over its
+    largest value (exact in 16 bits for maxima that are multiples of 7), and
+    in fp32 their neighbours; results below the smallest normal value among them."""
+    top = TOP[fmt]
+    bits, low = (3, -6) if fmt == "e4m3" else (2, -14)
+    rows, cols = 256, 128
+    x = torch.zeros((rows, cols), dtype=torch.float64)
+    step = 2.0 ** (low - bits)
+    mids = [(2 * j + 1) / 2 * step for j in range(2 ** bits)]                               # below the smallest normal
+    mids += [2.0 ** e * (1 + (2 * j + 1) / 2 ** (bits + 1)) for e in range(-5, 8) for j in range(2 ** bits)]
+    for r in range(rows):
+        big = (128 + r % 128) * 2.0 ** (r // 128 * 3 - 4)
+        x[r, 0] = big
+        for c in range(1, cols):
+            x[r, c] = (-1) ** c * mids[(c + 31 * r) % len(mids)] * big / top
+    x = x.float() if dtype == "fp32" else x.to(TYPES[dtype])
+    if dtype == "fp32":
+        x[::3] = torch.nextafter(x[::3], torch.full_like(x[::3], float("inf")))
+        x[1::3] = torch.nextafter(x[1::3], torch.full_like(x[1::3], -float("inf")))
+        x[:, 0] = x.abs().amax(1)
     for got, want in zip(agmm.quantize(x.cuda(), fmt, block, out="both"), (x, x.t())):
         check_quantized(got, want, fmt, block)
 
