@@ -278,7 +278,17 @@ struct LossRows {
   float* rows;
   float* scale_all;
 };
-hipError_t launch_loss_rows(const LossRows& c, int dtype, hipStream_t stream);
+
+// Copy of 16-bit rows as rows of whole 16-byte vectors (zeros past cols):
+// out [num_groups][rows][8 * chunks], chunks = ceil(cols / 8).  Sources need
+// element alignment only.
+struct PadRows {
+  const void* group[kMaxGroups];
+  int64_t num_groups, rows, cols, ld, chunks;
+  void* out;
+};
+// One launch: the rows' weights (r, or null) and a copy (c, or null).
+hipError_t launch_loss_prepare(const LossRows* r, const PadRows* c, int dtype, hipStream_t stream);
 
 // out [m][8 * chunks] = fp16 rows of A times rows[i][3] / scale_all[0], powers of two of at most 1.
 struct LossScaleRows {

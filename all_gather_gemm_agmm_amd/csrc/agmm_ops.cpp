@@ -384,6 +384,7 @@ struct agmm_loss_plan : PlanBase {
   bool with_gradient = true;
   int64_t lda = 0, ldw = 0, ldda = 0, lddw = 0;   // 0: dense
   int64_t piece_key = 0;                          // columns per piece; 0: automatic
+  int64_t tile_key = -1;                          // 128, 256; -1: automatic
 
   // What a call of a pass uses, derived from the settings.
   struct Layout {
@@ -403,11 +404,22 @@ struct agmm_loss_plan : PlanBase {
   int64_t ld_w() const { return ldw ? ldw : k; }
   int64_t m8() const { return round_up(m, 8); }
 
-  // 256 x 256 tiles unless 128 x 128 ones (two per CU, 0.8 of the rate) need
-  // fewer rounds of the CUs.
+  // Microseconds of one workgroup, measured on MI355X over sums of 300 to 4096:
+  // 20 and 2.1 per 64 of its sum for the 256 x 256 tile (one to a CU), 5 and
+  // 1.25 for the 128 x 128 one (two to a CU; 0.7 where it has the CU alone).
+  static double workgroup_us(int tile, int64_t sum) {
+    return tile == 256 ? 20.0 + 2.1 * (double)cdiv(sum, 64) : 5.0 + 1.25 * (double)cdiv(sum, 64);
+  }
+
+  // Tile of the products with W: the one whose rounds of the CUs take less.
+  // 1000 x 700 over 30000 columns twice: 111 us by 128, 143 by 256; 8192 x 4096
+  // over 131072: 7.4 ms by 128, 6.2 by 256.
   int pick_tile(int64_t rows, int64_t cols) const {
-    const double big = (double)cdiv(cdiv(rows, 256) * cdiv(cols, 256), cu_count) * 4.0;
-    const double small = (double)cdiv(cdiv(rows, 128) * cdiv(cols, 128), cu_count) / 0.8;
+    if (tile_key > 0) return (int)tile_key;
+    const double big = (double)cdiv(cdiv(rows, 256) * cdiv(cols, 256), cu_count) * workgroup_us(256, k);
+    const int64_t tiles = cdiv(rows, 128) * cdiv(cols, 128), rest = tiles % (2 * cu_count);
+    const double small = (double)(tiles / (2 * cu_count)) * workgroup_us(128, k) +
+                         (rest == 0 ? 0.0 : rest > cu_count ? workgroup_us(128, k) : 5.0 + 0.7 * (double)cdiv(k, 64));
     return big <= small ? 256 : 128;
   }
 
@@ -440,15 +452,25 @@ struct agmm_loss_plan : PlanBase {
       L.scale_all = reinterpret_cast<float*>(c.take(4));
       L.d = c.take((size_t)m * round_up(L.piece, 8) * 2);
       L.dt = c.take((size_t)L.piece * m8() * 2);
-      // one launch computes both products, in tiles that suit their sum
-      const double big = (double)cdiv(cdiv(m, 256) * cdiv(k, 256) + cdiv(L.piece, 256) * cdiv(k, 256), cu_count) * 4.0;
-      const double small = (double)cdiv(cdiv(m, 128) * cdiv(k, 128) + cdiv(L.piece, 128) * cdiv(k, 128), cu_count) / 0.8;
-      L.tile_grads = big <= small ? 256 : 128;
-      // ranges of a piece's columns where dA has too few output tiles
-      const int64_t tiles = cdiv(m, L.tile_grads) * cdiv(k, L.tile_grads);
-      const int64_t slots = (int64_t)cu_count * (L.tile_grads == 128 ? 2 : 1);
+      // One launch computes both products; dA's sum (the piece's columns) is
+      // cut into ranges.  Tile and ranges are those that take the least: the
+      // workgroups' time spread over the CUs and half of one for the last
+      // round, but no less than the longest of them; and the ranges' sums,
+      // written and read at 4 TB/s.  1500 x 300 over 8000 columns takes 33 us
+      // by 128, 68 by 256; 800 x 4000 over 50000 takes 921 and 955.
+      double best = -1;
       int64_t want = 1;
-      while (want * 2 * tiles <= slots && L.piece / (want * 2) >= 512) want *= 2;
+      for (int t : {256, 128}) {
+        if (tile_key > 0 && t != tile_key) continue;
+        const int64_t a_tiles = cdiv(m, t) * cdiv(k, t), w_tiles = cdiv(L.piece, t) * cdiv(k, t);
+        const double slots = cu_count * (t == 128 ? 2 : 1), w_us = workgroup_us(t, m);
+        for (int64_t r = 1; r == 1 || (r <= 64 && a_tiles * r <= 4 * cu_count && L.piece / r >= 256); r *= 2) {
+          const double a_us = workgroup_us(t, cdiv(L.piece, r));
+          const double us = std::max({((double)(a_tiles * r) * a_us + (double)w_tiles * w_us) / slots + w_us / 2, a_us, w_us}) +
+                            (double)(r * m) * (double)k * 8 / 4e6;
+          if (best < 0 || us < best) best = us, L.tile_grads = t, want = r;
+        }
+      }
       L.per_range = round_up(cdiv(L.piece, want), 64);
       L.ranges = (int)cdiv(L.piece, L.per_range);
       L.sums = reinterpret_cast<float*>(c.take((size_t)L.ranges * m * round_up(k, 4) * 4));
@@ -480,61 +502,31 @@ struct agmm_loss_plan : PlanBase {
     return r;
   }
 
-  // The gathered, zero-padded rows of A into L.a.
-  int copy_a(const Layout& L, const void* const* shards, hipStream_t s) const {
-    hipError_t err;
-    if (!L.pad_a) {
-      agmm::GatherProblem g{};
-      for (int r = 0; r < N; ++r) g.src_group[r] = shards[r];
-      g.num_groups = N;
-      g.rows = m_s;
-      g.row_bytes = k * 2;
-      g.src_ld_bytes = ld_a() * 2;
-      g.dst = L.a;
-      g.dst_group_rows = m_s;
-      err = agmm::launch_gather(g, 0, s);
-    } else {
-      agmm::PadCopyProblem g{};
-      for (int r = 0; r < N; ++r) g.src_group[r] = shards[r];
-      g.num_groups = N;
-      g.elem_bytes = 2;
-      g.src_rows = m_s;
-      g.src_ld = ld_a();
-      g.cols = k;
-      g.rows = m_s;
-      g.dst = L.a;
-      g.dst_group_rows = m_s;
-      g.dst_ld = L.kp;
-      g.dst_cols = L.kp;
-      err = agmm::launch_pad_copy(g, s);
-    }
-    return err == hipSuccess ? AGMM_OK : hip_err(err, "gather launch");
+  // `count` groups of `rows` rows of k elements, `ld` apart, as rows of whole
+  // 16-byte vectors at `out`.
+  agmm::PadRows copy_of(const Layout& L, const void* const* groups, int count, int64_t rows, int64_t ld, void* out) const {
+    agmm::PadRows c{};
+    for (int g = 0; g < count; ++g) c.group[g] = groups[g];
+    c.num_groups = count;
+    c.rows = rows;
+    c.cols = k;
+    c.ld = ld;
+    c.chunks = L.kp / 8;
+    c.out = out;
+    return c;
   }
 
   // Rows [v0, v0 + vn) of W as whole 16-byte vectors: in place, or copied.
   int piece_w(const Layout& L, const void* W, int64_t v0, int64_t vn, hipStream_t s, const void** w, int64_t* ld) const {
-    const char* src = static_cast<const char*>(W) + v0 * ld_w() * 2;
-    if (!L.pad_w) {
-      *w = src;
-      *ld = ld_w();
-      return AGMM_OK;
-    }
-    agmm::PadCopyProblem g{};
-    g.src_group[0] = src;
-    g.num_groups = 1;
-    g.elem_bytes = 2;
-    g.src_rows = vn;
-    g.src_ld = ld_w();
-    g.cols = k;
-    g.rows = vn;
-    g.dst = L.w;
-    g.dst_group_rows = vn;
-    g.dst_ld = L.kp;
-    g.dst_cols = L.kp;
-    const hipError_t err = agmm::launch_pad_copy(g, s);
+    const void* src = static_cast<const char*>(W) + v0 * ld_w() * 2;
+    *w = src;
+    *ld = ld_w();
+    if (!L.pad_w) return AGMM_OK;
+    const agmm::PadRows c = copy_of(L, &src, 1, vn, ld_w(), L.w);
     *w = L.w;
     *ld = L.kp;
-    return err == hipSuccess ? AGMM_OK : hip_err(err, "pad copy launch");
+    const hipError_t err = agmm::launch_loss_prepare(nullptr, &c, dtype, s);
+    return err == hipSuccess ? AGMM_OK : hip_err(err, "weight copy launch");
   }
 
   agmm::RowMap rows_of_a(const Layout& L, const void* const* shards) const {
@@ -569,7 +561,12 @@ struct agmm_loss_plan : PlanBase {
   int forward(const void* const* shards, const void* W, const int64_t* labels, float* loss, float* lse, float* target,
               hipStream_t s) {
     const Layout L = layout(false, ws);
-    int rc = L.a ? copy_a(L, shards, s) : AGMM_OK;
+    int rc = AGMM_OK;
+    if (L.a) {
+      const agmm::PadRows c = copy_of(L, shards, N, m_s, ld_a(), L.a);
+      const hipError_t err = agmm::launch_loss_prepare(nullptr, &c, dtype, s);
+      if (err != hipSuccess) return hip_err(err, "row copy launch");
+    }
     const agmm::RowMap rows = rows_of_a(L, shards);
     for (int64_t v0 = 0; v0 < n && rc == AGMM_OK; v0 += L.piece) {
       const int64_t vn = std::min(L.piece, n - v0);
@@ -606,8 +603,7 @@ struct agmm_loss_plan : PlanBase {
   int backward(const void* const* shards, const void* W, const int64_t* labels, const float* lse,
                const float* grad_loss, const float* grad_lse, void* dA, void* dW, hipStream_t s) {
     const Layout L = layout(true, ws);
-    int rc = L.a ? copy_a(L, shards, s) : AGMM_OK;
-    if (rc != AGMM_OK) return rc;
+    int rc;
     const agmm::RowMap rows = rows_of_a(L, shards);
     agmm::LossRows lr{};
     lr.m = m;
@@ -619,7 +615,9 @@ struct agmm_loss_plan : PlanBase {
     lr.grad_lse = grad_lse;
     lr.rows = L.rows;
     lr.scale_all = L.scale_all;
-    hipError_t err = agmm::launch_loss_rows(lr, dtype, s);
+    agmm::PadRows copy{};
+    if (L.a) copy = copy_of(L, shards, N, m_s, ld_a(), L.a);
+    hipError_t err = agmm::launch_loss_prepare(&lr, L.a ? &copy : nullptr, dtype, s);
     if (err != hipSuccess) return hip_err(err, "loss rows launch");
     if (L.as && dW) {
       agmm::LossScaleRows r{};
@@ -923,6 +921,9 @@ int agmm_loss_plan_set_int(agmm_loss_plan_t p, const char* key, int64_t v) {
   } else if (k == "piece") {
     if (v < 0 || v >= kDimLimit) return bad();
     field = &p->piece_key;
+  } else if (k == "tile") {
+    if (v != -1 && v != 128 && v != 256) return bad();
+    field = &p->tile_key;
   } else if (k == "ignore_index") {
     p->ignore = v;
     return ok();

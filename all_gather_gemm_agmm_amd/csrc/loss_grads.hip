@@ -20,6 +20,10 @@ namespace agmm {
 
 namespace {
 
+// Vectors of 16-bit results in global memory: element alignment only.
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+typedef u32x2_t u32x2_any_t __attribute__((aligned(2)));
+
 struct GradPair {
   GemmProblem a, w;        // dA and dW
   int32_t a_tiles;         // workgroups of dA: the first ones
@@ -88,14 +92,13 @@ void loss_grads_kernel(GradPair gp) {
     constexpr int ROWS = T::THREADS / CH;
     const int c = tid % CH, left = N - (n0 + c * 8);   // columns from this lane's chunk on
     uint16_t* out = static_cast<uint16_t*>(p.c) + (int64_t)m0 * p.ldc + n0 + c * 8;
-    const bool vec = left >= 8 && p.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0;
 #pragma unroll 8
     for (int r = tid / CH; r < BM; r += ROWS) {
       const u32x4_t v = *reinterpret_cast<const u32x4_t*>(smem + r * RB + ((c ^ (r & (CH - 1))) << 4));
       uint16_t* d = out + (int64_t)r * p.ldc;
       if (m0 + r >= M) continue;
-      if (vec) {
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(d));
+      if (left >= 8) {
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any_t*>(d));
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -128,8 +131,8 @@ __global__ __launch_bounds__(256) void loss_da_finish_kernel(LossFinish c) {
     }
     v *= f;
     uint16_t* d = static_cast<uint16_t*>(c.da) + row * c.ldda + col;
-    if (c.k % 4 == 0 && c.ldda % 4 == 0) {
-      *reinterpret_cast<u32x2_t*>(d) = u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+    if (col + 4 <= c.k) {
+      *reinterpret_cast<u32x2_any_t*>(d) = u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)

@@ -13,7 +13,7 @@
 //    row by row, then once more through transposing reads.  Rounding d to 16
 //    bits (the operands' own precision) is what lets the matrix cores compute
 //    both gradients; the sums are fp32.  d is scaled by 1 / S, S the rows'
-//    largest weight (loss_rows_kernel).  bf16 has the range of fp32.  fp16 has
+//    largest weight (loss_rows).  bf16 has the range of fp32.  fp16 has
 //    not: each row of d is scaled by a further power of two (exact) that brings
 //    its weight near 1, and by 2^14, which keeps a probability of 2^-28 a
 //    normal number; dA's rows are scaled back in fp32, and the copy of A that
@@ -281,7 +281,7 @@ __device__ __forceinline__ float power_below(float x) {
 // times the power of two, at most 1, that brings the larger of |a_i| and |b_i|
 // near 1.  One workgroup: the maxima are over all rows.
 template <int DT>
-__global__ __launch_bounds__(1024) void loss_rows_kernel(LossRows c) {
+__device__ __forceinline__ void loss_rows(const LossRows& c) {
   __shared__ float top[2][16];
   float most[2] = {0.0f, 0.0f};
   for (int64_t row = threadIdx.x; row < c.m; row += 1024) {
@@ -316,6 +316,38 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(LossRows c) {
     }
     *reinterpret_cast<f32x4_t*>(c.rows + 4 * row) = f32x4_t{c.lse[row], a, b, s};
   }
+}
+
+// Rows of 16-bit elements, `cols` of each, as rows of whole 16-byte vectors:
+// out[(g * rows + t) * chunks * 8 + c] = group[g][t * ld + c], zeros past cols.
+// A source row may start at any element (16-byte accesses to global memory
+// need no alignment); its last chunk is read element by element.
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+__device__ __forceinline__ void pad_rows(const PadRows& c, int64_t block) {
+  const int64_t u = block * 1024 + threadIdx.x;
+  const int64_t row = u / (uint32_t)c.chunks;
+  const int ch = (int)(u - row * c.chunks);
+  const int64_t g = row / (uint32_t)c.rows;
+  if (g >= c.num_groups) return;
+  const uint16_t* src = static_cast<const uint16_t*>(c.group[g]) + (row - g * c.rows) * c.ld + ch * 8;
+  const int count = (int)c.cols - ch * 8;
+  u32x4_t v = {0u, 0u, 0u, 0u};
+  if (count >= 8) {
+    v = *reinterpret_cast<const u32x4_any_t*>(src);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < count) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+  }
+  *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(c.out) + row * c.chunks * 8 + ch * 8) = v;
+}
+
+// The rows' weights (workgroup 0, where asked for) and the copy of A (the
+// others) in one launch.
+template <int DT, bool ROWS>
+__global__ __launch_bounds__(1024) void loss_prepare_kernel(LossRows r, PadRows c) {
+  if (ROWS && blockIdx.x == 0) loss_rows<DT>(r);
+  else pad_rows(c, (int64_t)blockIdx.x - (ROWS ? 1 : 0));
 }
 
 // The fp16 copy of A that dW's product reads: row i times s_i / S, a power of
@@ -370,9 +402,24 @@ hipError_t launch_loss_combine(const LossCombine& c, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_loss_rows(const LossRows& c, int dtype, hipStream_t stream) {
-  if (dtype == kDtypeBf16) hipLaunchKernelGGL((loss_rows_kernel<kDtypeBf16>), dim3(1), dim3(1024), 0, stream, c);
-  else hipLaunchKernelGGL((loss_rows_kernel<kDtypeFp16>), dim3(1), dim3(1024), 0, stream, c);
+hipError_t launch_loss_prepare(const LossRows* r, const PadRows* c, int dtype, hipStream_t stream) {
+  int64_t copies = 0;
+  if (c) {
+    if (c->rows < 1 || c->rows > INT32_MAX || c->chunks < 1 || c->chunks > INT32_MAX || c->cols <= (c->chunks - 1) * 8 ||
+        c->cols > c->chunks * 8 || c->num_groups < 1 || c->num_groups > kMaxGroups)
+      return hipErrorInvalidValue;
+    copies = (c->num_groups * c->rows * c->chunks + 1023) / 1024;
+  }
+  const int64_t grid = copies + (r ? 1 : 0);
+  if (grid < 1 || grid >= (int64_t(1) << 22)) return hipErrorInvalidValue;
+  const PadRows none{};
+  const LossRows no_rows{};
+  if (!r)
+    hipLaunchKernelGGL((loss_prepare_kernel<kDtypeBf16, false>), dim3((unsigned)grid), dim3(1024), 0, stream, no_rows, *c);
+  else if (dtype == kDtypeBf16)
+    hipLaunchKernelGGL((loss_prepare_kernel<kDtypeBf16, true>), dim3((unsigned)grid), dim3(1024), 0, stream, *r, c ? *c : none);
+  else
+    hipLaunchKernelGGL((loss_prepare_kernel<kDtypeFp16, true>), dim3((unsigned)grid), dim3(1024), 0, stream, *r, c ? *c : none);
   return hipGetLastError();
 }
 

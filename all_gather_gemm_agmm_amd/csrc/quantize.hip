@@ -58,6 +58,8 @@ constexpr float kTinyScale = 1.17549435082228750797e-38f;   // 2^-126: 1 / s sta
 template <int FMT>
 __device__ __forceinline__ float top_value() { return FMT == kFmtE4M3 ? 448.0f : 57344.0f; }
 
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+
 // 8 consecutive elements of a row, as they are stored.  Sizes (the bits of
 // |x|, which order like |x|) are kept two to a word for the 16-bit types.
 template <int DT>
@@ -67,13 +69,13 @@ struct Eight {
   uint32_t w[W];
 
   // from column c of a row; elements at or past `left` (columns that remain)
-  // are zero.  VEC: 16-byte aligned rows.
-  template <bool VEC>
+  // are zero.  Rows need element alignment only: 16-byte accesses to global
+  // memory may start at any address.
   __device__ __forceinline__ void load(const char* row, int64_t c, int64_t left) {
-    if (VEC && left >= 8) {
+    if (left >= 8) {
 #pragma unroll
       for (int q = 0; q < W / 4; ++q) {
-        const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(row + c * (kWide ? 4 : 2)) + q);
+        const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any_t*>(row + c * (kWide ? 4 : 2)) + q);
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[4 * q + e] = v[e];
       }
@@ -264,7 +266,7 @@ __device__ __forceinline__ void exact8(const float* x, int64_t step, int count, 
   }
 }
 
-template <int DT, int FMT, bool VEC, int RPW>
+template <int DT, int FMT, int RPW>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantProblem p) {
   constexpr int ES = DT == kDtypeFp32 ? 4 : 2;
   using E = Eight<DT>;
@@ -276,7 +278,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantProblem p) {
   E v[RPW];
 #pragma unroll
   for (int i = 0; i < RPW; ++i)
-    if (r0 + i < p.rows && left > 0) v[i].template load<VEC>(static_cast<const char*>(p.x) + (r0 + i) * p.ldx * ES, c, left);
+    if (r0 + i < p.rows && left > 0) v[i].load(static_cast<const char*>(p.x) + (r0 + i) * p.ldx * ES, c, left);
     else v[i].zero();
 #pragma unroll
   for (int i = 0; i < RPW; ++i) {
@@ -305,7 +307,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantProblem p) {
 // much as the rest of the work on an element, so each scale and its inverse
 // are computed once per row (by one lane of 16, then broadcast) and once per
 // column (by one thread, then read from LDS).
-template <int DT, int FMT, bool VEC, bool SQUARE>
+template <int DT, int FMT, bool SQUARE>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantProblem p) {
   constexpr int ES = DT == kDtypeFp32 ? 4 : 2;
   using E = Eight<DT>;
@@ -321,7 +323,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantProblem p) {
   E v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (r0 + i < p.rows && left > 0) v[i].template load<VEC>(static_cast<const char*>(p.x) + (r0 + i) * p.ldx * ES, c0, left);
+    if (r0 + i < p.rows && left > 0) v[i].load(static_cast<const char*>(p.x) + (r0 + i) * p.ldx * ES, c0, left);
     else v[i].zero();
 
   uint32_t col[E::W], row[8];   // sizes of the piece's columns (by words) and rows
@@ -500,7 +502,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantProblem p) {
   }
 }
 
-template <int DT, int FMT, bool VEC>
+template <int DT, int FMT>
 hipError_t launch(const QuantProblem& p, hipStream_t stream) {
   if (p.block_rows == 1 && !p.qt) {
     const int64_t cw = (p.cols + 511) / 512;
@@ -509,15 +511,15 @@ hipError_t launch(const QuantProblem& p, hipStream_t stream) {
     const bool deep = cw * ((p.rows + 31) / 32) >= 1024;
     const int64_t grid = cw * ((p.rows + (deep ? 32 : 4) - 1) / (deep ? 32 : 4));
     if (grid > INT32_MAX) return hipErrorInvalidValue;
-    if (deep) hipLaunchKernelGGL((quantize_rows_kernel<DT, FMT, VEC, 8>), dim3((unsigned)grid), dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL((quantize_rows_kernel<DT, FMT, VEC, 1>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+    if (deep) hipLaunchKernelGGL((quantize_rows_kernel<DT, FMT, 8>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL((quantize_rows_kernel<DT, FMT, 1>), dim3((unsigned)grid), dim3(256), 0, stream, p);
   } else {
     const int64_t grid = ((p.cols + 127) / 128) * ((p.rows + 127) / 128);
     if (grid > INT32_MAX) return hipErrorInvalidValue;
     if (p.block_rows == 1)
-      hipLaunchKernelGGL((quantize_tile_kernel<DT, FMT, VEC, false>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+      hipLaunchKernelGGL((quantize_tile_kernel<DT, FMT, false>), dim3((unsigned)grid), dim3(256), 0, stream, p);
     else
-      hipLaunchKernelGGL((quantize_tile_kernel<DT, FMT, VEC, true>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+      hipLaunchKernelGGL((quantize_tile_kernel<DT, FMT, true>), dim3((unsigned)grid), dim3(256), 0, stream, p);
   }
   return hipGetLastError();
 }
@@ -525,9 +527,7 @@ hipError_t launch(const QuantProblem& p, hipStream_t stream) {
 template <int DT>
 hipError_t launch_dt(const QuantProblem& p, hipStream_t s) {
   constexpr int ES = DT == kDtypeFp32 ? 4 : 2;
-  const bool vec = (p.ldx * ES) % 16 == 0 && (reinterpret_cast<uintptr_t>(p.x) & 15) == 0;
-  if (p.format == kFmtE4M3) return vec ? launch<DT, kFmtE4M3, true>(p, s) : launch<DT, kFmtE4M3, false>(p, s);
-  return vec ? launch<DT, kFmtE5M2, true>(p, s) : launch<DT, kFmtE5M2, false>(p, s);
+  return p.format == kFmtE4M3 ? launch<DT, kFmtE4M3>(p, s) : launch<DT, kFmtE5M2>(p, s);
 }
 
 }  // namespace

@@ -110,7 +110,10 @@ __device__ __forceinline__ void load_lds4_buf(const u32x4_t& rsrc, uint32_t voff
                : "m0");
 }
 
-// One element, and four consecutive ones (aligned to four), of an output type.
+// One element, and four consecutive ones, of an output type.  Vectors in
+// global memory need element alignment only.
+typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
+typedef u32x2_t u32x2_any_t __attribute__((aligned(2)));
 template <int CT>
 struct OutOf {
   typedef uint16_t type;
@@ -126,14 +129,14 @@ __device__ __forceinline__ void put1(P* c, float v) {
 }
 template <int CT, class P>
 __device__ __forceinline__ void put4(P* c, const f32x4_t& v) {
-  if constexpr (CT == kDtypeFp32) *reinterpret_cast<f32x4_t*>(c) = v;
-  else *reinterpret_cast<u32x2_t*>(c) = u32x2_t{pack2<CT>(v[0], v[1]), pack2<CT>(v[2], v[3])};
+  if constexpr (CT == kDtypeFp32) *reinterpret_cast<f32x4_any_t*>(c) = v;
+  else *reinterpret_cast<u32x2_any_t*>(c) = u32x2_t{pack2<CT>(v[0], v[1]), pack2<CT>(v[2], v[3])};
 }
 
 // Four consecutive columns (col % 4 == 0) of one row to C in its own type.
 __device__ __forceinline__ void store4(const ScaledProblem& p, int row, int col, const f32x4_t& v) {
   const int64_t at = (int64_t)row * p.ldc + col;
-  const bool whole = col + 3 < p.n && (p.ldc % 4) == 0;
+  const bool whole = col + 3 < p.n;
   const auto put = [&](auto type) {
     constexpr int CT = decltype(type)::value;
     typename OutOf<CT>::type* c = static_cast<typename OutOf<CT>::type*>(p.c) + at;
@@ -435,7 +438,7 @@ void scaled_gemm_kernel(ScaledProblem p) {
   const bool split_k = p.splits > 1;
   const int64_t ld = split_k ? p.part_ld : p.ldc;
   const int ncols = split_k ? (int)p.part_ld : p.n;   // padding columns of the sums are never read as results
-  const bool inside = m0 + BM <= p.m && n0 + BN <= ncols && ld % 4 == 0;
+  const bool inside = m0 + BM <= p.m && n0 + BN <= ncols;
   const auto store = [&](auto type) {
     constexpr int CT = decltype(type)::value;
     typedef typename OutOf<CT>::type out_t;
@@ -446,7 +449,7 @@ void scaled_gemm_kernel(ScaledProblem p) {
       for (int j = 0; j < FN; ++j) {
         if (inside) {
           put4<CT>(base + 16 * j, acc[i][j]);
-        } else if (row0 + 16 * i < p.m && ld % 4 == 0 && col0 + 16 * j + 4 <= ncols) {
+        } else if (row0 + 16 * i < p.m && col0 + 16 * j + 4 <= ncols) {
           put4<CT>(base + 16 * j, acc[i][j]);
         } else if (row0 + 16 * i < p.m) {
 #pragma unroll

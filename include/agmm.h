@@ -455,8 +455,9 @@ int agmm_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t 
  * products of one block of 128 of k are summed by the matrix cores, scaled in
  * fp32 and added in fp32; C is rounded once.  With a 16-bit C and k >= 1024
  * the sums of 128 are those of the 8-bit matrix instruction, whose adder may
- * lose up to 2^-12 of the sum of a block's |terms|; otherwise (and for
- * m <= 128) they are fp32 sums of exact products.
+ * lose up to 2^-12 of the sum of a block's |terms|; otherwise, and in the
+ * tiles 2 and 3 (see agmm_scaled_plan_set_int), they are fp32 sums of exact
+ * products.
  * A linear layer y = x W^T trains with three such products: y from x and W;
  * dx from dy and W transposed (the weight's blocks are square, so W and its
  * transpose hold the same values); dW from dy transposed and x transposed,
@@ -506,8 +507,8 @@ int agmm_scaled_run(agmm_scaled_plan_t plan, const void *const *shard_ptrs,
  *                 least k rounded up to 16
  *   "ldc"         elements between rows of C: 0 (dense) or at least n_local
  *   "tile"        -1 automatic, 0 256 x 256 (always on the 8-bit matrix instruction), 1 128 x 128,
- *                 2 16 x 32, 3 32 x 32 (rows x columns; 2 and 3 share k out over the waves of a
- *                 workgroup; automatic for m <= 16 and m <= 128)
+ *                 2 16 x 16 or 16 x 32, 3 32 x 32 or 64 x 64 (rows x columns; 2 and 3 share k
+ *                 out over the waves of a workgroup)
  *   "splits"      0 automatic, else k ranges summed in a fixed order
  * Settings are fixed once a call was captured into a graph.  get reads the
  * values in use, and "captured".
@@ -593,10 +594,12 @@ int agmm_loss_backward(agmm_loss_plan_t plan, const void *const *shard_ptrs, con
  *   "lda", "ldw", "ldda", "lddw"  elements between rows: 0 (dense) or at least k
  *   "piece"         columns of the vocabulary computed at a time: 0 automatic (512 MiB of
  *                   intermediate values), rounded down to a multiple of 256, at least 256
+ *   "tile"          -1 automatic, 128 or 256: rows and columns of the products' tiles
  *   "ignore_index"  the label of rows without a loss (default -100)
  * A change that needs more workspace reallocates it; the plan keeps its
  * previous settings when that fails.  Settings are fixed once a call was
- * captured into a graph.  get also reads "tile" and "captured".
+ * captured into a graph.  get reads the values in use (of "tile" that of the
+ * products with W), and "captured".
  */
 int agmm_loss_plan_set_int(agmm_loss_plan_t plan, const char *key, int64_t value);
 int agmm_loss_plan_get_int(agmm_loss_plan_t plan, const char *key, int64_t *value);

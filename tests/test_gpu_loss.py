@@ -168,12 +168,29 @@ def test_pieces(k):
     assert torch.equal(one[2], many[2])
 
 
-def test_large_tiles():
-    """Enough rows and columns for 256 x 256 tiles in every pass."""
+@pytest.mark.parametrize("tile", [128, 256])
+def test_large_tiles(tile):
+    """Rows and columns for rounds of either tile in every pass."""
     c = Case(2, 2048, 512, 8192, agmm.AGMM_BF16, seed=1)
     with c.plan() as plan:
+        plan.set("tile", tile)
+        assert plan.get("tile") == tile
+    run_both(c, tile=tile)
+
+
+def test_tile_by_the_sum():
+    """Long sums over many rows and columns take 256 x 256 tiles, a few rows 128 x 128."""
+    with agmm.LossPlan(1, 4096, 4096, 65536, agmm.AGMM_BF16) as plan:
         assert plan.get("tile") == 256
-    run_both(c)
+    with agmm.LossPlan(1, 64, 4096, 65536, agmm.AGMM_BF16) as plan:
+        assert plan.get("tile") == 128
+
+
+@pytest.mark.parametrize("tile", [128, 256])
+@pytest.mark.parametrize("shape", [(1, 1, 8, 3), (3, 45, 203, 777), (2, 129, 72, 258)])
+@pytest.mark.parametrize("dt", [agmm.AGMM_BF16, agmm.AGMM_FP16])
+def test_each_tile_at_ragged_sizes(shape, dt, tile):
+    run_both(Case(*shape, dt, seed=21), tile=tile)
 
 
 def test_one_pass_of_two():
