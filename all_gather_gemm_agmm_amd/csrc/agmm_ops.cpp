@@ -47,7 +47,8 @@ int check_sizes(int N, int64_t m_s, int64_t k, int64_t n) {
   if (m_s < 1 || k < 1 || n < 1)
     return set_err(AGMM_ERR_INVALID_ARG, "sizes must be >= 1 (m_per_shard=%lld, k=%lld, n_local=%lld)",
                    (long long)m_s, (long long)k, (long long)n);
-  const int64_t m = N * m_s;
+  // m_s first: N * m_s must not overflow
+  const int64_t m = m_s < kDimLimit ? N * m_s : m_s;
   if (m >= kDimLimit || k >= kDimLimit || n >= kDimLimit || m * k >= kElemLimit || k * n >= kElemLimit ||
       m * n >= kElemLimit)
     return set_err(AGMM_ERR_UNSUPPORTED, "problem too large (m=%lld, k=%lld, n=%lld)", (long long)m, (long long)k,
@@ -354,9 +355,9 @@ int validate_loss(int N, int64_t m_s, int64_t k, int64_t n, int dtype, int64_t s
   if (dtype == AGMM_FP32)
     return set_err(AGMM_ERR_UNSUPPORTED, "the vocabulary loss takes bf16 or fp16 operands");
   if (dtype != AGMM_BF16 && dtype != AGMM_FP16) return set_err(AGMM_ERR_INVALID_ARG, "unknown dtype %d", dtype);
-  if (start < 0 || total < 1 || total >= kElemLimit || start + n > total)
-    return set_err(AGMM_ERR_INVALID_ARG, "columns [%lld, %lld) do not lie in a vocabulary of %lld", (long long)start,
-                   (long long)(start + n), (long long)total);
+  if (start < 0 || total < 1 || total >= kElemLimit || start > total - n)
+    return set_err(AGMM_ERR_INVALID_ARG, "%lld columns from %lld on do not lie in a vocabulary of %lld", (long long)n,
+                   (long long)start, (long long)total);
   if (N * m_s >= (int64_t(1) << 27) || n >= (int64_t(1) << 27))
     return set_err(AGMM_ERR_UNSUPPORTED, "problem too large (m=%lld, n_local=%lld)", (long long)(N * m_s), (long long)n);
   return ok();
@@ -705,6 +706,9 @@ int agmm_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t 
   if (rows >= kQuantDim || cols >= kQuantDim || rows * cols >= kQuantElems)
     return set_err(AGMM_ERR_UNSUPPORTED, "matrix too large (rows=%lld, cols=%lld)", (long long)rows, (long long)cols);
   if (ldx < cols) return set_err(AGMM_ERR_INVALID_ARG, "ldx %lld is less than cols %lld", (long long)ldx, (long long)cols);
+  if (ldx >= kQuantElems || ldq >= kQuantElems || ldqt >= kQuantElems)
+    return set_err(AGMM_ERR_UNSUPPORTED, "row length too large (ldx=%lld, ldq=%lld, ldqt=%lld)", (long long)ldx,
+                   (long long)ldq, (long long)ldqt);
   if (!q && !qt) return set_err(AGMM_ERR_INVALID_ARG, "q and qt are both NULL");
   const int64_t es = dtype == AGMM_FP32 ? 4 : 2;
   if (!aligned(x, es)) return set_err(AGMM_ERR_UNSUPPORTED, "x is not aligned to its elements");

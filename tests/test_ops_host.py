@@ -73,12 +73,23 @@ def test_quantize_rejects():
             (dict(x=None), INVALID, "x is NULL"), (dict(dtype=3), INVALID, "dtype"), (dict(fmt=2), INVALID, "format"),
             (dict(block=2), INVALID, "block_rows"), (dict(rows=0), INVALID, "sizes"), (dict(cols=-1), INVALID, "sizes"),
             (dict(rows=1 << 28), UNSUPPORTED, "too large"), (dict(rows=1 << 20, cols=1 << 17, ldx=1 << 17), UNSUPPORTED, "too large"),
+            (dict(ldx=1 << 60), UNSUPPORTED, "row length"), (dict(ldq=1 << 60), UNSUPPORTED, "row length"),
             (dict(ldx=19), INVALID, "ldx"), (dict(q=None, qt=None), INVALID, "both NULL"), (dict(x=base + 1), UNSUPPORTED, "aligned"),
             (dict(ldq=16), INVALID, "ldq"), (dict(ldq=40), UNSUPPORTED, "16-byte"), (dict(q=base + 8), UNSUPPORTED, "16-byte"),
             (dict(s=None), INVALID, "scale"), (dict(ldqt=8), INVALID, "ldqt"), (dict(st=None), INVALID, "scale"),
             (dict(st=base + 2), UNSUPPORTED, "4-byte")]:
         assert call(**kw) == status, (kw, agmm.agmm_last_error())
         assert fragment in agmm.agmm_last_error(), kw
+
+
+@pytest.mark.parametrize("ms", [1 << 30, 1 << 57, 1 << 58, (1 << 58) + 1, (1 << 63) - 1])
+def test_sizes_whose_products_overflow(ms):
+    """64 * m_per_shard may pass 2^63: refused, not wrapped."""
+    lib = agmm.load_library()
+    assert lib.agmm_scaled_plan_validate(64, ms, 8, 8, 0, 1, 0) == UNSUPPORTED
+    assert lib.agmm_loss_plan_validate(64, ms, 8, 8, 0, 0, 8) == UNSUPPORTED
+    assert lib.agmm_loss_plan_validate(1, 8, ms, 8, 0, 0, 8) == UNSUPPORTED
+    assert lib.agmm_loss_plan_validate(1, 8, 8, 8, 0, ms, 1 << 30) == INVALID
 
 
 def test_null_handles_are_rejected():
