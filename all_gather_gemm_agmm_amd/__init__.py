@@ -663,7 +663,7 @@ class ScaledPlan(_OpPlan):
         self._make(num_shards, m_per_shard, k, n_local, a_format, b_block_rows, c_dtype)
         self.num_shards, self.m_per_shard, self.k, self.n_local = num_shards, m_per_shard, k, n_local
         self.a_format, self.b_block_rows, self.c_dtype = a_format, b_block_rows, c_dtype
-        self._a, self._s = (ctypes.c_void_p * num_shards)(), (ctypes.c_void_p * num_shards)()
+        self._table = ctypes.c_void_p * num_shards   # a new one per call: calls of several threads may overlap
         self._run = load_library().agmm_scaled_run
         self._expect()
         for key, val in settings.items():
@@ -688,7 +688,7 @@ class ScaledPlan(_OpPlan):
     def run(self, shards, B, C=None, stream=None):
         if len(shards) != self.num_shards:
             raise ValueError(f"expected {self.num_shards} shards, got {len(shards)}")
-        k, la, ls, on, pa, ps = self.k, self._la, self._ls, self._on, self._a, self._s
+        k, la, ls, on, pa, ps = self.k, self._la, self._ls, self._on, self._table(), self._table()
         r = 0
         for x in shards:
             if x.__class__ is not Scaled or x.k != k or x.block_rows != 1:
@@ -721,7 +721,7 @@ class LossPlan(_OpPlan):
         self._make(num_shards, m_per_shard, k, n_local, dtype, vocab_start,
                    vocab_start + n_local if vocab_size is None else vocab_size, int(bool(with_gradient)))
         self.num_shards, self.m_per_shard, self.k, self.n_local, self.dtype = num_shards, m_per_shard, k, n_local, dtype
-        self._a = (ctypes.c_void_p * num_shards)()
+        self._table = ctypes.c_void_p * num_shards   # a new one per call: calls of several threads may overlap
         self._fwd, self._bwd = load_library().agmm_loss_forward, load_library().agmm_loss_backward
         self._expect()
         for key, val in settings.items():
@@ -741,18 +741,18 @@ class LossPlan(_OpPlan):
     def _operands(self, shards, W, labels):
         if len(shards) != self.num_shards:
             raise ValueError(f"expected {self.num_shards} shards, got {len(shards)}")
-        la, on, pa = self._la, self._on, self._a
+        la, on, pa = self._la, self._on, self._table()
         for r, s in enumerate(shards):
             pa[r] = on(s, la, "shards")
-        return on(W, self._lw, "W"), on(labels, self._llab, "labels")
+        return pa, on(W, self._lw, "W"), on(labels, self._llab, "labels")
 
     def forward(self, shards, W, labels, stream=None):
         """(loss, lse, target), fp32 [m] each."""
-        w, lab = self._operands(shards, W, labels)
+        a, w, lab = self._operands(shards, W, labels)
         with _device_and_stream(self.device, stream):
             new = self._new
             loss, lse, target = new(self._lrow), new(self._lrow), new(self._lrow)
-            _check(self._fwd(self.handle, self._a, w, lab, loss.data_ptr(), lse.data_ptr(), target.data_ptr(),
+            _check(self._fwd(self.handle, a, w, lab, loss.data_ptr(), lse.data_ptr(), target.data_ptr(),
                              _stream_handle(stream, self.device)))
         return loss, lse, target
 
@@ -760,7 +760,7 @@ class LossPlan(_OpPlan):
                  need_dW: bool = True, stream=None):
         """(dA [m, k], dW [n_local, k]) for upstream gradients of loss and,
         optionally, lse; None in the place of one that is not needed."""
-        w, lab = self._operands(shards, W, labels)
+        a, w, lab = self._operands(shards, W, labels)
         on = self._on
         ls, gl = on(lse, self._lrow, "lse"), on(grad_loss, self._lrow, "grad_loss")
         gz = None if grad_lse is None else on(grad_lse, self._lrow, "grad_lse")
@@ -769,7 +769,7 @@ class LossPlan(_OpPlan):
                 dA = self._new(self._lda)
             if dW is None and need_dW:
                 dW = self._new(self._ldw)
-            _check(self._bwd(self.handle, self._a, w, lab, ls, gl, gz, None if dA is None else on(dA, self._lda, "dA"),
+            _check(self._bwd(self.handle, a, w, lab, ls, gl, gz, None if dA is None else on(dA, self._lda, "dA"),
                              None if dW is None else on(dW, self._ldw, "dW"), _stream_handle(stream, self.device)))
         return dA, dW
 

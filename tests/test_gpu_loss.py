@@ -368,6 +368,27 @@ def test_calls_on_several_streams_and_twice_the_same():
             assert all(torch.equal(x, y) for x, y in zip(g, want[i]))
 
 
+def test_calls_that_overlap_keep_their_operands():
+    """A call that another one of the same plan overtakes, as one of another
+    thread can, between the reading of its shards: both are right."""
+    cases = [Case(2, 30, 72, 300, agmm.AGMM_BF16, seed=51 + i) for i in range(2)]
+    sets = [(c.shards(), c.w.cuda(), c.labels.cuda()) for c in cases]
+    other = []
+    with cases[0].plan() as plan:
+        want = [plan.forward(*s) for s in sets]
+
+        class Overtaken(list):
+            def __iter__(self):
+                yield self[0]
+                yield self[1]
+                other.append(plan.forward(*sets[1]))
+
+        got = plan.forward(Overtaken(sets[0][0]), *sets[0][1:])
+        torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want[0]))
+    assert all(torch.equal(g, w) for g, w in zip(other[0], want[1]))
+
+
 def test_in_a_graph():
     c = Case(2, 60, 128, 900, agmm.AGMM_BF16, seed=14)
     with c.plan() as plan:

@@ -347,6 +347,27 @@ def test_product_calls_share_a_plan_across_streams():
         assert all(torch.equal(g, want[i]) for g in got[i])
 
 
+def test_product_calls_that_overlap_keep_their_operands():
+    """A call that another one of the same plan overtakes, as one of another
+    thread can, between the reading of its shards: both are right."""
+    N, ms, k, n = 2, 5, 200, 40
+    sets = [([operand(ms, k, "e4m3", 1, 30 + 2 * i), operand(ms, k, "e4m3", 1, 31 + 2 * i)], operand(n, k, "e4m3", 128, 40 + i))
+            for i in range(2)]
+    other = []
+    with agmm.ScaledPlan(N, ms, k, n) as plan:
+        want = [plan.run(*s) for s in sets]
+
+        class Overtaken(list):
+            def __iter__(self):
+                yield self[0]
+                yield self[1]
+                other.append(plan.run(*sets[1]))
+
+        got = plan.run(Overtaken(sets[0][0]), sets[0][1])
+        torch.cuda.synchronize()
+    assert torch.equal(got, want[0]) and torch.equal(other[0], want[1])
+
+
 def test_product_in_a_graph():
     N, ms, k, n = 2, 8, 2048, 96
     shards = [operand(ms, k, "e4m3", 1, r) for r in range(N)]
