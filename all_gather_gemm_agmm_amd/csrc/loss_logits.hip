@@ -201,12 +201,13 @@ void loss_grad_kernel(LossProblem lp) {
 
 // Merge `parts` partial (maximum, sum) pairs of each row with the running
 // ones of earlier pieces (first: none); the last piece also writes the outputs.
-// ROWS rows x 256 / ROWS partials at a time.
+// ROWS rows x 256 / ROWS partials at a time; the lanes of a row in a wave merge
+// by shuffles, the four waves through LDS, always in the same order.
 template <int ROWS>
 __global__ __launch_bounds__(256) void loss_combine_kernel(LossCombine c) {
   constexpr int LANES = 256 / ROWS;
-  __shared__ float sm[LANES][ROWS], ss[LANES][ROWS];
-  const int r = threadIdx.x % ROWS, l = threadIdx.x / ROWS;
+  __shared__ float sm[4][ROWS], ss[4][ROWS];
+  const int r = threadIdx.x % ROWS, l = threadIdx.x / ROWS, wave = threadIdx.x >> 6;
   const int64_t row = (int64_t)blockIdx.x * ROWS + r;
   float m = -__builtin_inff(), s = 0.0f;
   const auto merge = [&](float pm, float ps) {
@@ -234,11 +235,16 @@ __global__ __launch_bounds__(256) void loss_combine_kernel(LossCombine c) {
       for (int e = 0; e < 8; ++e) sum += v[e][1] * exp_of(v[e][0] - off);
       merge(top, sum);
     }
-  sm[l][r] = m;
-  ss[l][r] = s;
+#pragma unroll
+  for (int d = ROWS; d < 64; d *= 2) merge(__shfl_xor(m, d), __shfl_xor(s, d));
+  if ((threadIdx.x & 63) < ROWS) {
+    sm[wave][r] = m;
+    ss[wave][r] = s;
+  }
   __syncthreads();
   if (l != 0 || row >= c.m) return;
-  for (int q = 1; q < LANES; ++q) merge(sm[q][r], ss[q][r]);
+#pragma unroll
+  for (int q = 1; q < 4; ++q) merge(sm[q][r], ss[q][r]);
   if (!c.first) merge(c.running[2 * row], c.running[2 * row + 1]);
   if (!c.last) {
     c.running[2 * row] = m;
@@ -397,7 +403,7 @@ hipError_t launch_loss_logits(const LossProblem& p, int dtype, bool grad, hipStr
 
 hipError_t launch_loss_combine(const LossCombine& c, hipStream_t stream) {
   // few rows: more lanes share a row's partials
-  if (c.m <= 64) hipLaunchKernelGGL((loss_combine_kernel<4>), dim3((unsigned)((c.m + 3) / 4)), dim3(256), 0, stream, c);
+  if (c.m <= 256) hipLaunchKernelGGL((loss_combine_kernel<1>), dim3((unsigned)c.m), dim3(256), 0, stream, c);
   else hipLaunchKernelGGL((loss_combine_kernel<16>), dim3((unsigned)((c.m + 15) / 16)), dim3(256), 0, stream, c);
   return hipGetLastError();
 }
