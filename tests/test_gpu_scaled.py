@@ -287,6 +287,22 @@ def test_product_every_tile(tile, c_dtype, N, ms, k, n):
         assert used == (tile, -(-kb // -(-kb // splits)))   # ranges of equal whole blocks
 
 
+@pytest.mark.parametrize("fmt,k,c_dtype", [("e5m2", 300, agmm.AGMM_FP32), ("e4m3", 300, agmm.AGMM_FP32),
+                                           ("e5m2", 2048, agmm.AGMM_BF16), ("e4m3", 2048, agmm.AGMM_BF16)])
+@pytest.mark.parametrize("ms", [3, 200])
+def test_product_of_the_smallest_values(fmt, k, c_dtype, ms):
+    """Operands that are subnormal numbers of their formats count like others."""
+    a, b = operand(ms, k, fmt, 1, 61), operand(140, k, "e4m3", 128, 62)
+    for x, bits in ((a, 3 if fmt == "e5m2" else 7), (b, 7)):
+        bytes_ = x.values.view(torch.uint8)
+        bytes_ &= 0x80 | bits          # sign and mantissa only
+    with agmm.ScaledPlan(1, ms, k, 140, fmt, 128, c_dtype) as plan:
+        C = plan.run([a], b)
+        torch.cuda.synchronize()
+    check_product(C, spread64(a), spread64(b), c_dtype)
+    assert (C != 0).any()
+
+
 def test_product_strides():
     """Operands and C as views with row strides; bytes between C's rows stay."""
     N, ms, k, n = 2, 70, 300, 90
