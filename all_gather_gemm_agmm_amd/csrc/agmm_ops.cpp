@@ -16,7 +16,7 @@
 
 #include "agmm.h"
 #include "agmm_host.h"
-#include "agmm_kernels.h"
+#include "ops_kernels.h"
 
 namespace {
 

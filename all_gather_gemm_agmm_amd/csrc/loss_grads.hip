@@ -9,11 +9,17 @@
 // over the pieces of the vocabulary (and over ranges of a piece where few
 // output tiles would leave CUs idle) in fp32 sums [range][m][k] that each
 // piece adds to in place, in order; one last pass adds the ranges, scales and
-// casts.  dW of a piece is complete at once.  Bound: MFMA.
+// casts.  dW of a piece is complete at once.
+//
+// Bound: MFMA; with few rows the stores of dW.  Measured: 8192 x 4096 bf16 over
+// 16384 columns, both products 1.48 ms, 1490 TFLOP/s; 16 x 4096 over 65536
+// 286 us, 1.07 GB of W read and dW written: 3.8 TB/s; 30 x 500 over 50000 38 us
+// (80 with 256 x 256 tiles and dW, whose rows are then not whole 16-byte
+// vectors, stored by elements).  The last pass: 8192 x 4096 37 us, 5.4 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "agmm_kernels.h"
+#include "ops_kernels.h"
 #include "gemm_device.h"
 
 namespace agmm {

@@ -100,7 +100,7 @@ def log(msg):
 
 def kernel_source_sha() -> str:
     h = hashlib.sha256()
-    for f in ("gemm_mfma.hip", "skinny.hip", "gather_f32.hip", "agmm_kernels.h"):
+    for f in ("gemm_mfma.hip", "gemm_device.h", "gemm_m16_loop.inc", "skinny.hip", "gather_f32.hip", "agmm_kernels.h"):
         with open(os.path.join(ROOT, "all_gather_gemm_agmm_amd", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
