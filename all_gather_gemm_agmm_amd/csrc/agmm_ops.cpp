@@ -385,14 +385,15 @@ struct agmm_loss_plan : PlanBase {
   bool with_gradient = true;
   int64_t lda = 0, ldw = 0, ldda = 0, lddw = 0;   // 0: dense
   int64_t piece_key = 0;                          // columns per piece; 0: automatic
-  int64_t tile_key = -1;                          // 128, 256; -1: automatic
+  int64_t tile_key = -1;                          // 64 (few rows), 128, 256; -1: automatic
 
   // What a call of a pass uses, derived from the settings.
   struct Layout {
     bool pad_a = false, pad_w = false;   // rows that are not whole 16-byte vectors: zero-padded copies
     int64_t kp = 0;                      // k rounded up to 8
     int64_t piece = 0;                   // columns of the vocabulary per piece
-    int tile = 256, tile_grads = 256;
+    int tile = 256, tile_grads = 256;    // tile 64: the few-row form, in
+    int fm = 0, fn = 0;                  // blocks of 16 fm x 16 fn
     int ranges = 1;                      // k ranges of the dA product
     int64_t per_range = 0;
     // a: gathered or padded copy of A; as: fp16, its rows scaled for dW's product
@@ -412,17 +413,34 @@ struct agmm_loss_plan : PlanBase {
     return tile == 256 ? 20.0 + 2.1 * (double)cdiv(sum, 64) : 5.0 + 1.25 * (double)cdiv(sum, 64);
   }
 
-  // Tile of the products with W: the one whose rounds of the CUs take less.
-  // 1000 x 700 over 30000 columns twice: 111 us by 128, 143 by 256; 8192 x 4096
-  // over 131072: 7.4 ms by 128, 6.2 by 256.
-  int pick_tile(int64_t rows, int64_t cols) const {
-    if (tile_key > 0) return (int)tile_key;
-    const double big = (double)cdiv(cdiv(rows, 256) * cdiv(cols, 256), cu_count) * workgroup_us(256, k);
-    const int64_t tiles = cdiv(rows, 128) * cdiv(cols, 128), rest = tiles % (2 * cu_count);
+  // Form of the products with W: the one that takes the least.  1000 x 700 over
+  // 30000 columns twice: 111 us by 128, 143 by 256; 8192 x 4096 over 131072: 7.4
+  // ms by 128, 6.2 by 256.  `copied`: the tiles need a copy of W first, which
+  // the few-row form does not.
+  void pick_tile(Layout& L, bool copied) const {
+    const double big = (double)cdiv(cdiv(m, 256) * cdiv(n, 256), cu_count) * workgroup_us(256, k);
+    const int64_t tiles = cdiv(m, 128) * cdiv(n, 128), rest = tiles % (2 * cu_count);
     const double small = (double)(tiles / (2 * cu_count)) * workgroup_us(128, k) +
                          (rest == 0 ? 0.0 : rest > cu_count ? workgroup_us(128, k) : 5.0 + 0.7 * (double)cdiv(k, 64));
-    return big <= small ? 256 : 128;
+    const double bytes = (double)n * (double)k * 2;
+    L.tile = tile_key > 0 ? (int)tile_key : big <= small ? 256 : 128;
+    if (tile_key > 0 && tile_key != 64) return;
+    L.fm = m <= 16 ? 1 : 4;
+    L.fn = cdiv(n, 64) * cdiv(m, 16 * L.fm) >= 2 * cu_count ? 4 : 1;
+    const int64_t wgs = cdiv(m, 16 * L.fm) * cdiv(n, 16 * L.fn);
+    // its operands' way into the CUs at 10 MB/us together (6 in its largest
+    // blocks, which leave room for few waves), 1.7 times as long for odd strides
+    // in place, or W from HBM.  Measured (us), with the copy where one is
+    // needed: 16 x 3000 over 3000 columns 7, 34 by 128; 24 x 3121 over 5391 30,
+    // 50; 8 x 3001 over 20000 36, 70; 64 x 3000 over 60000 114, 84.
+    const double rate = (L.fm * L.fn == 16 ? 6e6 : 10e6) / (copied && (ld_a() % 2 != 0 || ld_w() % 2 != 0) ? 1.7 : 1.0);
+    const double few = 5.0 + std::max((double)wgs * 32 * (L.fm + L.fn) * (double)k / rate, bytes / 4.8e6);
+    if (tile_key == 64 || (few < std::min(big, small) + (copied ? 2.0 + 2 * bytes / 5e6 : 0.0) && wgs < kMaxGrid))
+      L.tile = 64;
   }
+
+  // Columns of one pair of statistics.
+  static int64_t stat_cols(const Layout& L) { return L.tile == 64 ? 16 * L.fn : L.tile / 2; }
 
   Layout layout(bool grad, char* base) const {
     Layout L;
@@ -438,12 +456,13 @@ struct agmm_loss_plan : PlanBase {
     if (!piece_key && L.pad_w) piece = std::min(piece, budget / (2 * L.kp));
     piece = std::max<int64_t>(256, piece / 256 * 256);
     L.piece = std::min(piece, n);
-    L.tile = pick_tile(m, L.piece);
+    pick_tile(L, !grad && L.pad_w);
+    if (!grad && L.tile == 64) L.pad_a = L.pad_w = false;   // read in place
     Cut c{base};
     if (L.pad_w) L.w = c.take((size_t)L.piece * L.kp * 2);
     if (!grad) {
       if (L.pad_a) L.a = c.take((size_t)m * L.kp * 2);
-      L.stats = reinterpret_cast<float*>(c.take((size_t)cdiv(L.piece, L.tile) * 2 * m * 8));
+      L.stats = reinterpret_cast<float*>(c.take((size_t)(cdiv(L.piece, stat_cols(L)) + 1) * m * 8));
       L.running = reinterpret_cast<float*>(c.take((size_t)m * 8));
     } else {
       const bool half = dtype == AGMM_FP16;
@@ -462,7 +481,7 @@ struct agmm_loss_plan : PlanBase {
       double best = -1;
       int64_t want = 1;
       for (int t : {256, 128}) {
-        if (tile_key > 0 && t != tile_key) continue;
+        if (tile_key > 64 && t != tile_key) continue;
         const int64_t a_tiles = cdiv(m, t) * cdiv(k, t), w_tiles = cdiv(L.piece, t) * cdiv(k, t);
         const double slots = cu_count * (t == 128 ? 2 : 1), w_us = workgroup_us(t, m);
         for (int64_t r = 1; r == 1 || (r <= 64 && a_tiles * r <= 4 * cu_count && L.piece / r >= 256); r *= 2) {
@@ -545,10 +564,15 @@ struct agmm_loss_plan : PlanBase {
                            int64_t vn, const int64_t* labels) const {
     agmm::LossProblem p{};
     p.gemm.rows = rows;
-    p.gemm.order = order(m, vn, L.tile);
+    if (L.tile == 64) {
+      p.gemm.order.num_rb = (int32_t)cdiv(m, 16 * L.fm);
+      p.gemm.order.num_cb = (int32_t)cdiv(vn, 16 * L.fn);
+    } else {
+      p.gemm.order = order(m, vn, L.tile);
+    }
     p.gemm.m = (int32_t)m;
     p.gemm.n = (int32_t)vn;
-    p.gemm.k = (int32_t)L.kp;
+    p.gemm.k = (int32_t)(L.tile == 64 ? k : L.kp);
     p.gemm.b = w;
     p.gemm.ldb = ldb;
     p.gemm.splits = 1;
@@ -557,6 +581,10 @@ struct agmm_loss_plan : PlanBase {
     p.labels = labels;
     p.label0 = start + v0;
     return p;
+  }
+
+  hipError_t launch_logits(const Layout& L, const agmm::LossProblem& p, bool grad, hipStream_t s) const {
+    return L.tile == 64 ? agmm::launch_loss_few(p, L.fm, L.fn, dtype, grad, s) : agmm::launch_loss_logits(p, dtype, grad, s);
   }
 
   int forward(const void* const* shards, const void* W, const int64_t* labels, float* loss, float* lse, float* target,
@@ -578,11 +606,11 @@ struct agmm_loss_plan : PlanBase {
       agmm::LossProblem p = logits(L, rows, w, ldb, v0, vn, labels);
       p.stats = L.stats;
       p.target = target;
-      hipError_t err = agmm::launch_loss_logits(p, dtype, false, s);
+      hipError_t err = launch_logits(L, p, false, s);
       if (err != hipSuccess) return hip_err(err, "loss logits launch");
       agmm::LossCombine c{};
       c.stats = L.stats;
-      c.parts = 2 * p.gemm.order.num_cb;
+      c.parts = (L.tile == 64 ? 1 : 2) * p.gemm.order.num_cb;
       c.m = m;
       c.running = L.running;
       c.first = v0 == 0;
@@ -645,7 +673,7 @@ struct agmm_loss_plan : PlanBase {
       p.ldd = round_up(vn, 8);
       p.dt = dW ? L.dt : nullptr;
       p.ldt = m8();
-      err = agmm::launch_loss_logits(p, dtype, true, s);
+      err = launch_logits(L, p, true, s);
       if (err != hipSuccess) return hip_err(err, "loss gradient launch");
       agmm::GemmProblem ga{}, gw{};
       ga.rows = dense(L.d, m, round_up(vn, 8));
@@ -926,7 +954,9 @@ int agmm_loss_plan_set_int(agmm_loss_plan_t p, const char* key, int64_t v) {
     if (v < 0 || v >= kDimLimit) return bad();
     field = &p->piece_key;
   } else if (k == "tile") {
-    if (v != -1 && v != 128 && v != 256) return bad();
+    if (v != -1 && v != 64 && v != 128 && v != 256) return bad();
+    if (v == 64 && cdiv(p->m, 64) * cdiv(p->n, 64) >= kMaxGrid)
+      return set_err(AGMM_ERR_UNSUPPORTED, "too many workgroups for tile 64");
     field = &p->tile_key;
   } else if (k == "ignore_index") {
     p->ignore = v;

@@ -206,6 +206,190 @@ void loss_grad_kernel(LossProblem lp) {
   loss_body<BM, BN, 64, DT, 4, OCC, true>(lp, smem);
 }
 
+// Few rows: FM x FN blocks of 16 rows x 16 columns per workgroup.  The waves
+// share out k, 64 elements (whole 128-byte lines) at a time, and load their
+// operands straight into registers: 16-byte accesses to global memory may start
+// at any word, which loads into LDS may not, so neither operand is copied first
+// whatever k and the strides are.  UN pieces are on their way at a time.  The
+// waves' sums are added in LDS in a fixed order, wave w taking row block w.
+// ODD (a stride is odd): rows that start in the middle of a word are read from
+// that word on, with one word more, and shifted; accesses that start there take
+// three times as long (24 rows of 3121 over 5391 columns: 55 us, 30 shifted, 18
+// at 3122).  Bound: HBM on W (8 rows of 3008 over 20000 columns 23 us, 5.2
+// TB/s), with more rows the operands' way into the CUs.
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+
+template <int DT, int FM, int FN, int UN, bool ODD, bool GRAD>
+__global__ __launch_bounds__(256) void loss_few_kernel(LossProblem lp) {
+  const GemmProblem& p = lp.gemm;
+  __shared__ float part[4][FM][FN][4][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g4 = lane >> 4, i16 = lane & 15;
+  const int M = p.m, N = p.n, K = p.k;
+  const int cb = (int)blockIdx.x / p.order.num_rb, rb = (int)blockIdx.x - cb * p.order.num_rb;
+  const int m0 = rb * 16 * FM, n0 = cb * 16 * FN;
+  // rows and columns past the end read the last one and are never used
+  const uint16_t *a[FM], *b[FN];
+#pragma unroll
+  for (int f = 0; f < FM; ++f) {
+    const int i = min(m0 + 16 * f + i16, M - 1), g = i / p.rows.rows_per_group;
+    a[f] = static_cast<const uint16_t*>(p.rows.a_group[g]) + (int64_t)(i - g * p.rows.rows_per_group) * p.rows.a_ld + 8 * g4;
+  }
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+    b[f] = static_cast<const uint16_t*>(p.b) + (int64_t)min(n0 + 16 * f + i16, N - 1) * p.ldb + 8 * g4;
+
+  f32x4_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const auto multiply = [&](const u32x4_t (&fa)[FM], const u32x4_t (&fb)[FN]) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = mfma16_builtin<DT>(fb[j], fa[i], acc[i][j]);
+  };
+  // halves 2u, 2u + 1 of piece c + u: elements 64 (c + u) + 32 h + 8 g4 on;
+  // ODD: their words and the one behind
+  constexpr int W = ODD ? 2 * UN : 1;
+  typedef u32x4_t u32x4_word_t __attribute__((aligned(4)));
+  const auto load = [&](int c, u32x4_t (&fa)[2 * UN][FM], u32x4_t (&fb)[2 * UN][FN], uint32_t (&wa)[W][FM], uint32_t (&wb)[W][FN]) {
+    const auto one = [&](const uint16_t* x, u32x4_t& v, uint32_t& w) {
+      if constexpr (ODD) {
+        const char* q = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(x) & ~uintptr_t(2));
+        v = *reinterpret_cast<const u32x4_word_t*>(q);
+        w = *reinterpret_cast<const uint32_t*>(q + 16);
+      } else {
+        v = *reinterpret_cast<const u32x4_word_t*>(x);
+      }
+    };
+#pragma unroll
+    for (int h = 0; h < 2 * UN; ++h) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) one(b[j] + (int64_t)c * 64 + 32 * h, fb[h][j], wb[ODD ? h : 0][j]);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) one(a[i] + (int64_t)c * 64 + 32 * h, fa[h][i], wa[ODD ? h : 0][i]);
+    }
+  };
+  const auto shift = [&](const uint16_t* x, u32x4_t& v, uint32_t w) {
+    const uint32_t by = (uint32_t)reinterpret_cast<uintptr_t>(x) & 2;
+    v = u32x4_t{__builtin_amdgcn_alignbyte(v[1], v[0], by), __builtin_amdgcn_alignbyte(v[2], v[1], by),
+                __builtin_amdgcn_alignbyte(v[3], v[2], by), __builtin_amdgcn_alignbyte(w, v[3], by)};
+  };
+  const auto use = [&](u32x4_t (&fa)[2 * UN][FM], u32x4_t (&fb)[2 * UN][FN], const uint32_t (&wa)[W][FM], const uint32_t (&wb)[W][FN]) {
+#pragma unroll
+    for (int h = 0; h < 2 * UN; ++h) {
+      if constexpr (ODD) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) shift(b[j], fb[h][j], wb[h][j]);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) shift(a[i], fa[h][i], wa[h][i]);
+      }
+      multiply(fa[h], fb[h]);
+    }
+  };
+  const int pieces = (ODD ? max(K - 2, 0) : K) / 64, groups = pieces / UN;   // the word behind lies in the row
+  u32x4_t fa[2][2 * UN][FM], fb[2][2 * UN][FN];
+  uint32_t wa[2][W][FM], wb[2][W][FN];
+  if (wave < groups) load(wave * UN, fa[0], fb[0], wa[0], wb[0]);
+  for (int c = wave; c < groups; c += 8) {
+    // two groups per turn, the last one loaded again where there is none
+    load((c + 4 < groups ? c + 4 : c) * UN, fa[1], fb[1], wa[1], wb[1]);
+    use(fa[0], fb[0], wa[0], wb[0]);
+    if (c + 4 >= groups) break;
+    load((c + 8 < groups ? c + 8 : c) * UN, fa[0], fb[0], wa[0], wb[0]);
+    use(fa[1], fb[1], wa[1], wb[1]);
+  }
+  // what is left: halves of 32 elements, shared out over the waves, those
+  // past k elementwise and zero
+  for (int at = groups * UN * 64 + 32 * wave; at < K; at += 128) {
+    u32x4_t ta[FM], tb[FN];
+    const int left = K - at - 8 * g4;
+    const auto get = [&](const uint16_t* x) {
+      u32x4_t v = {0u, 0u, 0u, 0u};
+      if (left >= 8) {
+        v = *reinterpret_cast<const u32x4_any_t*>(x + at);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < left) v[e >> 1] |= (uint32_t)x[at + e] << (16 * (e & 1));
+      }
+      return v;
+    };
+#pragma unroll
+    for (int j = 0; j < FN; ++j) tb[j] = get(b[j]);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) ta[i] = get(a[i]);
+    multiply(ta, tb);
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[wave][i][j][e][lane] = acc[i][j][e];
+  __syncthreads();
+  if (wave >= FM) return;
+  float x[FN][4];
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x[j][e] = part[0][wave][j][e][lane] + part[1][wave][j][e][lane] + part[2][wave][j][e][lane] + part[3][wave][j][e][lane];
+  const int row = m0 + 16 * wave + i16, col = n0 + 4 * g4;
+  const int64_t at = row < M ? lp.labels[row] - lp.label0 : -1;   // the label's column
+  if constexpr (!GRAD) {
+    float mx = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + 16 * j + e < N) mx = fmaxf(mx, x[j][e]);
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float off = finite_or_zero(mx);
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (col + 16 * j + e < N) sum += exp_of(x[j][e] - off);
+        if (at == col + 16 * j + e && at < N) lp.target[row] = x[j][e];
+      }
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (g4 == 0 && row < M) {
+      float* o = lp.stats + ((int64_t)cb * M + row) * 2;
+      o[0] = mx;
+      o[1] = sum;
+    }
+  } else {
+    const f32x4_t rv = *reinterpret_cast<const f32x4_t*>(lp.rows + 4 * (int64_t)min(row, M - 1));
+    const float f = (DT == kDtypeFp16 ? 16384.0f : 1.0f) / rv[3];
+    const float wa = rv[1] * f, wb = rv[2] * f;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = col + 16 * j + e;
+        v[e] = wa * exp_of(x[j][e] - rv[0]);
+        if (at == c) v[e] -= wb;
+        if (row >= M || c >= N) v[e] = 0.0f;
+      }
+      const u32x2_t w = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+      if (lp.d && row < M && col + 16 * j < lp.ldd)
+        *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(lp.d) + (int64_t)row * lp.ldd + col + 16 * j) = w;
+      if (lp.dt && row < lp.ldt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + 16 * j + e < N)
+            static_cast<uint16_t*>(lp.dt)[(int64_t)(col + 16 * j + e) * lp.ldt + row] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+}
+
 // Merge `parts` partial (maximum, sum) pairs of each row with the running
 // ones of earlier pieces (first: none); the last piece also writes the outputs.
 // ROWS rows x 256 / ROWS partials at a time; the lanes of a row in a wave merge
@@ -335,7 +519,6 @@ __device__ __forceinline__ void loss_rows(const LossRows& c) {
 // out[(g * rows + t) * chunks * 8 + c] = group[g][t * ld + c], zeros past cols.
 // A source row may start at any element (16-byte accesses to global memory
 // need no alignment); its last chunk is read element by element.
-typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
 __device__ __forceinline__ void pad_rows(const PadRows& c, int64_t block) {
   const int64_t u = block * 1024 + threadIdx.x;
   const int64_t row = u / (uint32_t)c.chunks;
@@ -396,6 +579,23 @@ hipError_t launch_body(const LossProblem& p, bool grad, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int DT, int FM, int FN, int UN>
+void launch_few_tile(const LossProblem& p, bool grad, unsigned grid, hipStream_t s) {
+  const bool odd = p.gemm.ldb % 2 != 0 || p.gemm.rows.a_ld % 2 != 0;
+  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, s, p); };
+  if (odd) grad ? go(loss_few_kernel<DT, FM, FN, UN, true, true>) : go(loss_few_kernel<DT, FM, FN, UN, true, false>);
+  else grad ? go(loss_few_kernel<DT, FM, FN, UN, false, true>) : go(loss_few_kernel<DT, FM, FN, UN, false, false>);
+}
+
+template <int DT>
+hipError_t launch_few(const LossProblem& p, int fm, int fn, bool grad, unsigned grid, hipStream_t s) {
+  if (fm == 1 && fn == 1) launch_few_tile<DT, 1, 1, 4>(p, grad, grid, s);
+  else if (fm == 1) launch_few_tile<DT, 1, 4, 2>(p, grad, grid, s);
+  else if (fn == 1) launch_few_tile<DT, 4, 1, 2>(p, grad, grid, s);
+  else launch_few_tile<DT, 4, 4, 1>(p, grad, grid, s);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_loss_logits(const LossProblem& p, int dtype, bool grad, hipStream_t stream) {
@@ -406,6 +606,17 @@ hipError_t launch_loss_logits(const LossProblem& p, int dtype, bool grad, hipStr
     return hipErrorInvalidValue;
   return dtype == kDtypeBf16 ? launch_body<kDtypeBf16>(p, grad, stream)
        : dtype == kDtypeFp16 ? launch_body<kDtypeFp16>(p, grad, stream) : hipErrorInvalidValue;
+}
+
+hipError_t launch_loss_few(const LossProblem& p, int fm, int fn, int dtype, bool grad, hipStream_t stream) {
+  const int64_t grid = (int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb;
+  if ((fm != 1 && fm != 4) || (fn != 1 && fn != 4) || p.gemm.order.num_rb != (p.gemm.m + 16 * fm - 1) / (16 * fm) ||
+      p.gemm.order.num_cb != (p.gemm.n + 16 * fn - 1) / (16 * fn) || grid < 1 || grid >= (int64_t(1) << 24) ||
+      (dtype != kDtypeBf16 && dtype != kDtypeFp16) || (int64_t)p.gemm.rows.num_groups * p.gemm.rows.rows_per_group != p.gemm.m ||
+      (grad && (p.ldd % 8 != 0 || p.ldt % 8 != 0)))
+    return hipErrorInvalidValue;
+  return dtype == kDtypeBf16 ? launch_few<kDtypeBf16>(p, fm, fn, grad, (unsigned)grid, stream)
+                             : launch_few<kDtypeFp16>(p, fm, fn, grad, (unsigned)grid, stream);
 }
 
 hipError_t launch_loss_combine(const LossCombine& c, hipStream_t stream) {

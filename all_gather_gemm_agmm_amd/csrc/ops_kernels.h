@@ -97,7 +97,7 @@ hipError_t launch_scaled(const ScaledProblem& p, int tile, hipStream_t stream);
 // rows of whole 16-byte vectors), label0 is the label of its column 0.
 struct LossProblem {
   GemmProblem gemm;
-  int32_t tile;            // 256 or 128
+  int32_t tile;            // 256 or 128 (launch_loss_logits)
   const int64_t* labels;   // [m]
   int64_t label0;
   // statistics: (maximum, sum of exp) pairs [2 * column block + half][m]
@@ -113,6 +113,10 @@ struct LossProblem {
   int64_t ldt;
 };
 hipError_t launch_loss_logits(const LossProblem& p, int dtype, bool grad, hipStream_t stream);
+// The same for few rows, in blocks of 16 fm rows x 16 fn columns (1 or 4 each;
+// order.num_rb and num_cb count those): any k and any strides, operands in
+// place; stats [column block][m][2].
+hipError_t launch_loss_few(const LossProblem& p, int fm, int fn, int dtype, bool grad, hipStream_t stream);
 
 struct LossCombine {
   const float* stats;

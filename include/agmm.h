@@ -594,7 +594,9 @@ int agmm_loss_backward(agmm_loss_plan_t plan, const void *const *shard_ptrs, con
  *   "lda", "ldw", "ldda", "lddw"  elements between rows: 0 (dense) or at least k
  *   "piece"         columns of the vocabulary computed at a time: 0 automatic (512 MiB of
  *                   intermediate values), rounded down to a multiple of 256, at least 256
- *   "tile"          -1 automatic, 128 or 256: rows and columns of the products' tiles
+ *   "tile"          -1 automatic, 128 or 256: rows and columns of the products' tiles; 64: blocks
+ *                   of up to 64 x 64 whose waves share out k, for few rows (the gradient's two
+ *                   products keep their automatic tiles)
  *   "ignore_index"  the label of rows without a loss (default -100)
  * A change that needs more workspace reallocates it; the plan keeps its
  * previous settings when that fails.  Settings are fixed once a call was

@@ -193,6 +193,37 @@ def test_each_tile_at_ragged_sizes(shape, dt, tile):
     run_both(Case(*shape, dt, seed=21), tile=tile)
 
 
+@pytest.mark.parametrize("N,ms,k,n", [
+    (1, 1, 1, 1), (1, 1, 64, 15), (1, 16, 333, 4100), (2, 8, 640, 35000), (3, 5, 72, 17), (1, 17, 31, 64), (4, 16, 513, 1025),
+    (1, 64, 1030, 70), (5, 13, 257, 300), (1, 150, 96, 33), (8, 3, 2049, 130), (2, 20, 100, 33001)])
+@pytest.mark.parametrize("dt", [agmm.AGMM_BF16, agmm.AGMM_FP16])
+def test_few_rows(N, ms, k, n, dt):
+    """The form for few rows, at every block size: its row, column and k ends."""
+    run_both(Case(N, ms, k, n, dt, seed=31), tile=64)
+
+
+def test_few_rows_with_strides_and_pieces():
+    """Rows of any length apart, no copies, several pieces."""
+    c = Case(2, 9, 203, 1400, agmm.AGMM_FP16, seed=32)
+    fwd, got = run_both(c, tile=64, piece=512)
+    shards = [torch.zeros((c.ms, 211), dtype=torch.float16, device="cuda")[:, :203].copy_(s) for s in c.shards()]
+    w = torch.zeros((c.n, 205), dtype=torch.float16, device="cuda")[:, :203].copy_(c.w.cuda())
+    with c.plan(tile=64, piece=512, lda=211, ldw=205) as plan:
+        strided = plan.forward(shards, w, c.labels.cuda())
+        back = plan.backward(shards, w, c.labels.cuda(), strided[1], c.gl.cuda(), c.gz.cuda())
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(fwd, strided))
+    check_backward(c, back, strided[1].cpu(), c.gl, c.gz)
+
+
+def test_form_by_the_sizes():
+    """An unaligned W is read in place for few rows; long aligned ones by tiles."""
+    with agmm.LossPlan(1, 8, 1001, 50000, agmm.AGMM_BF16, with_gradient=False) as plan:
+        assert plan.get("tile") == 64 and plan.workspace_bytes() < 1 << 20
+    with agmm.LossPlan(1, 4096, 1001, 50000, agmm.AGMM_BF16, with_gradient=False) as plan:
+        assert plan.get("tile") > 64
+
+
 def test_one_pass_of_two():
     c = Case(1, 40, 64, 300, agmm.AGMM_BF16, seed=2)
     with c.plan() as plan:
