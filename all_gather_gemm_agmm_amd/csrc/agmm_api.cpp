@@ -16,13 +16,12 @@
 // take the place of the tutorial's barrier_all per chunk and of the
 // semaphores of the tpu-inference kernel.
 //
-// Calls on one plan are ordered with each other wherever they are enqueued:
-// every call ends by recording the plan's `done` event on the caller's
-// stream (after the internal streams have joined it), and the next call's
-// stream waits on that event before any of its work, so no call overwrites
-// ring slots or split-K partial sums a previous call on another stream is
-// still reading (the tutorial's rule that a slot is not refilled before the
-// chunk that reads it has been consumed).
+// Calls on one plan are ordered with each other wherever they are enqueued
+// (CallOrder): a call ends on the caller's stream (the internal streams have
+// joined it), and the next call's stream waits for that end before any of its
+// work, so no call overwrites ring slots or split-K partial sums a previous
+// call on another stream is still reading (the tutorial's rule that a slot is
+// not refilled before the chunk that reads it has been consumed).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -42,6 +41,7 @@
 
 namespace {
 
+using agmm::Call;
 using agmm::g_msg;
 using agmm::g_status;
 using agmm::hip_err;
@@ -142,9 +142,6 @@ struct Layout {
   }
 };
 
-// Where the plan's previous call recorded its `done` event.
-enum DoneState { kDoneNone = 0, kDoneEager = 1, kDoneCaptured = 2 };
-
 }  // namespace
 
 struct agmm_plan {
@@ -172,12 +169,9 @@ struct agmm_plan {
   hipEvent_t ev_entry = nullptr;    // start of a call on the caller's stream
   hipEvent_t ev_side = nullptr;     // end of the copy stream's work
   hipEvent_t ev_c2 = nullptr;       // end of the second GEMM stream's work
-  hipEvent_t ev_done = nullptr;     // end of the plan's previous call
   std::vector<hipEvent_t> ev_ready, ev_free;
   // ordering between calls
-  int done_state = kDoneNone;
-  unsigned long long done_capture_id = 0;
-  hipStream_t done_stream = nullptr;
+  agmm::CallOrder calls;
   bool captured = false;            // some call was captured into a graph
   unsigned long long staged_capture_id = 0;   // capture holding a staged call, or 0
   int broken = AGMM_OK;             // status that left the plan unusable, or AGMM_OK
@@ -465,15 +459,6 @@ int derive(const agmm_plan* p, const Settings& s, Layout& L) {
   return AGMM_OK;
 }
 
-// Wait until no enqueued work of the plan can still use its workspace.
-int wait_idle(agmm_plan* p) {
-  if (p->done_state == kDoneEager) {
-    const hipError_t err = hipEventSynchronize(p->ev_done);
-    if (err != hipSuccess) return hip_err(err, "hipEventSynchronize(done)");
-  }
-  return AGMM_OK;
-}
-
 int alloc_ws(agmm_plan* p, size_t bytes) {
   if (bytes == 0) return AGMM_OK;
   // test hook: AGMM_TEST_FAIL_ALLOC=<n> makes every workspace allocation of
@@ -505,7 +490,7 @@ int apply(agmm_plan* p, const Settings& s) {
   Layout L;
   int rc = derive(p, s, L);
   if (rc != AGMM_OK) return rc;
-  rc = wait_idle(p);   // the previous call may still read the workspace
+  rc = p->calls.idle();   // the previous call may still read the workspace
   if (rc != AGMM_OK) return rc;
   const size_t total = L.total_bytes();
   if (total > p->ws_cap) {
@@ -576,51 +561,18 @@ int apply(agmm_plan* p, const Settings& s) {
   return ok();
 }
 
-// One call's view of the caller's stream.
-struct Call {
-  hipStream_t s = nullptr;
-  bool capturing = false;
-  unsigned long long capture_id = 0;
-};
-
 // Start a call: refuse an unusable plan, find out whether the stream is being
-// captured into a graph, and order the call after the plan's previous one.
-// Across a capture boundary (a call captured into a graph after eager calls,
-// or an eager call after a captured one) no event links them: waiting on an
-// event recorded on the other side of the boundary is not allowed while a
-// stream is capturing, and a captured call's work happens at each replay;
-// the caller's streams order graph replays against other work.
+// captured into a graph, and order the call after the plan's previous one
+// (every internal stream joins the caller's before leave()).
 int enter(agmm_plan* p, hipStream_t s, Call& c) {
   if (p->broken != AGMM_OK) return set_err(p->broken, "plan is unusable: %s", p->broken_msg.c_str());
-  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
-  unsigned long long id = 0;
-  hipError_t err = hipStreamGetCaptureInfo(s, &st, &id);
-  if (err != hipSuccess) return hip_err(err, "hipStreamGetCaptureInfo");
-  if (st == hipStreamCaptureStatusInvalidated)
-    return set_err(AGMM_ERR_HIP, "the stream's graph capture has been invalidated");
-  c.s = s;
-  c.capturing = st == hipStreamCaptureStatusActive;
-  c.capture_id = c.capturing ? id : 0;
+  const int rc = agmm::CallOrder::look(s, c);
+  if (rc != AGMM_OK) return rc;
   if (c.capturing) p->captured = true;
-  const bool linked = p->done_state == kDoneEager
-                          ? !c.capturing
-                          : (p->done_state == kDoneCaptured && c.capturing && p->done_capture_id == id);
-  if (linked && p->done_stream != s) {
-    err = hipStreamWaitEvent(s, p->ev_done, 0);
-    if (err != hipSuccess) return hip_err(err, "hipStreamWaitEvent(done)");
-  }
-  return AGMM_OK;
+  return p->calls.enter(c);
 }
 
-// End a call that enqueued work: every internal stream has joined `c.s`.
-int leave(agmm_plan* p, const Call& c) {
-  const hipError_t err = hipEventRecord(p->ev_done, c.s);
-  if (err != hipSuccess) return hip_err(err, "hipEventRecord(done)");
-  p->done_state = c.capturing ? kDoneCaptured : kDoneEager;
-  p->done_capture_id = c.capture_id;
-  p->done_stream = c.s;
-  return AGMM_OK;
-}
+int leave(agmm_plan* p, const Call& c) { return p->calls.leave(c); }
 
 agmm::RowMap shard_rows(const agmm_plan* p, const void* const* shards) {
   agmm::RowMap r{};
@@ -1080,9 +1032,8 @@ agmm_plan_t agmm_plan_create(int num_shards, int64_t m_per_shard, int64_t k, int
   if (err == hipSuccess) err = hipEventCreateWithFlags(&p->ev_entry, hipEventDisableTiming);
   if (err == hipSuccess) err = hipEventCreateWithFlags(&p->ev_side, hipEventDisableTiming);
   if (err == hipSuccess) err = hipEventCreateWithFlags(&p->ev_c2, hipEventDisableTiming);
-  if (err == hipSuccess) err = hipEventCreateWithFlags(&p->ev_done, hipEventDisableTiming);
-  if (err != hipSuccess) {
-    hip_err(err, "creating the plan's streams and events");
+  if (err != hipSuccess) hip_err(err, "creating the plan's streams and events");
+  if (err != hipSuccess || p->calls.create(p->device) != AGMM_OK) {
     const int st = g_status;
     const std::string msg = g_msg;
     agmm_plan_destroy(p);
@@ -1546,7 +1497,7 @@ void agmm_plan_destroy(agmm_plan_t p) {
     std::lock_guard<std::mutex> lk(p->mu);
     // the plan's own work: its last call (which the internal streams joined)
     // and anything still queued on the internal streams
-    if (p->done_state == kDoneEager && p->ev_done) hipEventSynchronize(p->ev_done);
+    (void)p->calls.idle();
     if (p->copy_stream) hipStreamSynchronize(p->copy_stream);
     if (p->compute2) hipStreamSynchronize(p->compute2);
     (void)hipGetLastError();
@@ -1555,8 +1506,9 @@ void agmm_plan_destroy(agmm_plan_t p) {
   for (hipEvent_t e : p->ev_ready) hipEventDestroy(e);
   for (hipEvent_t e : p->ev_free) hipEventDestroy(e);
   for (hipEvent_t e : p->tev) hipEventDestroy(e);
-  for (hipEvent_t e : {p->ev_entry, p->ev_side, p->ev_c2, p->ev_done})
+  for (hipEvent_t e : {p->ev_entry, p->ev_side, p->ev_c2})
     if (e) hipEventDestroy(e);
+  p->calls.destroy();
   if (p->compute2) hipStreamDestroy(p->compute2);
   if (p->copy_stream) hipStreamDestroy(p->copy_stream);
   delete p;

@@ -2,10 +2,9 @@
 // block-scaled 8-bit quantiser and product, and the vocabulary loss.
 //
 // Their plans are used as the all-gather matmul's are: a plan validates its
-// problem, owns a workspace when a call needs one, and orders its calls: every
-// call records the plan's completion event on its stream and the next call's
-// stream waits for it, so that calls on different streams or threads never
-// share the workspace at one time.
+// problem, owns a workspace when a call needs one, and orders its calls
+// (CallOrder), so that calls on different streams or threads never share the
+// workspace at one time.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -56,17 +55,14 @@ int check_sizes(int N, int64_t m_s, int64_t k, int64_t n) {
   return AGMM_OK;
 }
 
-// What every plan here owns: its device, a workspace, and the event that
-// orders its calls.
+// What every plan here owns: its device, a workspace, and the order of its
+// calls.
 struct PlanBase {
   int device = 0;
   int cu_count = 256;
   char* ws = nullptr;
   size_t ws_bytes = 0;
-  hipEvent_t ev_done = nullptr;
-  enum { kNone, kEager, kCaptured } done = kNone;
-  unsigned long long done_capture = 0;
-  hipStream_t done_stream = nullptr;
+  agmm::CallOrder order;
   bool captured = false;
   std::mutex mu;
 
@@ -76,8 +72,7 @@ struct PlanBase {
     int cus = 0;
     if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) == hipSuccess && cus > 0)
       cu_count = cus;
-    err = hipEventCreateWithFlags(&ev_done, hipEventDisableTiming);
-    return err == hipSuccess ? AGMM_OK : hip_err(err, "hipEventCreate");
+    return order.create(device);
   }
 
   // Replace the workspace by one of at least `bytes` (kept when it is large
@@ -97,7 +92,7 @@ struct PlanBase {
       (void)hipGetLastError();
       return set_err(AGMM_ERR_OOM, "workspace allocation of %zu bytes failed: %s", bytes, hipGetErrorString(err));
     }
-    const int rc = idle();   // the previous call may still use the old one
+    const int rc = order.idle();   // the previous call may still use the old one
     if (rc != AGMM_OK) {
       hipFree(q);
       return rc;
@@ -108,72 +103,13 @@ struct PlanBase {
     return AGMM_OK;
   }
 
-  // The default stream needs no event of its own per call: it never ends, so
-  // what orders a later call after it (and what the plan's end waits for) is
-  // recorded, or waited for, when that time comes.
-  int on_device(hipError_t (*f)(PlanBase*), const char* what) {
-    int dev = device;
-    hipError_t err = hipGetDevice(&dev);
-    if (err == hipSuccess && dev != device) err = hipSetDevice(device);
-    if (err == hipSuccess) err = f(this);
-    if (dev != device) (void)hipSetDevice(dev);
-    return err == hipSuccess ? AGMM_OK : hip_err(err, what);
-  }
-
-  int idle() {
-    if (done != kEager) return AGMM_OK;
-    if (!done_stream) return on_device([](PlanBase*) { return hipStreamSynchronize(nullptr); }, "hipStreamSynchronize");
-    const hipError_t err = hipEventSynchronize(ev_done);
-    return err == hipSuccess ? AGMM_OK : hip_err(err, "hipEventSynchronize(done)");
-  }
-
-  // Find out whether `s` is being captured into a graph (the default stream
-  // cannot be).
-  int look(hipStream_t s, bool& capturing, unsigned long long& id) {
-    capturing = false;
-    id = 0;
-    if (!s) return AGMM_OK;
-    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
-    const hipError_t err = hipStreamGetCaptureInfo(s, &st, &id);
-    if (err != hipSuccess) return hip_err(err, "hipStreamGetCaptureInfo");
-    if (st == hipStreamCaptureStatusInvalidated)
-      return set_err(AGMM_ERR_HIP, "the stream's graph capture has been invalidated");
-    capturing = st == hipStreamCaptureStatusActive;
-    if (capturing) captured = true;
-    return AGMM_OK;
-  }
-
-  // Order a call on `s` after the plan's previous one.  Across a graph-capture
-  // boundary no event links calls: the caller's streams order replays.
-  int enter(hipStream_t s, bool capturing, unsigned long long id) {
-    const bool linked = done == kEager ? !capturing : done == kCaptured && capturing && done_capture == id;
-    if (!linked || done_stream == s) return AGMM_OK;
-    if (!done_stream) {
-      const int rc = on_device([](PlanBase* p) { return hipEventRecord(p->ev_done, nullptr); }, "hipEventRecord(done)");
-      if (rc != AGMM_OK) return rc;
-    }
-    const hipError_t err = hipStreamWaitEvent(s, ev_done, 0);
-    return err == hipSuccess ? AGMM_OK : hip_err(err, "hipStreamWaitEvent(done)");
-  }
-
-  int leave(hipStream_t s, bool capturing, unsigned long long id) {
-    if (s) {
-      const hipError_t err = hipEventRecord(ev_done, s);
-      if (err != hipSuccess) return hip_err(err, "hipEventRecord(done)");
-    }
-    done = capturing ? kCaptured : kEager;
-    done_capture = capturing ? id : 0;
-    done_stream = s;
-    return AGMM_OK;
-  }
-
   // A call that enqueues work.  One that uses no workspace needs no ordering.
   template <class F>
   int run(hipStream_t s, bool ordered, F&& body) {
-    bool capturing;
-    unsigned long long id;
-    int rc = look(s, capturing, id);
-    if (rc == AGMM_OK && ordered) rc = enter(s, capturing, id);
+    agmm::Call c;
+    int rc = agmm::CallOrder::look(s, c);
+    if (rc == AGMM_OK && c.capturing) captured = true;
+    if (rc == AGMM_OK && ordered) rc = order.enter(c);
     if (rc != AGMM_OK) return rc;
     rc = body();
     if (!ordered) return rc == AGMM_OK ? ok() : rc;
@@ -181,18 +117,18 @@ struct PlanBase {
       // whatever was enqueued before the failure still counts
       const int st = agmm::g_status;
       const std::string msg = agmm::g_msg;
-      leave(s, capturing, id);
+      order.leave(c);
       return set_err(st, "%s", msg.c_str());
     }
-    rc = leave(s, capturing, id);
+    rc = order.leave(c);
     return rc == AGMM_OK ? ok() : rc;
   }
 
   ~PlanBase() {
-    (void)idle();
+    (void)order.idle();
     (void)hipGetLastError();
     if (ws) hipFree(ws);
-    if (ev_done) hipEventDestroy(ev_done);
+    order.destroy();
   }
 };
 
@@ -504,7 +440,7 @@ struct agmm_loss_plan : PlanBase {
     return reserve(with_gradient ? std::max(fwd, layout(true, nullptr).bytes) : fwd);
   }
 
-  agmm::TileOrder order(int64_t rows, int64_t cols, int tile) const {
+  agmm::TileOrder tiles_of(int64_t rows, int64_t cols, int tile) const {
     agmm::TileOrder o{};
     o.num_rb = (int32_t)cdiv(rows, tile);
     o.num_cb = (int32_t)cdiv(cols, tile);
@@ -568,7 +504,7 @@ struct agmm_loss_plan : PlanBase {
       p.gemm.order.num_rb = (int32_t)cdiv(m, 16 * L.fm);
       p.gemm.order.num_cb = (int32_t)cdiv(vn, 16 * L.fn);
     } else {
-      p.gemm.order = order(m, vn, L.tile);
+      p.gemm.order = tiles_of(m, vn, L.tile);
     }
     p.gemm.m = (int32_t)m;
     p.gemm.n = (int32_t)vn;
@@ -677,7 +613,7 @@ struct agmm_loss_plan : PlanBase {
       if (err != hipSuccess) return hip_err(err, "loss gradient launch");
       agmm::GemmProblem ga{}, gw{};
       ga.rows = dense(L.d, m, round_up(vn, 8));
-      ga.order = order(m, k, L.tile_grads);
+      ga.order = tiles_of(m, k, L.tile_grads);
       ga.m = (int32_t)m;
       ga.n = (int32_t)k;
       ga.k = (int32_t)vn;
@@ -688,7 +624,7 @@ struct agmm_loss_plan : PlanBase {
       ga.splits = (int32_t)cdiv(vn, L.per_range);
       ga.partials = L.sums;
       gw.rows = dense(L.dt, vn, m8());
-      gw.order = order(vn, k, L.tile_grads);
+      gw.order = tiles_of(vn, k, L.tile_grads);
       gw.m = (int32_t)vn;
       gw.n = (int32_t)k;
       gw.k = (int32_t)m;

@@ -152,8 +152,10 @@ agmm_plan_t agmm_plan_create(int num_shards, int64_t m_per_shard, int64_t k, int
  * the other on the GPU and never overwrite ring slots or split-K partial sums
  * a previous call still reads (the Ascend tutorial's "Double Buffering": a
  * slot is not refilled before the chunk reading it has been consumed).
- * Within one graph capture calls are ordered the same way.  Across a capture
- * boundary (a graph replay against eager calls) no event links them: the
+ * The calls of one graph capture are ordered among themselves the same way,
+ * whatever eager calls or other captures come between them, and eager calls
+ * whatever is captured between them.  Across a capture boundary (a graph
+ * replay against eager calls or another graph's) no event links them: the
  * caller orders replays with its streams, as for any graph.
  * Graph capture of the staged variant is limited to the replayed and tested
  * form: one staged call of a plan per captured graph, and at most as many
