@@ -87,7 +87,7 @@ class CallOrder {
   // Order a call after its chain's previous one.
   int enter(const Call& c) {
     const Chain* chain = find(c);
-    if (!chain || !chain->begun || chain->stream == c.s) return AGMM_OK;
+    if (!chain || !chain->begun || same_stream(*chain, c)) return AGMM_OK;
     if (!chain->stream) {
       const int rc = on_device([](CallOrder* o) { return hipEventRecord(o->eager_.event, nullptr); }, "hipEventRecord(done)");
       if (rc != AGMM_OK) return rc;
@@ -134,6 +134,15 @@ class CallOrder {
     bool begun = false;
     unsigned long long capture = 0;
   };
+
+  // Whether the chain's last call is on the call's very stream, which orders the
+  // two by itself.  Equal handles do not say so: a stream's handle is given to
+  // another after its end, while its work may still run, and
+  // hipStreamPerThread is a stream of each host thread.  The default stream
+  // does not end, nor does a stream during its capture.
+  static bool same_stream(const Chain& chain, const Call& c) {
+    return chain.stream == c.s && (c.capturing ? c.s != hipStreamPerThread : !c.s);
+  }
 
   // The chain a call belongs to, or NULL for the first call of a capture.
   Chain* find(const Call& c) {

@@ -238,8 +238,20 @@ void check(int kind) {
   // the default stream, before and after others
   const std::vector<int> e4 = p.call(nullptr);
   expect(after(e4, e3), says("the default stream after another"));
-  const std::vector<int> e5 = p.call(&s[3]);
+  std::vector<int> e5 = p.call(&s[3]);
   expect(after(e5, e4), says("another stream after the default one"));
+
+  // handles that do not name one stream: a thread's own default stream, and a
+  // handle that a new stream got after the old one's end
+  const std::vector<int> t0 = p.call(hipStreamPerThread);
+  thread_now = 1;
+  const std::vector<int> t1 = p.call(hipStreamPerThread);
+  thread_now = 0;
+  expect(after(t1, t0), says("the default streams of two threads"));
+  const std::vector<int> old = p.call(&s[0]);
+  s[0] = ihipStream_t{};
+  e5 = p.call(&s[0]);
+  expect(after(e5, old), says("a stream with the handle of one that ended"));
 
   // a plan's end waits for its last eager call, also where one was captured after it
   d1 = ihipStream_t{};
