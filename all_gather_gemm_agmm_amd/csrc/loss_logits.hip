@@ -15,7 +15,7 @@
 //    both gradients; the sums are fp32.  d is scaled by 1 / S, S the rows'
 //    largest weight (loss_rows).  bf16 has the range of fp32.  fp16 has
 //    not: each row of d is scaled by a further power of two (exact) that brings
-//    its weight near 1, and by 2^14, which keeps a probability of 2^-28 a
+//    its weight near 1, and by 2^14, which keeps a probability of 2^-27 a
 //    normal number; dA's rows are scaled back in fp32, and the copy of A that
 //    dW's product reads carries each row's power of two (loss_scale_rows_kernel).
 //
@@ -475,8 +475,10 @@ __device__ __forceinline__ float power_below(float x) {
 // |a| <= 2 S: where all rows weigh the same (a mean over tokens) the label's
 // entry of d is exactly -1 plus its probability, instead of every row being
 // off by the rounding of one and the same weight.  bf16: s_i = S.  fp16: S
-// times the power of two, at most 1, that brings the larger of |a_i| and |b_i|
-// near 1.  One workgroup: the maxima are over all rows.
+// times the power of two, at most 1, that brings |a_i| + |b_i|, which bounds
+// |d|, near 1: (|a_i| + |b_i|) / s_i is below 2, or, where s_i = S, at most 3,
+// so that 2^14 d / s_i stays below 49152 (the type ends at 65504) whatever the
+// signs of a and b.  One workgroup: the maxima are over all rows.
 template <int DT>
 __device__ __forceinline__ void loss_rows(const LossRows& c) {
   __shared__ float top[2][16];
@@ -508,7 +510,7 @@ __device__ __forceinline__ void loss_rows(const LossRows& c) {
     row_weights(c, row, a, b);
     float s = all;
     if constexpr (DT == kDtypeFp16) {
-      const float part = fmaxf(finite_size(a), finite_size(b)) / all;
+      const float part = finite_size(a) / all + finite_size(b) / all;
       if (part > 0.0f) s = all * fminf(fmaxf(power_below(fmaxf(part, kLow)), kLow / all), 1.0f);
     }
     *reinterpret_cast<f32x4_t*>(c.rows + 4 * row) = f32x4_t{c.lse[row], a, b, s};
