@@ -332,8 +332,8 @@ struct agmm_loss_plan : PlanBase {
     int fm = 0, fn = 0;                  // blocks of 16 fm x 16 fn
     int ranges = 1;                      // k ranges of the dA product
     int64_t per_range = 0;
-    // a: gathered or padded copy of A; as: fp16, its rows scaled for dW's product
-    char *a = nullptr, *as = nullptr, *w = nullptr, *d = nullptr, *dt = nullptr;
+    // a, w: gathered or padded copies of A and of a piece of W
+    char *a = nullptr, *w = nullptr, *d = nullptr, *dt = nullptr;
     float *stats = nullptr, *running = nullptr, *rows = nullptr, *scale_all = nullptr, *sums = nullptr;
     size_t bytes = 0;
   };
@@ -401,9 +401,7 @@ struct agmm_loss_plan : PlanBase {
       L.stats = reinterpret_cast<float*>(c.take((size_t)(cdiv(L.piece, stat_cols(L)) + 1) * m * 8));
       L.running = reinterpret_cast<float*>(c.take((size_t)m * 8));
     } else {
-      const bool half = dtype == AGMM_FP16;
-      if (L.pad_a || (N > 1 && !half)) L.a = c.take((size_t)m * L.kp * 2);
-      if (half) L.as = c.take((size_t)m * L.kp * 2);
+      if (L.pad_a || N > 1) L.a = c.take((size_t)m * L.kp * 2);   // dW's product reads it k x n, in one piece
       L.rows = reinterpret_cast<float*>(c.take((size_t)m * 16));
       L.scale_all = reinterpret_cast<float*>(c.take(4));
       L.d = c.take((size_t)m * round_up(L.piece, 8) * 2);
@@ -584,19 +582,6 @@ struct agmm_loss_plan : PlanBase {
     if (L.a) copy = copy_of(L, shards, N, m_s, ld_a(), L.a);
     hipError_t err = agmm::launch_loss_prepare(&lr, L.a ? &copy : nullptr, dtype, s);
     if (err != hipSuccess) return hip_err(err, "loss rows launch");
-    if (L.as && dW) {
-      agmm::LossScaleRows r{};
-      for (int g = 0; g < rows.num_groups; ++g) r.group[g] = rows.a_group[g];
-      r.rows_per_group = rows.rows_per_group;
-      r.ld = rows.a_ld;
-      r.m = m;
-      r.chunks = L.kp / 8;
-      r.rows = L.rows;
-      r.scale_all = L.scale_all;
-      r.out = L.as;
-      err = agmm::launch_loss_scale_rows(r, s);
-      if (err != hipSuccess) return hip_err(err, "row scaling launch");
-    }
     for (int64_t v0 = 0; v0 < n; v0 += L.piece) {
       const int64_t vn = std::min(L.piece, n - v0);
       const void* w;
@@ -605,6 +590,7 @@ struct agmm_loss_plan : PlanBase {
       if (rc != AGMM_OK) return rc;
       agmm::LossProblem p = logits(L, rows, w, ldb, v0, vn, labels);
       p.rows = L.rows;
+      p.scale_all = L.scale_all;
       p.d = dA ? L.d : nullptr;
       p.ldd = round_up(vn, 8);
       p.dt = dW ? L.dt : nullptr;
@@ -628,8 +614,8 @@ struct agmm_loss_plan : PlanBase {
       gw.m = (int32_t)vn;
       gw.n = (int32_t)k;
       gw.k = (int32_t)m;
-      gw.b = L.as ? L.as : L.a ? L.a : shards[0];
-      gw.ldb = L.as || L.a ? L.kp : ld_a();
+      gw.b = L.a ? L.a : shards[0];
+      gw.ldb = L.a ? L.kp : ld_a();
       gw.splits = 1;
       gw.k_per_split = (int32_t)round_up(m, 64);
       gw.ldc = lddw ? lddw : k;

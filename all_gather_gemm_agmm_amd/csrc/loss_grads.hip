@@ -2,7 +2,7 @@
 // d[i, v] that loss_grad_kernel leaves:
 //
 //     dA[i, :] = s_i * sum_v d[i, v] * W[v, :]         (rows of d, W k x n as stored)
-//     dW[v, :] = S   * sum_i dt[v, i] * A[i, :]        (d transposed, A k x n as gathered)
+//     dW[v, :] = S   * sum_i dt[v, i] * A[i, :]        (d transposed, all over S; A k x n as gathered)
 //
 // Both are the part-ring GEMM (gemm_m16_loop.inc) with B stored k x n, and
 // share a launch: with few rows neither fills the CUs alone.  dA is summed

@@ -16,8 +16,12 @@
 //    largest weight (loss_rows).  bf16 has the range of fp32.  fp16 has
 //    not: each row of d is scaled by a further power of two (exact) that brings
 //    its weight near 1, and by 2^14, which keeps a probability of 2^-27 a
-//    normal number; dA's rows are scaled back in fp32, and the copy of A that
-//    dW's product reads carries each row's power of two (loss_scale_rows_kernel).
+//    normal number; dA's rows are scaled back in fp32.  dW sums over rows, so
+//    its operand d^T has one scale, 2^14 / S: row i times s_i / S, a power of
+//    two of at least 2^-24, as it leaves the tile.  What that takes from a small
+//    row is at most S 2^-38 of a d, where dW's own steps are 2^-24 or more.  (A
+//    copy of A that carried the rows' powers instead lost rows of weight 2^-20
+//    to 2%, of 2^-27 wholly.)
 //
 // Bound: MFMA; with few rows HBM on W.  The exponentials cost 256 (256 x 256
 // tile) per lane once per tile, 3-5% beside the k loop of a 4096-deep product.
@@ -129,12 +133,18 @@ __device__ __forceinline__ void loss_body(const LossProblem& lp, char* smem) {
     }
     __syncthreads();   // the LDS now holds d: chunk c (8 columns) of tile row r at c ^ (r mod 16)
     constexpr int RB = BN * 2, CH = RB / 16;
+    // fp16: behind d, the rows' powers of two s_i / S
+    constexpr bool kRowPowers = DT == kDtypeFp16;
+    static_assert(BM * RB + BM * 2 <= T::LDS_BYTES, "d and the rows' powers of two");
+    _Float16* const power = reinterpret_cast<_Float16*>(smem + BM * RB);
+    const float all = kRowPowers ? lp.scale_all[0] : 1.0f;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int r = wm * T::TM + 16 * i + i16;
       const bool in = m0 + r < M;
       const float f = (DT == kDtypeFp16 ? 16384.0f : 1.0f) / rv[i][3];
       const float lse = rv[i][0], a = rv[i][1] * f, b = rv[i][2] * f;
+      if (kRowPowers && wn == 0 && g4 == 0) power[r] = (_Float16)(rv[i][3] / all);
       const bool hit = __any(at[i] >= 0);
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
@@ -183,6 +193,13 @@ __device__ __forceinline__ void loss_body(const LossProblem& lp, char* smem) {
         for (int h = 0; h < 2; ++h) {
           const int r = mb + 4 * h + (i16 >> 2), c = nb + 4 * (i16 & 3);
           half[h] = read_tr(smem + r * RB + (((c >> 3) ^ (r & 15)) << 4) + (c & 4) * 2);
+        }
+        if constexpr (kRowPowers) {
+          const f16x8_t f = *reinterpret_cast<const f16x8_t*>(power + mb);   // of rows mb .. mb + 7
+          const f16x8_t v = __builtin_bit_cast(f16x8_t, u32x4_t{half[0][0], half[0][1], half[1][0], half[1][1]}) * f;
+          const u32x4_t w = __builtin_bit_cast(u32x4_t, v);
+          half[0] = u32x2_t{w[0], w[1]};
+          half[1] = u32x2_t{w[2], w[3]};
         }
         if (n0 + nb + i16 < N && m0 + mb < lp.ldt)
           *reinterpret_cast<u32x4_t*>(out + (int64_t)(nb + i16) * lp.ldt + mb) =
@@ -368,6 +385,7 @@ __global__ __launch_bounds__(256) void loss_few_kernel(LossProblem lp) {
     const f32x4_t rv = *reinterpret_cast<const f32x4_t*>(lp.rows + 4 * (int64_t)min(row, M - 1));
     const float f = (DT == kDtypeFp16 ? 16384.0f : 1.0f) / rv[3];
     const float wa = rv[1] * f, wb = rv[2] * f;
+    const float power = DT == kDtypeFp16 ? rv[3] / lp.scale_all[0] : 1.0f;   // d^T's scale is one for all rows
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       float v[4];
@@ -385,7 +403,8 @@ __global__ __launch_bounds__(256) void loss_few_kernel(LossProblem lp) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (col + 16 * j + e < N)
-            static_cast<uint16_t*>(lp.dt)[(int64_t)(col + 16 * j + e) * lp.ldt + row] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            static_cast<uint16_t*>(lp.dt)[(int64_t)(col + 16 * j + e) * lp.ldt + row] =
+                DT == kDtypeFp16 ? cvt1<DT>(v[e] * power) : (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
     }
   }
 }
@@ -499,7 +518,8 @@ __device__ __forceinline__ void loss_rows(const LossRows& c) {
 #pragma unroll
   for (int q = 0; q < 2; ++q)
     for (int w = 0; w < 16; ++w) most[q] = fmaxf(most[q], top[q][w]);
-  constexpr float kLow = 7.888609052210118e-31f, kHigh = 1.2676506002282294e30f;   // 2^-100, 2^100: inverses are normal
+  // 2^-100 (fp16, whose s_i may be 2^-24 S: 2^-60) and 2^100: 2^14 over any s_i is normal
+  constexpr float kLow = DT == kDtypeFp16 ? 8.673617379884035e-19f : 7.888609052210118e-31f, kHigh = 1.2676506002282294e30f;
   float all = most[1] > 0.0f ? most[1] : most[0] > 0.0f ? most[0] : 1.0f;
   all = fminf(fmaxf(all, kLow), kHigh);
   const float over = most[0] / all;
@@ -511,7 +531,7 @@ __device__ __forceinline__ void loss_rows(const LossRows& c) {
     float s = all;
     if constexpr (DT == kDtypeFp16) {
       const float part = finite_size(a) / all + finite_size(b) / all;
-      if (part > 0.0f) s = all * fminf(fmaxf(power_below(fmaxf(part, kLow)), kLow / all), 1.0f);
+      if (part > 0.0f) s = all * fminf(fmaxf(power_below(part), 5.9604644775390625e-08f), 1.0f);   // 2^-24: a power of two in fp16
     }
     *reinterpret_cast<f32x4_t*>(c.rows + 4 * row) = f32x4_t{c.lse[row], a, b, s};
   }
@@ -546,26 +566,6 @@ template <int DT, bool ROWS>
 __global__ __launch_bounds__(1024) void loss_prepare_kernel(LossRows r, PadRows c) {
   if (ROWS && blockIdx.x == 0) loss_rows<DT>(r);
   else pad_rows(c, (int64_t)blockIdx.x - (ROWS ? 1 : 0));
-}
-
-// The fp16 copy of A that dW's product reads: row i times s_i / S, a power of
-// two of at most 1.  16 bytes per thread.
-__global__ __launch_bounds__(256) void loss_scale_rows_kernel(LossScaleRows c) {
-  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = u / c.chunks;
-  if (row >= c.m) return;
-  const int64_t at = row * c.chunks * 8 + (u - row * c.chunks) * 8;
-  const int64_t g = row / c.rows_per_group;
-  const uint16_t* src = static_cast<const uint16_t*>(c.group[g]) + (row - g * c.rows_per_group) * c.ld + (u - row * c.chunks) * 8;
-  u32x4_t v = *reinterpret_cast<const u32x4_t*>(src);
-  const float f = c.rows[4 * row + 3] / c.scale_all[0];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t w = v[e];
-    v[e] = pack2<kDtypeFp16>((float)__builtin_bit_cast(_Float16, (uint16_t)w) * f,
-                             (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16)) * f);
-  }
-  *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(c.out) + at) = v;
 }
 
 template <int DT>
@@ -646,13 +646,6 @@ hipError_t launch_loss_prepare(const LossRows* r, const PadRows* c, int dtype, h
     hipLaunchKernelGGL((loss_prepare_kernel<kDtypeBf16, true>), dim3((unsigned)grid), dim3(1024), 0, stream, *r, c ? *c : none);
   else
     hipLaunchKernelGGL((loss_prepare_kernel<kDtypeFp16, true>), dim3((unsigned)grid), dim3(1024), 0, stream, *r, c ? *c : none);
-  return hipGetLastError();
-}
-
-hipError_t launch_loss_scale_rows(const LossScaleRows& c, hipStream_t stream) {
-  const int64_t blocks = (c.m * c.chunks + 255) / 256;
-  if (blocks < 1 || blocks >= (int64_t(1) << 24) || c.ld % 8 != 0) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(loss_scale_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, c);
   return hipGetLastError();
 }
 

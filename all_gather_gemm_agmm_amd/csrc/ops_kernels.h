@@ -103,10 +103,12 @@ struct LossProblem {
   // statistics: (maximum, sum of exp) pairs [2 * column block + half][m]
   float* stats;
   float* target;           // [m], written where the piece holds the label
-  // gradient: rows {lse, a, b, s} [m]; d [m][ldd] and dt [n][ldt] (either
-  // may be null), the columns past n (m) up to ldd (ldt) as zeros; both
-  // strides are multiples of 8
+  // gradient: rows {lse, a, b, s} [m] and scale_all (see LossRows); d [m][ldd],
+  // row i over s_i, and dt [n][ldt], all over scale_all (either may be null),
+  // the columns past n (m) up to ldd (ldt) as zeros; both strides are
+  // multiples of 8
   const float* rows;
+  const float* scale_all;
   void* d;
   int64_t ldd;
   void* dt;
@@ -149,16 +151,6 @@ struct PadRows {
 };
 // One launch: the rows' weights (r, or null) and a copy (c, or null).
 hipError_t launch_loss_prepare(const LossRows* r, const PadRows* c, int dtype, hipStream_t stream);
-
-// out [m][8 * chunks] = fp16 rows of A times rows[i][3] / scale_all[0], powers of two of at most 1.
-struct LossScaleRows {
-  const void* group[kMaxGroups];
-  int64_t rows_per_group, ld, m, chunks;
-  const float* rows;
-  const float* scale_all;
-  void* out;
-};
-hipError_t launch_loss_scale_rows(const LossScaleRows& c, hipStream_t stream);
 
 // The two gradient products, B k x n, in one launch: fp32 sums of d W (A = d
 // [m][ldd]) into a->partials [splits][m][n rounded up to 4], added to what is there

@@ -543,9 +543,11 @@ void agmm_scaled_plan_destroy(agmm_scaled_plan_t plan);
  *
  * gl: gradient of loss (taken as 0 in ignored rows), gz: of lse (a z-loss
  * c lse^2 has 2 c lse; NULL: none).  d is rounded to the operands' type, as
- * their products need (scaled by powers of two so that fp16 keeps its small
- * values); sums, maxima and the exponentials are fp32; dA and dW are rounded
- * once.  dA is this device's part of the gathered rows' gradient [m, k], to be
+ * their products need; sums, maxima and the exponentials are fp32; dA and dW
+ * are rounded once.  In fp16 d is scaled so that its range ends where it does
+ * not show: with S the largest row weight (|gl|, |gl + gz|), an entry of d is
+ * off by 2^-12 of itself and, below that, for dA by at most 2^-37 of its row's
+ * weight or 2^-62 S, for dW by at most 2^-37 S.  dA is this device's part of the gathered rows' gradient [m, k], to be
  * reduce-scattered over the devices.
  * A label that is neither ignore_index nor in [0, vocab_size) gives a NaN loss
  * and NaN gradients.  A row of logits with a NaN gives NaN.

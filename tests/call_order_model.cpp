@@ -131,7 +131,6 @@ hipError_t launch_loss_logits(const LossProblem&, int, bool, hipStream_t s) { re
 hipError_t launch_loss_few(const LossProblem&, int, int, int, bool, hipStream_t s) { return enqueue(s); }
 hipError_t launch_loss_combine(const LossCombine&, hipStream_t s) { return enqueue(s); }
 hipError_t launch_loss_prepare(const LossRows*, const PadRows*, int, hipStream_t s) { return enqueue(s); }
-hipError_t launch_loss_scale_rows(const LossScaleRows&, hipStream_t s) { return enqueue(s); }
 hipError_t launch_loss_grads(const GemmProblem*, bool, const GemmProblem*, const float*, int, int, hipStream_t s) { return enqueue(s); }
 hipError_t launch_loss_da_finish(const LossFinish&, int, hipStream_t s) { return enqueue(s); }
 }  // namespace agmm

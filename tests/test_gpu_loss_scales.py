@@ -44,3 +44,20 @@ def test_gradients_of_opposite_sign(gl, gz, largest, tile, shape):
     c.gl, c.gz = torch.full((c.m,), gl), torch.full((c.m,), gz)
     c.gl[1], c.gz[1] = largest, 0.0
     run_backward(c, tile)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("tile", [64, 128, 256])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 10])
+def test_small_weights_under_a_loss_scale(scale, tile, shape):
+    """Upstream gradients from 1e-8 to 1, zeros among them, times a loss scale
+    that makes the smallest rows' parts of dW ordinary numbers of the type.  The
+    rows are certain of one column each, so that no large row covers a small
+    one's column."""
+    c = Case(*shape, agmm.AGMM_FP16, seed=43, spread=40.0)
+    c.a, c.w = c.a * 2, c.w / 2          # neither gradient leaves the type's range
+    c.gl = scale * torch.pow(10.0, -8 * torch.rand(c.m, generator=torch.Generator().manual_seed(44)))
+    c.gl[0], c.gl[1], c.gl[5::8] = scale, scale * 1e-8, 0.0
+    c.gz = torch.zeros(c.m)
+    c.labels = torch.randperm(c.n, generator=torch.Generator().manual_seed(45)).repeat(3)[:c.m]
+    run_backward(c, tile)
