@@ -653,7 +653,9 @@ class ScaledPlan(_OpPlan):
     """C = concat_r(shards[r]) @ B^T for block-scaled 8-bit operands
     (agmm_scaled_run): shards are Scaled [m_per_shard, k] with block_rows 1 in
     `a_format`, B a Scaled [n_local, k] in e4m3 with `b_block_rows`, C of
-    `c_dtype` (AGMM_BF16, AGMM_FP16 or AGMM_FP32)."""
+    `c_dtype` (AGMM_BF16, AGMM_FP16 or AGMM_FP32).  Long products to 16 bits use
+    the 8-bit matrix instruction, whose sums cut small terms beside large ones;
+    `exact_sums=1` asks for fp32 sums instead, at about half the rate."""
 
     _prefix = "agmm_scaled_plan"
 

@@ -189,14 +189,20 @@ struct agmm_scaled_plan : PlanBase {
   int a_format = 0, b_block_rows = 0, c_dtype = 0;
   int64_t lda = 0, ldb = 0, ldc = 0;   // 0: dense
   int tile_key = -1, splits_key = 0;
+  bool exact = false;
   int tile = 0, splits = 1, kb_per_split = 0, group_m = 1;
   bool deep = false;
 
-  // Sums of 128 by bf16 MFMAs.  The 8-bit ones lose up to about 3700 units of
-  // 2^-24 of a block's sum of sizes (scaled.hip): below the rounding of a
-  // 16-bit C, and below what fp32 additions over the whole of k may lose from
-  // k = 1024 on, so they are used there and where C is 16 bits.
-  bool wide() const { return c_dtype == AGMM_FP32 || k < 1024; }
+  // Sums of 128 by bf16 MFMAs, whose products and sums are those of fp32.  The
+  // 8-bit ones, twice as fast, cut each product to 2^-13 of the largest beside
+  // it (scaled.hip).  They are a choice for speed, taken where C is 16 bits and
+  // k long: on normally distributed operands the cut is 2^-15 of a block's sum
+  // of sizes (rms), where the operands' own rounding to 8 bits moves every
+  // product by up to 2^-3 of itself; but a block with one large product among
+  // many small ones may lose up to 2^-10 of its sum of sizes, and one whose
+  // large product cancels may be wrong in all its digits.  "exact_sums" is for
+  // callers who need the other.
+  bool wide() const { return exact || c_dtype == AGMM_FP32 || k < 1024; }
 
   int64_t kb() const { return cdiv(k, agmm::kScaleBlock); }
 
@@ -265,7 +271,17 @@ struct agmm_scaled_plan : PlanBase {
 
   size_t need(int sp) const { return sp > 1 ? (size_t)sp * m * part_ld() * sizeof(float) : 0; }
 
-  int apply(int tile_k, int splits_k) {
+  int apply(int tile_k, int splits_k, bool exact_sums) {
+    if (exact_sums && tile_k == agmm::kScaled256)
+      return set_err(AGMM_ERR_UNSUPPORTED, "tile 0 sums on the 8-bit matrix instruction: not with exact_sums");
+    const bool was = exact;
+    exact = exact_sums;   // wide() goes by it
+    const int rc = apply_tiles(tile_k, splits_k);
+    if (rc != AGMM_OK) exact = was;
+    return rc;
+  }
+
+  int apply_tiles(int tile_k, int splits_k) {
     int t, sp, per;
     derive(tile_k, splits_k, t, sp, per);
     if (cdiv(m, agmm::scaled_tile_rows(t)) * cdiv(n, agmm::scaled_tile_cols(t)) * sp >= kMaxGrid)
@@ -715,7 +731,7 @@ agmm_scaled_plan_t agmm_scaled_plan_create(int num_shards, int64_t m_per_shard, 
   p->a_format = a_format;
   p->b_block_rows = b_block_rows;
   p->c_dtype = c_dtype;
-  if (p->init() != AGMM_OK || p->apply(-1, 0) != AGMM_OK) {
+  if (p->init() != AGMM_OK || p->apply(-1, 0, false) != AGMM_OK) {
     const int st = agmm::g_status;
     const std::string msg = agmm::g_msg;
     delete p;
@@ -738,11 +754,15 @@ int agmm_scaled_plan_set_int(agmm_scaled_plan_t p, const char* key, int64_t v) {
   };
   if (k == "tile") {
     if (v < -1 || v > 3) return bad();
-    return p->apply((int)v, p->splits_key);
+    return p->apply((int)v, p->splits_key, p->exact);
   }
   if (k == "splits") {
     if (v < 0 || v > 4096) return bad();
-    return p->apply(p->tile_key, (int)v);
+    return p->apply(p->tile_key, (int)v, p->exact);
+  }
+  if (k == "exact_sums") {
+    if (v != 0 && v != 1) return bad();
+    return p->apply(p->tile_key, p->splits_key, v == 1);
   }
   if (k == "lda" || k == "ldb" || k == "ldc") {
     const int64_t row = k == "ldc" ? p->n : p->k16;
@@ -760,6 +780,7 @@ int agmm_scaled_plan_get_int(agmm_scaled_plan_t p, const char* key, int64_t* val
   const std::string k(key);
   if (k == "tile") *value = p->tile == agmm::kScaledSkinny16n ? 2 : p->tile == agmm::kScaledSkinny64 ? 3 : p->tile;
   else if (k == "splits") *value = p->splits;
+  else if (k == "exact_sums") *value = p->exact;
   else if (k == "lda") *value = p->lda ? p->lda : p->k16;
   else if (k == "ldb") *value = p->ldb ? p->ldb : p->k16;
   else if (k == "ldc") *value = p->ldc ? p->ldc : p->n;
