@@ -169,6 +169,103 @@ __device__ __forceinline__ void store4(const ScaledProblem& p, int row, int col,
   else put(IntTag<kDtypeFp16>{});
 }
 
+// One element to C.
+__device__ __forceinline__ void store1(const ScaledProblem& p, int row, int col, float v) {
+  const int64_t at = (int64_t)row * p.ldc + col;
+  if (p.c_dtype == kDtypeFp32) static_cast<float*>(p.c)[at] = v;
+  else static_cast<uint16_t*>(p.c)[at] = p.c_dtype == kDtypeBf16 ? cvt1<kDtypeBf16>(v) : cvt1<kDtypeFp16>(v);
+}
+
+// ---- products of two scales beyond fp32 ---------------------------------------
+// The kernels form sa * sb in fp32 (one operation less per element than scaling
+// the sums twice).  Where that overflows, a block's contribution becomes
+// infinite, or NaN if its sum is 0, although sa * sb * sum may be a finite number
+// or 0.  No such result is finite, so a lane whose results all are has nothing
+// to do; one that holds another looks whether scales were the cause, and
+// computes those elements anew from the operands, in 64 bits.
+
+// `t` if v is four finite numbers, else NaN.
+__device__ __forceinline__ float finite_or_nan(f32x4_t v, float t) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) t = __builtin_fmaf(v[e], 0.0f, t);
+  return t;
+}
+
+__device__ __forceinline__ bool overflows(float a, float b) {
+  const float inf = __builtin_inff();
+  return __builtin_fabsf(a) < inf && __builtin_fabsf(b) < inf && !(__builtin_fabsf(a * b) < inf);
+}
+
+// The scales of row `row` (column `col`), one every `step` k blocks.
+__device__ __forceinline__ const float* row_scales(const ScaledProblem& p, int row, int64_t& step) {
+  const int g = p.by_rows.quotient(row);
+  step = p.rows_per_group;
+  return p.a_scale[g] + (row - g * p.rows_per_group);
+}
+__device__ __forceinline__ const float* col_scales(const ScaledProblem& p, int col, int64_t& step) {
+  step = p.nb;
+  return p.b_scale + (p.b_block_rows == 1 ? col : col >> 7);
+}
+
+// The largest finite |scale| of k blocks [b0, b1).
+__device__ __forceinline__ float largest(const float* s, int64_t step, int b0, int b1) {
+  float top = 0.0f;
+#pragma unroll 8
+  for (int b = b0; b < b1; ++b) {
+    const float v = __builtin_fabsf(s[b * step]);
+    top = v < __builtin_inff() ? fmaxf(top, v) : top;
+  }
+  return top;
+}
+
+template <int FMT>
+__device__ __forceinline__ void four_values(uint32_t w, float (&v)[4]) {
+  if constexpr (FMT == kFmtE4M3) {
+    v[0] = __builtin_amdgcn_cvt_f32_fp8(w, 0);
+    v[1] = __builtin_amdgcn_cvt_f32_fp8(w, 1);
+    v[2] = __builtin_amdgcn_cvt_f32_fp8(w, 2);
+    v[3] = __builtin_amdgcn_cvt_f32_fp8(w, 3);
+  } else {
+    v[0] = __builtin_amdgcn_cvt_f32_bf8(w, 0);
+    v[1] = __builtin_amdgcn_cvt_f32_bf8(w, 1);
+    v[2] = __builtin_amdgcn_cvt_f32_bf8(w, 2);
+    v[3] = __builtin_amdgcn_cvt_f32_bf8(w, 3);
+  }
+}
+
+// Element (row, col) over k blocks [b0, b1) in 64 bits, into `value`, if a
+// product of its scales overflows; else false.
+template <int FMTA>
+__device__ __forceinline__ bool recompute(const ScaledProblem& p, int row, int col, int b0, int b1, float& value) {
+  int64_t sa_step, sb_step;
+  const float* sa = row_scales(p, row, sa_step);
+  const float* sb = col_scales(p, col, sb_step);
+  bool over = false;
+#pragma unroll 8
+  for (int b = b0; b < b1; ++b) over |= overflows(sa[b * sa_step], sb[b * sb_step]);
+  if (!over) return false;
+  const int g = p.by_rows.quotient(row);
+  const char* qa = static_cast<const char*>(p.a_group[g]) + (int64_t)(row - g * p.rows_per_group) * p.a_ld;
+  const char* qb = static_cast<const char*>(p.b) + (int64_t)col * p.ldb;
+  double sum = 0.0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    double part = 0.0;
+    const int end = min(p.k16, b * 128 + 128);
+#pragma unroll 1
+    for (int k = b * 128; k < end; k += 4) {
+      float x[4], y[4];
+      four_values<FMTA>(*reinterpret_cast<const uint32_t*>(qa + k), x);
+      four_values<kFmtE4M3>(*reinterpret_cast<const uint32_t*>(qb + k), y);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part += (double)x[e] * (double)y[e];
+    }
+    sum += (double)sa[b * sa_step] * (double)sb[b * sb_step] * part;
+  }
+  value = (float)sum;
+  return true;
+}
+
 // Tile and k range of a workgroup: k ranges outermost; of a range, XCD x
 // (workgroup id mod 8) takes consecutive tiles, in groups of group_m row
 // blocks walked column by column.
@@ -344,7 +441,7 @@ void scaled_gemm_kernel(ScaledProblem p) {
     auto add = [&](int i, int j, float f) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        acc[i][j][e] += f * (BROW ? part[j][e] * sb[BROW ? j : 0][e] : part[j][e]);
+        acc[i][j][e] += (BROW ? f * sb[BROW ? j : 0][e] : f) * part[j][e];
     };
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
@@ -477,6 +574,32 @@ void scaled_gemm_kernel(ScaledProblem p) {
   if (split_k || p.c_dtype == kDtypeFp32) store(IntTag<kDtypeFp32>{});
   else if (p.c_dtype == kDtypeBf16) store(IntTag<kDtypeBf16>{});
   else store(IntTag<kDtypeFp16>{});
+
+  float all = 0.0f;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) all = finite_or_nan(acc[i][j], all);
+  if (all == 0.0f) return;
+  float top_a = 0.0f, top_b = 0.0f;
+  int64_t step;
+#pragma unroll 1
+  for (int i = 0; i < FM; ++i)
+    if (row0 + 16 * i < p.m) top_a = fmaxf(top_a, largest(row_scales(p, row0 + 16 * i, step), step, t0, t0 + nk));
+#pragma unroll 1
+  for (int c = 0; c < FN * 4; ++c) {
+    const int col = col0 + 16 * (c >> 2) + (c & 3);
+    if (col < p.n) top_b = fmaxf(top_b, largest(col_scales(p, col, step), step, t0, t0 + nk));
+  }
+  if (!overflows(top_a, top_b)) return;
+#pragma unroll 1
+  for (int u = 0; u < FM * FN * 4; ++u) {
+    const int row = row0 + 16 * (u / (FN * 4)), col = col0 + 16 * (u / 4 % FN) + u % 4;
+    float v;
+    if (row >= p.m || col >= p.n || !recompute<FMTA>(p, row, col, t0, t0 + nk, v)) continue;
+    if (split_k) p.partials[((int64_t)split * p.m + row) * p.part_ld + col] = v;
+    else store1(p, row, col, v);
+  }
 }
 
 // Few rows: ROWS x COLS outputs per workgroup, over all of k or one of
@@ -638,6 +761,7 @@ void scaled_skinny_kernel(ScaledProblem p) {
     for (int f = 0; f < FN; ++f)
       *reinterpret_cast<f32x4_t*>(red + (16 * i + i16) * RLD + 16 * f + 4 * g4) = acc[i][f];
   __syncthreads();
+  float all = 0.0f;
   for (int e4 = tid; e4 < ROWS * COLS / 4; e4 += 64 * WAVES) {
     const int r = e4 / (COLS / 4), c = (e4 % (COLS / 4)) * 4;
     f32x4_t v = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(smem) + r * RLD + c);
@@ -646,11 +770,21 @@ void scaled_skinny_kernel(ScaledProblem p) {
       v += *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(smem + w * WAVE_LDS) + r * RLD + c);
     const int row = row0 + r, col = n0 + c;
     if (row >= p.m || col >= p.n) continue;
+    all = finite_or_nan(v, all);
     if (p.splits > 1) {
       *reinterpret_cast<f32x4_t*>(p.partials + ((int64_t)split * p.m + row) * p.part_ld + col) = v;
     } else {
       store4(p, row, col, v);
     }
+  }
+  if (all == 0.0f) return;
+#pragma unroll 1
+  for (int e = 4 * tid; e < ROWS * COLS; e += e % 4 == 3 ? 256 * WAVES - 3 : 1) {
+    const int row = row0 + e / COLS, col = n0 + e % COLS;
+    float v;
+    if (row >= p.m || col >= p.n || !recompute<FMTA>(p, row, col, t0, t1, v)) continue;
+    if (p.splits > 1) p.partials[((int64_t)split * p.m + row) * p.part_ld + col] = v;
+    else store1(p, row, col, v);
   }
 }
 

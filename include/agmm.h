@@ -465,6 +465,9 @@ int agmm_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t 
  * 2^-15; where large terms cancel that may be all of the result.  Otherwise,
  * with "exact_sums" set, and in the tiles 2 and 3, they are fp32 sums of exact
  * products.
+ * Scales may be any fp32 numbers.  The product of two scales is formed in fp32;
+ * an element with one beyond its range is computed anew in 64 bits (slowly),
+ * and one below 2^-126 takes at most 2^-124 from its block's contribution.
  * A linear layer y = x W^T trains with three such products: y from x and W;
  * dx from dy and W transposed (the weight's blocks are square, so W and its
  * transpose hold the same values); dW from dy transposed and x transposed,
