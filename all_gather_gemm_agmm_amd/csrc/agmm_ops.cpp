@@ -406,6 +406,10 @@ struct agmm_loss_plan : PlanBase {
     int64_t piece = piece_key;
     if (!piece) piece = grad ? budget / (4 * m8()) : budget / (m * 8) * 64;
     if (!piece_key && L.pad_w) piece = std::min(piece, budget / (2 * L.kp));
+    if (!piece_key && grad) {   // and no more than a launch of the gradient products holds by its smaller tile
+      const int64_t a_tiles = std::max<int64_t>(cdiv(m, 128) * cdiv(k, 128), 4 * cu_count);
+      piece = std::min(piece, (agmm::kLossGrid - 1 - a_tiles) / cdiv(k, 128) * 128);
+    }
     piece = std::max<int64_t>(256, piece / 256 * 256);
     L.piece = std::min(piece, n);
     pick_tile(L, !grad && L.pad_w);
@@ -449,9 +453,25 @@ struct agmm_loss_plan : PlanBase {
     return L;
   }
 
+  // Whether the launches over a piece stay within kLossGrid: automatic pieces
+  // do, one that the caller set may not.
+  bool fits(const Layout& L, bool grad) const {
+    const int64_t rows = L.tile == 64 ? 16 * L.fm : L.tile, cols = L.tile == 64 ? 16 * L.fn : L.tile, t = L.tile_grads;
+    return cdiv(m, rows) * cdiv(L.piece, cols) < agmm::kLossGrid &&
+           (!grad || cdiv(k, t) * (cdiv(m, t) * L.ranges + cdiv(L.piece, t)) < agmm::kLossGrid);
+  }
+
   int apply() {
-    const size_t fwd = layout(false, nullptr).bytes;
-    return reserve(with_gradient ? std::max(fwd, layout(true, nullptr).bytes) : fwd);
+    size_t bytes = 0;
+    for (bool grad : {false, true}) {
+      if (grad && !with_gradient) continue;
+      const Layout L = layout(grad, nullptr);
+      if (!fits(L, grad))
+        return set_err(AGMM_ERR_UNSUPPORTED, "too many workgroups for pieces of %lld columns by tile %d", (long long)L.piece,
+                       L.tile);
+      bytes = std::max(bytes, L.bytes);
+    }
+    return reserve(bytes);
   }
 
   agmm::TileOrder tiles_of(int64_t rows, int64_t cols, int tile) const {

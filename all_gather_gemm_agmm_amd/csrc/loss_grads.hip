@@ -151,7 +151,7 @@ bool fits(const GemmProblem& p, int tile) {
   return (tile == 256 || tile == 128) && p.order.num_rb == (p.m + tile - 1) / tile &&
          p.order.num_cb == (p.n + tile - 1) / tile && p.splits >= 1 && p.k_per_split % 64 == 0 &&
          (int64_t)p.splits * p.k_per_split >= p.k && (int64_t)(p.splits - 1) * p.k_per_split < p.k &&
-         (int64_t)p.order.num_rb * p.order.num_cb * p.splits < (int64_t(1) << 24);
+         (int64_t)p.order.num_rb * p.order.num_cb * p.splits < kLossGrid;
 }
 
 }  // namespace
@@ -173,7 +173,7 @@ hipError_t launch_loss_grads(const GemmProblem* a, bool add, const GemmProblem* 
     grid += (int64_t)w->order.num_rb * w->order.num_cb;
   }
   gp.scale = scale;
-  if (grid >= (int64_t(1) << 24)) return hipErrorInvalidValue;
+  if (grid >= kLossGrid) return hipErrorInvalidValue;
   if (tile == 256) {
     if (dtype == kDtypeBf16) hipLaunchKernelGGL((loss_grads_kernel<256, 256, kDtypeBf16, 1>), dim3((unsigned)grid), dim3(256), 0, s, gp);
     else hipLaunchKernelGGL((loss_grads_kernel<256, 256, kDtypeFp16, 1>), dim3((unsigned)grid), dim3(256), 0, s, gp);

@@ -541,23 +541,24 @@ __device__ __forceinline__ void loss_rows(const LossRows& c) {
 // out[(g * rows + t) * chunks * 8 + c] = group[g][t * ld + c], zeros past cols.
 // A source row may start at any element (16-byte accesses to global memory
 // need no alignment); its last chunk is read element by element.
-__device__ __forceinline__ void pad_rows(const PadRows& c, int64_t block) {
-  const int64_t u = block * 1024 + threadIdx.x;
-  const int64_t row = u / (uint32_t)c.chunks;
-  const int ch = (int)(u - row * c.chunks);
-  const int64_t g = row / (uint32_t)c.rows;
-  if (g >= c.num_groups) return;
-  const uint16_t* src = static_cast<const uint16_t*>(c.group[g]) + (row - g * c.rows) * c.ld + ch * 8;
-  const int count = (int)c.cols - ch * 8;
-  u32x4_t v = {0u, 0u, 0u, 0u};
-  if (count >= 8) {
-    v = *reinterpret_cast<const u32x4_any_t*>(src);
-  } else {
+__device__ __forceinline__ void pad_rows(const PadRows& c, int64_t block, int64_t blocks) {
+  const int64_t chunks = c.num_groups * c.rows * c.chunks;
+  for (int64_t u = block * 1024 + threadIdx.x; u < chunks; u += blocks * 1024) {
+    const int64_t row = u / (uint32_t)c.chunks;
+    const int ch = (int)(u - row * c.chunks);
+    const int64_t g = row / (uint32_t)c.rows;
+    const uint16_t* src = static_cast<const uint16_t*>(c.group[g]) + (row - g * c.rows) * c.ld + ch * 8;
+    const int count = (int)c.cols - ch * 8;
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (count >= 8) {
+      v = *reinterpret_cast<const u32x4_any_t*>(src);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < count) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+      for (int e = 0; e < 8; ++e)
+        if (e < count) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+    }
+    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(c.out) + row * c.chunks * 8 + ch * 8) = v;
   }
-  *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(c.out) + row * c.chunks * 8 + ch * 8) = v;
 }
 
 // The rows' weights (workgroup 0, where asked for) and the copy of A (the
@@ -565,7 +566,7 @@ __device__ __forceinline__ void pad_rows(const PadRows& c, int64_t block) {
 template <int DT, bool ROWS>
 __global__ __launch_bounds__(1024) void loss_prepare_kernel(LossRows r, PadRows c) {
   if (ROWS && blockIdx.x == 0) loss_rows<DT>(r);
-  else pad_rows(c, (int64_t)blockIdx.x - (ROWS ? 1 : 0));
+  else pad_rows(c, (int64_t)blockIdx.x - (ROWS ? 1 : 0), (int64_t)gridDim.x - (ROWS ? 1 : 0));
 }
 
 template <int DT>
@@ -604,7 +605,7 @@ hipError_t launch_loss_logits(const LossProblem& p, int dtype, bool grad, hipStr
   const int t = p.tile;
   if ((t != 256 && t != 128) || p.gemm.order.num_rb != (p.gemm.m + t - 1) / t ||
       p.gemm.order.num_cb != (p.gemm.n + t - 1) / t ||
-      (int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb >= (int64_t(1) << 24) || p.gemm.k % 8 != 0)
+      (int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb >= kLossGrid || p.gemm.k % 8 != 0)
     return hipErrorInvalidValue;
   return dtype == kDtypeBf16 ? launch_body<kDtypeBf16>(p, grad, stream)
        : dtype == kDtypeFp16 ? launch_body<kDtypeFp16>(p, grad, stream) : hipErrorInvalidValue;
@@ -613,7 +614,7 @@ hipError_t launch_loss_logits(const LossProblem& p, int dtype, bool grad, hipStr
 hipError_t launch_loss_few(const LossProblem& p, int fm, int fn, int dtype, bool grad, hipStream_t stream) {
   const int64_t grid = (int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb;
   if ((fm != 1 && fm != 4) || (fn != 1 && fn != 4) || p.gemm.order.num_rb != (p.gemm.m + 16 * fm - 1) / (16 * fm) ||
-      p.gemm.order.num_cb != (p.gemm.n + 16 * fn - 1) / (16 * fn) || grid < 1 || grid >= (int64_t(1) << 24) ||
+      p.gemm.order.num_cb != (p.gemm.n + 16 * fn - 1) / (16 * fn) || grid < 1 || grid >= kLossGrid ||
       (dtype != kDtypeBf16 && dtype != kDtypeFp16) || (int64_t)p.gemm.rows.num_groups * p.gemm.rows.rows_per_group != p.gemm.m ||
       (grad && (p.ldd % 8 != 0 || p.ldt % 8 != 0)))
     return hipErrorInvalidValue;
@@ -628,16 +629,20 @@ hipError_t launch_loss_combine(const LossCombine& c, hipStream_t stream) {
   return hipGetLastError();
 }
 
+constexpr int64_t kCopyGroups = 1 << 14;
+
 hipError_t launch_loss_prepare(const LossRows* r, const PadRows* c, int dtype, hipStream_t stream) {
   int64_t copies = 0;
   if (c) {
     if (c->rows < 1 || c->rows > INT32_MAX || c->chunks < 1 || c->chunks > INT32_MAX || c->cols <= (c->chunks - 1) * 8 ||
         c->cols > c->chunks * 8 || c->num_groups < 1 || c->num_groups > kMaxGroups)
       return hipErrorInvalidValue;
+    // beyond 2^14 workgroups (256 MiB) each copies several pieces: any size fits a launch
     copies = (c->num_groups * c->rows * c->chunks + 1023) / 1024;
+    copies = copies < kCopyGroups ? copies : kCopyGroups;
   }
   const int64_t grid = copies + (r ? 1 : 0);
-  if (grid < 1 || grid >= (int64_t(1) << 22)) return hipErrorInvalidValue;
+  if (grid < 1) return hipErrorInvalidValue;
   const PadRows none{};
   const LossRows no_rows{};
   if (!r)

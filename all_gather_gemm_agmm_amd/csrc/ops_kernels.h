@@ -92,6 +92,9 @@ constexpr int scaled_tile_cols(int t) {
 }
 hipError_t launch_scaled(const ScaledProblem& p, int tile, hipStream_t stream);
 
+// Workgroups of one launch of the loss's products.
+constexpr int64_t kLossGrid = int64_t(1) << 24;
+
 // Vocabulary loss over one piece of the vocabulary: gemm describes the logits
 // of the piece (A rows through the row map, B the piece's rows of W, n x k;
 // rows of whole 16-byte vectors), label0 is the label of its column 0.

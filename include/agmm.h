@@ -612,6 +612,7 @@ int agmm_loss_backward(agmm_loss_plan_t plan, const void *const *shard_ptrs, con
  *                   of up to 64 x 64 whose waves share out k, for few rows (the gradient's two
  *                   products keep their automatic tiles)
  *   "ignore_index"  the label of rows without a loss (default -100)
+ * A piece whose launches would pass 2^24 workgroups is AGMM_ERR_UNSUPPORTED.
  * A change that needs more workspace reallocates it; the plan keeps its
  * previous settings when that fails.  Settings are fixed once a call was
  * captured into a graph.  get reads the values in use (of "tile" that of the

@@ -127,11 +127,20 @@ hipError_t launch_transpose16(const void*, int64_t, int64_t, int64_t, void*, hip
 hipError_t noalloc_scratch(void**) { return hipErrorInvalidSymbol; }
 hipError_t launch_quantize(const QuantProblem&, hipStream_t s) { return enqueue(s); }
 hipError_t launch_scaled(const ScaledProblem&, int, hipStream_t s) { return enqueue(s); }
-hipError_t launch_loss_logits(const LossProblem&, int, bool, hipStream_t s) { return enqueue(s); }
-hipError_t launch_loss_few(const LossProblem&, int, int, int, bool, hipStream_t s) { return enqueue(s); }
+// (the loss's products: with the limit on the workgroups of a launch)
+constexpr int64_t kGrid = int64_t(1) << 24;
+int64_t tiles(const GemmProblem& p) { return (int64_t)p.order.num_rb * p.order.num_cb; }
+hipError_t launch_loss_logits(const LossProblem& p, int, bool, hipStream_t s) {
+  return tiles(p.gemm) < kGrid ? enqueue(s) : hipErrorInvalidValue;
+}
+hipError_t launch_loss_few(const LossProblem& p, int, int, int, bool, hipStream_t s) {
+  return tiles(p.gemm) < kGrid ? enqueue(s) : hipErrorInvalidValue;
+}
 hipError_t launch_loss_combine(const LossCombine&, hipStream_t s) { return enqueue(s); }
 hipError_t launch_loss_prepare(const LossRows*, const PadRows*, int, hipStream_t s) { return enqueue(s); }
-hipError_t launch_loss_grads(const GemmProblem*, bool, const GemmProblem*, const float*, int, int, hipStream_t s) { return enqueue(s); }
+hipError_t launch_loss_grads(const GemmProblem* a, bool, const GemmProblem* w, const float*, int, int, hipStream_t s) {
+  return (a ? tiles(*a) * a->splits : 0) + (w ? tiles(*w) : 0) < kGrid ? enqueue(s) : hipErrorInvalidValue;
+}
 hipError_t launch_loss_da_finish(const LossFinish&, int, hipStream_t s) { return enqueue(s); }
 }  // namespace agmm
 
@@ -262,10 +271,40 @@ void check(int kind) {
   for (int o : e5) expect(!freed_early.count(o), says("freed while an eager call may run"));
 }
 
+// Pieces and tiles of the loss that a launch cannot hold are refused when they
+// are set; what was accepted runs.
+void check_pieces(int64_t m, int64_t k, int64_t n, int64_t tile, int64_t piece, bool gradient, bool accepted) {
+  const std::string what = "piece of " + std::to_string(piece) + " by tile " + std::to_string(tile) + (gradient ? ", gradient" : "");
+  agmm_loss_plan_t p = agmm_loss_plan_create(1, m, k, n, AGMM_BF16, 0, n, gradient);
+  expect(p && agmm_loss_plan_set_int(p, "tile", tile) == AGMM_OK, what + ": tile");
+  int64_t before = 0, after = 0;
+  agmm_loss_plan_get_int(p, "piece", &before);
+  const int rc = agmm_loss_plan_set_int(p, "piece", piece);
+  expect(rc == (accepted ? AGMM_OK : AGMM_ERR_UNSUPPORTED), what + ": status " + std::to_string(rc));
+  agmm_loss_plan_get_int(p, "piece", &after);
+  expect(accepted || after == before, what + ": the plan keeps its piece");
+  float* f = reinterpret_cast<float*>(memory);
+  int64_t* l = reinterpret_cast<int64_t*>(memory);
+  ihipStream_t s;
+  int run = agmm_loss_forward(p, shard_list, memory, l, f, f, f, &s);
+  if (run == AGMM_OK && gradient) run = agmm_loss_backward(p, shard_list, memory, l, f, f, f, memory, memory, &s);
+  expect(run == AGMM_OK, what + ": " + agmm_last_error());
+  agmm_loss_plan_destroy(p);
+}
+
 }  // namespace
 
-int main() {
-  for (int kind = 0; kind < 5; ++kind) check(kind);
+int main(int argc, char** argv) {
+  if (argc > 1) {
+    check_pieces(int64_t(1) << 19, 8, int64_t(1) << 20, 128, int64_t(1) << 20, false, false);   // 2^25 tiles
+    check_pieces(int64_t(1) << 19, 8, int64_t(1) << 20, 256, int64_t(1) << 20, false, true);    // 2^23
+    check_pieces(int64_t(1) << 19, 8, int64_t(1) << 20, 128, int64_t(1) << 18, false, true);
+    check_pieces(8, int64_t(1) << 16, int64_t(1) << 23, 128, int64_t(1) << 23, true, false);    // dW: 2^25 tiles
+    check_pieces(8, int64_t(1) << 16, int64_t(1) << 23, 128, int64_t(1) << 20, true, true);
+    check_pieces(16, 64, (int64_t(1) << 27) - 1, 64, (int64_t(1) << 30) - 1, false, true);
+  } else {
+    for (int kind = 0; kind < 5; ++kind) check(kind);
+  }
   if (!failures) std::printf("all in order\n");
   return failures != 0;
 }
