@@ -541,32 +541,40 @@ __device__ __forceinline__ void loss_rows(const LossRows& c) {
 // out[(g * rows + t) * chunks * 8 + c] = group[g][t * ld + c], zeros past cols.
 // A source row may start at any element (16-byte accesses to global memory
 // need no alignment); its last chunk is read element by element.
-__device__ __forceinline__ void pad_rows(const PadRows& c, int64_t block, int64_t blocks) {
-  const int64_t chunks = c.num_groups * c.rows * c.chunks;
-  for (int64_t u = block * 1024 + threadIdx.x; u < chunks; u += blocks * 1024) {
-    const int64_t row = u / (uint32_t)c.chunks;
-    const int ch = (int)(u - row * c.chunks);
-    const int64_t g = row / (uint32_t)c.rows;
-    const uint16_t* src = static_cast<const uint16_t*>(c.group[g]) + (row - g * c.rows) * c.ld + ch * 8;
-    const int count = (int)c.cols - ch * 8;
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if (count >= 8) {
-      v = *reinterpret_cast<const u32x4_any_t*>(src);
-    } else {
+__device__ __forceinline__ void pad_chunk(const PadRows& c, int64_t u) {
+  const int64_t row = u / (uint32_t)c.chunks;
+  const int ch = (int)(u - row * c.chunks);
+  const int64_t g = row / (uint32_t)c.rows;
+  if (g >= c.num_groups) return;
+  const uint16_t* src = static_cast<const uint16_t*>(c.group[g]) + (row - g * c.rows) * c.ld + ch * 8;
+  const int count = (int)c.cols - ch * 8;
+  u32x4_t v = {0u, 0u, 0u, 0u};
+  if (count >= 8) {
+    v = *reinterpret_cast<const u32x4_any_t*>(src);
+  } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < count) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
-    }
-    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(c.out) + row * c.chunks * 8 + ch * 8) = v;
+    for (int e = 0; e < 8; ++e)
+      if (e < count) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
   }
+  *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(c.out) + row * c.chunks * 8 + ch * 8) = v;
 }
 
 // The rows' weights (workgroup 0, where asked for) and the copy of A (the
-// others) in one launch.
-template <int DT, bool ROWS>
+// others) in one launch.  LONG: more chunks than a launch has threads, so each
+// takes several (the loop alone costs a small copy 0.3 us).
+template <int DT, bool ROWS, bool LONG>
 __global__ __launch_bounds__(1024) void loss_prepare_kernel(LossRows r, PadRows c) {
-  if (ROWS && blockIdx.x == 0) loss_rows<DT>(r);
-  else pad_rows(c, (int64_t)blockIdx.x - (ROWS ? 1 : 0), (int64_t)gridDim.x - (ROWS ? 1 : 0));
+  if (ROWS && blockIdx.x == 0) {
+    loss_rows<DT>(r);
+    return;
+  }
+  int64_t u = ((int64_t)blockIdx.x - (ROWS ? 1 : 0)) * 1024 + threadIdx.x;
+  if constexpr (LONG) {
+    const int64_t chunks = c.num_groups * c.rows * c.chunks, step = ((int64_t)gridDim.x - (ROWS ? 1 : 0)) * 1024;
+    for (; u < chunks; u += step) pad_chunk(c, u);
+  } else {
+    pad_chunk(c, u);
+  }
 }
 
 template <int DT>
@@ -645,12 +653,13 @@ hipError_t launch_loss_prepare(const LossRows* r, const PadRows* c, int dtype, h
   if (grid < 1) return hipErrorInvalidValue;
   const PadRows none{};
   const LossRows no_rows{};
-  if (!r)
-    hipLaunchKernelGGL((loss_prepare_kernel<kDtypeBf16, false>), dim3((unsigned)grid), dim3(1024), 0, stream, no_rows, *c);
-  else if (dtype == kDtypeBf16)
-    hipLaunchKernelGGL((loss_prepare_kernel<kDtypeBf16, true>), dim3((unsigned)grid), dim3(1024), 0, stream, *r, c ? *c : none);
-  else
-    hipLaunchKernelGGL((loss_prepare_kernel<kDtypeFp16, true>), dim3((unsigned)grid), dim3(1024), 0, stream, *r, c ? *c : none);
+  const auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(1024), 0, stream, r ? *r : no_rows, c ? *c : none);
+  };
+  const bool half = dtype == kDtypeFp16, more = copies == kCopyGroups;
+  if (!r) more ? go(loss_prepare_kernel<kDtypeBf16, false, true>) : go(loss_prepare_kernel<kDtypeBf16, false, false>);
+  else if (half) more ? go(loss_prepare_kernel<kDtypeFp16, true, true>) : go(loss_prepare_kernel<kDtypeFp16, true, false>);
+  else more ? go(loss_prepare_kernel<kDtypeBf16, true, true>) : go(loss_prepare_kernel<kDtypeBf16, true, false>);
   return hipGetLastError();
 }
 
