@@ -81,7 +81,6 @@ enum ScaledTile : int {
   kScaledSkinny32 = 3,     // 32 x 32
   kScaledSkinny16n = 4,    // 16 x 16, 8 waves
   kScaledSkinny64 = 5,     // 64 x 64
-  kScaledTiles = 6,
 };
 constexpr int scaled_tile_rows(int t) {
   return t == kScaled256 ? 256 : t == kScaled128 ? 128 : t == kScaledSkinny16 || t == kScaledSkinny16n ? 16

@@ -529,7 +529,6 @@ hipError_t launch(const QuantProblem& p, hipStream_t stream) {
 
 template <int DT>
 hipError_t launch_dt(const QuantProblem& p, hipStream_t s) {
-  constexpr int ES = DT == kDtypeFp32 ? 4 : 2;
   return p.format == kFmtE4M3 ? launch<DT, kFmtE4M3>(p, s) : launch<DT, kFmtE5M2>(p, s);
 }
 
