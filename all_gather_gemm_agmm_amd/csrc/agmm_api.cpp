@@ -48,7 +48,7 @@ using agmm::hip_err;
 using agmm::ok;
 using agmm::set_err;
 
-constexpr int64_t kDimLimit = int64_t(1) << 30;
+using agmm::kDimLimit;
 // automatic transposed copy of B (stored k x n) from this many rows of m
 constexpr int64_t kBtMinRows = 24576;
 constexpr int kTimingPairs = 4096;
@@ -58,23 +58,13 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t elem_bytes(int dtype) { return dtype == AGMM_FP32 ? 4 : 2; }
 
 int validate(int N, int64_t m_s, int64_t k, int64_t n, int dtype, int rt) {
-  if (N < 1) return set_err(AGMM_ERR_INVALID_ARG, "num_shards must be >= 1 (got %d)", N);
-  if (N > agmm::kMaxGroups)
-    return set_err(AGMM_ERR_UNSUPPORTED, "num_shards %d exceeds the supported maximum %d", N,
-                   agmm::kMaxGroups);
-  if (m_s < 1 || k < 1 || n < 1)
-    return set_err(AGMM_ERR_INVALID_ARG,
-                   "sizes must be >= 1 (m_per_shard=%lld, k=%lld, n_local=%lld)", (long long)m_s,
-                   (long long)k, (long long)n);
+  const int rc = agmm::check_counts(N, m_s, k, n);
+  if (rc != AGMM_OK) return rc;
   if (dtype != AGMM_BF16 && dtype != AGMM_FP16 && dtype != AGMM_FP32)
     return set_err(AGMM_ERR_INVALID_ARG, "unknown dtype %d", dtype);
   if (rt != 0 && rt != 1) return set_err(AGMM_ERR_INVALID_ARG, "rhs_transpose must be 0 or 1");
-  const int64_t m = (int64_t)N * m_s;
-  if (m >= kDimLimit || k >= kDimLimit || n >= kDimLimit || m * k >= (int64_t(1) << 40) ||
-      k * n >= (int64_t(1) << 40) || m * n >= (int64_t(1) << 40))
-    return set_err(AGMM_ERR_UNSUPPORTED, "problem too large (m=%lld, k=%lld, n=%lld)",
-                   (long long)m, (long long)k, (long long)n);
-  return ok();
+  const int rl = agmm::check_limits(N, m_s, k, n);
+  return rl == AGMM_OK ? ok() : rl;
 }
 
 // bf16/fp16 rows that are not whole 16-byte vectors (k, or n for B stored

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "agmm.h"
+#include "agmm_kernels.h"
 
 namespace agmm {
 
@@ -36,6 +37,31 @@ inline int ok() {
 
 inline int hip_err(hipError_t e, const char* what) {
   return set_err(AGMM_ERR_HIP, "%s failed: %s", what, hipGetErrorString(e));
+}
+
+// Limits of a plan's sizes: m = num_shards * m_per_shard, k and n, and the
+// elements of any matrix between them.
+constexpr int64_t kDimLimit = int64_t(1) << 30;
+constexpr int64_t kElemLimit = int64_t(1) << 40;
+
+inline int check_counts(int N, int64_t m_s, int64_t k, int64_t n) {
+  if (N < 1) return set_err(AGMM_ERR_INVALID_ARG, "num_shards must be >= 1 (got %d)", N);
+  if (N > kMaxGroups)
+    return set_err(AGMM_ERR_UNSUPPORTED, "num_shards %d exceeds the supported maximum %d", N, kMaxGroups);
+  if (m_s < 1 || k < 1 || n < 1)
+    return set_err(AGMM_ERR_INVALID_ARG, "sizes must be >= 1 (m_per_shard=%lld, k=%lld, n_local=%lld)",
+                   (long long)m_s, (long long)k, (long long)n);
+  return AGMM_OK;
+}
+
+inline int check_limits(int N, int64_t m_s, int64_t k, int64_t n) {
+  // m_s first: N * m_s must not overflow
+  const int64_t m = m_s < kDimLimit ? N * m_s : m_s;
+  if (m >= kDimLimit || k >= kDimLimit || n >= kDimLimit || m * k >= kElemLimit || k * n >= kElemLimit ||
+      m * n >= kElemLimit)
+    return set_err(AGMM_ERR_UNSUPPORTED, "problem too large (m=%lld, k=%lld, n=%lld)", (long long)m, (long long)k,
+                   (long long)n);
+  return AGMM_OK;
 }
 
 // One call's view of the caller's stream.

@@ -34,25 +34,13 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
-constexpr int64_t kDimLimit = int64_t(1) << 30;
-constexpr int64_t kElemLimit = int64_t(1) << 40;
+using agmm::kDimLimit;
 
 // Shard counts and sizes every plan here accepts (the all-gather matmul's
 // rules).
 int check_sizes(int N, int64_t m_s, int64_t k, int64_t n) {
-  if (N < 1) return set_err(AGMM_ERR_INVALID_ARG, "num_shards must be >= 1 (got %d)", N);
-  if (N > agmm::kMaxGroups)
-    return set_err(AGMM_ERR_UNSUPPORTED, "num_shards %d exceeds the supported maximum %d", N, agmm::kMaxGroups);
-  if (m_s < 1 || k < 1 || n < 1)
-    return set_err(AGMM_ERR_INVALID_ARG, "sizes must be >= 1 (m_per_shard=%lld, k=%lld, n_local=%lld)",
-                   (long long)m_s, (long long)k, (long long)n);
-  // m_s first: N * m_s must not overflow
-  const int64_t m = m_s < kDimLimit ? N * m_s : m_s;
-  if (m >= kDimLimit || k >= kDimLimit || n >= kDimLimit || m * k >= kElemLimit || k * n >= kElemLimit ||
-      m * n >= kElemLimit)
-    return set_err(AGMM_ERR_UNSUPPORTED, "problem too large (m=%lld, k=%lld, n=%lld)", (long long)m, (long long)k,
-                   (long long)n);
-  return AGMM_OK;
+  const int rc = agmm::check_counts(N, m_s, k, n);
+  return rc == AGMM_OK ? agmm::check_limits(N, m_s, k, n) : rc;
 }
 
 // What every plan here owns: its device, a workspace, and the order of its
@@ -307,7 +295,7 @@ int validate_loss(int N, int64_t m_s, int64_t k, int64_t n, int dtype, int64_t s
   if (dtype == AGMM_FP32)
     return set_err(AGMM_ERR_UNSUPPORTED, "the vocabulary loss takes bf16 or fp16 operands");
   if (dtype != AGMM_BF16 && dtype != AGMM_FP16) return set_err(AGMM_ERR_INVALID_ARG, "unknown dtype %d", dtype);
-  if (start < 0 || total < 1 || total >= kElemLimit || start > total - n)
+  if (start < 0 || total < 1 || total >= agmm::kElemLimit || start > total - n)
     return set_err(AGMM_ERR_INVALID_ARG, "%lld columns from %lld on do not lie in a vocabulary of %lld", (long long)n,
                    (long long)start, (long long)total);
   if (N * m_s >= (int64_t(1) << 27) || n >= (int64_t(1) << 27))
