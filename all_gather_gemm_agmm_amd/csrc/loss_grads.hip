@@ -12,10 +12,10 @@
 // casts.  dW of a piece is complete at once.
 //
 // Bound: MFMA; with few rows the stores of dW.  Measured: 8192 x 4096 bf16 over
-// 16384 columns, both products 1.48 ms, 1490 TFLOP/s; 16 x 4096 over 65536
+// 16384 columns, both products 1.48-1.57 ms, 1400-1490 TFLOP/s; 16 x 4096 over 65536
 // 286 us, 1.07 GB of W read and dW written: 3.8 TB/s; 30 x 500 over 50000 38 us
 // (80 with 256 x 256 tiles and dW, whose rows are then not whole 16-byte
-// vectors, stored by elements).  The last pass: 8192 x 4096 37 us, 5.4 TB/s.
+// vectors, stored by elements).  The last pass: 8192 x 4096 37-40 us, 5.0-5.4 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

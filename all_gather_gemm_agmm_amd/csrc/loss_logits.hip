@@ -25,10 +25,10 @@
 //
 // Bound: MFMA; with few rows HBM on W.  The exponentials cost 256 (256 x 256
 // tile) per lane once per tile, 3-5% beside the k loop of a 4096-deep product.
-// Measured: loss_stats_kernel, 8192 x 4096 bf16 over 131072 columns 5.9-6.1 ms,
-// 1450-1490 TFLOP/s (a library's product alone: 1310-1580); 8 x 4096 fp16 over
-// 131072 176 us, 6.1 TB/s of W.  loss_grad_kernel, 8192 x 4096 over 16384
-// columns 0.84 ms, 1310 TFLOP/s: it also writes d twice, 512 MiB.
+// Measured: loss_stats_kernel, 8192 x 4096 bf16 over 131072 columns 5.9-6.3 ms,
+// 1400-1490 TFLOP/s (a library's product alone: 1310-1580); 8 x 4096 fp16 over
+// 131072 176-179 us, 6.0 TB/s of W.  loss_grad_kernel, 8192 x 4096 over 16384
+// columns 0.84-0.90 ms, 1220-1310 TFLOP/s: it also writes d twice, 512 MiB.
 // loss_combine_kernel, 8192 rows of 1024 partials 13 us, 5.2 TB/s.
 // loss_prepare_kernel's copy of 40000 x 2500 elements (a row length that is no
 // multiple of 8) 84 us, 4.8 TB/s; element by element it took 136.

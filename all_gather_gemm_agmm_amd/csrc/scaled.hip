@@ -25,18 +25,20 @@
 //    VALU and MFMA share the accumulators, which therefore live in ordinary
 //    registers: two waves per SIMD with 128 accumulators each.  Bound: MFMA
 //    (8-bit form: power, at 1.74 GHz; the pipe is busy 63% of the cycles).
-//    Measured: 32768 x 8192 -> 7168 to bf16 1.52-1.57 ms, 2450-2530 TFLOP/s
+//    Measured: 32768 x 8192 -> 7168 to bf16 1.52-1.62 ms, 2380-2530 TFLOP/s
 //    (a library's 8-bit product with one scale: 2660 at 8192^3); 1011 x 4040 ->
 //    2051 to fp16 28.8 us: 136 tiles of 128 x 128, each its CU's operand stream.
 //    In bf16 MFMAs (below) the conversions and the scaling cost about as many
-//    cycles as the MFMAs: 3584 x 8192 -> 4096 to fp32 228-237 us, 1015-1055
+//    cycles as the MFMAs: 3584 x 8192 -> 4096 to fp32 228-245 us, 980-1055
 //    TFLOP/s.
 //  * scaled_skinny_kernel: few rows.  Every wave streams its own k-tiles
 //    through a private LDS ring (no barrier in the loop); the waves' sums are
-//    added in LDS in a fixed order.  Bound: the operands' way into a CU, 26
-//    bytes per cycle; a tile of 64 columns and rows needs half as many as two
-//    of 32.  Measured: 8 x 4096 -> 1792 5.5 us; 128 x 8192 -> 3584 in two k
-//    ranges 17 us and 3.5 for their sum.
+//    added in LDS in a fixed order.  Bound: what one workgroup with all of a
+//    CU's LDS streams, 26 bytes per cycle (two with half of it each reach 38, so
+//    this is the form's limit, not the CU's; the 64 x 64 tile's rings hold two
+//    k-tiles per wave); a tile of 64 columns and rows needs half as many bytes
+//    as two of 32.  Measured: 8 x 4096 -> 1792 5.6 us; 128 x 8192 -> 3584 in two
+//    k ranges 17-20 us and 3.5-3.9 for their sum.
 //  * scaled_reduce_kernel: fixed-order sum of k ranges.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
