@@ -146,8 +146,9 @@ def _keep(case, p):
     group = full.view(m, parts, -1, 32)
     mantissa, e = torch.frexp(group.abs().amax(3))           # mantissa in [0.5, 1): 448 = 0.875 * 2^9
     e = torch.clamp(e - 9 + (mantissa > 0.875), min=-126)
-    e = torch.where(mantissa == 0, torch.full_like(e, -126), e)
-    values = torch.ldexp(group, -e[..., None]).view(full.shape).to(torch.float8_e4m3fn)
+    e = torch.where(mantissa == 0, torch.full_like(e, -126), e).to(torch.int32)
+    inverse = ((127 - e) << 23).view(torch.float32)          # 2^-e, exactly
+    values = (group * inverse[..., None]).view(full.shape).to(torch.float8_e4m3fn)
     return values, (e + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
 
 
@@ -271,7 +272,7 @@ def work(case):
 def _nearest_e4m3(v):
     """Nearest e4m3 value (even mantissa on a tie) of finite 64-bit v within its range."""
     _, e = torch.frexp(v)
-    step = torch.ldexp(torch.ones_like(v), torch.clamp(e - 1, min=-6) - 3)
+    step = ((torch.clamp(e - 1, min=-6).long() - 3 + 1023) << 52).view(torch.float64)
     return torch.round(v / step) * step
 
 
@@ -314,7 +315,7 @@ def _exact_forward(state):
         return [y, kept]
     top = kept.view(m, parts, wide // 32, 32).abs().amax(3)
     power = torch.ceil(torch.log2(torch.where(top > 0, top, torch.full_like(top, 2.0 ** -130)) / 448)).clamp(min=-126)
-    scale = torch.exp2(power)
+    scale = ((power.long() + 1023) << 52).view(torch.float64)
     return [y, _nearest_e4m3(kept / scale.repeat_interleave(32, dim=2)), scale]
 
 
