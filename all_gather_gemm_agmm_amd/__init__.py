@@ -23,6 +23,8 @@ AGMM_BF16, AGMM_FP16, AGMM_FP32 = 0, 1, 2
 AGMM_E4M3, AGMM_E5M2 = 0, 1
 FORMATS = {"e4m3": AGMM_E4M3, "e5m2": AGMM_E5M2}
 SCALE_BLOCK = 128   # elements of k that share one scale
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+KEPT_BLOCK = 32     # columns of a row that share one scale of 8-bit pre-activations
 AGMM_OK, AGMM_ERR_INVALID_ARG, AGMM_ERR_UNSUPPORTED, AGMM_ERR_OOM, AGMM_ERR_HIP = 0, 1, 2, 3, 4
 (AGMM_VARIANT_AUTO, AGMM_VARIANT_FUSED, AGMM_VARIANT_STAGED, AGMM_VARIANT_UNFUSED,
  AGMM_VARIANT_SKINNY) = 0, 1, 2, 3, 4
@@ -75,6 +77,23 @@ EXPORTS = [
     ("agmm_loss_plan_get_int", _ci, [_vp, _cc, ctypes.POINTER(_i64)]),
     ("agmm_loss_plan_workspace_bytes", ctypes.c_size_t, [_vp]),
     ("agmm_loss_plan_destroy", None, [_vp]),
+    ("agmm_ff_plan_validate", _ci, [_ci, _i64, _i64, _i64, _ci, _ci, _ci]),
+    ("agmm_ff_plan_create", _vp, [_ci, _i64, _i64, _i64, _ci, _ci, _ci, _ci]),
+    ("agmm_ff_forward", _ci, [_vp, ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("agmm_ff_backward", _ci, [_vp, ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("agmm_ff_recompute", _ci, [_vp, _vp, _vp, _vp, _vp]),
+    ("agmm_ff_plan_set_int", _ci, [_vp, _cc, _i64]),
+    ("agmm_ff_plan_get_int", _ci, [_vp, _cc, ctypes.POINTER(_i64)]),
+    ("agmm_ff_plan_workspace_bytes", ctypes.c_size_t, [_vp]),
+    ("agmm_ff_plan_destroy", None, [_vp]),
+    ("agmm_norm_plan_validate", _ci, [_i64, _i64, _ci, _ci]),
+    ("agmm_norm_plan_create", _vp, [_i64, _i64, _ci, _ci]),
+    ("agmm_norm_forward", _ci, [_vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp]),
+    ("agmm_norm_backward", _ci, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("agmm_norm_plan_set_int", _ci, [_vp, _cc, _i64]),
+    ("agmm_norm_plan_get_int", _ci, [_vp, _cc, ctypes.POINTER(_i64)]),
+    ("agmm_norm_plan_workspace_bytes", ctypes.c_size_t, [_vp]),
+    ("agmm_norm_plan_destroy", None, [_vp]),
     ("agmm_last_status", _ci, []),
     ("agmm_last_error", _cc, []),
     ("agmm_version", _cc, []),
@@ -787,6 +806,223 @@ def merge_vocab_slices(lse, target, labels, vocab_size: int, ignore_index: int =
     bad = (labels < 0) | (labels >= vocab_size)
     loss = torch.where(bad, torch.full_like(loss, float("nan")), loss)
     return torch.where(labels == ignore_index, torch.zeros_like(loss), loss), whole
+
+
+class Checkpoint:
+    """Pre-activations kept by FeedForwardPlan.forward for its backward pass:
+    `values` [m, parts, n rounded up to 32] (zeros past n) in the plan's dtype,
+    or in e4m3 with `scales` [m, parts, columns / 32] (e8m0: powers of two); `n`
+    is the true number of columns."""
+
+    __slots__ = ("values", "scales", "n")
+
+    def __init__(self, values, scales, n: int):
+        self.values, self.scales, self.n = values, scales, int(n)
+
+    def dequantize(self):
+        """The fp32 matrix [m, parts * n] this stands for (torch operations; for
+        checks, not for speed)."""
+        v = self.values.float()
+        if self.scales is not None:
+            v = v * self.scales.float().repeat_interleave(KEPT_BLOCK, dim=2)
+        return v[:, :, :self.n].reshape(v.shape[0], -1)
+
+
+class FeedForwardPlan(_OpPlan):
+    """The product of the gathered rows with an epilogue, y = act(p) + residual
+    with p = concat_r(shards[r]) @ W^T + bias, or, `gated`, y = act(p[:, :n]) *
+    p[:, n:] in one kernel, and its gradient (agmm_ff_forward, agmm_ff_backward).
+    W is [n_local, k], gated [2 * n_local, k] with the gate's rows first.
+    `activation` is one of ACTIVATIONS."""
+
+    _prefix = "agmm_ff_plan"
+
+    def __init__(self, num_shards: int, m_per_shard: int, k: int, n_local: int, dtype: int = AGMM_BF16,
+                 activation: str = "none", gated: bool = False, with_gradient: bool = True, **settings):
+        code = ACTIVATIONS.get(activation)
+        if code is None:
+            raise ValueError(f"unknown activation {activation!r} (one of {sorted(ACTIVATIONS)})")
+        self._make(num_shards, m_per_shard, k, n_local, dtype, code, int(bool(gated)), int(bool(with_gradient)))
+        self.num_shards, self.m_per_shard, self.k, self.n_local, self.dtype = num_shards, m_per_shard, k, n_local, dtype
+        self.activation, self.gated, self.parts = activation, bool(gated), 2 if gated else 1
+        self._table = ctypes.c_void_p * num_shards   # a new one per call: calls of several threads may overlap
+        lib = load_library()
+        self._fwd, self._bwd, self._again = lib.agmm_ff_forward, lib.agmm_ff_backward, lib.agmm_ff_recompute
+        self._expect()
+        for key, val in settings.items():
+            if val is not None:
+                self.set(key, val)
+
+    def _expect(self):
+        import torch
+        t, m, k, n, parts = _torch_dtype(self.dtype), self.m, self.k, self.n_local, self.parts
+        wide = self.get("saved_cols")
+        self._la = self._like((self.m_per_shard, k), t, self.get("lda"))
+        self._lw = self._like((parts * n, k), t, self.get("ldw"))
+        self._lb = self._like((parts * n,), t)
+        self._lr = self._like((m, n), t, self.get("ldr"))
+        self._ly = self._like((m, n), t, self.get("ldy"))
+        self._ldy = self._like((m, n), t, self.get("lddy"))
+        self._lda = self._like((m, k), t, self.get("ldda"))
+        self._ldw = self._like((parts * n, k), t, self.get("lddw"))
+        # kept pre-activations, seen as matrices of their rows
+        self._kept_shape, self._scales_shape = torch.Size((m, parts, wide)), torch.Size((m, parts, wide // KEPT_BLOCK))
+        self._kept_types = {t: None, torch.float8_e4m3fn: torch.float8_e8m0fnu}
+
+    def _shards(self, shards):
+        if len(shards) != self.num_shards:
+            raise ValueError(f"expected {self.num_shards} shards, got {len(shards)}")
+        la, on, pa = self._la, self._on, self._table()
+        for r, s in enumerate(shards):
+            # the common case in one comparison
+            pa[r] = s.data_ptr() if (s.dtype, s.device, s.shape, s.stride()) == la else on(s, la, "shards")
+        return pa
+
+    def _kept(self, saved):
+        """The addresses of a Checkpoint of this plan."""
+        if saved is None:
+            return None, None
+        if not isinstance(saved, Checkpoint):
+            raise TypeError("saved must be a Checkpoint")
+        if saved.n != self.n_local:
+            raise ValueError(f"saved has {saved.n} columns, expected {self.n_local}")
+        v, s = saved.values, saved.scales
+        if v.dtype not in self._kept_types:
+            raise TypeError(f"saved has dtype {v.dtype}, plan expects one of {list(self._kept_types)}")
+        kind = self._kept_types[v.dtype]
+        for t, shape, dtype, name in ((v, self._kept_shape, v.dtype, "saved.values"), (s, self._scales_shape, kind, "saved.scales")):
+            if dtype is None:
+                if t is not None:
+                    raise ValueError(f"{name} must be None for 16-bit values")
+                continue
+            if t is None or t.dtype != dtype:
+                raise TypeError(f"{name} must be a tensor of {dtype}")
+            if t.device.type != "cuda" or t.get_device() != self.device:
+                raise ValueError(f"{name} is on {t.device}; the plan was created on cuda:{self.device}")
+            if t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {tuple(shape)} (got {tuple(t.shape)})")
+        return v.data_ptr(), None if s is None else s.data_ptr()
+
+    def forward(self, shards, W, bias=None, residual=None, out=None, keep: int = 0, stream=None):
+        """y [m, n_local]; with keep 16 or 8 also the pre-activations in so many
+        bits, as a Checkpoint: (y, saved)."""
+        import torch
+        if keep != 0 and keep != 8 and keep != 16:
+            raise ValueError(f"keep must be 0, 8 or 16 (got {keep!r})")
+        on, a = self._on, self._shards(shards)
+        w = on(W, self._lw, "W")
+        b = None if bias is None else on(bias, self._lb, "bias")
+        r = None if residual is None else on(residual, self._lr, "residual")
+        saved = v = s = None
+        with _device_and_stream(self.device, stream):
+            if out is None:
+                out = self._new(self._ly)
+                y = out.data_ptr()
+            else:
+                y = on(out, self._ly, "out")
+            if keep:
+                device = self._la[1]
+                values = torch.empty(self._kept_shape, dtype=torch.float8_e4m3fn if keep == 8 else self._la[0], device=device)
+                scales = torch.empty(self._scales_shape, dtype=torch.float8_e8m0fnu, device=device) if keep == 8 else None
+                saved = Checkpoint(values, scales, self.n_local)
+                v, s = values.data_ptr(), None if scales is None else scales.data_ptr()
+            _check(self._fwd(self.handle, a, w, b, r, y, v, s, _stream_handle(stream, self.device)))
+        return (out, saved) if keep else out
+
+    def backward(self, shards, W, saved, dy, dA=None, dW=None, dbias=None, need_dA: bool = True, need_dW: bool = True,
+                 need_dbias: bool = False, stream=None):
+        """(dA [m, k], dW [parts * n_local, k], dbias [parts * n_local]) for the
+        upstream gradient dy of y and what forward kept (None without a gate and
+        an activation); None in the place of one that is not needed."""
+        on, a = self._on, self._shards(shards)
+        w = on(W, self._lw, "W")
+        v, s = self._kept(saved)
+        g = on(dy, self._ldy, "dy")
+        with _device_and_stream(self.device, stream):
+            if dA is None and need_dA:
+                dA = self._new(self._lda)
+            if dW is None and need_dW:
+                dW = self._new(self._ldw)
+            if dbias is None and need_dbias:
+                dbias = self._new(self._lb)
+            _check(self._bwd(self.handle, a, w, v, s, g, None if dA is None else on(dA, self._lda, "dA"),
+                             None if dW is None else on(dW, self._ldw, "dW"),
+                             None if dbias is None else on(dbias, self._lb, "dbias"), _stream_handle(stream, self.device)))
+        return dA, dW, dbias
+
+    def recompute(self, saved, out=None, stream=None):
+        """y without its residual, again from what forward kept."""
+        if saved is None:
+            raise TypeError("saved must be a Checkpoint")
+        v, s = self._kept(saved)
+        with _device_and_stream(self.device, stream):
+            if out is None:
+                out = self._new(self._ly)
+            _check(self._again(self.handle, v, s, self._on(out, self._ly, "out"), _stream_handle(stream, self.device)))
+        return out
+
+
+class NormPlan(_OpPlan):
+    """Layer norm of rows [rows, cols] and its gradient (agmm_norm_forward,
+    agmm_norm_backward).  `dtype` is the rows', `weight_dtype` the weights' (the
+    same, the default, or AGMM_FP32)."""
+
+    _prefix = "agmm_norm_plan"
+
+    def __init__(self, rows: int, cols: int, dtype: int = AGMM_BF16, weight_dtype: Optional[int] = None, **settings):
+        weight_dtype = dtype if weight_dtype is None else weight_dtype
+        self._make(rows, cols, dtype, weight_dtype)
+        self.rows, self.cols, self.dtype, self.weight_dtype = rows, cols, dtype, weight_dtype
+        self._fwd, self._bwd = load_library().agmm_norm_forward, load_library().agmm_norm_backward
+        self._expect()
+        for key, val in settings.items():
+            if val is not None:
+                self.set(key, val)
+
+    def _expect(self):
+        import torch
+        t, shape = _torch_dtype(self.dtype), (self.rows, self.cols)
+        self._lx, self._ly = self._like(shape, t, self.get("ldx")), self._like(shape, t, self.get("ldy"))
+        self._ldy, self._ldx = self._like(shape, t, self.get("lddy")), self._like(shape, t, self.get("lddx"))
+        self._lw = self._like((self.cols,), _torch_dtype(self.weight_dtype))
+        self._ls = self._like((self.rows,), torch.float32)
+
+    @property
+    def m(self) -> int:
+        return self.rows
+
+    def forward(self, x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
+        """(y, mean, rstd): y [rows, cols] and the rows' fp32 statistics."""
+        on, new = self._on, self._new
+        px = on(x, self._lx, "x")
+        w = None if weight is None else on(weight, self._lw, "weight")
+        b = None if bias is None else on(bias, self._lw, "bias")
+        with _device_and_stream(self.device, stream):
+            if out is None:
+                out = new(self._ly)
+            mean, rstd = new(self._ls), new(self._ls)
+            _check(self._fwd(self.handle, px, w, b, eps, on(out, self._ly, "out"), mean.data_ptr(), rstd.data_ptr(),
+                             _stream_handle(stream, self.device)))
+        return out, mean, rstd
+
+    def backward(self, x, dy, weight, mean, rstd, dx=None, need_dx: bool = True, need_dweight: bool = True,
+                 need_dbias: bool = True, stream=None):
+        """(dx, dweight, dbias) for the upstream gradient dy of y and the
+        statistics that forward returned; None in the place of one that is not
+        needed."""
+        on, new = self._on, self._new
+        px, g = on(x, self._lx, "x"), on(dy, self._ldy, "dy")
+        w = None if weight is None else on(weight, self._lw, "weight")
+        mu, rs = on(mean, self._ls, "mean"), on(rstd, self._ls, "rstd")
+        with _device_and_stream(self.device, stream):
+            if dx is None and need_dx:
+                dx = new(self._ldx)
+            dw = new(self._lw) if need_dweight else None
+            db = new(self._lw) if need_dbias else None
+            _check(self._bwd(self.handle, px, g, w, mu, rs, None if dx is None else on(dx, self._ldx, "dx"),
+                             None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
+                             _stream_handle(stream, self.device)))
+        return dx, dw, db
 
 
 # ------------------------------------------------ one call, cached plans

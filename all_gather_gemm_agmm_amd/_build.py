@@ -41,6 +41,12 @@ SOURCES = {
     "scaled.hip": [],
     "loss_logits.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
     "loss_grads.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
+    "agmm_feed.cpp": [],
+    "feed_tiles.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
+    "feed_few.hip": [],
+    "feed_back.hip": [],
+    "feed_grads.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
+    "norm.hip": [],
 }
 
 

@@ -1,0 +1,670 @@
+// C ABI of the feed-forward block's operators (host side): the product with an
+// epilogue and the gated product, their way back, and layer norm.  Their plans
+// are used as those of agmm_ops.cpp are.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <string>
+
+#include "agmm.h"
+#include "feed_kernels.h"
+#include "ops_kernels.h"
+#include "plan_base.h"
+
+namespace {
+
+using agmm::aligned;
+using agmm::cdiv;
+using agmm::check_ptr;
+using agmm::check_sizes;
+using agmm::Cut;
+using agmm::group_rows;
+using agmm::hip_err;
+using agmm::kDimLimit;
+using agmm::ok;
+using agmm::PlanBase;
+using agmm::round_up;
+using agmm::set_err;
+
+int validate_ff(int N, int64_t m_s, int64_t k, int64_t n, int dtype, int act, int gated) {
+  const int rc = check_sizes(N, m_s, k, n);
+  if (rc != AGMM_OK) return rc;
+  if (dtype == AGMM_FP32)
+    return set_err(AGMM_ERR_UNSUPPORTED, "the feed-forward product takes bf16 or fp16 operands");
+  if (dtype != AGMM_BF16 && dtype != AGMM_FP16) return set_err(AGMM_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (act < AGMM_ACT_NONE || act > AGMM_ACT_SILU) return set_err(AGMM_ERR_INVALID_ARG, "unknown activation %d", act);
+  if (gated != 0 && gated != 1) return set_err(AGMM_ERR_INVALID_ARG, "gated must be 0 or 1 (got %d)", gated);
+  // every launch then stays within kFeedGrid by its smallest tile but the few-row
+  // form, which is chosen only where it fits
+  const int64_t m = N * m_s, cols = (1 + gated) * n;
+  if (m >= (int64_t(1) << 27) || cols >= (int64_t(1) << 27) || m * cols >= (int64_t(1) << 36) || m * k >= (int64_t(1) << 36) ||
+      cols * k >= (int64_t(1) << 36))
+    return set_err(AGMM_ERR_UNSUPPORTED, "problem too large (m=%lld, k=%lld, n_local=%lld)", (long long)m, (long long)k, (long long)n);
+  return ok();
+}
+
+agmm::Activation activation_of(int act) {
+  const float c = 1.5957691216057308f;   // sqrt(8 / pi)
+  switch (act) {
+    case AGMM_ACT_RELU: return {agmm::kActRelu, 0.0f, 0.0f};
+    case AGMM_ACT_GELU: return {agmm::kActNormal, 0.0f, 0.0f};
+    case AGMM_ACT_GELU_TANH: return {agmm::kActLogistic, c, c * 0.044715f};   // x (1 + tanh u) / 2 = x / (1 + exp(-2 u))
+    case AGMM_ACT_SILU: return {agmm::kActLogistic, 1.0f, 0.0f};
+    default: return {agmm::kActLinear, 0.0f, 0.0f};
+  }
+}
+
+}  // namespace
+
+struct agmm_ff_plan : PlanBase {
+  int N = 0;
+  int64_t m_s = 0, k = 0, n = 0, m = 0;
+  int dtype = 0, act = 0, parts = 1;
+  bool with_gradient = true;
+  int64_t lda = 0, ldw = 0, ldr = 0, ldy = 0, lddy = 0, ldda = 0, lddw = 0;   // 0: dense
+  int64_t tile_key = -1;                          // 64 (few rows), 128, 256; -1: automatic
+
+  // What a call of a pass uses, derived from the settings.
+  struct Layout {
+    bool pad_a = false, pad_w = false;   // rows that are not whole 16-byte vectors: zero-padded copies
+    int64_t kp = 0;                      // k rounded up to 8
+    int tile = 256;                      // forward; 64: the few-row form, in
+    int fm = 0, fn = 0;                  // blocks of 16 fm x 16 fn (kept pre-activations: fn 4)
+    int tile_grads = 256;
+    int a_ranges = 1, w_ranges = 1;      // ranges of the gradient products' sums
+    int64_t a_per = 0, w_per = 0;
+    char *a = nullptr, *w = nullptr, *d = nullptr, *dt = nullptr;
+    float *a_sums = nullptr, *w_sums = nullptr, *b_sums = nullptr;
+    size_t bytes = 0;
+  };
+
+  int64_t ld_a() const { return lda ? lda : k; }
+  int64_t ld_w() const { return ldw ? ldw : k; }
+  int64_t m8() const { return round_up(m, 8); }
+  int64_t cols() const { return parts * n; }
+  int64_t wide() const { return round_up(n, agmm::kKeptBlock); }
+  // Columns of the forward product's tiles (feed_kernels.h).
+  int64_t tile_cols() const { return parts == 2 ? 2 * round_up(n, 16) : n; }
+
+  // Microseconds of one workgroup, measured on MI355X: 20 and 2.1 per 64 of its
+  // sum for the 256 x 256 tile (one to a CU), 5 and 1.25 for the 128 x 128 one
+  // (two to a CU; 0.7 where it has the CU alone).
+  static double workgroup_us(int tile, int64_t sum) {
+    return tile == 256 ? 20.0 + 2.1 * (double)cdiv(sum, 64) : 5.0 + 1.25 * (double)cdiv(sum, 64);
+  }
+
+  // Form of the forward product: the one that takes the least.  `copied`: the
+  // tiles need a copy of W first, which the few-row form does not.
+  void pick_tile(Layout& L, bool copied) const {
+    const int64_t nc = tile_cols();
+    const double big = (double)cdiv(cdiv(m, 256) * cdiv(nc, 256), cu_count) * workgroup_us(256, k);
+    const int64_t tiles = cdiv(m, 128) * cdiv(nc, 128), rest = tiles % (2 * cu_count);
+    const double small = (double)(tiles / (2 * cu_count)) * workgroup_us(128, k) +
+                         (rest == 0 ? 0.0 : rest > cu_count ? workgroup_us(128, k) : 5.0 + 0.7 * (double)cdiv(k, 64));
+    const double bytes = (double)cols() * (double)k * 2;
+    L.tile = tile_key > 0 ? (int)tile_key : big <= small ? 256 : 128;
+    if (tile_key > 0 && tile_key != 64) return;
+    L.fm = m <= 16 ? 1 : 4;
+    L.fn = cdiv(nc, 64) * cdiv(m, 16 * L.fm) >= 2 * cu_count ? 4 : parts;
+    const int64_t wgs = cdiv(m, 16 * L.fm) * cdiv(nc, 16 * L.fn);
+    const double rate = (L.fm * L.fn == 16 ? 6e6 : 10e6) / (copied && (ld_a() % 2 != 0 || ld_w() % 2 != 0) ? 1.7 : 1.0);
+    const double few = 5.0 + std::max((double)wgs * 32 * (L.fm + L.fn) * (double)k / rate, bytes / 4.8e6);
+    if (tile_key == 64 || (few < std::min(big, small) + (copied ? 2.0 + 2 * bytes / 5e6 : 0.0) && few_fits())) L.tile = 64;
+  }
+
+  // Whether every form of the few-row kernel stays within a launch.
+  bool few_fits() const { return cdiv(m, 16 * (m <= 16 ? 1 : 4)) * cdiv(tile_cols(), 16 * parts) < agmm::kFeedGrid; }
+
+  Layout layout(bool grad, char* base) const {
+    Layout L;
+    L.kp = round_up(k, 8);
+    L.pad_a = k % 8 != 0 || ld_a() % 8 != 0;
+    L.pad_w = k % 8 != 0 || ld_w() % 8 != 0;
+    Cut c{base};
+    if (!grad) {
+      pick_tile(L, L.pad_w);
+      if (L.tile == 64) L.pad_a = L.pad_w = false;   // read in place
+      if (L.pad_a) L.a = c.take((size_t)m * L.kp * 2);
+      if (L.pad_w) L.w = c.take((size_t)cols() * L.kp * 2);
+    } else {
+      if (L.pad_a || N > 1) L.a = c.take((size_t)m * L.kp * 2);   // dW's product reads it k x n, in one piece
+      if (L.pad_w) L.w = c.take((size_t)cols() * L.kp * 2);
+      L.d = c.take((size_t)m * round_up(cols(), 8) * 2);
+      L.dt = c.take((size_t)cols() * m8() * 2);
+      L.b_sums = reinterpret_cast<float*>(c.take((size_t)cdiv(m, agmm::kDRows) * cols() * 4));
+      // One launch computes both products; each sum may be cut into ranges.
+      // Tile and ranges are those that take the least: the workgroups' time
+      // spread over the CUs and half of one for the last round, but no less than
+      // the longest of them; and the ranges' sums, written and read at 4 TB/s,
+      // with a launch more.
+      double best = -1;
+      int64_t want_a = 1, want_w = 1;
+      for (int t : {256, 128}) {
+        if (tile_key > 64 && t != tile_key) continue;
+        const int64_t a_tiles = cdiv(m, t) * cdiv(k, t), w_tiles = cdiv(cols(), t) * cdiv(k, t);
+        const double slots = cu_count * (t == 128 ? 2 : 1);
+        for (int64_t ra = 1; ra == 1 || (ra <= 64 && a_tiles * ra <= 4 * cu_count && cols() / ra >= 256); ra *= 2)
+          for (int64_t rw = 1; rw == 1 || (rw <= 64 && w_tiles * rw <= 4 * cu_count && m / rw >= 256); rw *= 2) {
+            const double a_us = workgroup_us(t, cdiv(cols(), ra)), w_us = workgroup_us(t, cdiv(m, rw));
+            const double sums = (ra > 1 ? (double)(ra * m) : 0.0) + (rw > 1 ? (double)(rw * cols()) : 0.0);
+            const double us = std::max({((double)(a_tiles * ra) * a_us + (double)(w_tiles * rw) * w_us) / slots + w_us / 2, a_us, w_us}) +
+                              sums * (double)k * 8 / 4e6 + (sums > 0 ? 3.0 : 0.0);
+            if (best < 0 || us < best) best = us, L.tile_grads = t, want_a = ra, want_w = rw;
+          }
+      }
+      L.a_per = round_up(cdiv(cols(), want_a), 64);
+      L.a_ranges = (int)cdiv(cols(), L.a_per);
+      L.w_per = round_up(cdiv(m, want_w), 64);
+      L.w_ranges = (int)cdiv(m, L.w_per);
+      if (L.a_ranges > 1) L.a_sums = reinterpret_cast<float*>(c.take((size_t)L.a_ranges * m * round_up(k, 4) * 4));
+      if (L.w_ranges > 1) L.w_sums = reinterpret_cast<float*>(c.take((size_t)L.w_ranges * cols() * round_up(k, 4) * 4));
+    }
+    L.bytes = c.at;
+    return L;
+  }
+
+  int apply() {
+    size_t bytes = 0;
+    for (bool grad : {false, true})
+      if (!grad || with_gradient) bytes = std::max(bytes, layout(grad, nullptr).bytes);
+    return reserve(bytes);
+  }
+
+  agmm::TileOrder tiles_of(int64_t rows, int64_t columns, int tile) const {
+    agmm::TileOrder o{};
+    o.num_rb = (int32_t)cdiv(rows, tile);
+    o.num_cb = (int32_t)cdiv(columns, tile);
+    o.group_m = group_rows(o.num_rb, o.num_cb);
+    o.xcd_remap = 1;
+    return o;
+  }
+
+  static agmm::RowMap dense(const void* a, int64_t rows, int64_t ld) {
+    agmm::RowMap r{};
+    r.a_group[0] = a;
+    r.a_ld = ld;
+    r.rows_per_group = (int32_t)rows;
+    r.num_groups = 1;
+    return r;
+  }
+
+  // Copies of A and W as rows of whole 16-byte vectors, where the layout has them.
+  int copies(const Layout& L, const void* const* shards, const void* W, hipStream_t s) const {
+    const auto copy = [&](const void* const* groups, int count, int64_t rows, int64_t ld, void* out) {
+      agmm::PadRows c{};
+      for (int g = 0; g < count; ++g) c.group[g] = groups[g];
+      c.num_groups = count;
+      c.rows = rows;
+      c.cols = k;
+      c.ld = ld;
+      c.chunks = L.kp / 8;
+      c.out = out;
+      return agmm::launch_loss_prepare(nullptr, &c, dtype, s);
+    };
+    if (L.a && shards) {
+      const hipError_t err = copy(shards, N, m_s, ld_a(), L.a);
+      if (err != hipSuccess) return hip_err(err, "row copy launch");
+    }
+    if (L.w && W) {
+      const hipError_t err = copy(&W, 1, cols(), ld_w(), L.w);
+      if (err != hipSuccess) return hip_err(err, "weight copy launch");
+    }
+    return AGMM_OK;
+  }
+
+  agmm::KeptRows kept_rows(const void* values, const void* scales) const {
+    return {const_cast<void*>(values), static_cast<uint8_t*>(const_cast<void*>(scales)), wide()};
+  }
+
+  int forward(const Layout& L, const void* const* shards, const void* W, const void* bias, const void* residual, void* Y,
+              void* saved, void* saved_scales, hipStream_t s) {
+    const int rc = copies(L, shards, W, s);
+    if (rc != AGMM_OK) return rc;
+    agmm::FeedProblem p{};
+    if (L.a) {
+      p.gemm.rows = dense(L.a, m, L.kp);
+    } else {
+      for (int g = 0; g < N; ++g) p.gemm.rows.a_group[g] = shards[g];
+      p.gemm.rows.a_ld = ld_a();
+      p.gemm.rows.rows_per_group = (int32_t)m_s;
+      p.gemm.rows.num_groups = N;
+      p.gemm.rows.c_group_rows = m_s;
+    }
+    // kept rows are written in blocks of 32 columns of a part
+    const int fn = L.tile == 64 && saved ? 4 : L.fn;
+    if (L.tile == 64) {
+      p.gemm.order.num_rb = (int32_t)cdiv(m, 16 * L.fm);
+      p.gemm.order.num_cb = (int32_t)cdiv(tile_cols(), 16 * fn);
+    } else {
+      p.gemm.order = tiles_of(m, tile_cols(), L.tile);
+    }
+    p.gemm.m = (int32_t)m;
+    p.gemm.n = (int32_t)tile_cols();
+    p.gemm.k = (int32_t)(L.tile == 64 ? k : L.kp);
+    p.gemm.b = L.w ? L.w : W;
+    p.gemm.ldb = L.w ? L.kp : ld_w();
+    p.gemm.splits = 1;
+    p.gemm.k_per_split = (int32_t)L.kp;
+    p.n = (int32_t)n;
+    p.gated = parts == 2;
+    p.act = activation_of(act);
+    p.bias = bias;
+    p.residual = residual;
+    p.ldr = ldr ? ldr : n;
+    p.y = Y;
+    p.ldy = ldy ? ldy : n;
+    p.kept = kept_rows(saved, saved_scales);
+    const hipError_t err = L.tile == 64 ? agmm::launch_feed_few(p, L.fm, fn, dtype, s) : agmm::launch_feed_tiles(p, L.tile, dtype, s);
+    return err == hipSuccess ? AGMM_OK : hip_err(err, "feed-forward launch");
+  }
+
+  int backward(const void* const* shards, const void* W, const void* saved, const void* saved_scales, const void* dY, void* dA,
+               void* dW, void* dbias, hipStream_t s) {
+    const Layout L = layout(true, ws);
+    const int rc = copies(L, dW ? shards : nullptr, dA ? W : nullptr, s);
+    if (rc != AGMM_OK) return rc;
+    agmm::FeedDProblem e{};
+    e.m = m;
+    e.n = (int32_t)n;
+    e.gated = parts == 2;
+    e.act = activation_of(act);
+    e.kept = kept_rows(saved, saved_scales);
+    e.dy = dY;
+    e.lddy = lddy ? lddy : n;
+    e.d = dA ? L.d : nullptr;
+    e.ldd = round_up(cols(), 8);
+    e.dt = dW ? L.dt : nullptr;
+    e.ldt = m8();
+    e.sums = dbias ? L.b_sums : nullptr;
+    hipError_t err = agmm::launch_feed_d(e, dtype, s);
+    if (err != hipSuccess) return hip_err(err, "feed-forward gradient launch");
+    agmm::GemmProblem ga{}, gw{};
+    ga.rows = dense(L.d, m, e.ldd);
+    ga.order = tiles_of(m, k, L.tile_grads);
+    ga.m = (int32_t)m;
+    ga.n = (int32_t)k;
+    ga.k = (int32_t)cols();
+    ga.b = L.w ? L.w : W;
+    ga.ldb = L.w ? L.kp : ld_w();
+    ga.splits = L.a_ranges;
+    ga.k_per_split = (int32_t)L.a_per;
+    ga.partials = L.a_sums;
+    ga.c = dA;
+    ga.ldc = ldda ? ldda : k;
+    gw.rows = dense(L.dt, cols(), m8());
+    gw.order = tiles_of(cols(), k, L.tile_grads);
+    gw.m = (int32_t)cols();
+    gw.n = (int32_t)k;
+    gw.k = (int32_t)m;
+    gw.b = L.a ? L.a : shards[0];
+    gw.ldb = L.a ? L.kp : ld_a();
+    gw.splits = L.w_ranges;
+    gw.k_per_split = (int32_t)L.w_per;
+    gw.partials = L.w_sums;
+    gw.c = dW;
+    gw.ldc = lddw ? lddw : k;
+    if (dA || dW) {
+      err = agmm::launch_feed_grads(dA ? &ga : nullptr, dW ? &gw : nullptr, L.tile_grads, dtype, s);
+      if (err != hipSuccess) return hip_err(err, "gradient products launch");
+    }
+    const auto ranges = [&](const agmm::GemmProblem& g) { return agmm::SumRanges{g.partials, g.splits, g.m, g.n, g.c, g.ldc}; };
+    const agmm::SumRanges sa = ranges(ga), sw = ranges(gw);
+    const bool more_a = dA && L.a_ranges > 1, more_w = dW && L.w_ranges > 1;
+    if (more_a || more_w) {
+      err = agmm::launch_sum_ranges(more_a ? &sa : nullptr, more_w ? &sw : nullptr, dtype, s);
+      if (err != hipSuccess) return hip_err(err, "gradient sums launch");
+    }
+    if (dbias) {
+      agmm::SumColumns b{};
+      b.sums = L.b_sums;
+      b.groups = cdiv(m, agmm::kDRows);
+      b.cols = b.first = cols();
+      b.out = dbias;
+      b.dtype = dtype;
+      err = agmm::launch_sum_columns(b, s);
+      if (err != hipSuccess) return hip_err(err, "bias gradient launch");
+    }
+    return AGMM_OK;
+  }
+};
+
+namespace {
+
+// Rows and columns: a launch of the column sums stays below 2^22 workgroups of
+// 1024 threads.
+constexpr int64_t kNormRows = int64_t(1) << 28;
+constexpr int64_t kNormCols = int64_t(1) << 26;
+constexpr int64_t kNormElems = int64_t(1) << 37;
+
+int validate_norm(int64_t rows, int64_t cols, int dtype, int wtype) {
+  if (rows < 1 || cols < 1)
+    return set_err(AGMM_ERR_INVALID_ARG, "sizes must be >= 1 (rows=%lld, cols=%lld)", (long long)rows, (long long)cols);
+  if (dtype != AGMM_BF16 && dtype != AGMM_FP16 && dtype != AGMM_FP32) return set_err(AGMM_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (wtype != AGMM_BF16 && wtype != AGMM_FP16 && wtype != AGMM_FP32)
+    return set_err(AGMM_ERR_INVALID_ARG, "unknown weight dtype %d", wtype);
+  if (wtype != dtype && wtype != AGMM_FP32)
+    return set_err(AGMM_ERR_UNSUPPORTED, "weights have the rows' dtype %d or fp32 (got %d)", dtype, wtype);
+  if (rows >= kNormRows || cols >= kNormCols || rows * cols >= kNormElems)
+    return set_err(AGMM_ERR_UNSUPPORTED, "matrix too large (rows=%lld, cols=%lld)", (long long)rows, (long long)cols);
+  return ok();
+}
+
+}  // namespace
+
+struct agmm_norm_plan : PlanBase {
+  int64_t rows = 0, cols = 0;
+  int dtype = 0, wtype = 0, groups = 0;
+  int64_t ldx = 0, ldy = 0, lddy = 0, lddx = 0;   // 0: dense
+  uintptr_t elem() const { return dtype == AGMM_FP32 ? 4 : 2; }
+  uintptr_t weight_elem() const { return wtype == AGMM_FP32 ? 4 : 2; }
+  agmm::NormProblem problem(const void* x, const void* weight) const {
+    agmm::NormProblem p{};
+    p.rows = rows;
+    p.cols = cols;
+    p.dtype = dtype;
+    p.wtype = wtype;
+    p.x = x;
+    p.ldx = ldx ? ldx : cols;
+    p.weight = weight;
+    p.groups = groups;
+    return p;
+  }
+};
+
+extern "C" {
+
+int agmm_ff_plan_validate(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_local, int dtype, int activation, int gated) {
+  return validate_ff(num_shards, m_per_shard, k, n_local, dtype, activation, gated);
+}
+
+agmm_ff_plan_t agmm_ff_plan_create(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_local, int dtype, int activation,
+                                   int gated, int with_gradient) {
+  if (validate_ff(num_shards, m_per_shard, k, n_local, dtype, activation, gated) != AGMM_OK) return nullptr;
+  agmm_ff_plan* p = new (std::nothrow) agmm_ff_plan();
+  if (!p) {
+    set_err(AGMM_ERR_OOM, "out of host memory");
+    return nullptr;
+  }
+  p->N = num_shards;
+  p->m_s = m_per_shard;
+  p->k = k;
+  p->n = n_local;
+  p->m = num_shards * m_per_shard;
+  p->dtype = dtype;
+  p->act = activation;
+  p->parts = 1 + gated;
+  p->with_gradient = with_gradient != 0;
+  if (p->init() != AGMM_OK || p->apply() != AGMM_OK) {
+    const int st = agmm::g_status;
+    const std::string msg = agmm::g_msg;
+    delete p;
+    set_err(st, "%s", msg.c_str());
+    return nullptr;
+  }
+  ok();
+  return p;
+}
+
+int agmm_ff_plan_set_int(agmm_ff_plan_t p, const char* key, int64_t v) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!key) return set_err(AGMM_ERR_INVALID_ARG, "key is NULL");
+  std::lock_guard<std::mutex> lk(p->mu);
+  if (p->captured)
+    return set_err(AGMM_ERR_UNSUPPORTED,
+                   "the plan has been captured into a graph; its settings are fixed (create a new plan)");
+  const std::string k(key);
+  const auto bad = [&]() {
+    return set_err(AGMM_ERR_INVALID_ARG, "value %lld out of range for key '%s'", (long long)v, key);
+  };
+  int64_t* field = nullptr;
+  if (k == "lda" || k == "ldw" || k == "ldda" || k == "lddw") {
+    if (v != 0 && (v < p->k || v >= kDimLimit)) return bad();
+    field = k == "lda" ? &p->lda : k == "ldw" ? &p->ldw : k == "ldda" ? &p->ldda : &p->lddw;
+  } else if (k == "ldr" || k == "ldy" || k == "lddy") {
+    if (v != 0 && (v < p->n || v >= kDimLimit)) return bad();
+    field = k == "ldr" ? &p->ldr : k == "ldy" ? &p->ldy : &p->lddy;
+  } else if (k == "tile") {
+    if (v != -1 && v != 64 && v != 128 && v != 256) return bad();
+    if (v == 64 && !p->few_fits()) return set_err(AGMM_ERR_UNSUPPORTED, "too many workgroups for tile 64");
+    field = &p->tile_key;
+  } else {
+    return set_err(AGMM_ERR_INVALID_ARG, "unknown key '%s'", key);
+  }
+  const int64_t old = *field;
+  *field = v;
+  if (p->apply() != AGMM_OK) {   // the plan keeps its settings and workspace
+    *field = old;
+    return agmm::g_status;
+  }
+  return ok();
+}
+
+int agmm_ff_plan_get_int(agmm_ff_plan_t p, const char* key, int64_t* value) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!key || !value) return set_err(AGMM_ERR_INVALID_ARG, "key or value is NULL");
+  std::lock_guard<std::mutex> lk(p->mu);
+  const std::string k(key);
+  if (k == "lda") *value = p->ld_a();
+  else if (k == "ldw") *value = p->ld_w();
+  else if (k == "ldda") *value = p->ldda ? p->ldda : p->k;
+  else if (k == "lddw") *value = p->lddw ? p->lddw : p->k;
+  else if (k == "ldr") *value = p->ldr ? p->ldr : p->n;
+  else if (k == "ldy") *value = p->ldy ? p->ldy : p->n;
+  else if (k == "lddy") *value = p->lddy ? p->lddy : p->n;
+  else if (k == "saved_cols") *value = p->wide();
+  else if (k == "tile") *value = p->layout(false, nullptr).tile;
+  else if (k == "captured") *value = p->captured;
+  else return set_err(AGMM_ERR_INVALID_ARG, "unknown key '%s'", key);
+  return ok();
+}
+
+size_t agmm_ff_plan_workspace_bytes(agmm_ff_plan_t p) { return p ? p->ws_bytes : 0; }
+
+int agmm_ff_forward(agmm_ff_plan_t p, const void* const* shard_ptrs, const void* W, const void* bias, const void* residual, void* Y,
+                    void* saved, void* saved_scales, void* stream) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!shard_ptrs) return set_err(AGMM_ERR_INVALID_ARG, "shard_ptrs is NULL");
+  int rc = AGMM_OK;
+  for (int r = 0; r < p->N && rc == AGMM_OK; ++r) rc = check_ptr(shard_ptrs[r], "shard_ptrs", r, 16);
+  if (rc == AGMM_OK) rc = check_ptr(W, "W", -1, 16);
+  if (rc == AGMM_OK && bias) rc = check_ptr(bias, "bias", -1, 2);
+  if (rc == AGMM_OK && residual) rc = check_ptr(residual, "residual", -1, 2);
+  if (rc == AGMM_OK) rc = check_ptr(Y, "Y", -1, 2);
+  if (rc == AGMM_OK && saved) rc = check_ptr(saved, "saved", -1, 16);
+  if (rc != AGMM_OK) return rc;
+  if (residual && p->parts == 2) return set_err(AGMM_ERR_UNSUPPORTED, "a gated product takes no residual");
+  if (saved_scales && !saved) return set_err(AGMM_ERR_INVALID_ARG, "saved_scales without saved");
+  std::lock_guard<std::mutex> lk(p->mu);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const agmm_ff_plan::Layout L = p->layout(false, p->ws);
+  return p->run(s, L.a || L.w, [&] { return p->forward(L, shard_ptrs, W, bias, residual, Y, saved, saved_scales, s); });
+}
+
+// Whether the plan's way back needs kept pre-activations.
+static int check_saved(agmm_ff_plan_t p, const void* saved, const void* saved_scales) {
+  if (!saved && saved_scales) return set_err(AGMM_ERR_INVALID_ARG, "saved_scales without saved");
+  if (saved) return check_ptr(saved, "saved", -1, 16);
+  if (p->parts == 2 || p->act != AGMM_ACT_NONE) return set_err(AGMM_ERR_INVALID_ARG, "saved is NULL");
+  return AGMM_OK;
+}
+
+int agmm_ff_backward(agmm_ff_plan_t p, const void* const* shard_ptrs, const void* W, const void* saved, const void* saved_scales,
+                     const void* dY, void* dA, void* dW, void* dbias, void* stream) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!p->with_gradient) return set_err(AGMM_ERR_UNSUPPORTED, "the plan was created without the gradient's workspace");
+  if (!dA && !dW && !dbias) return set_err(AGMM_ERR_INVALID_ARG, "dA, dW and dbias are all NULL");
+  int rc = AGMM_OK;
+  if (dW) {
+    if (!shard_ptrs) return set_err(AGMM_ERR_INVALID_ARG, "shard_ptrs is NULL");
+    for (int r = 0; r < p->N && rc == AGMM_OK; ++r) rc = check_ptr(shard_ptrs[r], "shard_ptrs", r, 16);
+  }
+  if (rc == AGMM_OK && dA) rc = check_ptr(W, "W", -1, 16);
+  if (rc == AGMM_OK) rc = check_saved(p, saved, saved_scales);
+  if (rc == AGMM_OK) rc = check_ptr(dY, "dY", -1, 2);
+  if (rc == AGMM_OK && dA) rc = check_ptr(dA, "dA", -1, 2);
+  if (rc == AGMM_OK && dW) rc = check_ptr(dW, "dW", -1, 2);
+  if (rc == AGMM_OK && dbias) rc = check_ptr(dbias, "dbias", -1, 2);
+  if (rc != AGMM_OK) return rc;
+  std::lock_guard<std::mutex> lk(p->mu);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return p->run(s, true, [&] { return p->backward(shard_ptrs, W, saved, saved_scales, dY, dA, dW, dbias, s); });
+}
+
+int agmm_ff_recompute(agmm_ff_plan_t p, const void* saved, const void* saved_scales, void* Y, void* stream) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  int rc = check_ptr(saved, "saved", -1, 16);
+  if (rc == AGMM_OK) rc = check_ptr(Y, "Y", -1, 2);
+  if (rc != AGMM_OK) return rc;
+  std::lock_guard<std::mutex> lk(p->mu);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  agmm::FeedAgainProblem a{};
+  a.m = p->m;
+  a.n = (int32_t)p->n;
+  a.gated = p->parts == 2;
+  a.act = activation_of(p->act);
+  a.kept = p->kept_rows(saved, saved_scales);
+  a.y = Y;
+  a.ldy = p->ldy ? p->ldy : p->n;
+  return p->run(s, false, [&]() -> int {
+    const hipError_t err = agmm::launch_feed_again(a, p->dtype, s);
+    return err == hipSuccess ? AGMM_OK : hip_err(err, "recompute launch");
+  });
+}
+
+void agmm_ff_plan_destroy(agmm_ff_plan_t p) { delete p; }
+
+int agmm_norm_plan_validate(int64_t rows, int64_t cols, int dtype, int weight_dtype) {
+  return validate_norm(rows, cols, dtype, weight_dtype);
+}
+
+agmm_norm_plan_t agmm_norm_plan_create(int64_t rows, int64_t cols, int dtype, int weight_dtype) {
+  if (validate_norm(rows, cols, dtype, weight_dtype) != AGMM_OK) return nullptr;
+  agmm_norm_plan* p = new (std::nothrow) agmm_norm_plan();
+  if (!p) {
+    set_err(AGMM_ERR_OOM, "out of host memory");
+    return nullptr;
+  }
+  p->rows = rows;
+  p->cols = cols;
+  p->dtype = dtype;
+  p->wtype = weight_dtype;
+  int rc = p->init();
+  if (rc == AGMM_OK) {
+    p->groups = agmm::norm_groups(rows, cols, dtype, p->cu_count);
+    rc = p->reserve((size_t)p->groups * 2 * cols * sizeof(float));
+  }
+  if (rc != AGMM_OK) {
+    const int st = agmm::g_status;
+    const std::string msg = agmm::g_msg;
+    delete p;
+    set_err(st, "%s", msg.c_str());
+    return nullptr;
+  }
+  ok();
+  return p;
+}
+
+int agmm_norm_plan_set_int(agmm_norm_plan_t p, const char* key, int64_t v) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!key) return set_err(AGMM_ERR_INVALID_ARG, "key is NULL");
+  std::lock_guard<std::mutex> lk(p->mu);
+  if (p->captured)
+    return set_err(AGMM_ERR_UNSUPPORTED,
+                   "the plan has been captured into a graph; its settings are fixed (create a new plan)");
+  const std::string k(key);
+  int64_t* field = k == "ldx" ? &p->ldx : k == "ldy" ? &p->ldy : k == "lddy" ? &p->lddy : k == "lddx" ? &p->lddx : nullptr;
+  if (!field) return set_err(AGMM_ERR_INVALID_ARG, "unknown key '%s'", key);
+  if (v != 0 && (v < p->cols || v >= kDimLimit))
+    return set_err(AGMM_ERR_INVALID_ARG, "value %lld out of range for key '%s'", (long long)v, key);
+  *field = v;
+  return ok();
+}
+
+int agmm_norm_plan_get_int(agmm_norm_plan_t p, const char* key, int64_t* value) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!key || !value) return set_err(AGMM_ERR_INVALID_ARG, "key or value is NULL");
+  std::lock_guard<std::mutex> lk(p->mu);
+  const std::string k(key);
+  if (k == "ldx") *value = p->ldx ? p->ldx : p->cols;
+  else if (k == "ldy") *value = p->ldy ? p->ldy : p->cols;
+  else if (k == "lddy") *value = p->lddy ? p->lddy : p->cols;
+  else if (k == "lddx") *value = p->lddx ? p->lddx : p->cols;
+  else if (k == "captured") *value = p->captured;
+  else return set_err(AGMM_ERR_INVALID_ARG, "unknown key '%s'", key);
+  return ok();
+}
+
+size_t agmm_norm_plan_workspace_bytes(agmm_norm_plan_t p) { return p ? p->ws_bytes : 0; }
+
+int agmm_norm_forward(agmm_norm_plan_t p, const void* x, const void* weight, const void* bias, float eps, void* y, float* mean,
+                      float* rstd, void* stream) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  int rc = check_ptr(x, "x", -1, p->elem());
+  if (rc == AGMM_OK && weight) rc = check_ptr(weight, "weight", -1, p->weight_elem());
+  if (rc == AGMM_OK && bias) rc = check_ptr(bias, "bias", -1, p->weight_elem());
+  if (rc == AGMM_OK) rc = check_ptr(y, "y", -1, p->elem());
+  if (rc == AGMM_OK && mean) rc = check_ptr(mean, "mean", -1, 4);
+  if (rc == AGMM_OK && rstd) rc = check_ptr(rstd, "rstd", -1, 4);
+  if (rc != AGMM_OK) return rc;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return set_err(AGMM_ERR_INVALID_ARG, "eps must be a finite number >= 0 (got %g)", (double)eps);
+  std::lock_guard<std::mutex> lk(p->mu);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  agmm::NormProblem n = p->problem(x, weight);
+  n.bias = bias;
+  n.eps = eps;
+  n.y = y;
+  n.ldy = p->ldy ? p->ldy : p->cols;
+  n.mean = mean;
+  n.rstd = rstd;
+  return p->run(s, false, [&]() -> int {
+    const hipError_t err = agmm::launch_norm_forward(n, s);
+    return err == hipSuccess ? AGMM_OK : hip_err(err, "norm launch");
+  });
+}
+
+int agmm_norm_backward(agmm_norm_plan_t p, const void* x, const void* dy, const void* weight, const float* mean, const float* rstd,
+                       void* dx, void* dweight, void* dbias, void* stream) {
+  if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (!dx && !dweight && !dbias) return set_err(AGMM_ERR_INVALID_ARG, "dx, dweight and dbias are all NULL");
+  int rc = check_ptr(x, "x", -1, p->elem());
+  if (rc == AGMM_OK) rc = check_ptr(dy, "dy", -1, p->elem());
+  if (rc == AGMM_OK && weight) rc = check_ptr(weight, "weight", -1, p->weight_elem());
+  if (rc == AGMM_OK) rc = check_ptr(mean, "mean", -1, 4);
+  if (rc == AGMM_OK) rc = check_ptr(rstd, "rstd", -1, 4);
+  if (rc == AGMM_OK && dx) rc = check_ptr(dx, "dx", -1, p->elem());
+  if (rc == AGMM_OK && dweight) rc = check_ptr(dweight, "dweight", -1, p->weight_elem());
+  if (rc == AGMM_OK && dbias) rc = check_ptr(dbias, "dbias", -1, p->weight_elem());
+  if (rc != AGMM_OK) return rc;
+  std::lock_guard<std::mutex> lk(p->mu);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool sums = dweight || dbias;
+  agmm::NormProblem n = p->problem(x, weight);
+  n.dy = dy;
+  n.lddy = p->lddy ? p->lddy : p->cols;
+  n.mean = const_cast<float*>(mean);
+  n.rstd = const_cast<float*>(rstd);
+  n.dx = dx;
+  n.lddx = p->lddx ? p->lddx : p->cols;
+  n.sums = sums ? reinterpret_cast<float*>(p->ws) : nullptr;
+  return p->run(s, sums, [&]() -> int {
+    hipError_t err = agmm::launch_norm_backward(n, s);
+    if (err != hipSuccess) return hip_err(err, "norm gradient launch");
+    if (!sums) return AGMM_OK;
+    agmm::SumColumns c{};
+    c.sums = n.sums;
+    c.groups = p->groups;
+    c.cols = 2 * p->cols;
+    c.first = p->cols;
+    c.out = dweight;
+    c.out2 = dbias;
+    c.dtype = p->wtype;
+    err = agmm::launch_sum_columns(c, s);
+    return err == hipSuccess ? AGMM_OK : hip_err(err, "norm weight gradient launch");
+  });
+}
+
+void agmm_norm_plan_destroy(agmm_norm_plan_t p) { delete p; }
+
+}  // extern "C"

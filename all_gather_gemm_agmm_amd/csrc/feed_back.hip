@@ -1,0 +1,286 @@
+// The way back through the product with an epilogue and the gated product,
+// elementwise part (gfx950):
+//
+//     d = dy act'(p)     or, gated,     d_0 = dy p_1 act'(p_0),  d_1 = dy act(p_0)
+//
+// from the kept pre-activations, as 16-bit operands of the two gradient
+// products, by rows [m][parts * n] for dA = d W and transposed [parts * n][m]
+// for dW = d^T A, and the column sums of d for the bias.  A workgroup takes 128
+// rows x 64 columns of y: 16-byte pieces of rows in, d by rows out of the same
+// registers, and through LDS and transposing reads out again by columns.  Bound:
+// HBM, every value read once and d written twice (that the matrix cores can
+// read both operands along k).  d is rounded to the operands' type, as every
+// other operand of these products is; its sums are taken before that, in fp32.
+//
+// What is read again as fp32 sums over ranges of k, or over blocks of rows, is
+// added in a fixed order.
+#include "feed_device.h"
+
+namespace agmm {
+
+namespace {
+
+// Eight kept pre-activations of one part.
+template <int DT>
+__device__ __forceinline__ void kept8(const KeptRows& k, int64_t at, float (&v)[8]) {
+  if (k.scales) {
+    const u32x2_t q = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(k.values) + at);
+    const float s = scale_value(k.scales[at / kKeptBlock]);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      v[4 * w + 0] = __builtin_amdgcn_cvt_f32_fp8((int)q[w], 0) * s;
+      v[4 * w + 1] = __builtin_amdgcn_cvt_f32_fp8((int)q[w], 1) * s;
+      v[4 * w + 2] = __builtin_amdgcn_cvt_f32_fp8((int)q[w], 2) * s;
+      v[4 * w + 3] = __builtin_amdgcn_cvt_f32_fp8((int)q[w], 3) * s;
+    }
+  } else {
+    const u32x4_t q = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(k.values) + at);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e & 1 ? high16<DT>(q[e >> 1]) : low16<DT>(q[e >> 1]);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack8(u32x4_t q, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e & 1 ? high16<DT>(q[e >> 1]) : low16<DT>(q[e >> 1]);
+}
+template <int DT>
+__device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
+  return u32x4_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
+}
+
+template <int DT, bool GATED>
+__global__ __launch_bounds__(256) void feed_d_kernel(FeedDProblem p) {
+  constexpr int PARTS = GATED ? 2 : 1, RB = kDCols * 2, CH = RB / 16;
+  __shared__ __attribute__((aligned(1024))) char smem[PARTS * kDRows * RB];
+  __shared__ float sums[4][PARTS][kDCols];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int ncb = (p.n + kDCols - 1) / kDCols;
+  const int64_t rb = blockIdx.x / (unsigned)ncb;
+  const int cb = (int)(blockIdx.x - rb * ncb);
+  const int64_t m0 = rb * kDRows;
+  const int c = tid & 7, col = cb * kDCols + 8 * c, left = p.n - col;
+  const float c1 = p.act.c1, c3 = p.act.c3;
+  float total[PARTS][8] = {};
+  with_kind(p.act.kind, [&](auto kind) {
+    constexpr int KIND = decltype(kind)::value;
+#pragma unroll
+    for (int pass = 0; pass < kDRows / 32; ++pass) {
+      const int r = pass * 32 + (tid >> 3);
+      const int64_t row = m0 + r;
+      float d[PARTS][8] = {};
+      if (row < p.m && left > 0) {
+        float dy[8];
+        unpack8<DT>(load8(static_cast<const uint16_t*>(p.dy) + row * p.lddy + col, left), dy);
+        float x[8], u[8];
+        if (KIND != kActLinear || GATED) kept8<DT>(p.kept, row * PARTS * p.kept.wide + col, x);
+        if constexpr (GATED) kept8<DT>(p.kept, (row * PARTS + 1) * p.kept.wide + col, u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float value, slope;
+          if (KIND == kActLinear && !GATED) {
+            d[0][e] = dy[e];
+          } else {
+            act_both<KIND>(x[e], c1, c3, value, slope);
+            d[0][e] = dy[e] * (GATED ? u[e] * slope : slope);
+            if constexpr (GATED) d[1][e] = dy[e] * value;
+          }
+          if (e >= left)
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h) d[h][e] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) {
+        const u32x4_t w = pack8<DT>(d[h]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) total[h][e] += d[h][e];
+        if (p.dt) *reinterpret_cast<u32x4_t*>(smem + (h * kDRows + r) * RB + ((c ^ (r & (CH - 1))) << 4)) = w;
+        if (p.d && row < p.m && left > 0) {
+          uint16_t* out = static_cast<uint16_t*>(p.d) + row * p.ldd + (int64_t)h * p.n;
+          store8(out + col, w, left);
+          if (h == PARTS - 1 && left <= 8)   // the row's end, up to a whole 16-byte piece
+            for (int64_t e = p.n; h * (int64_t)p.n + e < p.ldd; ++e) out[e] = 0;
+        }
+      }
+    }
+  });
+  if (p.sums) {
+    // over the rows of the wave (lanes 8 apart hold the same columns), then the waves
+#pragma unroll
+    for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float t = total[h][e];
+        t += __shfl_xor(t, 8);
+        t += __shfl_xor(t, 16);
+        t += __shfl_xor(t, 32);
+        if (lane < 8) sums[wave][h][8 * c + e] = t;
+      }
+  }
+  __syncthreads();
+  if (p.sums && tid < PARTS * kDCols) {
+    const int h = tid / kDCols, x = tid % kDCols;
+    if (cb * kDCols + x < p.n)
+      p.sums[(rb * PARTS + h) * p.n + cb * kDCols + x] = (sums[0][h][x] + sums[1][h][x]) + (sums[2][h][x] + sums[3][h][x]);
+  }
+  if (p.dt) {
+    // Transposing reads: a wave takes 16 columns x 32 rows at a time, lane (g4,
+    // i16) the rows 8 g4 .. 8 g4 + 7 of column i16 (two reads of four rows, each
+    // lane of a group giving the address of row i16 / 4, columns 4 (i16 % 4) ..
+    // + 3 of the 4 x 16 block), 16 bytes of the column's row.
+    const int g4 = lane >> 4, i16 = lane & 15;
+    constexpr int UNITS = PARTS * (kDCols / 16) * (kDRows / 32);
+#pragma unroll
+    for (int q = 0; q < UNITS / 4; ++q) {
+      const int u = q * 4 + wave, h = u / (UNITS / PARTS), v = u % (UNITS / PARTS);
+      const int nb = (v / (kDRows / 32)) * 16, mb = (v % (kDRows / 32)) * 32 + 8 * g4;
+      u32x2_t half[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int r = mb + 4 * s + (i16 >> 2), x = nb + 4 * (i16 & 3);
+        half[s] = read_tr(smem + (h * kDRows + r) * RB + (((x >> 3) ^ (r & (CH - 1))) << 4) + (x & 4) * 2);
+      }
+      const int x = cb * kDCols + nb + i16;
+      if (x < p.n && m0 + mb < p.ldt)
+        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p.dt) + ((int64_t)h * p.n + x) * p.ldt + m0 + mb) =
+            u32x4_t{half[0][0], half[0][1], half[1][0], half[1][1]};
+    }
+  }
+}
+
+// y once more from the kept pre-activations, eight columns per thread.
+template <int DT>
+__global__ __launch_bounds__(256) void feed_again_kernel(FeedAgainProblem p) {
+  const uint32_t pieces = (uint32_t)((p.n + 7) / 8);
+  const int64_t all = p.m * pieces;
+  with_kind(p.act.kind, [&](auto kind) {
+    constexpr int KIND = decltype(kind)::value;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < all; u += (int64_t)gridDim.x * 256) {
+      const int64_t row = u / pieces;
+      const int col = (int)(u - row * pieces) * 8;
+      float x[8], f[8], y[8];
+      const int64_t at = row * (p.gated ? 2 : 1) * p.kept.wide + col;
+      kept8<DT>(p.kept, at, x);
+      if (p.gated) kept8<DT>(p.kept, at + p.kept.wide, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = act_value<KIND>(x[e], p.act.c1, p.act.c3);
+        if (p.gated) y[e] *= f[e];
+      }
+      store8(static_cast<uint16_t*>(p.y) + row * p.ldy + col, pack8<DT>(y), p.n - col);
+    }
+  });
+}
+
+struct SumPair {
+  SumRanges a, b;
+  int64_t a_pieces, pieces;
+};
+
+template <int DT>
+__global__ __launch_bounds__(256) void sum_ranges_kernel(SumPair s) {
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < s.pieces; u += (int64_t)gridDim.x * 256) {
+    const bool second = u >= s.a_pieces;
+    const SumRanges& c = second ? s.b : s.a;
+    const int64_t at = second ? u - s.a_pieces : u;
+    const int64_t n4 = (c.cols + 3) / 4, row = at / n4, col = (at - row * n4) * 4;
+    const int64_t plane = c.rows * n4 * 4;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    // eight ranges are on their way at a time, added in order
+    for (int q0 = 0; q0 < c.ranges; q0 += 8) {
+      f32x4_t w[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q0 + q < c.ranges) w[q] = *reinterpret_cast<const f32x4_t*>(c.sums + at * 4 + (q0 + q) * plane);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q0 + q < c.ranges) v += w[q];
+    }
+    store4(static_cast<uint16_t*>(c.out) + row * c.ldo + col, u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])},
+           (int)(c.cols - col < 4 ? c.cols - col : 4));
+  }
+}
+
+// 64 columns per workgroup, whose 16 waves share out the groups.
+__global__ __launch_bounds__(1024) void sum_columns_kernel(SumColumns p) {
+  __shared__ float part[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+  float t = 0.0f;
+  if (col < p.cols) {
+    int64_t g = wave;
+    for (; g + 112 < p.groups; g += 128) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = p.sums[(g + 16 * q) * p.cols + col];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) t += v[q];
+    }
+    for (; g < p.groups; g += 16) t += p.sums[g * p.cols + col];
+  }
+  part[wave][lane] = t;
+  __syncthreads();
+  if (wave || col >= p.cols) return;
+  float s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) s += part[w][lane];
+  const bool second = col >= p.first;
+  void* out = second ? p.out2 : p.out;
+  const int64_t at = second ? col - p.first : col;
+  if (!out) return;
+  if (p.dtype == kDtypeFp32) static_cast<float*>(out)[at] = s;
+  else static_cast<uint16_t*>(out)[at] = p.dtype == kDtypeBf16 ? cvt1<kDtypeBf16>(s) : cvt1<kDtypeFp16>(s);
+}
+
+constexpr int64_t kLoopGrid = 1 << 16;   // workgroups of the kernels that loop over their work
+
+}  // namespace
+
+hipError_t launch_feed_d(const FeedDProblem& p, int dtype, hipStream_t s) {
+  const int parts = p.gated ? 2 : 1;
+  const int64_t grid = (p.m + kDRows - 1) / kDRows * ((p.n + kDCols - 1) / kDCols);
+  if (p.m < 1 || p.n < 1 || grid >= kFeedGrid || (!p.kept.values && (p.gated || p.act.kind != kActLinear)) ||
+      (p.kept.values && p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock) ||
+      (p.d && (p.ldd < (int64_t)parts * p.n || p.ldd > (int64_t)parts * p.n + 7)) ||
+      (p.dt && (p.ldt % 8 != 0 || p.ldt < p.m || p.ldt > p.m + 7)) || (dtype != kDtypeBf16 && dtype != kDtypeFp16))
+    return hipErrorInvalidValue;
+  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, p); };
+  if (dtype == kDtypeBf16) p.gated ? go(feed_d_kernel<kDtypeBf16, true>) : go(feed_d_kernel<kDtypeBf16, false>);
+  else p.gated ? go(feed_d_kernel<kDtypeFp16, true>) : go(feed_d_kernel<kDtypeFp16, false>);
+  return hipGetLastError();
+}
+
+hipError_t launch_feed_again(const FeedAgainProblem& p, int dtype, hipStream_t s) {
+  if (p.m < 1 || p.n < 1 || !p.kept.values || (dtype != kDtypeBf16 && dtype != kDtypeFp16) ||
+      p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock)
+    return hipErrorInvalidValue;
+  const int64_t blocks = (p.m * ((p.n + 7) / 8) + 255) / 256;
+  const dim3 grid((unsigned)(blocks < kLoopGrid ? blocks : kLoopGrid));
+  if (dtype == kDtypeBf16) hipLaunchKernelGGL((feed_again_kernel<kDtypeBf16>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((feed_again_kernel<kDtypeFp16>), grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_sum_ranges(const SumRanges* a, const SumRanges* b, int dtype, hipStream_t s) {
+  SumPair c{};
+  if (a) c.a = *a, c.a_pieces = a->rows * ((a->cols + 3) / 4);
+  c.pieces = c.a_pieces;
+  if (b) c.b = *b, c.pieces += b->rows * ((b->cols + 3) / 4);
+  if (c.pieces < 1 || (dtype != kDtypeBf16 && dtype != kDtypeFp16)) return hipErrorInvalidValue;
+  const int64_t blocks = (c.pieces + 255) / 256;
+  const dim3 grid((unsigned)(blocks < kLoopGrid ? blocks : kLoopGrid));
+  if (dtype == kDtypeBf16) hipLaunchKernelGGL((sum_ranges_kernel<kDtypeBf16>), grid, dim3(256), 0, s, c);
+  else hipLaunchKernelGGL((sum_ranges_kernel<kDtypeFp16>), grid, dim3(256), 0, s, c);
+  return hipGetLastError();
+}
+
+hipError_t launch_sum_columns(const SumColumns& p, hipStream_t s) {
+  const int64_t grid = (p.cols + 63) / 64;
+  if (p.cols < 1 || p.groups < 1 || grid >= kFeedGrid / 4) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(sum_columns_kernel, dim3((unsigned)grid), dim3(1024), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace agmm

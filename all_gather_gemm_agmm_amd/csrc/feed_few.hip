@@ -1,0 +1,233 @@
+// Product with an epilogue, and the gated product: few rows (gfx950).
+//
+// FM x FN blocks of 16 rows x 16 tile columns per workgroup, whose waves share
+// out k, 64 elements at a time, and load their operands straight into
+// registers: 16-byte accesses to global memory may start at any word, which
+// loads into LDS may not, so k and the strides may be anything and nothing is
+// copied first.  The waves' sums are added in LDS in a fixed order, wave w
+// taking row block w, and bias, activation, product, residual and rounding
+// follow there (feed_tiles.hip says how).  Gated, blocks of 16 rows of the
+// first n rows of B and of the second n take turns.
+//
+// ODD (a stride is odd): rows that start in the middle of a word are read from
+// that word on, with one word more, and shifted; accesses that start there take
+// three times as long.
+#include "feed_device.h"
+
+namespace agmm {
+
+namespace {
+
+template <int DT, int FM, int FN, int UN, bool ODD, bool GATED>
+__global__ __launch_bounds__(256) void feed_few_kernel(FeedProblem fp) {
+  const GemmProblem& p = fp.gemm;
+  constexpr int PARTS = GATED ? 2 : 1, FQ = FN / PARTS;
+  __shared__ float part[4][FM][FN][4][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g4 = lane >> 4, i16 = lane & 15;
+  const int M = p.m, NC = fp.n, K = p.k;
+  const int cb = (int)blockIdx.x / p.order.num_rb, rb = (int)blockIdx.x - cb * p.order.num_rb;
+  const int m0 = rb * 16 * FM, y0 = cb * 16 * FQ;
+  // rows and columns past the end read the last one and are never used
+  const uint16_t *a[FM], *b[FN];
+#pragma unroll
+  for (int f = 0; f < FM; ++f) {
+    const int i = min(m0 + 16 * f + i16, M - 1), g = i / p.rows.rows_per_group;
+    a[f] = static_cast<const uint16_t*>(p.rows.a_group[g]) + (int64_t)(i - g * p.rows.rows_per_group) * p.rows.a_ld + 8 * g4;
+  }
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+    b[f] = static_cast<const uint16_t*>(p.b) + 8 * g4 +
+           ((int64_t)(f % PARTS) * NC + min(y0 + 16 * (f / PARTS) + i16, NC - 1)) * p.ldb;
+
+  f32x4_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const auto multiply = [&](const u32x4_t (&fa)[FM], const u32x4_t (&fb)[FN]) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = mfma16_builtin<DT>(fb[j], fa[i], acc[i][j]);
+  };
+  // halves 2u, 2u + 1 of piece c + u: elements 64 (c + u) + 32 h + 8 g4 on;
+  // ODD: their words and the one behind
+  constexpr int W = ODD ? 2 * UN : 1;
+  typedef u32x4_t u32x4_word_t __attribute__((aligned(4)));
+  const auto load = [&](int c, u32x4_t (&fa)[2 * UN][FM], u32x4_t (&fb)[2 * UN][FN], uint32_t (&wa)[W][FM], uint32_t (&wb)[W][FN]) {
+    const auto one = [&](const uint16_t* x, u32x4_t& v, uint32_t& w) {
+      if constexpr (ODD) {
+        const char* q = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(x) & ~uintptr_t(2));
+        v = *reinterpret_cast<const u32x4_word_t*>(q);
+        w = *reinterpret_cast<const uint32_t*>(q + 16);
+      } else {
+        v = *reinterpret_cast<const u32x4_word_t*>(x);
+      }
+    };
+#pragma unroll
+    for (int h = 0; h < 2 * UN; ++h) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) one(b[j] + (int64_t)c * 64 + 32 * h, fb[h][j], wb[ODD ? h : 0][j]);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) one(a[i] + (int64_t)c * 64 + 32 * h, fa[h][i], wa[ODD ? h : 0][i]);
+    }
+  };
+  const auto shift = [&](const uint16_t* x, u32x4_t& v, uint32_t w) {
+    const uint32_t by = (uint32_t)reinterpret_cast<uintptr_t>(x) & 2;
+    v = u32x4_t{__builtin_amdgcn_alignbyte(v[1], v[0], by), __builtin_amdgcn_alignbyte(v[2], v[1], by),
+                __builtin_amdgcn_alignbyte(v[3], v[2], by), __builtin_amdgcn_alignbyte(w, v[3], by)};
+  };
+  const auto use = [&](u32x4_t (&fa)[2 * UN][FM], u32x4_t (&fb)[2 * UN][FN], const uint32_t (&wa)[W][FM], const uint32_t (&wb)[W][FN]) {
+#pragma unroll
+    for (int h = 0; h < 2 * UN; ++h) {
+      if constexpr (ODD) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) shift(b[j], fb[h][j], wb[h][j]);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) shift(a[i], fa[h][i], wa[h][i]);
+      }
+      multiply(fa[h], fb[h]);
+    }
+  };
+  const int pieces = (ODD ? max(K - 2, 0) : K) / 64, groups = pieces / UN;   // the word behind lies in the row
+  u32x4_t fa[2][2 * UN][FM], fb[2][2 * UN][FN];
+  uint32_t wa[2][W][FM], wb[2][W][FN];
+  if (wave < groups) load(wave * UN, fa[0], fb[0], wa[0], wb[0]);
+  for (int c = wave; c < groups; c += 8) {
+    // two groups per turn, the last one loaded again where there is none
+    load((c + 4 < groups ? c + 4 : c) * UN, fa[1], fb[1], wa[1], wb[1]);
+    use(fa[0], fb[0], wa[0], wb[0]);
+    if (c + 4 >= groups) break;
+    load((c + 8 < groups ? c + 8 : c) * UN, fa[0], fb[0], wa[0], wb[0]);
+    use(fa[1], fb[1], wa[1], wb[1]);
+  }
+  // what is left: halves of 32 elements, shared out over the waves, those
+  // past k elementwise and zero
+  for (int at = groups * UN * 64 + 32 * wave; at < K; at += 128) {
+    u32x4_t ta[FM], tb[FN];
+    const int left = K - at - 8 * g4;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) tb[j] = load8(b[j] + at, left);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) ta[i] = load8(a[i] + at, left);
+    multiply(ta, tb);
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[wave][i][j][e][lane] = acc[i][j][e];
+  __syncthreads();
+  if (wave >= FM) return;
+  const int row = m0 + 16 * wave + i16;
+  const bool in = row < M;
+  float x[FN][4];
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int c = y0 + 16 * (j / PARTS) + 4 * g4, left = NC - c;
+    f32x4_t b4 = {0.f, 0.f, 0.f, 0.f};
+    if (fp.bias) b4 = load4<DT>(static_cast<const uint16_t*>(fp.bias) + (int64_t)(j % PARTS) * NC + c, left);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x[j][e] = (part[0][wave][j][e][lane] + part[1][wave][j][e][lane] + part[2][wave][j][e][lane] + part[3][wave][j][e][lane]) + b4[e];
+  }
+  if (fp.kept.values) {
+    const int64_t wide = fp.kept.wide;
+    // blocks of 32 columns of a part: two accumulator blocks (launched with FN 4)
+#pragma unroll
+    for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+      for (int q = 0; q + 1 < FQ; q += 2) {
+        float w[2][4], size = 0.0f;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[s][e] = y0 + 16 * (q + s) + 4 * g4 + e < NC ? x[PARTS * (q + s) + h][e] : 0.0f;
+            size = larger_finite(size, w[s][e]);
+          }
+        size = fmaxf(size, __shfl_xor(size, 16));
+        size = fmaxf(size, __shfl_xor(size, 32));
+        const uint32_t code = scale_code(size);
+        const float inv = scale_inverse(code);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int c = y0 + 16 * (q + s) + 4 * g4;
+          const int64_t out = ((int64_t)row * PARTS + h) * wide + c;
+          if (!in || c >= wide) continue;
+          if (fp.kept.scales)
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(fp.kept.values) + out) =
+                pack4_e4m3(w[s][0], w[s][1], w[s][2], w[s][3], inv);
+          else
+            *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(fp.kept.values) + out) =
+                u32x2_t{pack2<DT>(w[s][0], w[s][1]), pack2<DT>(w[s][2], w[s][3])};
+          if (fp.kept.scales && s == 0 && g4 == 0) fp.kept.scales[out / kKeptBlock] = (uint8_t)code;
+        }
+      }
+  }
+  if (!in) return;
+  with_kind(fp.act.kind, [&](auto kind) {
+    constexpr int KIND = decltype(kind)::value;
+#pragma unroll
+    for (int q = 0; q < FQ; ++q) {
+      const int c = y0 + 16 * q + 4 * g4, left = NC - c;
+      if (left <= 0) continue;
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[e] = act_value<KIND>(x[PARTS * q][e], fp.act.c1, fp.act.c3);
+        if constexpr (GATED) y[e] *= x[PARTS * q + PARTS - 1][e];
+      }
+      if (!GATED && fp.residual) {
+        const f32x4_t r = load4<DT>(static_cast<const uint16_t*>(fp.residual) + (int64_t)row * fp.ldr + c, left);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += r[e];
+      }
+      store4(static_cast<uint16_t*>(fp.y) + (int64_t)row * fp.ldy + c, u32x2_t{pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3])}, left);
+    }
+  });
+}
+
+template <int DT, int FM, int FN, int UN, bool GATED>
+void launch_shape(const FeedProblem& p, unsigned grid, hipStream_t s) {
+  const bool odd = p.gemm.ldb % 2 != 0 || p.gemm.rows.a_ld % 2 != 0;
+  if (odd) hipLaunchKernelGGL((feed_few_kernel<DT, FM, FN, UN, true, GATED>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((feed_few_kernel<DT, FM, FN, UN, false, GATED>), dim3(grid), dim3(256), 0, s, p);
+}
+
+template <int DT>
+hipError_t launch_type(const FeedProblem& p, int fm, int fn, unsigned grid, hipStream_t s) {
+  if (p.gated) {
+    if (fm == 1 && fn == 2) launch_shape<DT, 1, 2, 4, true>(p, grid, s);
+    else if (fm == 1) launch_shape<DT, 1, 4, 2, true>(p, grid, s);
+    else if (fn == 2) launch_shape<DT, 4, 2, 1, true>(p, grid, s);
+    else launch_shape<DT, 4, 4, 1, true>(p, grid, s);
+  } else {
+    if (fm == 1 && fn == 1) launch_shape<DT, 1, 1, 4, false>(p, grid, s);
+    else if (fm == 1 && fn == 2) launch_shape<DT, 1, 2, 4, false>(p, grid, s);
+    else if (fm == 1) launch_shape<DT, 1, 4, 2, false>(p, grid, s);
+    else if (fn == 1) launch_shape<DT, 4, 1, 2, false>(p, grid, s);
+    else if (fn == 2) launch_shape<DT, 4, 2, 1, false>(p, grid, s);
+    else launch_shape<DT, 4, 4, 1, false>(p, grid, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_feed_few(const FeedProblem& p, int fm, int fn, int dtype, hipStream_t stream) {
+  const int64_t grid = (int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb;
+  const int64_t cols = p.gated ? 2 * (((int64_t)p.n + 15) / 16 * 16) : p.n;
+  if ((fm != 1 && fm != 4) || (fn != 1 && fn != 2 && fn != 4) || (p.gated && (fn == 1 || p.residual)) || p.gemm.n != cols ||
+      p.gemm.order.num_rb != (p.gemm.m + 16 * fm - 1) / (16 * fm) || p.gemm.order.num_cb != (cols + 16 * fn - 1) / (16 * fn) ||
+      grid < 1 || grid >= kFeedGrid || (int64_t)p.gemm.rows.num_groups * p.gemm.rows.rows_per_group != p.gemm.m ||
+      (p.kept.values && p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock) ||
+      (p.kept.values && fn != 4))
+    return hipErrorInvalidValue;
+  return dtype == kDtypeBf16 ? launch_type<kDtypeBf16>(p, fm, fn, (unsigned)grid, stream)
+       : dtype == kDtypeFp16 ? launch_type<kDtypeFp16>(p, fm, fn, (unsigned)grid, stream) : hipErrorInvalidValue;
+}
+
+}  // namespace agmm

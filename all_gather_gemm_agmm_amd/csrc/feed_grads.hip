@@ -1,0 +1,112 @@
+// The way back through the product with an epilogue and the gated product, the
+// two products (gfx950), on the 16-bit d that feed_d_kernel leaves:
+//
+//     dA = d W        (rows of d [m][parts * n], W k x n as stored)
+//     dW = d^T A      (d transposed [parts * n][m], A k x n as gathered)
+//
+// Both are the part-ring GEMM (gemm_m16_loop.inc) with B stored k x n and
+// share a launch: with few rows neither fills the CUs alone.  Where few output
+// tiles would leave CUs idle, a product's sum is cut into ranges, whose fp32
+// sums a last pass adds in order and rounds; otherwise the tile is rounded and
+// stored here, whole rows through LDS.  Bound: MFMA.
+#include "feed_device.h"
+
+namespace agmm {
+
+namespace {
+
+struct FeedPair {
+  GemmProblem a, w;        // dA and dW
+  int32_t a_tiles;         // workgroups of dA: the first ones
+};
+
+template <int BM, int BN, int DT, int OCC>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
+void feed_grads_kernel(FeedPair gp) {
+  constexpr bool BT = false, SPLIT = true;
+  constexpr int BK = 64, WAVES = 4;
+  using T = GemmTile<BM, BN, BK, DT, BT, 5, WAVES, kLoopParts>;
+  constexpr int kBK = BK;
+  constexpr int FM = T::TM / 16, FN = T::TN / 16;
+  constexpr int STEPS = BK / 32;
+  __shared__ __attribute__((aligned(1024))) char smem[T::LDS_BYTES];
+  const bool is_a = (int)blockIdx.x < gp.a_tiles;
+  const GemmProblem& p = is_a ? gp.a : gp.w;
+
+#define AGMM_TILE_ID (is_a ? (int)blockIdx.x : (int)blockIdx.x - gp.a_tiles)
+#include "gemm_m16_loop.inc"
+
+  if (p.splits > 1) {
+    // rows of the sums are whole 16-byte vectors; what lies past n in the last
+    // one is never used
+    const int row0 = m0 + wm * T::TM + i16, col0 = n0 + wn * T::TN + 4 * g4;
+    const int64_t ld = (N + 3) & ~3;
+    float* base = p.partials + ((int64_t)split * M + row0) * ld + col0;
+#pragma unroll
+    for (int i = 0; i < FM; ++i, base += 16 * ld) {
+      if (row0 + 16 * i < M)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          if (col0 + 16 * j < N) *reinterpret_cast<f32x4_t*>(base + 16 * j) = acc[i][j];
+      __builtin_amdgcn_sched_barrier(0);   // one block row's values at a time
+    }
+  } else {
+    constexpr int RB = BN * 2, CH = RB / 16;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int r = wm * T::TM + i * 16 + i16;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int c = wn * T::TN + j * 16 + 4 * g4;
+        const f32x4_t v = acc[i][j];
+        *reinterpret_cast<u32x2_t*>(smem + r * RB + (((c >> 3) ^ (r & (CH - 1))) << 4) + (c & 4) * 2) =
+            u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+      }
+    }
+    __syncthreads();
+    constexpr int ROWS = T::THREADS / CH;
+    const int c = tid % CH, left = N - (n0 + c * 8);   // columns from this lane's piece on
+    uint16_t* out = static_cast<uint16_t*>(p.c) + (int64_t)m0 * p.ldc + n0 + c * 8;
+#pragma unroll 8
+    for (int r = tid / CH; r < BM; r += ROWS) {
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(smem + r * RB + ((c ^ (r & (CH - 1))) << 4));
+      uint16_t* d = out + (int64_t)r * p.ldc;
+      if (m0 + r >= M) continue;
+      if (left >= 8) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any_t*>(d));
+      else store8(d, v, left);
+    }
+  }
+}
+
+bool fits(const GemmProblem& p, int tile) {
+  return (tile == 256 || tile == 128) && p.order.num_rb == (p.m + tile - 1) / tile &&
+         p.order.num_cb == (p.n + tile - 1) / tile && p.splits >= 1 && p.k_per_split % 64 == 0 &&
+         (int64_t)p.splits * p.k_per_split >= p.k && (int64_t)(p.splits - 1) * p.k_per_split < p.k &&
+         (p.splits == 1 || p.partials) && (int64_t)p.order.num_rb * p.order.num_cb * p.splits < kFeedGrid;
+}
+
+}  // namespace
+
+hipError_t launch_feed_grads(const GemmProblem* a, const GemmProblem* w, int tile, int dtype, hipStream_t s) {
+  if ((!a && !w) || (a && !fits(*a, tile)) || (w && !fits(*w, tile))) return hipErrorInvalidValue;
+  FeedPair gp{};
+  int64_t grid = 0;
+  if (a) {
+    gp.a = *a;
+    grid += (int64_t)a->order.num_rb * a->order.num_cb * a->splits;
+  }
+  gp.a_tiles = (int32_t)grid;
+  if (w) {
+    gp.w = *w;
+    grid += (int64_t)w->order.num_rb * w->order.num_cb * w->splits;
+  }
+  if (grid >= kFeedGrid) return hipErrorInvalidValue;
+  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, gp); };
+  if (dtype == kDtypeBf16) tile == 256 ? go(feed_grads_kernel<256, 256, kDtypeBf16, 1>) : go(feed_grads_kernel<128, 128, kDtypeBf16, 2>);
+  else if (dtype == kDtypeFp16) tile == 256 ? go(feed_grads_kernel<256, 256, kDtypeFp16, 1>) : go(feed_grads_kernel<128, 128, kDtypeFp16, 2>);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+}  // namespace agmm

@@ -1,0 +1,143 @@
+// Launch interfaces of the feed-forward block's kernels and of layer norm.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "agmm_kernels.h"
+
+namespace agmm {
+
+// Activations y = x * share(x) by the form of their share.
+enum ActKind : int {
+  kActLinear = 0,      // 1
+  kActRelu = 1,        // 1 for x > 0, else 0
+  kActLogistic = 2,    // 1 / (1 + exp(-x (c1 + c3 x^2))): silu, and gelu's tanh form
+  kActNormal = 3,      // the normal distribution function: gelu
+};
+struct Activation {
+  int32_t kind;
+  float c1, c3;
+};
+
+// Columns of a row that share one scale of the 8-bit pre-activations, and what
+// a part's columns are padded to (with zeros) in either form.
+constexpr int kKeptBlock = 32;
+
+// Pre-activations kept for the way back, [m][parts][wide]: in the operands'
+// type (scales null) or e4m3 with a power of two per kKeptBlock columns, as its
+// biased exponent, in scales [m][parts][wide / kKeptBlock].
+struct KeptRows {
+  void* values;            // null: none
+  uint8_t* scales;
+  int64_t wide;            // n rounded up to kKeptBlock
+};
+
+// y = act(p) [* p of the second part] [+ residual], p = A B^T + bias.  gemm
+// describes the product in tile columns: plain, the n rows of B; gated,
+// interleaved blocks of 16 rows of the first and the second n rows
+// (gemm.n = 2 * (n rounded up to 16)).
+struct FeedProblem {
+  GemmProblem gemm;
+  int32_t n;               // columns of y
+  int32_t gated;
+  Activation act;
+  const void* bias;        // [parts * n] or null
+  const void* residual;    // or null
+  int64_t ldr;
+  void* y;
+  int64_t ldy;
+  KeptRows kept;
+};
+constexpr int64_t kFeedGrid = int64_t(1) << 24;
+// Tiles of 256 x 256 or 128 x 128 tile columns; rows of whole 16-byte vectors.
+hipError_t launch_feed_tiles(const FeedProblem& p, int tile, int dtype, hipStream_t stream);
+// Few rows: blocks of 16 fm rows x 16 fn tile columns (fm 1 or 4; fn 1, 2 or 4,
+// not 1 where gated, 4 where pre-activations are kept: their blocks of 32
+// columns of a part lie in one workgroup); any k and strides, operands in place.
+hipError_t launch_feed_few(const FeedProblem& p, int fm, int fn, int dtype, hipStream_t stream);
+
+// The elementwise part of the way back: d = dy * (derivative of y by p), by
+// rows [m][ldd] and transposed [parts * n][ldt] (zeros from m to ldt), each
+// where asked for, and the sums of d over blocks of kDRows rows.
+constexpr int kDRows = 128, kDCols = 64;
+struct FeedDProblem {
+  int64_t m;
+  int32_t n, gated;
+  Activation act;
+  KeptRows kept;           // values may be null for a linear product without a gate
+  const void* dy;
+  int64_t lddy;
+  void* d;
+  int64_t ldd;
+  void* dt;
+  int64_t ldt;
+  float* sums;             // [blocks of rows][parts * n] or null
+};
+hipError_t launch_feed_d(const FeedDProblem& p, int dtype, hipStream_t stream);
+
+// y = act(p) [* p of the second part] from the kept pre-activations.
+struct FeedAgainProblem {
+  int64_t m;
+  int32_t n, gated;
+  Activation act;
+  KeptRows kept;
+  void* y;
+  int64_t ldy;
+};
+hipError_t launch_feed_again(const FeedAgainProblem& p, int dtype, hipStream_t stream);
+
+// The products dA = d W and dW = dt A, B k x n, in one launch: with splits > 1
+// fp32 sums per k range into partials [splits][m][n rounded up to 4], else the
+// result itself, rounded.  Either may be null.
+hipError_t launch_feed_grads(const GemmProblem* a, const GemmProblem* w, int tile, int dtype, hipStream_t stream);
+
+// out[row][col] = sum over ranges, in order, of sums[range][row][cols rounded
+// up to 4], rounded to `dtype` (a 16-bit type).
+struct SumRanges {
+  const float* sums;
+  int32_t ranges;
+  int64_t rows, cols;
+  void* out;
+  int64_t ldo;
+};
+// One or two of them (null: none) in one launch.
+hipError_t launch_sum_ranges(const SumRanges* a, const SumRanges* b, int dtype, hipStream_t stream);
+
+// out[c] = sum over groups, in a fixed order, of sums[group][c], for c < cols,
+// rounded to `dtype`; columns from `first` on go to out2 (first = cols: none).
+// Either of out and out2 may be null.
+struct SumColumns {
+  const float* sums;
+  int64_t groups, cols, first;
+  void *out, *out2;
+  int32_t dtype;
+};
+hipError_t launch_sum_columns(const SumColumns& p, hipStream_t stream);
+
+// Layer norm over rows of any alignment.  weight and bias may be null (1, 0);
+// mean and rstd may be null on the way forward.
+struct NormProblem {
+  int64_t rows, cols;
+  int32_t dtype, wtype;
+  const void* x;
+  int64_t ldx;
+  const void* weight;
+  const void* bias;
+  float eps;
+  void* y;                 // forward
+  int64_t ldy;
+  float* mean;
+  float* rstd;
+  const void* dy;          // backward
+  int64_t lddy;
+  void* dx;                // or null
+  int64_t lddx;
+  float* sums;             // [groups][2][cols]: sums of dy * xhat and of dy; or null
+  int32_t groups;
+};
+hipError_t launch_norm_forward(const NormProblem& p, hipStream_t stream);
+hipError_t launch_norm_backward(const NormProblem& p, hipStream_t stream);
+// Workgroups (and groups of sums) of the backward pass.
+int norm_groups(int64_t rows, int64_t cols, int dtype, int cus);
+
+}  // namespace agmm

@@ -1,0 +1,428 @@
+// Layer norm over rows, forward and backward (gfx950).
+//
+//     y = (x - mean) rstd w + b                     mean, var over the row, rstd = 1 / sqrt(var + eps)
+//     dx = rstd (g - mean(g) - h mean(g h)),        g = dy w,  h = (x - mean) rstd
+//     dw = sum over rows of dy h,  db = sum over rows of dy
+//
+// A row is held in registers by THREADS lanes, CH 16-byte pieces each, so that
+// x is read once: the mean first, then the sums of x - mean, which is what the
+// mean's rounding left, and of its square (the difference of two large sums
+// would lose the variance of rows far from 0).
+// Rows longer than 1024 threads hold are read again for each sum.
+//
+// Backward, a workgroup takes every `groups`-th row; a lane's columns stay the
+// same, so the two column sums are registers too, and leave once at the end as
+// [groups][2][columns], which sum_columns_kernel adds in order.  The next row's
+// loads are on their way while a row is reduced.
+//
+// Bound: HBM.  Statistics and sums are fp32; results are rounded once.
+#include "feed_device.h"
+
+namespace agmm {
+
+namespace {
+
+template <int DT>
+struct Elem {
+  static constexpr int kBytes = DT == kDtypeFp32 ? 4 : 2;
+  static constexpr int V = 16 / kBytes;        // of a piece
+};
+
+// A piece of a row of any alignment as fp32 values, zeros past `left`.
+template <int DT>
+__device__ __forceinline__ u32x4_t load_piece(const void* x, int64_t at, int64_t left) {
+  if constexpr (DT == kDtypeFp32) {
+    typedef u32x4_t u32x4_word_t __attribute__((aligned(4)));
+    const uint32_t* p = static_cast<const uint32_t*>(x) + at;
+    if (left >= 4) return *reinterpret_cast<const u32x4_word_t*>(p);
+    u32x4_t v = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) v[e] = p[e];
+    return v;
+  } else {
+    return load8(static_cast<const uint16_t*>(x) + at, left < 8 ? (int)left : 8);
+  }
+}
+template <int DT>
+__device__ __forceinline__ float piece_value(const u32x4_t& v, int e) {
+  const uint32_t w = v[e];   // a bit cast of the vector's element itself takes element 0
+  if constexpr (DT == kDtypeFp32) return __builtin_bit_cast(float, w);
+  else return e & 1 ? high16<DT>(v[e >> 1]) : low16<DT>(v[e >> 1]);
+}
+template <int DT>
+__device__ __forceinline__ void store_piece(void* x, int64_t at, int64_t left, const float* v) {
+  if constexpr (DT == kDtypeFp32) {
+    typedef f32x4_t f32x4_word_t __attribute__((aligned(4)));
+    float* p = static_cast<float*>(x) + at;
+    if (left >= 4) {
+      *reinterpret_cast<f32x4_word_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < left) p[e] = v[e];
+    }
+  } else {
+    store8(static_cast<uint16_t*>(x) + at, u32x4_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])},
+           left < 8 ? (int)left : 8);
+  }
+}
+// V consecutive weights (of the rows' type or fp32) as fp32, `none` where there
+// are no weights or past `left`.
+template <int WT, int V>
+__device__ __forceinline__ void load_weights(const void* w, int64_t at, int64_t left, float none, float (&v)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] = none;
+  if (!w) return;
+  constexpr int U = Elem<WT>::V;
+#pragma unroll
+  for (int s = 0; s < V / (U < V ? U : V); ++s) {
+    if (left - s * U <= 0) break;
+    const u32x4_t q = load_piece<WT>(w, at + s * U, left - s * U);
+#pragma unroll
+    for (int e = 0; e < (U < V ? U : V); ++e)
+      if (s * U + e < left) v[s * U + e] = piece_value<WT>(q, e);
+  }
+}
+
+// Sums of N values over the lanes of a workgroup, in every lane, in a fixed
+// order.  Two buffers in turn: one barrier a call.
+template <int THREADS, int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float (*buf)[N], int& turn) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2)
+#pragma unroll
+    for (int q = 0; q < N; ++q) v[q] += __shfl_xor(v[q], d);
+  if constexpr (THREADS > 64) {
+    constexpr int W = THREADS / 64;
+    float(*b)[N] = buf + turn * W;
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int q = 0; q < N; ++q) b[threadIdx.x >> 6][q] = v[q];
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      v[q] = b[0][q];
+#pragma unroll
+      for (int w = 1; w < W; ++w) v[q] += b[w][q];
+    }
+  }
+}
+
+template <int DT, int WT, int THREADS, int CH>
+__global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormProblem p) {
+  constexpr int V = Elem<DT>::V;
+  __shared__ float buf[2 * THREADS / 64][1], buf2[2 * THREADS / 64][2];
+  int turn = 0, turn2 = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    u32x4_t x[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V;
+      x[c] = u32x4_t{0u, 0u, 0u, 0u};
+      if (col < p.cols) x[c] = load_piece<DT>(p.x, row * p.ldx + col, p.cols - col);
+    }
+    float s[1] = {0.0f}, t[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[0] += piece_value<DT>(x[c], e);
+    block_sum<THREADS>(s, buf, turn);
+    const float near = s[0] / (float)p.cols;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int64_t left = p.cols - ((int64_t)c * THREADS + threadIdx.x) * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = e < left ? piece_value<DT>(x[c], e) - near : 0.0f;
+        t[0] += d;
+        t[1] = __builtin_fmaf(d, d, t[1]);
+      }
+    }
+    block_sum<THREADS>(t, buf2, turn2);
+    const float rest = t[0] / (float)p.cols, var = __builtin_fmaf(-rest, rest, t[1] / (float)p.cols);
+    const float rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + p.eps);
+    if (threadIdx.x == 0) {
+      if (p.mean) p.mean[row] = near + rest;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V, left = p.cols - col;
+      if (left <= 0) continue;
+      float w[V], b[V], y[V];
+      load_weights<WT>(p.weight, col, left, 1.0f, w);
+      load_weights<WT>(p.bias, col, left, 0.0f, b);
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] = __builtin_fmaf((piece_value<DT>(x[c], e) - near - rest) * rstd, w[e], b[e]);
+      store_piece<DT>(p.y, row * p.ldy + col, left, y);
+    }
+  }
+}
+
+// Rows of any length, 1024 threads each, read once for every sum.
+template <int DT, int WT>
+__global__ __launch_bounds__(1024) void norm_forward_long_kernel(NormProblem p) {
+  constexpr int V = Elem<DT>::V;
+  __shared__ float buf[32][1], buf2[32][2];
+  int turn = 0, turn2 = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t at = row * p.ldx;
+    float s[1] = {0.0f}, t[2] = {0.0f, 0.0f};
+    for (int64_t col = (int64_t)threadIdx.x * V; col < p.cols; col += 1024 * V) {
+      const u32x4_t x = load_piece<DT>(p.x, at + col, p.cols - col);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[0] += piece_value<DT>(x, e);
+    }
+    block_sum<1024>(s, buf, turn);
+    const float near = s[0] / (float)p.cols;
+    for (int64_t col = (int64_t)threadIdx.x * V; col < p.cols; col += 1024 * V) {
+      const u32x4_t x = load_piece<DT>(p.x, at + col, p.cols - col);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = e < p.cols - col ? piece_value<DT>(x, e) - near : 0.0f;
+        t[0] += d;
+        t[1] = __builtin_fmaf(d, d, t[1]);
+      }
+    }
+    block_sum<1024>(t, buf2, turn2);
+    const float rest = t[0] / (float)p.cols, var = __builtin_fmaf(-rest, rest, t[1] / (float)p.cols);
+    const float rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + p.eps);
+    if (threadIdx.x == 0) {
+      if (p.mean) p.mean[row] = near + rest;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+    for (int64_t col = (int64_t)threadIdx.x * V; col < p.cols; col += 1024 * V) {
+      const int64_t left = p.cols - col;
+      const u32x4_t x = load_piece<DT>(p.x, at + col, left);
+      float w[V], b[V], y[V];
+      load_weights<WT>(p.weight, col, left, 1.0f, w);
+      load_weights<WT>(p.bias, col, left, 0.0f, b);
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] = __builtin_fmaf((piece_value<DT>(x, e) - near - rest) * rstd, w[e], b[e]);
+      store_piece<DT>(p.y, row * p.ldy + col, left, y);
+    }
+  }
+}
+
+template <int DT, int WT, int THREADS, int CH>
+__global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormProblem p) {
+  constexpr int V = Elem<DT>::V;
+  __shared__ float buf[2 * THREADS / 64][2];
+  int turn = 0;
+  float w[CH][V], dw[CH][V] = {}, db[CH][V] = {};
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V;
+    load_weights<WT>(p.weight, col, p.cols - col, 1.0f, w[c]);
+  }
+  u32x4_t x[CH], dy[CH];
+  float mean = 0.0f, rstd = 0.0f;
+  const auto load = [&](int64_t row) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V;
+      x[c] = dy[c] = u32x4_t{0u, 0u, 0u, 0u};
+      if (col < p.cols) {
+        x[c] = load_piece<DT>(p.x, row * p.ldx + col, p.cols - col);
+        dy[c] = load_piece<DT>(p.dy, row * p.lddy + col, p.cols - col);
+      }
+    }
+    mean = p.mean[row];
+    rstd = p.rstd[row];
+  };
+  const float inv = 1.0f / (float)p.cols;
+  int64_t row = blockIdx.x;
+  if (row < p.rows) load(row);
+  while (row < p.rows) {
+    float g[CH][V], h[CH][V], s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int64_t left = p.cols - ((int64_t)c * THREADS + threadIdx.x) * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = piece_value<DT>(dy[c], e);
+        h[c][e] = e < left ? (piece_value<DT>(x[c], e) - mean) * rstd : 0.0f;
+        g[c][e] = d * w[c][e];
+        s[0] += g[c][e];
+        s[1] = __builtin_fmaf(g[c][e], h[c][e], s[1]);
+        dw[c][e] = __builtin_fmaf(d, h[c][e], dw[c][e]);
+        db[c][e] += d;
+      }
+    }
+    const int64_t here = row;
+    const float scale = rstd;
+    row += gridDim.x;
+    if (row < p.rows) load(row);
+    if (p.dx) {
+      block_sum<THREADS>(s, buf, turn);
+      const float a = s[0] * inv, b = s[1] * inv;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V;
+        if (col >= p.cols) continue;
+        float v[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = scale * (g[c][e] - __builtin_fmaf(h[c][e], b, a));
+        store_piece<DT>(p.dx, here * p.lddx + col, p.cols - col, v);
+      }
+    }
+  }
+  if (!p.sums) return;
+  float* out = p.sums + (int64_t)blockIdx.x * 2 * p.cols;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V;
+    if (col >= p.cols) continue;
+#pragma unroll
+    for (int s = 0; s < V / 4; ++s) {
+      store_piece<kDtypeFp32>(out, col + 4 * s, p.cols - col - 4 * s, dw[c] + 4 * s);
+      store_piece<kDtypeFp32>(out + p.cols, col + 4 * s, p.cols - col - 4 * s, db[c] + 4 * s);
+    }
+  }
+}
+
+// Rows of any length: dx by rows, read twice.
+template <int DT, int WT>
+__global__ __launch_bounds__(1024) void norm_dx_long_kernel(NormProblem p) {
+  constexpr int V = Elem<DT>::V;
+  __shared__ float buf[32][2];
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    const auto piece = [&](int64_t col, float (&g)[V], float (&h)[V]) {
+      const int64_t left = p.cols - col;
+      const u32x4_t x = load_piece<DT>(p.x, row * p.ldx + col, left), dy = load_piece<DT>(p.dy, row * p.lddy + col, left);
+      float w[V];
+      load_weights<WT>(p.weight, col, left, 1.0f, w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        h[e] = e < left ? (piece_value<DT>(x, e) - mean) * rstd : 0.0f;
+        g[e] = piece_value<DT>(dy, e) * w[e];
+      }
+    };
+    float s[2] = {0.0f, 0.0f};
+    for (int64_t col = (int64_t)threadIdx.x * V; col < p.cols; col += 1024 * V) {
+      float g[V], h[V];
+      piece(col, g, h);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        s[0] += g[e];
+        s[1] = __builtin_fmaf(g[e], h[e], s[1]);
+      }
+    }
+    block_sum<1024>(s, buf, turn);
+    const float a = s[0] / (float)p.cols, b = s[1] / (float)p.cols;
+    for (int64_t col = (int64_t)threadIdx.x * V; col < p.cols; col += 1024 * V) {
+      float g[V], h[V], v[V];
+      piece(col, g, h);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = rstd * (g[e] - __builtin_fmaf(h[e], b, a));
+      store_piece<DT>(p.dx, row * p.lddx + col, p.cols - col, v);
+    }
+  }
+}
+
+// and the column sums: 256 V columns of every `groups`-th row per workgroup.
+template <int DT>
+__global__ __launch_bounds__(256) void norm_sums_long_kernel(NormProblem p) {
+  constexpr int V = Elem<DT>::V;
+  const int64_t strips = (p.cols + 256 * V - 1) / (256 * V);
+  const int64_t group = blockIdx.x / strips, col = ((blockIdx.x - group * strips) * 256 + threadIdx.x) * V, left = p.cols - col;
+  if (left <= 0) return;
+  float dw[V] = {}, db[V] = {};
+#pragma unroll 4
+  for (int64_t row = group; row < p.rows; row += p.groups) {
+    const u32x4_t x = load_piece<DT>(p.x, row * p.ldx + col, left), dy = load_piece<DT>(p.dy, row * p.lddy + col, left);
+    const float mean = p.mean[row], rstd = p.rstd[row];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float d = piece_value<DT>(dy, e);
+      dw[e] = __builtin_fmaf(d, (piece_value<DT>(x, e) - mean) * rstd, dw[e]);
+      db[e] += d;
+    }
+  }
+  float* out = p.sums + group * 2 * p.cols;
+#pragma unroll
+  for (int s = 0; s < V / 4; ++s) {
+    store_piece<kDtypeFp32>(out, col + 4 * s, left - 4 * s, dw + 4 * s);
+    store_piece<kDtypeFp32>(out + p.cols, col + 4 * s, left - 4 * s, db + 4 * s);
+  }
+}
+
+constexpr int64_t kRowGrid = 1 << 20;   // workgroups of the kernels that take a row at a time
+
+int64_t pieces_of(int64_t cols, int dtype) { return (cols + (dtype == kDtypeFp32 ? 3 : 7)) / (dtype == kDtypeFp32 ? 4 : 8); }
+
+template <int DT, int WT>
+hipError_t forward_type(const NormProblem& p, hipStream_t s) {
+  const int64_t pieces = pieces_of(p.cols, DT);
+  const dim3 grid((unsigned)(p.rows < kRowGrid ? p.rows : kRowGrid));
+  const auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, s, p); };
+  if (pieces <= 64) go(norm_forward_kernel<DT, WT, 64, 1>, 64);
+  else if (pieces <= 256) go(norm_forward_kernel<DT, WT, 256, 1>, 256);
+  else if (pieces <= 512) go(norm_forward_kernel<DT, WT, 256, 2>, 256);
+  else if (pieces <= 1024) go(norm_forward_kernel<DT, WT, 256, 4>, 256);
+  else if (pieces <= 4096) go(norm_forward_kernel<DT, WT, 1024, 4>, 1024);
+  else go(norm_forward_long_kernel<DT, WT>, 1024);
+  return hipGetLastError();
+}
+
+template <int DT, int WT>
+hipError_t backward_type(const NormProblem& p, hipStream_t s) {
+  const int64_t pieces = pieces_of(p.cols, DT);
+  const auto go = [&](auto kernel, int64_t grid, int threads) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), 0, s, p);
+  };
+  if (pieces <= 64) go(norm_backward_kernel<DT, WT, 64, 1>, p.groups, 64);
+  else if (pieces <= 256) go(norm_backward_kernel<DT, WT, 256, 1>, p.groups, 256);
+  else if (pieces <= 512) go(norm_backward_kernel<DT, WT, 512, 1>, p.groups, 512);
+  else if (pieces <= 1024) go(norm_backward_kernel<DT, WT, 1024, 1>, p.groups, 1024);
+  else if (DT == kDtypeFp32 && pieces <= 2048) go(norm_backward_kernel<DT, WT, 1024, DT == kDtypeFp32 ? 2 : 1>, p.groups, 1024);
+  else {
+    // the sums first: dx may overwrite dy
+    if (p.sums) go(norm_sums_long_kernel<DT>, (pieces + 255) / 256 * p.groups, 256);
+    if (p.dx) go(norm_dx_long_kernel<DT, WT>, p.rows < kRowGrid ? p.rows : kRowGrid, 1024);
+  }
+  return hipGetLastError();
+}
+
+bool valid(const NormProblem& p) {
+  return p.rows >= 1 && p.rows < (int64_t(1) << 31) && p.cols >= 1 && p.cols < (int64_t(1) << 31) && p.x &&
+         (p.wtype == p.dtype || p.wtype == kDtypeFp32);
+}
+
+template <class F>
+hipError_t by_type(const NormProblem& p, F&& f) {
+  const bool wide = p.wtype == kDtypeFp32;
+  if (p.dtype == kDtypeBf16) return wide ? f(IntTag<kDtypeBf16>{}, IntTag<kDtypeFp32>{}) : f(IntTag<kDtypeBf16>{}, IntTag<kDtypeBf16>{});
+  if (p.dtype == kDtypeFp16) return wide ? f(IntTag<kDtypeFp16>{}, IntTag<kDtypeFp32>{}) : f(IntTag<kDtypeFp16>{}, IntTag<kDtypeFp16>{});
+  return p.dtype == kDtypeFp32 ? f(IntTag<kDtypeFp32>{}, IntTag<kDtypeFp32>{}) : hipErrorInvalidValue;
+}
+
+}  // namespace
+
+int norm_groups(int64_t rows, int64_t cols, int dtype, int cus) {
+  const int64_t pieces = pieces_of(cols, dtype);
+  // as many workgroups as the CUs hold at a time, but two rows of sums for
+  // eight of x and dy at most
+  const int64_t per = pieces <= 64 ? 16 : pieces <= 256 ? 4 : pieces <= 512 ? 2 : 1;
+  int64_t groups = cus * per;
+  if (pieces > (dtype == kDtypeFp32 ? 2048 : 1024)) groups = 4 * cus / ((pieces + 255) / 256);
+  if (groups > rows) groups = rows;
+  return (int)(groups < 1 ? 1 : groups);
+}
+
+hipError_t launch_norm_forward(const NormProblem& p, hipStream_t s) {
+  if (!valid(p) || !p.y) return hipErrorInvalidValue;
+  return by_type(p, [&](auto t, auto w) { return forward_type<decltype(t)::value, decltype(w)::value>(p, s); });
+}
+
+hipError_t launch_norm_backward(const NormProblem& p, hipStream_t s) {
+  if (!valid(p) || !p.dy || !p.mean || !p.rstd || (!p.dx && !p.sums) || p.groups < 1 || p.groups > p.rows)
+    return hipErrorInvalidValue;
+  return by_type(p, [&](auto t, auto w) { return backward_type<decltype(t)::value, decltype(w)::value>(p, s); });
+}
+
+}  // namespace agmm

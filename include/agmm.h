@@ -625,6 +625,160 @@ size_t agmm_loss_plan_workspace_bytes(agmm_loss_plan_t plan);
 /* Wait for the plan's last call, then free it.  NULL is a no-op. */
 void agmm_loss_plan_destroy(agmm_loss_plan_t plan);
 
+/*
+ * Feed-forward block of a column-parallel layer: the product of the gathered
+ * rows with an epilogue,
+ *
+ *     p = concat_r(A_r) @ W^T + bias,     y = act(p) + residual
+ *
+ * or the gated product, both projections, the activation and their product in
+ * one kernel,
+ *
+ *     p = concat_r(A_r) @ W^T + bias,     y = act(p[:, :n]) * p[:, n:]
+ *
+ * with W stored [n, k] (gated: [2 n, k], the gate's n rows first), n = n_local.
+ * Sums, bias, activation, product and residual are fp32; y is rounded once.
+ *
+ * The forward pass can keep p for the way back, in `saved` [m][parts][ns], parts
+ * 1 or 2 (gated), ns = n rounded up to 32 (columns past n are written as zeros):
+ *   16 bits  rounded to the plan's dtype (saved_scales NULL);
+ *   8 bits   e4m3, every 32 columns of a row and part over the smallest power of
+ *            two s >= 2^-126 with max |p| <= 448 s, rounded once to nearest even;
+ *            saved_scales [m][parts][ns / 32] holds the biased exponents of s
+ *            (e8m0: s = 2^(code - 127)).  Infinities and NaN do not enter the
+ *            maximum and become NaN.  33/64 of the 16-bit form's bytes.
+ * The backward pass takes p as it was kept:
+ *
+ *     d = dY act'(p)     gated: d_0 = dY p_1 act'(p_0), d_1 = dY act(p_0)
+ *     dA = d W,  dW = d^T A,  dbias = column sums of d
+ *
+ * The residual's gradient is dY.  d is rounded to the plan's dtype, as the
+ * operand of two products; sums are fp32 and dA, dW, dbias rounded once.  dA is
+ * this device's part of the gathered rows' gradient [m, k].  A fp16 d beyond
+ * 65504 is infinite: scale fp16 losses as usual.
+ */
+typedef enum {
+  AGMM_ACT_NONE = 0,
+  AGMM_ACT_RELU = 1,
+  AGMM_ACT_GELU = 2,      /* x Phi(x), Phi the normal distribution function */
+  AGMM_ACT_GELU_TANH = 3, /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+  AGMM_ACT_SILU = 4       /* x / (1 + exp(-x)) */
+} agmm_activation;
+
+typedef struct agmm_ff_plan agmm_ff_plan;
+typedef agmm_ff_plan *agmm_ff_plan_t;
+
+/* Check a problem without touching the GPU: agmm_plan_validate's rules for the
+ * sizes, m and parts * n_local < 2^27, m * parts * n_local, m * k and
+ * parts * n_local * k < 2^36, dtype AGMM_BF16 or AGMM_FP16 (AGMM_FP32 is not
+ * supported), an agmm_activation, gated 0 or 1.  Rows that are not whole 16-byte
+ * vectors (k or a stride not a multiple of 8) run on zero-padded copies of A and
+ * W, or, few rows, in place. */
+int agmm_ff_plan_validate(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_local,
+                          int dtype, int activation, int gated);
+
+/* Create a plan on the current HIP device (NULL on failure), with everything
+ * its calls need; with_gradient 0 leaves out the backward pass and its
+ * workspace. */
+agmm_ff_plan_t agmm_ff_plan_create(int num_shards, int64_t m_per_shard, int64_t k, int64_t n_local,
+                                   int dtype, int activation, int gated, int with_gradient);
+
+/*
+ * Enqueue the forward pass on `stream`.
+ *   shard_ptrs  host array of num_shards device pointers [m_per_shard, k], rows "lda" apart
+ *   W           device [parts * n_local, k], rows "ldw" apart
+ *   bias        device [parts * n_local] of the plan's dtype, or NULL
+ *   residual    device [m, n_local], rows "ldr" apart, or NULL (gated: NULL); may be Y itself
+ *   Y           device [m, n_local], rows "ldy" apart
+ *   saved, saved_scales  as above, or NULL (no scales: 16 bits)
+ * Shards, W and saved are 16-byte aligned, the others to their elements.
+ * Outputs must not overlap inputs, but for residual = Y with equal strides.
+ * Stream, capture and ordering rules are agmm_run's (a call that copies nothing
+ * shares no workspace with others and is not ordered with them).
+ */
+int agmm_ff_forward(agmm_ff_plan_t plan, const void *const *shard_ptrs, const void *W,
+                    const void *bias, const void *residual, void *Y, void *saved,
+                    void *saved_scales, void *stream);
+
+/*
+ * Enqueue the backward pass.
+ *   saved, saved_scales  what the forward pass kept (NULL only without a gate and an activation)
+ *   dY          device [m, n_local], rows "lddy" apart
+ *   dA          device [m, k] of the plan's dtype, rows "ldda" apart, or NULL
+ *   dW          device [parts * n_local, k], rows "lddw" apart, or NULL
+ *   dbias       device [parts * n_local] of the plan's dtype, or NULL (not all three)
+ * shard_ptrs may be NULL without dW, and W without dA.
+ */
+int agmm_ff_backward(agmm_ff_plan_t plan, const void *const *shard_ptrs, const void *W,
+                     const void *saved, const void *saved_scales, const void *dY, void *dA,
+                     void *dW, void *dbias, void *stream);
+
+/* Enqueue Y = act(p), or act(p_0) * p_1, again from what the forward pass kept:
+ * for callers who keep 8 bits of p instead of y for the next layer's weight
+ * gradient.  Uses no workspace. */
+int agmm_ff_recompute(agmm_ff_plan_t plan, const void *saved, const void *saved_scales, void *Y,
+                      void *stream);
+
+/*
+ * Tune a plan.  Keys:
+ *   "lda", "ldw", "ldda", "lddw"  elements between rows: 0 (dense) or at least k
+ *   "ldr", "ldy", "lddy"          the same: 0 or at least n_local
+ *   "tile"          -1 automatic, 128 or 256: rows and columns of the products' tiles; 64: blocks
+ *                   of up to 64 x 64 whose waves share out k, for few rows (forward only)
+ * A change that needs more workspace reallocates it; the plan keeps its
+ * previous settings when that fails.  Settings are fixed once a call was
+ * captured into a graph.  get reads the values in use, "saved_cols" (ns), and
+ * "captured".
+ */
+int agmm_ff_plan_set_int(agmm_ff_plan_t plan, const char *key, int64_t value);
+int agmm_ff_plan_get_int(agmm_ff_plan_t plan, const char *key, int64_t *value);
+size_t agmm_ff_plan_workspace_bytes(agmm_ff_plan_t plan);
+
+/* Wait for the plan's last call, then free it.  NULL is a no-op. */
+void agmm_ff_plan_destroy(agmm_ff_plan_t plan);
+
+/*
+ * Layer norm of rows (a layer's own rows, before they are gathered):
+ *
+ *     y = (x - mean) rstd weight + bias,     rstd = 1 / sqrt(var + eps)
+ *     dx = rstd (g - mean(g) - h mean(g h)),  g = dy weight, h = (x - mean) rstd
+ *     dweight = sum over rows of dy h,  dbias = sum over rows of dy
+ *
+ * var is the row's mean squared deviation.  Statistics and sums are fp32,
+ * results rounded once; the sums over rows are added in a fixed order.
+ */
+typedef struct agmm_norm_plan agmm_norm_plan;
+typedef agmm_norm_plan *agmm_norm_plan_t;
+
+/* rows >= 1 and < 2^28, cols >= 1 and < 2^26, rows * cols < 2^37; dtype of x, y,
+ * dy and dx: agmm_dtype; weight_dtype of weight, bias and their gradients: the
+ * same or AGMM_FP32. */
+int agmm_norm_plan_validate(int64_t rows, int64_t cols, int dtype, int weight_dtype);
+agmm_norm_plan_t agmm_norm_plan_create(int64_t rows, int64_t cols, int dtype, int weight_dtype);
+
+/* Enqueue the forward pass: x, y [rows, cols], rows "ldx" and "ldy" elements
+ * apart; weight, bias [cols] or NULL (1, 0); mean, rstd fp32 [rows], written, or
+ * NULL; eps finite and >= 0.  Pointers are aligned to their elements (rows of
+ * whole 16-byte vectors are read faster); y may be x itself with equal strides.
+ * Uses no workspace. */
+int agmm_norm_forward(agmm_norm_plan_t plan, const void *x, const void *weight, const void *bias,
+                      float eps, void *y, float *mean, float *rstd, void *stream);
+
+/* Enqueue the backward pass from the forward pass's mean and rstd: dx, rows
+ * "lddx" apart, dweight and dbias [cols], each or NULL (not all); dy rows "lddy"
+ * apart; dx may be dy itself with equal strides.  Calls with dweight or dbias
+ * share the plan's workspace and are ordered as agmm_run's are. */
+int agmm_norm_backward(agmm_norm_plan_t plan, const void *x, const void *dy, const void *weight,
+                       const float *mean, const float *rstd, void *dx, void *dweight, void *dbias,
+                       void *stream);
+
+/* Keys "ldx", "ldy", "lddy", "lddx": 0 (dense) or at least cols; get reads also
+ * "captured". */
+int agmm_norm_plan_set_int(agmm_norm_plan_t plan, const char *key, int64_t value);
+int agmm_norm_plan_get_int(agmm_norm_plan_t plan, const char *key, int64_t *value);
+size_t agmm_norm_plan_workspace_bytes(agmm_norm_plan_t plan);
+void agmm_norm_plan_destroy(agmm_norm_plan_t plan);
+
 /* Thread-local status / message of this thread's most recent call into the
  * library (AGMM_OK and "" after a call that succeeded; calls on other threads
  * never change them). */
