@@ -589,6 +589,7 @@ class _OpPlan:
         import torch
         lib = load_library()
         self.handle = None
+        self._empty = torch.empty
         self.device = torch.cuda.current_device()
         self.handle = getattr(lib, self._prefix + "_create")(*args)
         if not self.handle:
@@ -640,11 +641,10 @@ class _OpPlan:
 
     def _new(self, like):
         """A new tensor as `like` describes it."""
-        import torch
         dtype, device, shape, stride = like
         if len(shape) == 1 or stride[0] == shape[1]:
-            return torch.empty(shape, dtype=dtype, device=device)
-        return torch.empty((shape[0], stride[0]), dtype=dtype, device=device)[:, :shape[1]]
+            return self._empty(shape, dtype=dtype, device=device)
+        return self._empty((shape[0], stride[0]), dtype=dtype, device=device)[:, :shape[1]]
 
     @property
     def m(self) -> int:
@@ -867,7 +867,8 @@ class FeedForwardPlan(_OpPlan):
         self._ldw = self._like((parts * n, k), t, self.get("lddw"))
         # kept pre-activations, seen as matrices of their rows
         self._kept_shape, self._scales_shape = torch.Size((m, parts, wide)), torch.Size((m, parts, wide // KEPT_BLOCK))
-        self._kept_types = {t: None, torch.float8_e4m3fn: torch.float8_e8m0fnu}
+        self._kept_types = {16: t, 8: torch.float8_e4m3fn}
+        self._scale_types = {t: None, torch.float8_e4m3fn: torch.float8_e8m0fnu}
 
     def _shards(self, shards):
         if len(shards) != self.num_shards:
@@ -887,9 +888,9 @@ class FeedForwardPlan(_OpPlan):
         if saved.n != self.n_local:
             raise ValueError(f"saved has {saved.n} columns, expected {self.n_local}")
         v, s = saved.values, saved.scales
-        if v.dtype not in self._kept_types:
-            raise TypeError(f"saved has dtype {v.dtype}, plan expects one of {list(self._kept_types)}")
-        kind = self._kept_types[v.dtype]
+        if v.dtype not in self._scale_types:
+            raise TypeError(f"saved has dtype {v.dtype}, plan expects one of {list(self._scale_types)}")
+        kind = self._scale_types[v.dtype]
         for t, shape, dtype, name in ((v, self._kept_shape, v.dtype, "saved.values"), (s, self._scales_shape, kind, "saved.scales")):
             if dtype is None:
                 if t is not None:
@@ -906,24 +907,22 @@ class FeedForwardPlan(_OpPlan):
     def forward(self, shards, W, bias=None, residual=None, out=None, keep: int = 0, stream=None):
         """y [m, n_local]; with keep 16 or 8 also the pre-activations in so many
         bits, as a Checkpoint: (y, saved)."""
-        import torch
         if keep != 0 and keep != 8 and keep != 16:
             raise ValueError(f"keep must be 0, 8 or 16 (got {keep!r})")
         on, a = self._on, self._shards(shards)
         w = on(W, self._lw, "W")
         b = None if bias is None else on(bias, self._lb, "bias")
         r = None if residual is None else on(residual, self._lr, "residual")
+        y = None if out is None else on(out, self._ly, "out")
         saved = v = s = None
         with _device_and_stream(self.device, stream):
             if out is None:
                 out = self._new(self._ly)
                 y = out.data_ptr()
-            else:
-                y = on(out, self._ly, "out")
             if keep:
-                device = self._la[1]
-                values = torch.empty(self._kept_shape, dtype=torch.float8_e4m3fn if keep == 8 else self._la[0], device=device)
-                scales = torch.empty(self._scales_shape, dtype=torch.float8_e8m0fnu, device=device) if keep == 8 else None
+                empty, device, t = self._empty, self._la[1], self._kept_types[keep]
+                values = empty(self._kept_shape, dtype=t, device=device)
+                scales = empty(self._scales_shape, dtype=self._scale_types[t], device=device) if keep == 8 else None
                 saved = Checkpoint(values, scales, self.n_local)
                 v, s = values.data_ptr(), None if scales is None else scales.data_ptr()
             _check(self._fwd(self.handle, a, w, b, r, y, v, s, _stream_handle(stream, self.device)))
@@ -938,16 +937,20 @@ class FeedForwardPlan(_OpPlan):
         w = on(W, self._lw, "W")
         v, s = self._kept(saved)
         g = on(dy, self._ldy, "dy")
+        pa = None if dA is None else on(dA, self._lda, "dA")
+        pw = None if dW is None else on(dW, self._ldw, "dW")
+        pb = None if dbias is None else on(dbias, self._lb, "dbias")
         with _device_and_stream(self.device, stream):
             if dA is None and need_dA:
                 dA = self._new(self._lda)
+                pa = dA.data_ptr()
             if dW is None and need_dW:
                 dW = self._new(self._ldw)
+                pw = dW.data_ptr()
             if dbias is None and need_dbias:
                 dbias = self._new(self._lb)
-            _check(self._bwd(self.handle, a, w, v, s, g, None if dA is None else on(dA, self._lda, "dA"),
-                             None if dW is None else on(dW, self._ldw, "dW"),
-                             None if dbias is None else on(dbias, self._lb, "dbias"), _stream_handle(stream, self.device)))
+                pb = dbias.data_ptr()
+            _check(self._bwd(self.handle, a, w, v, s, g, pa, pw, pb, _stream_handle(stream, self.device)))
         return dA, dW, dbias
 
     def recompute(self, saved, out=None, stream=None):
@@ -997,12 +1000,13 @@ class NormPlan(_OpPlan):
         px = on(x, self._lx, "x")
         w = None if weight is None else on(weight, self._lw, "weight")
         b = None if bias is None else on(bias, self._lw, "bias")
+        y = None if out is None else on(out, self._ly, "out")
         with _device_and_stream(self.device, stream):
             if out is None:
                 out = new(self._ly)
+                y = out.data_ptr()
             mean, rstd = new(self._ls), new(self._ls)
-            _check(self._fwd(self.handle, px, w, b, eps, on(out, self._ly, "out"), mean.data_ptr(), rstd.data_ptr(),
-                             _stream_handle(stream, self.device)))
+            _check(self._fwd(self.handle, px, w, b, eps, y, mean.data_ptr(), rstd.data_ptr(), _stream_handle(stream, self.device)))
         return out, mean, rstd
 
     def backward(self, x, dy, weight, mean, rstd, dx=None, need_dx: bool = True, need_dweight: bool = True,
@@ -1014,14 +1018,15 @@ class NormPlan(_OpPlan):
         px, g = on(x, self._lx, "x"), on(dy, self._ldy, "dy")
         w = None if weight is None else on(weight, self._lw, "weight")
         mu, rs = on(mean, self._ls, "mean"), on(rstd, self._ls, "rstd")
+        d = None if dx is None else on(dx, self._ldx, "dx")
         with _device_and_stream(self.device, stream):
             if dx is None and need_dx:
                 dx = new(self._ldx)
+                d = dx.data_ptr()
             dw = new(self._lw) if need_dweight else None
             db = new(self._lw) if need_dbias else None
-            _check(self._bwd(self.handle, px, g, w, mu, rs, None if dx is None else on(dx, self._ldx, "dx"),
-                             None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
-                             _stream_handle(stream, self.device)))
+            _check(self._bwd(self.handle, px, g, w, mu, rs, d, None if dw is None else dw.data_ptr(),
+                             None if db is None else db.data_ptr(), _stream_handle(stream, self.device)))
         return dx, dw, db
 
 

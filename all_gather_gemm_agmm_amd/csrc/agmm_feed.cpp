@@ -71,7 +71,7 @@ struct agmm_ff_plan : PlanBase {
     bool pad_a = false, pad_w = false;   // rows that are not whole 16-byte vectors: zero-padded copies
     int64_t kp = 0;                      // k rounded up to 8
     int tile = 256;                      // forward; 64: the few-row form, in
-    int fm = 0, fn = 0;                  // blocks of 16 fm x 16 fn (kept pre-activations: fn 4)
+    int fm = 0, yc = 0;                  // blocks of 16 fm rows x yc columns of y (kept pre-activations: most_yc())
     int tile_grads = 256;
     int a_ranges = 1, w_ranges = 1;      // ranges of the gradient products' sums
     int64_t a_per = 0, w_per = 0;
@@ -79,6 +79,7 @@ struct agmm_ff_plan : PlanBase {
     float *a_sums = nullptr, *w_sums = nullptr, *b_sums = nullptr;
     size_t bytes = 0;
   };
+  Layout forward_layout, backward_layout;   // those of the settings and the workspace
 
   int64_t ld_a() const { return lda ? lda : k; }
   int64_t ld_w() const { return ldw ? ldw : k; }
@@ -107,15 +108,18 @@ struct agmm_ff_plan : PlanBase {
     L.tile = tile_key > 0 ? (int)tile_key : big <= small ? 256 : 128;
     if (tile_key > 0 && tile_key != 64) return;
     L.fm = m <= 16 ? 1 : 4;
-    L.fn = cdiv(nc, 64) * cdiv(m, 16 * L.fm) >= 2 * cu_count ? 4 : parts;
-    const int64_t wgs = cdiv(m, 16 * L.fm) * cdiv(nc, 16 * L.fn);
-    const double rate = (L.fm * L.fn == 16 ? 6e6 : 10e6) / (copied && (ld_a() % 2 != 0 || ld_w() % 2 != 0) ? 1.7 : 1.0);
-    const double few = 5.0 + std::max((double)wgs * 32 * (L.fm + L.fn) * (double)k / rate, bytes / 4.8e6);
+    const int64_t rows = cdiv(m, 16 * L.fm);
+    L.yc = cdiv(n, most_yc()) * rows >= 2 * cu_count ? most_yc() : L.fm == 1 && cdiv(n, 16) < cu_count ? 8 : 16;
+    const int64_t wgs = rows * cdiv(n, L.yc);
+    const double rate = (L.fm == 4 && L.yc == most_yc() ? 6e6 : 10e6) / (copied && (ld_a() % 2 != 0 || ld_w() % 2 != 0) ? 1.7 : 1.0);
+    const double few = 5.0 + std::max((double)wgs * 2 * (16 * L.fm + parts * L.yc) * (double)k / rate, bytes / 4.8e6);
     if (tile_key == 64 || (few < std::min(big, small) + (copied ? 2.0 + 2 * bytes / 5e6 : 0.0) && few_fits())) L.tile = 64;
   }
 
+  int most_yc() const { return parts == 2 ? 32 : 64; }
+
   // Whether every form of the few-row kernel stays within a launch.
-  bool few_fits() const { return cdiv(m, 16 * (m <= 16 ? 1 : 4)) * cdiv(tile_cols(), 16 * parts) < agmm::kFeedGrid; }
+  bool few_fits() const { return cdiv(m, m <= 16 ? 16 : 64) * cdiv(n, m <= 16 ? 8 : 16) < agmm::kFeedGrid; }
 
   Layout layout(bool grad, char* base) const {
     Layout L;
@@ -169,7 +173,11 @@ struct agmm_ff_plan : PlanBase {
     size_t bytes = 0;
     for (bool grad : {false, true})
       if (!grad || with_gradient) bytes = std::max(bytes, layout(grad, nullptr).bytes);
-    return reserve(bytes);
+    const int rc = reserve(bytes);
+    if (rc != AGMM_OK) return rc;
+    forward_layout = layout(false, ws);
+    if (with_gradient) backward_layout = layout(true, ws);
+    return AGMM_OK;
   }
 
   agmm::TileOrder tiles_of(int64_t rows, int64_t columns, int tile) const {
@@ -218,8 +226,9 @@ struct agmm_ff_plan : PlanBase {
     return {const_cast<void*>(values), static_cast<uint8_t*>(const_cast<void*>(scales)), wide()};
   }
 
-  int forward(const Layout& L, const void* const* shards, const void* W, const void* bias, const void* residual, void* Y,
+  int forward(const void* const* shards, const void* W, const void* bias, const void* residual, void* Y,
               void* saved, void* saved_scales, hipStream_t s) {
+    const Layout& L = forward_layout;
     const int rc = copies(L, shards, W, s);
     if (rc != AGMM_OK) return rc;
     agmm::FeedProblem p{};
@@ -233,10 +242,10 @@ struct agmm_ff_plan : PlanBase {
       p.gemm.rows.c_group_rows = m_s;
     }
     // kept rows are written in blocks of 32 columns of a part
-    const int fn = L.tile == 64 && saved ? 4 : L.fn;
+    const int yc = saved ? most_yc() : L.yc;
     if (L.tile == 64) {
       p.gemm.order.num_rb = (int32_t)cdiv(m, 16 * L.fm);
-      p.gemm.order.num_cb = (int32_t)cdiv(tile_cols(), 16 * fn);
+      p.gemm.order.num_cb = (int32_t)cdiv(n, yc);
     } else {
       p.gemm.order = tiles_of(m, tile_cols(), L.tile);
     }
@@ -256,13 +265,13 @@ struct agmm_ff_plan : PlanBase {
     p.y = Y;
     p.ldy = ldy ? ldy : n;
     p.kept = kept_rows(saved, saved_scales);
-    const hipError_t err = L.tile == 64 ? agmm::launch_feed_few(p, L.fm, fn, dtype, s) : agmm::launch_feed_tiles(p, L.tile, dtype, s);
+    const hipError_t err = L.tile == 64 ? agmm::launch_feed_few(p, L.fm, yc, dtype, s) : agmm::launch_feed_tiles(p, L.tile, dtype, s);
     return err == hipSuccess ? AGMM_OK : hip_err(err, "feed-forward launch");
   }
 
   int backward(const void* const* shards, const void* W, const void* saved, const void* saved_scales, const void* dY, void* dA,
                void* dW, void* dbias, hipStream_t s) {
-    const Layout L = layout(true, ws);
+    const Layout& L = backward_layout;
     const int rc = copies(L, dW ? shards : nullptr, dA ? W : nullptr, s);
     if (rc != AGMM_OK) return rc;
     agmm::FeedDProblem e{};
@@ -454,7 +463,7 @@ int agmm_ff_plan_get_int(agmm_ff_plan_t p, const char* key, int64_t* value) {
   else if (k == "ldy") *value = p->ldy ? p->ldy : p->n;
   else if (k == "lddy") *value = p->lddy ? p->lddy : p->n;
   else if (k == "saved_cols") *value = p->wide();
-  else if (k == "tile") *value = p->layout(false, nullptr).tile;
+  else if (k == "tile") *value = p->forward_layout.tile;
   else if (k == "captured") *value = p->captured;
   else return set_err(AGMM_ERR_INVALID_ARG, "unknown key '%s'", key);
   return ok();
@@ -478,8 +487,8 @@ int agmm_ff_forward(agmm_ff_plan_t p, const void* const* shard_ptrs, const void*
   if (saved_scales && !saved) return set_err(AGMM_ERR_INVALID_ARG, "saved_scales without saved");
   std::lock_guard<std::mutex> lk(p->mu);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const agmm_ff_plan::Layout L = p->layout(false, p->ws);
-  return p->run(s, L.a || L.w, [&] { return p->forward(L, shard_ptrs, W, bias, residual, Y, saved, saved_scales, s); });
+  const bool ordered = p->forward_layout.a || p->forward_layout.w;
+  return p->run(s, ordered, [&] { return p->forward(shard_ptrs, W, bias, residual, Y, saved, saved_scales, s); });
 }
 
 // Whether the plan's way back needs kept pre-activations.

@@ -1,7 +1,6 @@
 // Product with an epilogue, and the gated product: few rows (gfx950).
 //
-// FM x FN blocks of 16 rows x 16 tile columns per workgroup, whose waves share
-// out k, 64 elements at a time, and load their operands straight into
+// 16 FM rows x YC columns of y per workgroup, whose waves share out k, 64 elements at a time, and load their operands straight into
 // registers: 16-byte accesses to global memory may start at any word, which
 // loads into LDS may not, so k and the strides may be anything and nothing is
 // copied first.  The waves' sums are added in LDS in a fixed order, wave w
@@ -18,16 +17,21 @@ namespace agmm {
 
 namespace {
 
-template <int DT, int FM, int FN, int UN, bool ODD, bool GATED>
-__global__ __launch_bounds__(256) void feed_few_kernel(FeedProblem fp) {
+// YC: columns of y per workgroup.  FN = 1 with YC = 8 fills twice the CUs of a
+// short y: plain, both halves of the block read the same 8 rows of B (the same
+// cache lines); gated, its halves are 8 rows of each part.
+template <int DT, int FM, int YC, int UN, int WAVES, bool ODD, bool GATED>
+__global__ __launch_bounds__(64 * WAVES) void feed_few_kernel(FeedProblem fp) {
   const GemmProblem& p = fp.gemm;
-  constexpr int PARTS = GATED ? 2 : 1, FQ = FN / PARTS;
-  __shared__ float part[4][FM][FN][4][64];
+  constexpr int PARTS = GATED ? 2 : 1;
+  constexpr bool HALF = YC == 8;
+  constexpr int FN = HALF ? 1 : YC / 16 * PARTS, FQ = HALF ? 1 : YC / 16;
+  __shared__ float part[WAVES][FM][FN][4][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g4 = lane >> 4, i16 = lane & 15;
   const int M = p.m, NC = fp.n, K = p.k;
   const int cb = (int)blockIdx.x / p.order.num_rb, rb = (int)blockIdx.x - cb * p.order.num_rb;
-  const int m0 = rb * 16 * FM, y0 = cb * 16 * FQ;
+  const int m0 = rb * 16 * FM, y0 = cb * YC;
   // rows and columns past the end read the last one and are never used
   const uint16_t *a[FM], *b[FN];
 #pragma unroll
@@ -36,9 +40,10 @@ __global__ __launch_bounds__(256) void feed_few_kernel(FeedProblem fp) {
     a[f] = static_cast<const uint16_t*>(p.rows.a_group[g]) + (int64_t)(i - g * p.rows.rows_per_group) * p.rows.a_ld + 8 * g4;
   }
 #pragma unroll
-  for (int f = 0; f < FN; ++f)
-    b[f] = static_cast<const uint16_t*>(p.b) + 8 * g4 +
-           ((int64_t)(f % PARTS) * NC + min(y0 + 16 * (f / PARTS) + i16, NC - 1)) * p.ldb;
+  for (int f = 0; f < FN; ++f) {
+    const int h = HALF ? (GATED ? i16 >> 3 : 0) : f % PARTS, c = HALF ? i16 & 7 : 16 * (f / PARTS) + i16;
+    b[f] = static_cast<const uint16_t*>(p.b) + 8 * g4 + ((int64_t)h * NC + min(y0 + c, NC - 1)) * p.ldb;
+  }
 
   f32x4_t acc[FM][FN];
 #pragma unroll
@@ -94,17 +99,20 @@ __global__ __launch_bounds__(256) void feed_few_kernel(FeedProblem fp) {
   u32x4_t fa[2][2 * UN][FM], fb[2][2 * UN][FN];
   uint32_t wa[2][W][FM], wb[2][W][FN];
   if (wave < groups) load(wave * UN, fa[0], fb[0], wa[0], wb[0]);
-  for (int c = wave; c < groups; c += 8) {
-    // two groups per turn, the last one loaded again where there is none
-    load((c + 4 < groups ? c + 4 : c) * UN, fa[1], fb[1], wa[1], wb[1]);
+  for (int c = wave; c < groups; c += 2 * WAVES) {
+    // two groups per turn, the last one loaded again where there is none; all of
+    // a group's loads are issued before the other's products
+    load((c + WAVES < groups ? c + WAVES : c) * UN, fa[1], fb[1], wa[1], wb[1]);
+    __builtin_amdgcn_sched_barrier(0);
     use(fa[0], fb[0], wa[0], wb[0]);
-    if (c + 4 >= groups) break;
-    load((c + 8 < groups ? c + 8 : c) * UN, fa[0], fb[0], wa[0], wb[0]);
+    if (c + WAVES >= groups) break;
+    load((c + 2 * WAVES < groups ? c + 2 * WAVES : c) * UN, fa[0], fb[0], wa[0], wb[0]);
+    __builtin_amdgcn_sched_barrier(0);
     use(fa[1], fb[1], wa[1], wb[1]);
   }
   // what is left: halves of 32 elements, shared out over the waves, those
   // past k elementwise and zero
-  for (int at = groups * UN * 64 + 32 * wave; at < K; at += 128) {
+  for (int at = groups * UN * 64 + 32 * wave; at < K; at += 32 * WAVES) {
     u32x4_t ta[FM], tb[FN];
     const int left = K - at - 8 * g4;
 #pragma unroll
@@ -126,16 +134,20 @@ __global__ __launch_bounds__(256) void feed_few_kernel(FeedProblem fp) {
   float x[FN][4];
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
-    const int c = y0 + 16 * (j / PARTS) + 4 * g4, left = NC - c;
+    const int h = HALF ? (GATED ? g4 >> 1 : 0) : j % PARTS, c = y0 + (HALF ? 4 * (g4 & 1) : 16 * (j / PARTS) + 4 * g4), left = NC - c;
     f32x4_t b4 = {0.f, 0.f, 0.f, 0.f};
-    if (fp.bias) b4 = load4<DT>(static_cast<const uint16_t*>(fp.bias) + (int64_t)(j % PARTS) * NC + c, left);
+    if (fp.bias) b4 = load4<DT>(static_cast<const uint16_t*>(fp.bias) + (int64_t)h * NC + c, left);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      x[j][e] = (part[0][wave][j][e][lane] + part[1][wave][j][e][lane] + part[2][wave][j][e][lane] + part[3][wave][j][e][lane]) + b4[e];
+    for (int e = 0; e < 4; ++e) {
+      float t = part[0][wave][j][e][lane];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) t += part[w][wave][j][e][lane];
+      x[j][e] = t + b4[e];
+    }
   }
-  if (fp.kept.values) {
+  if (YC >= kKeptBlock && fp.kept.values) {
     const int64_t wide = fp.kept.wide;
-    // blocks of 32 columns of a part: two accumulator blocks (launched with FN 4)
+    // blocks of 32 columns of a part: two accumulator blocks 
 #pragma unroll
     for (int h = 0; h < PARTS; ++h)
 #pragma unroll
@@ -167,7 +179,11 @@ __global__ __launch_bounds__(256) void feed_few_kernel(FeedProblem fp) {
         }
       }
   }
-  if (!in) return;
+  float factor[4];   // YC 8: the second part's, from the lane that holds it
+  if constexpr (HALF && GATED)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) factor[e] = __shfl_xor(x[0][e], 32);
+  if (!in || (HALF && g4 >= 2)) return;
   with_kind(fp.act.kind, [&](auto kind) {
     constexpr int KIND = decltype(kind)::value;
 #pragma unroll
@@ -177,8 +193,8 @@ __global__ __launch_bounds__(256) void feed_few_kernel(FeedProblem fp) {
       float y[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        y[e] = act_value<KIND>(x[PARTS * q][e], fp.act.c1, fp.act.c3);
-        if constexpr (GATED) y[e] *= x[PARTS * q + PARTS - 1][e];
+        y[e] = act_value<KIND>(x[HALF ? 0 : PARTS * q][e], fp.act.c1, fp.act.c3);
+        if constexpr (GATED) y[e] *= HALF ? factor[e] : x[HALF ? 0 : PARTS * q + PARTS - 1][e];
       }
       if (!GATED && fp.residual) {
         const f32x4_t r = load4<DT>(static_cast<const uint16_t*>(fp.residual) + (int64_t)row * fp.ldr + c, left);
@@ -190,44 +206,43 @@ __global__ __launch_bounds__(256) void feed_few_kernel(FeedProblem fp) {
   });
 }
 
-template <int DT, int FM, int FN, int UN, bool GATED>
+template <int DT, int FM, int YC, int UN, int WAVES, bool GATED>
 void launch_shape(const FeedProblem& p, unsigned grid, hipStream_t s) {
   const bool odd = p.gemm.ldb % 2 != 0 || p.gemm.rows.a_ld % 2 != 0;
-  if (odd) hipLaunchKernelGGL((feed_few_kernel<DT, FM, FN, UN, true, GATED>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((feed_few_kernel<DT, FM, FN, UN, false, GATED>), dim3(grid), dim3(256), 0, s, p);
+  if (odd) hipLaunchKernelGGL((feed_few_kernel<DT, FM, YC, UN, WAVES, true, GATED>), dim3(grid), dim3(64 * WAVES), 0, s, p);
+  else hipLaunchKernelGGL((feed_few_kernel<DT, FM, YC, UN, WAVES, false, GATED>), dim3(grid), dim3(64 * WAVES), 0, s, p);
 }
 
 template <int DT>
-hipError_t launch_type(const FeedProblem& p, int fm, int fn, unsigned grid, hipStream_t s) {
+hipError_t launch_type(const FeedProblem& p, int fm, int yc, unsigned grid, hipStream_t s) {
   if (p.gated) {
-    if (fm == 1 && fn == 2) launch_shape<DT, 1, 2, 4, true>(p, grid, s);
-    else if (fm == 1) launch_shape<DT, 1, 4, 2, true>(p, grid, s);
-    else if (fn == 2) launch_shape<DT, 4, 2, 1, true>(p, grid, s);
-    else launch_shape<DT, 4, 4, 1, true>(p, grid, s);
+    if (fm == 1 && yc == 8) launch_shape<DT, 1, 8, 4, 8, true>(p, grid, s);
+    else if (fm == 1 && yc == 16) launch_shape<DT, 1, 16, 2, 8, true>(p, grid, s);
+    else if (fm == 1) launch_shape<DT, 1, 32, 2, 4, true>(p, grid, s);
+    else if (yc == 16) launch_shape<DT, 4, 16, 1, 4, true>(p, grid, s);
+    else launch_shape<DT, 4, 32, 1, 4, true>(p, grid, s);
   } else {
-    if (fm == 1 && fn == 1) launch_shape<DT, 1, 1, 4, false>(p, grid, s);
-    else if (fm == 1 && fn == 2) launch_shape<DT, 1, 2, 4, false>(p, grid, s);
-    else if (fm == 1) launch_shape<DT, 1, 4, 2, false>(p, grid, s);
-    else if (fn == 1) launch_shape<DT, 4, 1, 2, false>(p, grid, s);
-    else if (fn == 2) launch_shape<DT, 4, 2, 1, false>(p, grid, s);
-    else launch_shape<DT, 4, 4, 1, false>(p, grid, s);
+    if (fm == 1 && yc == 8) launch_shape<DT, 1, 8, 4, 8, false>(p, grid, s);
+    else if (fm == 1 && yc == 16) launch_shape<DT, 1, 16, 4, 8, false>(p, grid, s);
+    else if (fm == 1) launch_shape<DT, 1, 64, 2, 4, false>(p, grid, s);
+    else if (yc == 16) launch_shape<DT, 4, 16, 2, 4, false>(p, grid, s);
+    else launch_shape<DT, 4, 64, 1, 4, false>(p, grid, s);
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_feed_few(const FeedProblem& p, int fm, int fn, int dtype, hipStream_t stream) {
+hipError_t launch_feed_few(const FeedProblem& p, int fm, int yc, int dtype, hipStream_t stream) {
   const int64_t grid = (int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb;
-  const int64_t cols = p.gated ? 2 * (((int64_t)p.n + 15) / 16 * 16) : p.n;
-  if ((fm != 1 && fm != 4) || (fn != 1 && fn != 2 && fn != 4) || (p.gated && (fn == 1 || p.residual)) || p.gemm.n != cols ||
-      p.gemm.order.num_rb != (p.gemm.m + 16 * fm - 1) / (16 * fm) || p.gemm.order.num_cb != (cols + 16 * fn - 1) / (16 * fn) ||
+  const int most = p.gated ? 32 : 64;
+  if ((fm != 1 && fm != 4) || (yc != 8 && yc != 16 && yc != most) || (yc == 8 && fm != 1) || (p.gated && p.residual) ||
+      p.gemm.order.num_rb != (p.gemm.m + 16 * fm - 1) / (16 * fm) || p.gemm.order.num_cb != (p.n + (int64_t)yc - 1) / yc ||
       grid < 1 || grid >= kFeedGrid || (int64_t)p.gemm.rows.num_groups * p.gemm.rows.rows_per_group != p.gemm.m ||
-      (p.kept.values && p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock) ||
-      (p.kept.values && fn != 4))
+      (p.kept.values && (yc != most || p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock)))
     return hipErrorInvalidValue;
-  return dtype == kDtypeBf16 ? launch_type<kDtypeBf16>(p, fm, fn, (unsigned)grid, stream)
-       : dtype == kDtypeFp16 ? launch_type<kDtypeFp16>(p, fm, fn, (unsigned)grid, stream) : hipErrorInvalidValue;
+  return dtype == kDtypeBf16 ? launch_type<kDtypeBf16>(p, fm, yc, (unsigned)grid, stream)
+       : dtype == kDtypeFp16 ? launch_type<kDtypeFp16>(p, fm, yc, (unsigned)grid, stream) : hipErrorInvalidValue;
 }
 
 }  // namespace agmm

@@ -51,10 +51,11 @@ struct FeedProblem {
 constexpr int64_t kFeedGrid = int64_t(1) << 24;
 // Tiles of 256 x 256 or 128 x 128 tile columns; rows of whole 16-byte vectors.
 hipError_t launch_feed_tiles(const FeedProblem& p, int tile, int dtype, hipStream_t stream);
-// Few rows: blocks of 16 fm rows x 16 fn tile columns (fm 1 or 4; fn 1, 2 or 4,
-// not 1 where gated, 4 where pre-activations are kept: their blocks of 32
+// Few rows: blocks of 16 fm rows x yc columns of y (fm 1 or 4; yc 8 with fm 1,
+// 16, or 64, gated 32: that where pre-activations are kept, whose blocks of 32
 // columns of a part lie in one workgroup); any k and strides, operands in place.
-hipError_t launch_feed_few(const FeedProblem& p, int fm, int fn, int dtype, hipStream_t stream);
+// order.num_cb counts blocks of yc columns.
+hipError_t launch_feed_few(const FeedProblem& p, int fm, int yc, int dtype, hipStream_t stream);
 
 // The elementwise part of the way back: d = dy * (derivative of y by p), by
 // rows [m][ldd] and transposed [parts * n][ldt] (zeros from m to ldt), each
