@@ -34,15 +34,46 @@ __global__ __launch_bounds__(64 * WAVES) void feed_few_kernel(FeedProblem fp) {
   const int m0 = rb * 16 * FM, y0 = cb * YC;
   // rows and columns past the end read the last one and are never used
   const uint16_t *a[FM], *b[FN];
+  if constexpr (FM == 1) {
+    // the shards' addresses of up to 16 rows by scalar loads and a choice per
+    // lane: a load per lane from the kernel's arguments, on whose result the
+    // rows' own loads wait, takes as long as those
+    const int rpg = p.rows.rows_per_group, i = min(m0 + i16, M - 1), g = i / rpg, first = m0 / rpg;
+    const void* base = p.rows.a_group[first];
 #pragma unroll
-  for (int f = 0; f < FM; ++f) {
-    const int i = min(m0 + 16 * f + i16, M - 1), g = i / p.rows.rows_per_group;
-    a[f] = static_cast<const uint16_t*>(p.rows.a_group[g]) + (int64_t)(i - g * p.rows.rows_per_group) * p.rows.a_ld + 8 * g4;
+    for (int q = 1; q < 16; ++q) {
+      const void* other = p.rows.a_group[min(first + q, p.rows.num_groups - 1)];
+      if (g == first + q) base = other;
+    }
+    a[0] = static_cast<const uint16_t*>(base) + (int64_t)(i - g * rpg) * p.rows.a_ld + 8 * g4;
+  } else {
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+      const int i = min(m0 + 16 * f + i16, M - 1), g = i / p.rows.rows_per_group;
+      a[f] = static_cast<const uint16_t*>(p.rows.a_group[g]) + (int64_t)(i - g * p.rows.rows_per_group) * p.rows.a_ld + 8 * g4;
+    }
   }
 #pragma unroll
   for (int f = 0; f < FN; ++f) {
     const int h = HALF ? (GATED ? i16 >> 3 : 0) : f % PARTS, c = HALF ? i16 & 7 : 16 * (f / PARTS) + i16;
     b[f] = static_cast<const uint16_t*>(p.b) + 8 * g4 + ((int64_t)h * NC + min(y0 + c, NC - 1)) * p.ldb;
+  }
+
+  // what the epilogue adds, on its way early
+  f32x4_t bias[FN], res[FQ];
+  const int row = m0 + 16 * wave + i16;       // wave w ends with row block w
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int h = HALF ? (GATED ? g4 >> 1 : 0) : j % PARTS, c = y0 + (HALF ? 4 * (g4 & 1) : 16 * (j / PARTS) + 4 * g4);
+    bias[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (fp.bias && wave < FM) bias[j] = load4<DT>(static_cast<const uint16_t*>(fp.bias) + (int64_t)h * NC + c, NC - c);
+  }
+#pragma unroll
+  for (int q = 0; q < FQ; ++q) {
+    const int c = y0 + (HALF ? 4 * (g4 & 1) : 16 * q + 4 * g4);
+    res[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (!GATED && fp.residual && wave < FM && row < M)
+      res[q] = load4<DT>(static_cast<const uint16_t*>(fp.residual) + (int64_t)row * fp.ldr + c, NC - c);
   }
 
   f32x4_t acc[FM][FN];
@@ -70,12 +101,21 @@ __global__ __launch_bounds__(64 * WAVES) void feed_few_kernel(FeedProblem fp) {
         v = *reinterpret_cast<const u32x4_word_t*>(x);
       }
     };
+    // B first: it comes from furthest.  Lanes without a row of their own load
+    // nothing (the way into a CU is what bounds 8 rows); what they hold reaches
+    // no result that is used.
+    if (!HALF || GATED || i16 < 8) {
 #pragma unroll
-    for (int h = 0; h < 2 * UN; ++h) {
+      for (int h = 0; h < 2 * UN; ++h)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) one(b[j] + (int64_t)c * 64 + 32 * h, fb[h][j], wb[ODD ? h : 0][j]);
+        for (int j = 0; j < FN; ++j) one(b[j] + (int64_t)c * 64 + 32 * h, fb[h][j], wb[ODD ? h : 0][j]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (FM > 1 || i16 < M - m0) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) one(a[i] + (int64_t)c * 64 + 32 * h, fa[h][i], wa[ODD ? h : 0][i]);
+      for (int h = 0; h < 2 * UN; ++h)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) one(a[i] + (int64_t)c * 64 + 32 * h, fa[h][i], wa[ODD ? h : 0][i]);
     }
   };
   const auto shift = [&](const uint16_t* x, u32x4_t& v, uint32_t w) {
@@ -96,17 +136,17 @@ __global__ __launch_bounds__(64 * WAVES) void feed_few_kernel(FeedProblem fp) {
     }
   };
   const int pieces = (ODD ? max(K - 2, 0) : K) / 64, groups = pieces / UN;   // the word behind lies in the row
-  u32x4_t fa[2][2 * UN][FM], fb[2][2 * UN][FN];
-  uint32_t wa[2][W][FM], wb[2][W][FN];
+  u32x4_t fa[2][2 * UN][FM] = {}, fb[2][2 * UN][FN] = {};
+  uint32_t wa[2][W][FM] = {}, wb[2][W][FN] = {};
   if (wave < groups) load(wave * UN, fa[0], fb[0], wa[0], wb[0]);
   for (int c = wave; c < groups; c += 2 * WAVES) {
-    // two groups per turn, the last one loaded again where there is none; all of
-    // a group's loads are issued before the other's products
-    load((c + WAVES < groups ? c + WAVES : c) * UN, fa[1], fb[1], wa[1], wb[1]);
+    // two groups per turn; all of a group's loads are issued before the other's
+    // products
+    if (c + WAVES < groups) load((c + WAVES) * UN, fa[1], fb[1], wa[1], wb[1]);
     __builtin_amdgcn_sched_barrier(0);
     use(fa[0], fb[0], wa[0], wb[0]);
     if (c + WAVES >= groups) break;
-    load((c + 2 * WAVES < groups ? c + 2 * WAVES : c) * UN, fa[0], fb[0], wa[0], wb[0]);
+    if (c + 2 * WAVES < groups) load((c + 2 * WAVES) * UN, fa[0], fb[0], wa[0], wb[0]);
     __builtin_amdgcn_sched_barrier(0);
     use(fa[1], fb[1], wa[1], wb[1]);
   }
@@ -129,20 +169,16 @@ __global__ __launch_bounds__(64 * WAVES) void feed_few_kernel(FeedProblem fp) {
       for (int e = 0; e < 4; ++e) part[wave][i][j][e][lane] = acc[i][j][e];
   __syncthreads();
   if (wave >= FM) return;
-  const int row = m0 + 16 * wave + i16;
   const bool in = row < M;
   float x[FN][4];
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
-    const int h = HALF ? (GATED ? g4 >> 1 : 0) : j % PARTS, c = y0 + (HALF ? 4 * (g4 & 1) : 16 * (j / PARTS) + 4 * g4), left = NC - c;
-    f32x4_t b4 = {0.f, 0.f, 0.f, 0.f};
-    if (fp.bias) b4 = load4<DT>(static_cast<const uint16_t*>(fp.bias) + (int64_t)h * NC + c, left);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float t = part[0][wave][j][e][lane];
 #pragma unroll
       for (int w = 1; w < WAVES; ++w) t += part[w][wave][j][e][lane];
-      x[j][e] = t + b4[e];
+      x[j][e] = t + bias[j][e];
     }
   }
   if (YC >= kKeptBlock && fp.kept.values) {
@@ -196,11 +232,9 @@ __global__ __launch_bounds__(64 * WAVES) void feed_few_kernel(FeedProblem fp) {
         y[e] = act_value<KIND>(x[HALF ? 0 : PARTS * q][e], fp.act.c1, fp.act.c3);
         if constexpr (GATED) y[e] *= HALF ? factor[e] : x[HALF ? 0 : PARTS * q + PARTS - 1][e];
       }
-      if (!GATED && fp.residual) {
-        const f32x4_t r = load4<DT>(static_cast<const uint16_t*>(fp.residual) + (int64_t)row * fp.ldr + c, left);
+      if (!GATED && fp.residual)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] += r[e];
-      }
+        for (int e = 0; e < 4; ++e) y[e] += res[q][e];
       store4(static_cast<uint16_t*>(fp.y) + (int64_t)row * fp.ldy + c, u32x2_t{pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3])}, left);
     }
   });
