@@ -33,6 +33,7 @@ void feed_grads_kernel(FeedPair gp) {
   const bool is_a = (int)blockIdx.x < gp.a_tiles;
   const GemmProblem& p = is_a ? gp.a : gp.w;
 
+#define AGMM_CLAMP
 #define AGMM_TILE_ID (is_a ? (int)blockIdx.x : (int)blockIdx.x - gp.a_tiles)
 #include "gemm_m16_loop.inc"
 

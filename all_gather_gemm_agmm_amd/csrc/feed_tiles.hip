@@ -40,8 +40,10 @@ void feed_tile_kernel(FeedProblem fp) {
   const int NC = fp.n;                         // columns of y
 
 // Tile column r of a gated tile: block r / 32 of y's columns, part (r / 16) % 2.
-#define AGMM_B_ROW(r) (GATED ? (n0 >> 1) + (((r) >> 5) << 4) + ((r) & 15) + (((r) >> 4) & 1) * NC : n0 + (r))
-#define AGMM_B_IN(r) (GATED ? (n0 >> 1) + (((r) >> 5) << 4) + ((r) & 15) < NC : n0 + (r) < N)
+#define AGMM_CLAMP
+#define AGMM_B_ROW(r) \
+  (GATED ? min((n0 >> 1) + (((r) >> 5) << 4) + ((r) & 15), NC - 1) + (((r) >> 4) & 1) * NC : min(n0 + (r), N - 1))
+#define AGMM_B_IN(r) true
 #define AGMM_B_FIRST (GATED ? n0 >> 1 : n0)
 #define AGMM_B_LAST (GATED ? (n0 >> 1) + BN / 2 - 1 + NC : n0 + BN - 1)
 #define AGMM_B_WHOLE (GATED ? (n0 + BN) >> 1 <= NC : n0 + BN <= N)
