@@ -68,52 +68,100 @@ struct agmm_ff_plan : PlanBase {
 
   // What a call of a pass uses, derived from the settings.
   struct Layout {
-    bool pad_a = false, pad_w = false;   // rows that are not whole 16-byte vectors: zero-padded copies
-    int64_t kp = 0;                      // k rounded up to 8
+    bool pad_a = false, pad_w = false;   // zero-padded copies
+    int64_t kp = 0;                      // row length of a copy: whole 128-byte lines
     int tile = 256;                      // forward; 64: the few-row form, in
+    int splits = 1;                      // ranges of k (tile 128)
+    int64_t per = 0;
     int fm = 0, yc = 0;                  // blocks of 16 fm rows x yc columns of y (kept pre-activations: most_yc())
     int tile_grads = 256;
     int a_ranges = 1, w_ranges = 1;      // ranges of the gradient products' sums
     int64_t a_per = 0, w_per = 0;
     char *a = nullptr, *w = nullptr, *d = nullptr, *dt = nullptr;
-    float *a_sums = nullptr, *w_sums = nullptr, *b_sums = nullptr;
+    float *parts = nullptr, *a_sums = nullptr, *w_sums = nullptr, *b_sums = nullptr;
     size_t bytes = 0;
   };
   Layout forward_layout, backward_layout;   // those of the settings and the workspace
 
   int64_t ld_a() const { return lda ? lda : k; }
   int64_t ld_w() const { return ldw ? ldw : k; }
-  int64_t m8() const { return round_up(m, 8); }
+  // Row lengths of d and d transposed: whole 128-byte lines.
+  int64_t ld_d() const { return round_up(cols(), 64); }
+  int64_t ld_dt() const { return round_up(m, 64); }
   int64_t cols() const { return parts * n; }
   int64_t wide() const { return round_up(n, agmm::kKeptBlock); }
   // Columns of the forward product's tiles (feed_kernels.h).
   int64_t tile_cols() const { return parts == 2 ? 2 * round_up(n, 16) : n; }
 
-  // Microseconds of one workgroup, measured on MI355X: 20 and 2.1 per 64 of its
-  // sum for the 256 x 256 tile (one to a CU), 5 and 1.25 for the 128 x 128 one
-  // (two to a CU; 0.7 where it has the CU alone).
-  static double workgroup_us(int tile, int64_t sum) {
-    return tile == 256 ? 20.0 + 2.1 * (double)cdiv(sum, 64) : 5.0 + 1.25 * (double)cdiv(sum, 64);
+  // Microseconds of the products' tiles, measured on MI355X: of a launch of
+  // `tiles` of them, each over `sum` elements of k.  A 256 x 256 tile has a CU to
+  // itself, 10 and 1.4 per 64 of its sum, 1.1 where half the CUs have none; a
+  // 128 x 128 one shares it, 5 and 0.92, or 0.48 alone.  `lines`: the operands'
+  // rows start on 128-byte lines; where they do not, a tile's loads take twice
+  // the lines, which slows the smaller tile (1011 x 4040 -> 2 x 2051: 74 us, 40
+  // at 4096).
+  double tiles_us(int t, int64_t tiles, int64_t sum, bool lines) const {
+    const double steps = (double)cdiv(sum, 64);
+    if (t == 256) return (double)cdiv(tiles, cu_count) * (10.0 + (2 * tiles <= cu_count ? 1.1 : 1.4) * steps * (lines ? 1.0 : 1.05));
+    const double by = steps * (lines ? 1.0 : 1.8);
+    const int64_t rest = tiles % (2 * cu_count);
+    const double shared = std::max(0.0, (double)rest / cu_count - 1.0);   // CUs with two in the last round
+    return (double)(tiles / (2 * cu_count)) * (5.0 + 0.92 * by) + (rest == 0 ? 0.0 : 5.0 + (0.48 + 0.44 * shared) * by);
   }
 
-  // Form of the forward product: the one that takes the least.  `copied`: the
-  // tiles need a copy of W first, which the few-row form does not.
-  void pick_tile(Layout& L, bool copied) const {
+  // Microseconds of copies of A and W as rows of whole lines.
+  double copy_us() const { return 5.0 + (double)(m + cols()) * (double)k * 4 / 4.8e6; }
+
+  // The few-row form in blocks of yc columns of y: 4.5 and 21 per MB of a CU's
+  // rows and columns (27 where four waves share out k, 1.7 times that for odd
+  // strides), or W at 4.5 TB/s, and a tenth of the other.  E.g. (us) 8 x 4096 -> 1792: 7.8 by 8 columns, 8.7
+  // by 16, 21 by 64; 128 x 4096 -> 7168: 73 by 16, 35 by 64; 8 x 8192 -> 3584: 24
+  // by 8, 16 by 16.
+  double few_us(int fm, int yc) const {
+    const double mb = 2e-6 * (double)k * (double)(std::min<int64_t>(m, 16 * fm) + parts * yc);
+    const double each = (fm == 1 && yc <= 16 ? 21.0 : 27.0) * (ld_a() % 2 != 0 || ld_w() % 2 != 0 ? 1.7 : 1.0);
+    const int64_t wgs = cdiv(m, 16 * fm) * cdiv(n, yc);
+    const double in = 4.5 + (double)cdiv(wgs, cu_count) * each * mb, read = 2.0 + (double)cols() * (double)k * 2 / 4.5e6;
+    return std::max(in, read) + 0.1 * std::min(in, read);
+  }
+
+  // Form of the forward product: the one that takes the least, with the copies
+  // it needs.  Copies have rows of whole lines; rows that are whole 16-byte
+  // vectors already are copied where that pays.
+  void pick_tile(Layout& L, bool must_copy) const {
     const int64_t nc = tile_cols();
-    const double big = (double)cdiv(cdiv(m, 256) * cdiv(nc, 256), cu_count) * workgroup_us(256, k);
-    const int64_t tiles = cdiv(m, 128) * cdiv(nc, 128), rest = tiles % (2 * cu_count);
-    const double small = (double)(tiles / (2 * cu_count)) * workgroup_us(128, k) +
-                         (rest == 0 ? 0.0 : rest > cu_count ? workgroup_us(128, k) : 5.0 + 0.7 * (double)cdiv(k, 64));
-    const double bytes = (double)cols() * (double)k * 2;
-    L.tile = tile_key > 0 ? (int)tile_key : big <= small ? 256 : 128;
-    if (tile_key > 0 && tile_key != 64) return;
+    const bool lines = ld_a() % 64 == 0 && ld_w() % 64 == 0;
+    double best = -1;
+    const auto offer = [&](int tile, bool copied, int splits, double us) {
+      if (tile_key > 0 && tile != tile_key) return;
+      us += copied ? copy_us() : 0.0;
+      if (best >= 0 && us >= best) return;
+      best = us;
+      L.tile = tile;
+      L.splits = splits;
+      L.pad_a = L.pad_w = copied;
+    };
+    for (bool copied : {false, true}) {
+      if (!copied && must_copy) continue;
+      if (copied && !must_copy && lines) continue;
+      offer(256, copied, 1, tiles_us(256, cdiv(m, 256) * cdiv(nc, 256), k, lines || copied));
+      const int64_t tiles = cdiv(m, 128) * cdiv(nc, 128);
+      for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        if (s > 1 && (k < 256 * s || tiles * s > 4 * cu_count)) break;
+        // the ranges' sums are written and read at 4 TB/s
+        const double join = s > 1 ? 4.0 + (double)(s * m) * (double)nc * 8 / 4e6 : 0.0;
+        offer(128, copied, s, tiles_us(128, tiles * s, cdiv(k, s), lines || copied) + join);
+      }
+    }
     L.fm = m <= 16 ? 1 : 4;
-    const int64_t rows = cdiv(m, 16 * L.fm);
-    L.yc = cdiv(n, most_yc()) * rows >= 2 * cu_count ? most_yc() : L.fm == 1 && cdiv(n, 16) < cu_count ? 8 : 16;
-    const int64_t wgs = rows * cdiv(n, L.yc);
-    const double rate = (L.fm == 4 && L.yc == most_yc() ? 6e6 : 10e6) / (copied && (ld_a() % 2 != 0 || ld_w() % 2 != 0) ? 1.7 : 1.0);
-    const double few = 5.0 + std::max((double)wgs * 2 * (16 * L.fm + parts * L.yc) * (double)k / rate, bytes / 4.8e6);
-    if (tile_key == 64 || (few < std::min(big, small) + (copied ? 2.0 + 2 * bytes / 5e6 : 0.0) && few_fits())) L.tile = 64;
+    if (!few_fits()) return;
+    double few = -1;
+    for (int yc : {8, 16, most_yc()}) {
+      if (yc == 8 && L.fm > 1) continue;
+      const double us = few_us(L.fm, yc);
+      if (few < 0 || us < few) few = us, L.yc = yc;
+    }
+    offer(64, false, 1, few);
   }
 
   int most_yc() const { return parts == 2 ? 32 : 64; }
@@ -123,20 +171,23 @@ struct agmm_ff_plan : PlanBase {
 
   Layout layout(bool grad, char* base) const {
     Layout L;
-    L.kp = round_up(k, 8);
-    L.pad_a = k % 8 != 0 || ld_a() % 8 != 0;
-    L.pad_w = k % 8 != 0 || ld_w() % 8 != 0;
+    L.kp = round_up(k, 64);
+    const bool must_a = k % 8 != 0 || ld_a() % 8 != 0, must_w = k % 8 != 0 || ld_w() % 8 != 0;   // not whole 16-byte vectors
     Cut c{base};
     if (!grad) {
-      pick_tile(L, L.pad_w);
-      if (L.tile == 64) L.pad_a = L.pad_w = false;   // read in place
+      pick_tile(L, must_a || must_w);
       if (L.pad_a) L.a = c.take((size_t)m * L.kp * 2);
       if (L.pad_w) L.w = c.take((size_t)cols() * L.kp * 2);
+      L.per = round_up(cdiv(L.pad_a ? L.kp : k, L.splits), 64);
+      L.splits = (int)cdiv(k, L.per);
+      if (L.splits > 1) L.parts = reinterpret_cast<float*>(c.take((size_t)L.splits * m * round_up(tile_cols(), 16) * 4));
     } else {
+      L.pad_a = must_a;
+      L.pad_w = must_w;
       if (L.pad_a || N > 1) L.a = c.take((size_t)m * L.kp * 2);   // dW's product reads it k x n, in one piece
       if (L.pad_w) L.w = c.take((size_t)cols() * L.kp * 2);
-      L.d = c.take((size_t)m * round_up(cols(), 8) * 2);
-      L.dt = c.take((size_t)cols() * m8() * 2);
+      L.d = c.take((size_t)m * ld_d() * 2);
+      L.dt = c.take((size_t)cols() * ld_dt() * 2);
       L.b_sums = reinterpret_cast<float*>(c.take((size_t)cdiv(m, agmm::kDRows) * cols() * 4));
       // One launch computes both products; each sum may be cut into ranges.
       // Tile and ranges are those that take the least: the workgroups' time
@@ -149,9 +200,10 @@ struct agmm_ff_plan : PlanBase {
         if (tile_key > 64 && t != tile_key) continue;
         const int64_t a_tiles = cdiv(m, t) * cdiv(k, t), w_tiles = cdiv(cols(), t) * cdiv(k, t);
         const double slots = cu_count * (t == 128 ? 2 : 1);
+        const auto one = [&](int64_t sum) { return t == 256 ? 10.0 + 1.4 * (double)cdiv(sum, 64) : 5.0 + 0.92 * (double)cdiv(sum, 64); };
         for (int64_t ra = 1; ra == 1 || (ra <= 64 && a_tiles * ra <= 4 * cu_count && cols() / ra >= 256); ra *= 2)
           for (int64_t rw = 1; rw == 1 || (rw <= 64 && w_tiles * rw <= 4 * cu_count && m / rw >= 256); rw *= 2) {
-            const double a_us = workgroup_us(t, cdiv(cols(), ra)), w_us = workgroup_us(t, cdiv(m, rw));
+            const double a_us = one(cdiv(cols(), ra)), w_us = one(cdiv(m, rw));
             const double sums = (ra > 1 ? (double)(ra * m) : 0.0) + (rw > 1 ? (double)(rw * cols()) : 0.0);
             const double us = std::max({((double)(a_tiles * ra) * a_us + (double)(w_tiles * rw) * w_us) / slots + w_us / 2, a_us, w_us}) +
                               sums * (double)k * 8 / 4e6 + (sums > 0 ? 3.0 : 0.0);
@@ -251,11 +303,12 @@ struct agmm_ff_plan : PlanBase {
     }
     p.gemm.m = (int32_t)m;
     p.gemm.n = (int32_t)tile_cols();
-    p.gemm.k = (int32_t)(L.tile == 64 ? k : L.kp);
+    p.gemm.k = (int32_t)(L.w ? L.kp : k);
     p.gemm.b = L.w ? L.w : W;
     p.gemm.ldb = L.w ? L.kp : ld_w();
-    p.gemm.splits = 1;
-    p.gemm.k_per_split = (int32_t)L.kp;
+    p.gemm.splits = L.splits;
+    p.gemm.k_per_split = (int32_t)L.per;
+    p.gemm.partials = L.parts;
     p.n = (int32_t)n;
     p.gated = parts == 2;
     p.act = activation_of(act);
@@ -283,9 +336,9 @@ struct agmm_ff_plan : PlanBase {
     e.dy = dY;
     e.lddy = lddy ? lddy : n;
     e.d = dA ? L.d : nullptr;
-    e.ldd = round_up(cols(), 8);
+    e.ldd = ld_d();
     e.dt = dW ? L.dt : nullptr;
-    e.ldt = m8();
+    e.ldt = ld_dt();
     e.sums = dbias ? L.b_sums : nullptr;
     hipError_t err = agmm::launch_feed_d(e, dtype, s);
     if (err != hipSuccess) return hip_err(err, "feed-forward gradient launch");
@@ -302,7 +355,7 @@ struct agmm_ff_plan : PlanBase {
     ga.partials = L.a_sums;
     ga.c = dA;
     ga.ldc = ldda ? ldda : k;
-    gw.rows = dense(L.dt, cols(), m8());
+    gw.rows = dense(L.dt, cols(), ld_dt());
     gw.order = tiles_of(cols(), k, L.tile_grads);
     gw.m = (int32_t)cols();
     gw.n = (int32_t)k;
@@ -374,6 +427,7 @@ struct agmm_norm_plan : PlanBase {
     p.cols = cols;
     p.dtype = dtype;
     p.wtype = wtype;
+    p.cus = cu_count;
     p.x = x;
     p.ldx = ldx ? ldx : cols;
     p.weight = weight;
@@ -487,7 +541,7 @@ int agmm_ff_forward(agmm_ff_plan_t p, const void* const* shard_ptrs, const void*
   if (saved_scales && !saved) return set_err(AGMM_ERR_INVALID_ARG, "saved_scales without saved");
   std::lock_guard<std::mutex> lk(p->mu);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool ordered = p->forward_layout.a || p->forward_layout.w;
+  const bool ordered = p->forward_layout.bytes > 0;
   return p->run(s, ordered, [&] { return p->forward(shard_ptrs, W, bias, residual, Y, saved, saved_scales, s); });
 }
 

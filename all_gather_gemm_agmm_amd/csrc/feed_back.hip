@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256) void feed_d_kernel(FeedDProblem p) {
           uint16_t* out = static_cast<uint16_t*>(p.d) + row * p.ldd + (int64_t)h * p.n;
           store8(out + col, w, left);
           if (h == PARTS - 1 && left <= 8)   // the row's end, up to a whole 16-byte piece
-            for (int64_t e = p.n; h * (int64_t)p.n + e < p.ldd; ++e) out[e] = 0;
+            for (int64_t e = p.n; (h * (int64_t)p.n + e) % 8 != 0; ++e) out[e] = 0;
         }
       }
     }
@@ -243,8 +243,7 @@ hipError_t launch_feed_d(const FeedDProblem& p, int dtype, hipStream_t s) {
   const int64_t grid = (p.m + kDRows - 1) / kDRows * ((p.n + kDCols - 1) / kDCols);
   if (p.m < 1 || p.n < 1 || grid >= kFeedGrid || (!p.kept.values && (p.gated || p.act.kind != kActLinear)) ||
       (p.kept.values && p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock) ||
-      (p.d && (p.ldd < (int64_t)parts * p.n || p.ldd > (int64_t)parts * p.n + 7)) ||
-      (p.dt && (p.ldt % 8 != 0 || p.ldt < p.m || p.ldt > p.m + 7)) || (dtype != kDtypeBf16 && dtype != kDtypeFp16))
+      (p.d && (p.ldd % 8 != 0 || p.ldd < (int64_t)parts * p.n)) || (p.dt && (p.ldt % 8 != 0 || p.ldt < p.m)) || (dtype != kDtypeBf16 && dtype != kDtypeFp16))
     return hipErrorInvalidValue;
   const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, p); };
   if (dtype == kDtypeBf16) p.gated ? go(feed_d_kernel<kDtypeBf16, true>) : go(feed_d_kernel<kDtypeBf16, false>);

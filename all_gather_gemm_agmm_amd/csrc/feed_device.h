@@ -174,6 +174,70 @@ __device__ __forceinline__ void with_kind(int kind, F&& f) {
   else f(IntTag<kActLinear>{});
 }
 
+// Eight columns of a row of the product, bias added: what is kept of them, and
+// y.  Four neighbouring lanes hold the 32 columns from `col` rounded down on,
+// and all of them come here together.
+template <int DT, bool GATED, int KIND>
+__device__ __forceinline__ void finish8(const FeedProblem& fp, const float (&v)[GATED ? 2 : 1][8], int64_t row, bool in, int col) {
+  constexpr int PARTS = GATED ? 2 : 1;
+  const int left = fp.n - col;
+  const int64_t wide = fp.kept.wide;
+  if (fp.kept.values && col < wide) {
+#pragma unroll
+    for (int h = 0; h < PARTS; ++h) {
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = e < left ? v[h][e] : 0.0f;
+      const int64_t out = (row * PARTS + h) * wide + col;
+      if (!fp.kept.scales) {
+        if (in)
+          *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(fp.kept.values) + out) =
+              u32x4_t{pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3]), pack2<DT>(w[4], w[5]), pack2<DT>(w[6], w[7])};
+      } else {
+        float size = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) size = larger_finite(size, w[e]);
+        size = fmaxf(size, __shfl_xor(size, 1));
+        size = fmaxf(size, __shfl_xor(size, 2));
+        const uint32_t code = scale_code(size);
+        const float inv = scale_inverse(code);
+        if (in) {
+          *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(fp.kept.values) + out) =
+              u32x2_t{pack4_e4m3(w[0], w[1], w[2], w[3], inv), pack4_e4m3(w[4], w[5], w[6], w[7], inv)};
+          if (col % kKeptBlock == 0) fp.kept.scales[out / kKeptBlock] = (uint8_t)code;
+        }
+      }
+    }
+  }
+  if (!in || left <= 0) return;
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    y[e] = act_value<KIND>(v[0][e], fp.act.c1, fp.act.c3);
+    if constexpr (GATED) y[e] *= v[1][e];
+  }
+  if (!GATED && fp.residual) {
+    const u32x4_t b = load8(static_cast<const uint16_t*>(fp.residual) + row * fp.ldr + col, left);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] += e & 1 ? high16<DT>(b[e >> 1]) : low16<DT>(b[e >> 1]);
+  }
+  store8(static_cast<uint16_t*>(fp.y) + row * fp.ldy + col,
+         u32x4_t{pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3]), pack2<DT>(y[4], y[5]), pack2<DT>(y[6], y[7])}, left);
+}
+
+// The bias of eight columns of each part, zeros where there is none.
+template <int DT, bool GATED>
+__device__ __forceinline__ void bias8(const FeedProblem& fp, int col, float (&bias)[GATED ? 2 : 1][8]) {
+  const int left = fp.n - col;
+#pragma unroll
+  for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+    u32x4_t b = {0u, 0u, 0u, 0u};
+    if (fp.bias && left > 0) b = load8(static_cast<const uint16_t*>(fp.bias) + (int64_t)h * fp.n + col, left);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bias[h][e] = e & 1 ? high16<DT>(b[e >> 1]) : low16<DT>(b[e >> 1]);
+  }
+}
+
 }  // namespace
 
 }  // namespace agmm

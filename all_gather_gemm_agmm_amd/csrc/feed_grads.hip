@@ -40,15 +40,15 @@ void feed_grads_kernel(FeedPair gp) {
   if (p.splits > 1) {
     // rows of the sums are whole 16-byte vectors; what lies past n in the last
     // one is never used
-    const int row0 = m0 + wm * T::TM + i16, col0 = n0 + wn * T::TN + 4 * g4;
+    const int out_row = m0 + wm * T::TM + i16, out_col = n0 + wn * T::TN + 4 * g4;
     const int64_t ld = (N + 3) & ~3;
-    float* base = p.partials + ((int64_t)split * M + row0) * ld + col0;
+    float* base = p.partials + ((int64_t)split * M + out_row) * ld + out_col;
 #pragma unroll
     for (int i = 0; i < FM; ++i, base += 16 * ld) {
-      if (row0 + 16 * i < M)
+      if (out_row + 16 * i < M)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-          if (col0 + 16 * j < N) *reinterpret_cast<f32x4_t*>(base + 16 * j) = acc[i][j];
+          if (out_col + 16 * j < N) *reinterpret_cast<f32x4_t*>(base + 16 * j) = acc[i][j];
       __builtin_amdgcn_sched_barrier(0);   // one block row's values at a time
     }
   } else {

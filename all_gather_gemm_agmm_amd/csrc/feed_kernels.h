@@ -50,6 +50,8 @@ struct FeedProblem {
 };
 constexpr int64_t kFeedGrid = int64_t(1) << 24;
 // Tiles of 256 x 256 or 128 x 128 tile columns; rows of whole 16-byte vectors.
+// gemm.splits > 1 (tile 128): ranges of k to gemm.partials [splits][m][tile
+// columns rounded up to 16], and a second launch that finishes.
 hipError_t launch_feed_tiles(const FeedProblem& p, int tile, int dtype, hipStream_t stream);
 // Few rows: blocks of 16 fm rows x yc columns of y (fm 1 or 4; yc 8 with fm 1,
 // 16, or 64, gated 32: that where pre-activations are kept, whose blocks of 32
@@ -58,8 +60,9 @@ hipError_t launch_feed_tiles(const FeedProblem& p, int tile, int dtype, hipStrea
 hipError_t launch_feed_few(const FeedProblem& p, int fm, int yc, int dtype, hipStream_t stream);
 
 // The elementwise part of the way back: d = dy * (derivative of y by p), by
-// rows [m][ldd] and transposed [parts * n][ldt] (zeros from m to ldt), each
-// where asked for, and the sums of d over blocks of kDRows rows.
+// rows [m][ldd] (zeros past parts * n up to a multiple of 8) and transposed
+// [parts * n][ldt] (the same past m), each where asked for, and the sums of d
+// over blocks of kDRows rows.
 constexpr int kDRows = 128, kDCols = 64;
 struct FeedDProblem {
   int64_t m;
@@ -120,6 +123,7 @@ hipError_t launch_sum_columns(const SumColumns& p, hipStream_t stream);
 struct NormProblem {
   int64_t rows, cols;
   int32_t dtype, wtype;
+  int32_t cus;             // of the GPU
   const void* x;
   int64_t ldx;
   const void* weight;

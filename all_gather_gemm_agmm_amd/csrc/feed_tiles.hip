@@ -56,21 +56,12 @@ void feed_tile_kernel(FeedProblem fp) {
   constexpr int PIECES = BN / PARTS / 8;       // of eight columns of y, a thread each
   constexpr int STEP = T::THREADS / PIECES;    // rows at a time
   const int c = tid % PIECES;
-  const int col = n0 / PARTS + 8 * c, left = NC - col;
+  const int col = n0 / PARTS + 8 * c;
   // 16-byte pieces of the thread's columns: pieces at, at + 1 of the first part
   // and, gated, at + 4, at + 5 of the second
   const int at = GATED ? 8 * (c >> 1) + 2 * (c & 1) : 2 * c;
   float bias[PARTS][8];
-#pragma unroll
-  for (int h = 0; h < PARTS; ++h) {
-    u32x4_t b = {0u, 0u, 0u, 0u};
-    if (fp.bias && left > 0) b = load8(static_cast<const uint16_t*>(fp.bias) + (int64_t)h * NC + col, left);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) bias[h][e] = e & 1 ? high16<DT>(b[e >> 1]) : low16<DT>(b[e >> 1]);
-  }
-  const int64_t wide = fp.kept.wide;
-  const bool keep = fp.kept.values && col < wide;
-  const float c1 = fp.act.c1, c3 = fp.act.c3;
+  bias8<DT, GATED>(fp, col, bias);
 
 #pragma unroll 1
   for (int half = 0; half < HALVES; ++half) {
@@ -100,59 +91,96 @@ void feed_tile_kernel(FeedProblem fp) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[h][4 * s + e] = x[e] + bias[h][4 * s + e];
           }
-        if (keep) {
-#pragma unroll
-          for (int h = 0; h < PARTS; ++h) {
-            float w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = e < left ? v[h][e] : 0.0f;
-            const int64_t out = (row * PARTS + h) * wide + col;
-            if (!fp.kept.scales) {
-              if (row < M)
-                *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(fp.kept.values) + out) =
-                    u32x4_t{pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3]), pack2<DT>(w[4], w[5]), pack2<DT>(w[6], w[7])};
-            } else {
-              float size = 0.0f;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) size = larger_finite(size, w[e]);
-              size = fmaxf(size, __shfl_xor(size, 1));
-              size = fmaxf(size, __shfl_xor(size, 2));
-              const uint32_t code = scale_code(size);
-              const float inv = scale_inverse(code);
-              if (row < M) {
-                *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(fp.kept.values) + out) =
-                    u32x2_t{pack4_e4m3(w[0], w[1], w[2], w[3], inv), pack4_e4m3(w[4], w[5], w[6], w[7], inv)};
-                if ((c & 3) == 0) fp.kept.scales[out / kKeptBlock] = (uint8_t)code;
-              }
-            }
-          }
-        }
-        if (row < M && left > 0) {
-          float y[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[e] = act_value<KIND>(v[0][e], c1, c3);
-            if constexpr (GATED) y[e] *= v[1][e];
-          }
-          if (!GATED && fp.residual) {
-            const u32x4_t b = load8(static_cast<const uint16_t*>(fp.residual) + row * fp.ldr + col, left);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] += e & 1 ? high16<DT>(b[e >> 1]) : low16<DT>(b[e >> 1]);
-          }
-          store8(static_cast<uint16_t*>(fp.y) + row * fp.ldy + col,
-                 u32x4_t{pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3]), pack2<DT>(y[4], y[5]), pack2<DT>(y[6], y[7])}, left);
-        }
+        finish8<DT, GATED, KIND>(fp, v, row, row < M, col);
       }
     });
   }
 }
 
+// Few tiles: ranges of k, 128 x 128 tile columns each, to fp32 sums [range][m]
+// [tile columns rounded up to 16] ...
+template <int DT, bool GATED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void feed_part_kernel(FeedProblem fp) {
+  constexpr bool BT = true, SPLIT = true;
+  constexpr int BM = 128, BN = 128, BK = 64, WAVES = 4, OCC = 2;
+  using T = GemmTile<BM, BN, BK, DT, BT, 5, WAVES, kLoopParts>;
+  constexpr int kBK = BK;
+  constexpr int FM = T::TM / 16, FN = T::TN / 16;
+  constexpr int STEPS = BK / 32;
+  __shared__ __attribute__((aligned(1024))) char smem[T::LDS_BYTES];
+  const GemmProblem& p = fp.gemm;
+  const int NC = fp.n;
+#include "gemm_m16_loop.inc"
+
+  const int out_row = m0 + wm * T::TM + i16, out_col = n0 + wn * T::TN + 4 * g4;
+  const int64_t ld = (N + 15) & ~15;
+  float* base = p.partials + ((int64_t)split * M + out_row) * ld + out_col;
+#pragma unroll
+  for (int i = 0; i < FM; ++i, base += 16 * ld)
+    if (out_row + 16 * i < M)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        if (out_col + 16 * j < ld) *reinterpret_cast<f32x4_t*>(base + 16 * j) = acc[i][j];
+}
+
+// ... which are added in order, and finished, by a thread per eight columns of y.
+template <int DT, bool GATED>
+__global__ __launch_bounds__(256) void feed_join_kernel(FeedProblem fp) {
+  constexpr int PARTS = GATED ? 2 : 1;
+  const GemmProblem& p = fp.gemm;
+  const uint32_t pieces = (uint32_t)((fp.n + kKeptBlock - 1) / kKeptBlock * (kKeptBlock / 8));   // of four lanes each
+  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x, row = u / pieces;
+  const int c = (int)(u - row * pieces), col = 8 * c;
+  const bool in = row < p.m;
+  const int64_t ld = (p.n + 15) & ~15, plane = p.m * ld;
+  const int at = GATED ? 32 * (c >> 1) + 8 * (c & 1) : col;
+  float v[PARTS][8];
+  bias8<DT, GATED>(fp, col, v);
+  if (in && col < fp.n) {
+    const float* src = p.partials + row * ld + at;
+    f32x4_t t[PARTS][2] = {};
+    for (int s0 = 0; s0 < p.splits; s0 += 4) {
+      f32x4_t x[4][PARTS][2];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (s0 + s < p.splits)
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) x[s][h][q] = *reinterpret_cast<const f32x4_t*>(src + (s0 + s) * plane + 16 * h + 4 * q);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (s0 + s < p.splits)
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) t[h][q] += x[s][h][q];
+    }
+#pragma unroll
+    for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[h][e] += t[h][e >> 2][e & 3];
+  }
+  with_kind(fp.act.kind, [&](auto kind) { finish8<DT, GATED, decltype(kind)::value>(fp, v, row, in, col); });
+}
+
 template <int DT>
 hipError_t launch_type(const FeedProblem& p, int tile, hipStream_t s) {
-  const unsigned grid = (unsigned)(p.gemm.order.num_rb * p.gemm.order.num_cb);
-  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, s, p); };
-  if (tile == 256) p.gated ? go(feed_tile_kernel<256, 256, DT, 1, true>) : go(feed_tile_kernel<256, 256, DT, 1, false>);
-  else p.gated ? go(feed_tile_kernel<128, 128, DT, 2, true>) : go(feed_tile_kernel<128, 128, DT, 2, false>);
+  const unsigned grid = (unsigned)((int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb * p.gemm.splits);
+  const auto go = [&](auto kernel, unsigned wgs) { hipLaunchKernelGGL(kernel, dim3(wgs), dim3(256), 0, s, p); };
+  if (p.gemm.splits > 1) {
+    p.gated ? go(feed_part_kernel<DT, true>, grid) : go(feed_part_kernel<DT, false>, grid);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    const int64_t pieces = ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * (kKeptBlock / 8);
+    const unsigned joins = (unsigned)((p.gemm.m * pieces + 255) / 256);
+    p.gated ? go(feed_join_kernel<DT, true>, joins) : go(feed_join_kernel<DT, false>, joins);
+  } else if (tile == 256) {
+    p.gated ? go(feed_tile_kernel<256, 256, DT, 1, true>, grid) : go(feed_tile_kernel<256, 256, DT, 1, false>, grid);
+  } else {
+    p.gated ? go(feed_tile_kernel<128, 128, DT, 2, true>, grid) : go(feed_tile_kernel<128, 128, DT, 2, false>, grid);
+  }
   return hipGetLastError();
 }
 
@@ -162,7 +190,11 @@ hipError_t launch_feed_tiles(const FeedProblem& p, int tile, int dtype, hipStrea
   const int64_t cols = p.gated ? 2 * (((int64_t)p.n + 15) / 16 * 16) : p.n;
   if ((tile != 256 && tile != 128) || p.gemm.n != cols || p.gemm.order.num_rb != (p.gemm.m + tile - 1) / tile ||
       p.gemm.order.num_cb != (p.gemm.n + tile - 1) / tile ||
-      (int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb >= kFeedGrid || p.gemm.k % 8 != 0 ||
+      p.gemm.splits < 1 || (int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb * p.gemm.splits >= kFeedGrid || p.gemm.k % 8 != 0 ||
+      (p.gemm.splits > 1 && (tile != 128 || !p.gemm.partials || p.gemm.k_per_split % 64 != 0 ||
+                             (int64_t)p.gemm.splits * p.gemm.k_per_split < p.gemm.k ||
+                             (int64_t)(p.gemm.splits - 1) * p.gemm.k_per_split >= p.gemm.k ||
+                             p.gemm.m * (((int64_t)p.n + 31) / 32 * 4) >= kFeedGrid * 256)) ||
       (p.gated && p.residual) || (p.kept.values && p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock))
     return hipErrorInvalidValue;
   return dtype == kDtypeBf16 ? launch_type<kDtypeBf16>(p, tile, s)

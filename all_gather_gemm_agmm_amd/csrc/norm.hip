@@ -113,16 +113,29 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*buf)[N], int& t
 template <int DT, int WT, int THREADS, int CH>
 __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormProblem p) {
   constexpr int V = Elem<DT>::V;
+  constexpr bool HOLD = CH <= 2;               // the weights stay in registers from row to row
   __shared__ float buf[2 * THREADS / 64][1], buf2[2 * THREADS / 64][2];
   int turn = 0, turn2 = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    u32x4_t x[CH];
+  const auto col_of = [&](int c) { return ((int64_t)c * THREADS + threadIdx.x) * V; };
+  u32x4_t x[CH], next[CH];
+  const auto load = [&](int64_t row, u32x4_t (&to)[CH]) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V;
-      x[c] = u32x4_t{0u, 0u, 0u, 0u};
-      if (col < p.cols) x[c] = load_piece<DT>(p.x, row * p.ldx + col, p.cols - col);
+      to[c] = u32x4_t{0u, 0u, 0u, 0u};
+      if (row < p.rows && col_of(c) < p.cols) to[c] = load_piece<DT>(p.x, row * p.ldx + col_of(c), p.cols - col_of(c));
     }
+  };
+  int64_t row = blockIdx.x;
+  load(row, x);
+  float w[HOLD ? CH : 1][V], b[HOLD ? CH : 1][V];
+  if constexpr (HOLD)
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      load_weights<WT>(p.weight, col_of(c), p.cols - col_of(c), 1.0f, w[c]);
+      load_weights<WT>(p.bias, col_of(c), p.cols - col_of(c), 0.0f, b[c]);
+    }
+  for (; row < p.rows; row += gridDim.x) {
+    load(row + gridDim.x, next);               // on its way while this row is reduced
     float s[1] = {0.0f}, t[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -132,7 +145,7 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormProblem p) {
     const float near = s[0] / (float)p.cols;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t left = p.cols - ((int64_t)c * THREADS + threadIdx.x) * V;
+      const int64_t left = p.cols - col_of(c);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float d = e < left ? piece_value<DT>(x[c], e) - near : 0.0f;
@@ -149,14 +162,19 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormProblem p) {
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V, left = p.cols - col;
-      if (left <= 0) continue;
-      float w[V], b[V], y[V];
-      load_weights<WT>(p.weight, col, left, 1.0f, w);
-      load_weights<WT>(p.bias, col, left, 0.0f, b);
+      const int64_t col = col_of(c), left = p.cols - col;
+      if (left > 0) {
+        float y[V];
+        if constexpr (!HOLD) {
+          load_weights<WT>(p.weight, col, left, 1.0f, w[0]);
+          load_weights<WT>(p.bias, col, left, 0.0f, b[0]);
+        }
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] = __builtin_fmaf((piece_value<DT>(x[c], e) - near - rest) * rstd, w[e], b[e]);
-      store_piece<DT>(p.y, row * p.ldy + col, left, y);
+        for (int e = 0; e < V; ++e)
+          y[e] = __builtin_fmaf((piece_value<DT>(x[c], e) - near - rest) * rstd, w[HOLD ? c : 0][e], b[HOLD ? c : 0][e]);
+        store_piece<DT>(p.y, row * p.ldy + col, left, y);
+      }
+      x[c] = next[c];
     }
   }
 }
@@ -351,19 +369,23 @@ __global__ __launch_bounds__(256) void norm_sums_long_kernel(NormProblem p) {
   }
 }
 
-constexpr int64_t kRowGrid = 1 << 20;   // workgroups of the kernels that take a row at a time
-
 int64_t pieces_of(int64_t cols, int dtype) { return (cols + (dtype == kDtypeFp32 ? 3 : 7)) / (dtype == kDtypeFp32 ? 4 : 8); }
 
 template <int DT, int WT>
 hipError_t forward_type(const NormProblem& p, hipStream_t s) {
   const int64_t pieces = pieces_of(p.cols, DT);
-  const dim3 grid((unsigned)(p.rows < kRowGrid ? p.rows : kRowGrid));
-  const auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, s, p); };
+  // as many workgroups as the CUs hold at a time (2048 lanes each), which take
+  // every so many-th row
+  const auto go = [&](auto kernel, int threads) {
+    const int64_t most = (int64_t)p.cus * (2048 / threads);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.rows < most ? p.rows : most)), dim3(threads), 0, s, p);
+  };
   if (pieces <= 64) go(norm_forward_kernel<DT, WT, 64, 1>, 64);
+  else if (pieces <= 128) go(norm_forward_kernel<DT, WT, 128, 1>, 128);
   else if (pieces <= 256) go(norm_forward_kernel<DT, WT, 256, 1>, 256);
-  else if (pieces <= 512) go(norm_forward_kernel<DT, WT, 256, 2>, 256);
-  else if (pieces <= 1024) go(norm_forward_kernel<DT, WT, 256, 4>, 256);
+  else if (pieces <= 512) go(norm_forward_kernel<DT, WT, 512, 1>, 512);
+  else if (pieces <= 1024) go(norm_forward_kernel<DT, WT, 1024, 1>, 1024);
+  else if (pieces <= 2048) go(norm_forward_kernel<DT, WT, 1024, 2>, 1024);
   else if (pieces <= 4096) go(norm_forward_kernel<DT, WT, 1024, 4>, 1024);
   else go(norm_forward_long_kernel<DT, WT>, 1024);
   return hipGetLastError();
@@ -383,13 +405,13 @@ hipError_t backward_type(const NormProblem& p, hipStream_t s) {
   else {
     // the sums first: dx may overwrite dy
     if (p.sums) go(norm_sums_long_kernel<DT>, (pieces + 255) / 256 * p.groups, 256);
-    if (p.dx) go(norm_dx_long_kernel<DT, WT>, p.rows < kRowGrid ? p.rows : kRowGrid, 1024);
+    if (p.dx) go(norm_dx_long_kernel<DT, WT>, p.rows < 2 * p.cus ? p.rows : 2 * p.cus, 1024);
   }
   return hipGetLastError();
 }
 
 bool valid(const NormProblem& p) {
-  return p.rows >= 1 && p.rows < (int64_t(1) << 31) && p.cols >= 1 && p.cols < (int64_t(1) << 31) && p.x &&
+  return p.rows >= 1 && p.rows < (int64_t(1) << 31) && p.cus >= 1 && p.cols >= 1 && p.cols < (int64_t(1) << 31) && p.x &&
          (p.wtype == p.dtype || p.wtype == kDtypeFp32);
 }
 

@@ -144,7 +144,7 @@ struct LossRows {
 };
 
 // Copy of 16-bit rows as rows of whole 16-byte vectors (zeros past cols):
-// out [num_groups][rows][8 * chunks], chunks = ceil(cols / 8).  Sources need
+// out [num_groups][rows][8 * chunks], chunks >= ceil(cols / 8).  Sources need
 // element alignment only.
 struct PadRows {
   const void* group[kMaxGroups];
