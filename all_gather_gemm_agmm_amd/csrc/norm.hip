@@ -28,21 +28,60 @@ struct Elem {
   static constexpr int V = 16 / kBytes;        // of a piece
 };
 
-// A piece of a row of any alignment as fp32 values, zeros past `left`.
-template <int DT>
-__device__ __forceinline__ u32x4_t load_piece(const void* x, int64_t at, int64_t left) {
-  if constexpr (DT == kDtypeFp32) {
-    typedef u32x4_t u32x4_word_t __attribute__((aligned(4)));
-    const uint32_t* p = static_cast<const uint32_t*>(x) + at;
-    if (left >= 4) return *reinterpret_cast<const u32x4_word_t*>(p);
-    u32x4_t v = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < left) v[e] = p[e];
-    return v;
-  } else {
-    return load8(static_cast<const uint16_t*>(x) + at, left < 8 ? (int)left : 8);
+// A lane's piece of a row of `cols`, at column `col`, of any alignment: zeros
+// past the row's end, in two steps.  load(): 16 bytes of the row, the piece
+// itself or, at its end, the last 16, unconditionally: a condition would make
+// every later wait for a load one for all stores too.  settle(), where the
+// values are needed, shifts out what lies before the piece.  SHORT rows, of less
+// than 16 bytes, are loaded by element.
+template <int DT, bool SHORT>
+struct Piece {
+  static constexpr int V = Elem<DT>::V;
+  int64_t at;              // column of the 16 bytes
+  int over;                // elements of them before the piece
+  int64_t col, cols;
+  __device__ __forceinline__ Piece(int64_t col, int64_t cols) : col(col), cols(cols) {
+    const int64_t last = SHORT ? 0 : cols - V;
+    at = col < last ? col : last;
+    over = SHORT ? 0 : col - at < V ? (int)(col - at) : V;
   }
+  __device__ __forceinline__ u32x4_t load(const void* row) const {
+    if constexpr (!SHORT) {
+      return *reinterpret_cast<const u32x4_any_t*>(static_cast<const char*>(row) + at * Elem<DT>::kBytes);
+    } else {
+      u32x4_t v = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (col + e < cols) {
+          if constexpr (DT == kDtypeFp32) v[e] = static_cast<const uint32_t*>(row)[col + e];
+          else v[e >> 1] |= (uint32_t)static_cast<const uint16_t*>(row)[col + e] << (16 * (e & 1));
+        }
+      return v;
+    }
+  }
+  __device__ __forceinline__ u32x4_t settle(u32x4_t v) const {
+    if (!SHORT && over) {
+      if (DT != kDtypeFp32 && (over & 1))
+        v = u32x4_t{__builtin_amdgcn_alignbyte(v[1], v[0], 2), __builtin_amdgcn_alignbyte(v[2], v[1], 2),
+                    __builtin_amdgcn_alignbyte(v[3], v[2], 2), v[3] >> 16};
+      const int words = DT != kDtypeFp32 ? over >> 1 : over;
+      if (words & 1) v = u32x4_t{v[1], v[2], v[3], 0u};
+      if (words & 2) v = u32x4_t{v[2], v[3], 0u, 0u};
+      if (words & 4) v = u32x4_t{0u, 0u, 0u, 0u};
+    }
+    return v;
+  }
+};
+template <int DT>
+__device__ __forceinline__ u32x4_t load_piece(const void* x, int64_t col, int64_t cols) {
+  if (cols < Elem<DT>::V) return Piece<DT, true>(col, cols).load(x);
+  const Piece<DT, false> p(col, cols);
+  return p.settle(p.load(x));
+}
+// Row r, `ld` elements apart.
+template <int DT>
+__device__ __forceinline__ const void* row_of(const void* x, int64_t r, int64_t ld) {
+  return static_cast<const char*>(x) + r * ld * Elem<DT>::kBytes;
 }
 template <int DT>
 __device__ __forceinline__ float piece_value(const u32x4_t& v, int e) {
@@ -68,20 +107,20 @@ __device__ __forceinline__ void store_piece(void* x, int64_t at, int64_t left, c
   }
 }
 // V consecutive weights (of the rows' type or fp32) as fp32, `none` where there
-// are no weights or past `left`.
+// are no weights or past the end.
 template <int WT, int V>
-__device__ __forceinline__ void load_weights(const void* w, int64_t at, int64_t left, float none, float (&v)[V]) {
+__device__ __forceinline__ void load_weights(const void* w, int64_t col, int64_t cols, float none, float (&v)[V]) {
 #pragma unroll
   for (int e = 0; e < V; ++e) v[e] = none;
   if (!w) return;
-  constexpr int U = Elem<WT>::V;
+  constexpr int U = Elem<WT>::V < V ? Elem<WT>::V : V;
 #pragma unroll
-  for (int s = 0; s < V / (U < V ? U : V); ++s) {
-    if (left - s * U <= 0) break;
-    const u32x4_t q = load_piece<WT>(w, at + s * U, left - s * U);
+  for (int s = 0; s < V / U; ++s) {
+    if (col + s * U >= cols) break;
+    const u32x4_t q = load_piece<WT>(w, col + s * U, cols);
 #pragma unroll
-    for (int e = 0; e < (U < V ? U : V); ++e)
-      if (s * U + e < left) v[s * U + e] = piece_value<WT>(q, e);
+    for (int e = 0; e < U; ++e)
+      if (col + s * U + e < cols) v[s * U + e] = piece_value<WT>(q, e);
   }
 }
 
@@ -110,20 +149,19 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*buf)[N], int& t
   }
 }
 
-template <int DT, int WT, int THREADS, int CH>
+template <int DT, int WT, int THREADS, int CH, bool SHORT = false>
 __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormProblem p) {
   constexpr int V = Elem<DT>::V;
-  constexpr bool HOLD = CH <= 2;               // the weights stay in registers from row to row
+  constexpr bool HOLD = THREADS <= 512;             // the weights stay in registers from row to row
   __shared__ float buf[2 * THREADS / 64][1], buf2[2 * THREADS / 64][2];
   int turn = 0, turn2 = 0;
   const auto col_of = [&](int c) { return ((int64_t)c * THREADS + threadIdx.x) * V; };
   u32x4_t x[CH], next[CH];
-  const auto load = [&](int64_t row, u32x4_t (&to)[CH]) {
+  const auto piece = [&](int c) { return Piece<DT, SHORT>(col_of(c), p.cols); };
+  const auto load = [&](int64_t row, u32x4_t (&to)[CH]) {   // past the last row: that one again
+    const void* at = row_of<DT>(p.x, row < p.rows ? row : p.rows - 1, p.ldx);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      to[c] = u32x4_t{0u, 0u, 0u, 0u};
-      if (row < p.rows && col_of(c) < p.cols) to[c] = load_piece<DT>(p.x, row * p.ldx + col_of(c), p.cols - col_of(c));
-    }
+    for (int c = 0; c < CH; ++c) to[c] = piece(c).load(at);
   };
   int64_t row = blockIdx.x;
   load(row, x);
@@ -131,12 +169,15 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormProblem p) {
   if constexpr (HOLD)
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      load_weights<WT>(p.weight, col_of(c), p.cols - col_of(c), 1.0f, w[c]);
-      load_weights<WT>(p.bias, col_of(c), p.cols - col_of(c), 0.0f, b[c]);
+      load_weights<WT>(p.weight, col_of(c), p.cols, 1.0f, w[c]);
+      load_weights<WT>(p.bias, col_of(c), p.cols, 0.0f, b[c]);
     }
   for (; row < p.rows; row += gridDim.x) {
     load(row + gridDim.x, next);               // on its way while this row is reduced
+    __builtin_amdgcn_sched_barrier(0);
     float s[1] = {0.0f}, t[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c) x[c] = piece(c).settle(x[c]);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -166,8 +207,8 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormProblem p) {
       if (left > 0) {
         float y[V];
         if constexpr (!HOLD) {
-          load_weights<WT>(p.weight, col, left, 1.0f, w[0]);
-          load_weights<WT>(p.bias, col, left, 0.0f, b[0]);
+          load_weights<WT>(p.weight, col, p.cols, 1.0f, w[0]);
+          load_weights<WT>(p.bias, col, p.cols, 0.0f, b[0]);
         }
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -186,17 +227,17 @@ __global__ __launch_bounds__(1024) void norm_forward_long_kernel(NormProblem p) 
   __shared__ float buf[32][1], buf2[32][2];
   int turn = 0, turn2 = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const int64_t at = row * p.ldx;
+    const void* at = row_of<DT>(p.x, row, p.ldx);
     float s[1] = {0.0f}, t[2] = {0.0f, 0.0f};
     for (int64_t col = (int64_t)threadIdx.x * V; col < p.cols; col += 1024 * V) {
-      const u32x4_t x = load_piece<DT>(p.x, at + col, p.cols - col);
+      const u32x4_t x = load_piece<DT>(at, col, p.cols);
 #pragma unroll
       for (int e = 0; e < V; ++e) s[0] += piece_value<DT>(x, e);
     }
     block_sum<1024>(s, buf, turn);
     const float near = s[0] / (float)p.cols;
     for (int64_t col = (int64_t)threadIdx.x * V; col < p.cols; col += 1024 * V) {
-      const u32x4_t x = load_piece<DT>(p.x, at + col, p.cols - col);
+      const u32x4_t x = load_piece<DT>(at, col, p.cols);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float d = e < p.cols - col ? piece_value<DT>(x, e) - near : 0.0f;
@@ -213,10 +254,10 @@ __global__ __launch_bounds__(1024) void norm_forward_long_kernel(NormProblem p) 
     }
     for (int64_t col = (int64_t)threadIdx.x * V; col < p.cols; col += 1024 * V) {
       const int64_t left = p.cols - col;
-      const u32x4_t x = load_piece<DT>(p.x, at + col, left);
+      const u32x4_t x = load_piece<DT>(at, col, p.cols);
       float w[V], b[V], y[V];
-      load_weights<WT>(p.weight, col, left, 1.0f, w);
-      load_weights<WT>(p.bias, col, left, 0.0f, b);
+      load_weights<WT>(p.weight, col, p.cols, 1.0f, w);
+      load_weights<WT>(p.bias, col, p.cols, 0.0f, b);
 #pragma unroll
       for (int e = 0; e < V; ++e) y[e] = __builtin_fmaf((piece_value<DT>(x, e) - near - rest) * rstd, w[e], b[e]);
       store_piece<DT>(p.y, row * p.ldy + col, left, y);
@@ -224,74 +265,118 @@ __global__ __launch_bounds__(1024) void norm_forward_long_kernel(NormProblem p) 
   }
 }
 
-template <int DT, int WT, int THREADS, int CH>
-__global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormProblem p) {
-  constexpr int V = Elem<DT>::V;
-  __shared__ float buf[2 * THREADS / 64][2];
+// THREADS lanes a row, CH pieces each, 1024 / THREADS rows at a time, whose
+// column sums are added at the end.
+template <int DT, int WT, int THREADS, int CH, bool SHORT = false>
+__global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p) {
+  constexpr int V = Elem<DT>::V, ROWS = 1024 / THREADS, W = THREADS / 64;
+  __shared__ float buf[2][16][2];
+  __shared__ float more[ROWS > 1 ? 2 * THREADS * V * CH : 1];
   int turn = 0;
+  const int lane = threadIdx.x % THREADS, sub = threadIdx.x / THREADS;
+  const auto col_of = [&](int c) { return ((int64_t)c * THREADS + lane) * V; };
   float w[CH][V], dw[CH][V] = {}, db[CH][V] = {};
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V;
-    load_weights<WT>(p.weight, col, p.cols - col, 1.0f, w[c]);
-  }
+  for (int c = 0; c < CH; ++c) load_weights<WT>(p.weight, col_of(c), p.cols, 1.0f, w[c]);
   u32x4_t x[CH], dy[CH];
   float mean = 0.0f, rstd = 0.0f;
-  const auto load = [&](int64_t row) {
+  const auto piece = [&](int c) { return Piece<DT, SHORT>(col_of(c), p.cols); };
+  const auto load = [&](int64_t row) {         // past the last row: that one again
+    row = row < p.rows ? row : p.rows - 1;
+    const void *ax = row_of<DT>(p.x, row, p.ldx), *ady = row_of<DT>(p.dy, row, p.lddy);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V;
-      x[c] = dy[c] = u32x4_t{0u, 0u, 0u, 0u};
-      if (col < p.cols) {
-        x[c] = load_piece<DT>(p.x, row * p.ldx + col, p.cols - col);
-        dy[c] = load_piece<DT>(p.dy, row * p.lddy + col, p.cols - col);
-      }
+      x[c] = piece(c).load(ax);
+      dy[c] = piece(c).load(ady);
     }
     mean = p.mean[row];
     rstd = p.rstd[row];
   };
   const float inv = 1.0f / (float)p.cols;
-  int64_t row = blockIdx.x;
-  if (row < p.rows) load(row);
-  while (row < p.rows) {
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  load((int64_t)blockIdx.x * ROWS + sub);
+  for (int64_t first = (int64_t)blockIdx.x * ROWS; first < p.rows; first += step) {
+    const int64_t row = first + sub;
     float g[CH][V], h[CH][V], s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t left = p.cols - ((int64_t)c * THREADS + threadIdx.x) * V;
+      x[c] = piece(c).settle(x[c]);
+      dy[c] = row < p.rows ? piece(c).settle(dy[c]) : u32x4_t{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float d = piece_value<DT>(dy[c], e);
-        h[c][e] = e < left ? (piece_value<DT>(x[c], e) - mean) * rstd : 0.0f;
+        h[c][e] = col_of(c) + e < p.cols && row < p.rows ? (piece_value<DT>(x[c], e) - mean) * rstd : 0.0f;
         g[c][e] = d * w[c][e];
         s[0] += g[c][e];
         s[1] = __builtin_fmaf(g[c][e], h[c][e], s[1]);
         dw[c][e] = __builtin_fmaf(d, h[c][e], dw[c][e]);
         db[c][e] += d;
       }
-    }
-    const int64_t here = row;
     const float scale = rstd;
-    row += gridDim.x;
-    if (row < p.rows) load(row);
-    if (p.dx) {
-      block_sum<THREADS>(s, buf, turn);
+    load(row + step);                          // on its way while this row is reduced
+    __builtin_amdgcn_sched_barrier(0);
+    if (!p.dx) continue;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) s[q] += __shfl_xor(s[q], d);
+    if constexpr (W > 1) {
+      if ((threadIdx.x & 63) == 0) {
+        buf[turn][threadIdx.x >> 6][0] = s[0];
+        buf[turn][threadIdx.x >> 6][1] = s[1];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        s[q] = buf[turn][sub * W][q];
+#pragma unroll
+        for (int v = 1; v < W; ++v) s[q] += buf[turn][sub * W + v][q];
+      }
+      turn ^= 1;                               // two buffers in turn: one barrier a row
+    }
+    if (row < p.rows) {
       const float a = s[0] * inv, b = s[1] * inv;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V;
-        if (col >= p.cols) continue;
+        if (col_of(c) >= p.cols) continue;
         float v[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = scale * (g[c][e] - __builtin_fmaf(h[c][e], b, a));
-        store_piece<DT>(p.dx, here * p.lddx + col, p.cols - col, v);
+        store_piece<DT>(p.dx, row * p.lddx + col_of(c), p.cols - col_of(c), v);
       }
     }
   }
   if (!p.sums) return;
+  if constexpr (ROWS > 1)
+#pragma unroll 1
+    for (int r = 1; r < ROWS; ++r) {
+      if (sub == r)
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            more[((c * V + e) * 2 + 0) * THREADS + lane] = dw[c][e];
+            more[((c * V + e) * 2 + 1) * THREADS + lane] = db[c][e];
+          }
+      __syncthreads();
+      if (sub == 0)
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            dw[c][e] += more[((c * V + e) * 2 + 0) * THREADS + lane];
+            db[c][e] += more[((c * V + e) * 2 + 1) * THREADS + lane];
+          }
+      __syncthreads();
+    }
+  if (sub) return;
   float* out = p.sums + (int64_t)blockIdx.x * 2 * p.cols;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int64_t col = ((int64_t)c * THREADS + threadIdx.x) * V;
+    const int64_t col = col_of(c);
     if (col >= p.cols) continue;
 #pragma unroll
     for (int s = 0; s < V / 4; ++s) {
@@ -311,9 +396,10 @@ __global__ __launch_bounds__(1024) void norm_dx_long_kernel(NormProblem p) {
     const float mean = p.mean[row], rstd = p.rstd[row];
     const auto piece = [&](int64_t col, float (&g)[V], float (&h)[V]) {
       const int64_t left = p.cols - col;
-      const u32x4_t x = load_piece<DT>(p.x, row * p.ldx + col, left), dy = load_piece<DT>(p.dy, row * p.lddy + col, left);
+      const u32x4_t x = load_piece<DT>(row_of<DT>(p.x, row, p.ldx), col, p.cols),
+                    dy = load_piece<DT>(row_of<DT>(p.dy, row, p.lddy), col, p.cols);
       float w[V];
-      load_weights<WT>(p.weight, col, left, 1.0f, w);
+      load_weights<WT>(p.weight, col, p.cols, 1.0f, w);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         h[e] = e < left ? (piece_value<DT>(x, e) - mean) * rstd : 0.0f;
@@ -352,7 +438,8 @@ __global__ __launch_bounds__(256) void norm_sums_long_kernel(NormProblem p) {
   float dw[V] = {}, db[V] = {};
 #pragma unroll 4
   for (int64_t row = group; row < p.rows; row += p.groups) {
-    const u32x4_t x = load_piece<DT>(p.x, row * p.ldx + col, left), dy = load_piece<DT>(p.dy, row * p.lddy + col, left);
+    const u32x4_t x = load_piece<DT>(row_of<DT>(p.x, row, p.ldx), col, p.cols),
+                    dy = load_piece<DT>(row_of<DT>(p.dy, row, p.lddy), col, p.cols);
     const float mean = p.mean[row], rstd = p.rstd[row];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -374,20 +461,20 @@ int64_t pieces_of(int64_t cols, int dtype) { return (cols + (dtype == kDtypeFp32
 template <int DT, int WT>
 hipError_t forward_type(const NormProblem& p, hipStream_t s) {
   const int64_t pieces = pieces_of(p.cols, DT);
-  // as many workgroups as the CUs hold at a time (2048 lanes each), which take
-  // every so many-th row
-  const auto go = [&](auto kernel, int threads) {
-    const int64_t most = (int64_t)p.cus * (2048 / threads);
+  // workgroups that the CUs hold at a time, which take every so many-th row
+  const auto go = [&](auto kernel, int threads, int per = 1) {
+    const int64_t most = (int64_t)p.cus * per;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(p.rows < most ? p.rows : most)), dim3(threads), 0, s, p);
   };
-  if (pieces <= 64) go(norm_forward_kernel<DT, WT, 64, 1>, 64);
-  else if (pieces <= 128) go(norm_forward_kernel<DT, WT, 128, 1>, 128);
-  else if (pieces <= 256) go(norm_forward_kernel<DT, WT, 256, 1>, 256);
-  else if (pieces <= 512) go(norm_forward_kernel<DT, WT, 512, 1>, 512);
-  else if (pieces <= 1024) go(norm_forward_kernel<DT, WT, 1024, 1>, 1024);
-  else if (pieces <= 2048) go(norm_forward_kernel<DT, WT, 1024, 2>, 1024);
-  else if (pieces <= 4096) go(norm_forward_kernel<DT, WT, 1024, 4>, 1024);
-  else go(norm_forward_long_kernel<DT, WT>, 1024);
+  if (p.cols < Elem<DT>::V) go(norm_forward_kernel<DT, WT, 64, 1, true>, 64, 24);
+  else if (pieces <= 64) go(norm_forward_kernel<DT, WT, 64, 1>, 64, 24);
+  else if (pieces <= 128) go(norm_forward_kernel<DT, WT, 64, 2>, 64, 16);
+  else if (pieces <= 256) go(norm_forward_kernel<DT, WT, 256, 1>, 256, 8);
+  else if (pieces <= 512) go(norm_forward_kernel<DT, WT, 256, 2>, 256, 5);
+  else if (pieces <= 1024) go(norm_forward_kernel<DT, WT, 256, 4>, 256, 3);
+  else if (pieces <= 2048) go(norm_forward_kernel<DT, WT, 512, 4>, 512, 2);
+  else if (pieces <= 4096) go(norm_forward_kernel<DT, WT, 1024, 4>, 1024, 2);
+  else go(norm_forward_long_kernel<DT, WT>, 1024, 2);
   return hipGetLastError();
 }
 
@@ -397,9 +484,11 @@ hipError_t backward_type(const NormProblem& p, hipStream_t s) {
   const auto go = [&](auto kernel, int64_t grid, int threads) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), 0, s, p);
   };
-  if (pieces <= 64) go(norm_backward_kernel<DT, WT, 64, 1>, p.groups, 64);
-  else if (pieces <= 256) go(norm_backward_kernel<DT, WT, 256, 1>, p.groups, 256);
-  else if (pieces <= 512) go(norm_backward_kernel<DT, WT, 512, 1>, p.groups, 512);
+  if (p.cols < Elem<DT>::V) go(norm_backward_kernel<DT, WT, 64, 1, true>, p.groups, 1024);
+  else if (pieces <= 64) go(norm_backward_kernel<DT, WT, 64, 1>, p.groups, 1024);
+  else if (pieces <= 128) go(norm_backward_kernel<DT, WT, 128, 1>, p.groups, 1024);
+  else if (pieces <= 256) go(norm_backward_kernel<DT, WT, 256, 1>, p.groups, 1024);
+  else if (pieces <= 512) go(norm_backward_kernel<DT, WT, 512, 1>, p.groups, 1024);
   else if (pieces <= 1024) go(norm_backward_kernel<DT, WT, 1024, 1>, p.groups, 1024);
   else if (DT == kDtypeFp32 && pieces <= 2048) go(norm_backward_kernel<DT, WT, 1024, DT == kDtypeFp32 ? 2 : 1>, p.groups, 1024);
   else {
@@ -427,11 +516,13 @@ hipError_t by_type(const NormProblem& p, F&& f) {
 
 int norm_groups(int64_t rows, int64_t cols, int dtype, int cus) {
   const int64_t pieces = pieces_of(cols, dtype);
-  // as many workgroups as the CUs hold at a time, but two rows of sums for
-  // eight of x and dy at most
-  const int64_t per = pieces <= 64 ? 16 : pieces <= 256 ? 4 : pieces <= 512 ? 2 : 1;
-  int64_t groups = cus * per;
+  int64_t at_once = 1;                         // rows that a workgroup takes at a time
+  while (at_once < 16 && pieces * at_once <= 512) at_once *= 2;
+  // one workgroup a CU, whose sums are one row of [groups]; long rows: so many
+  // strips that they fill the CUs four times
+  int64_t groups = cus;
   if (pieces > (dtype == kDtypeFp32 ? 2048 : 1024)) groups = 4 * cus / ((pieces + 255) / 256);
+  else rows = (rows + at_once - 1) / at_once;
   if (groups > rows) groups = rows;
   return (int)(groups < 1 ? 1 : groups);
 }
