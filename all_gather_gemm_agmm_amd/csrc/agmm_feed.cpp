@@ -74,6 +74,8 @@ struct agmm_ff_plan : PlanBase {
     int splits = 1;                      // ranges of k (tile 128)
     int64_t per = 0;
     int fm = 0, yc = 0;                  // blocks of 16 fm rows x yc columns of y (kept pre-activations: most_yc())
+    int d_rows = 128;                    // rows of a workgroup of the elementwise part
+    bool groups = false;                 // dW's product reads A in the shards
     int tile_grads = 256;
     int a_ranges = 1, w_ranges = 1;      // ranges of the gradient products' sums
     int64_t a_per = 0, w_per = 0;
@@ -184,11 +186,15 @@ struct agmm_ff_plan : PlanBase {
     } else {
       L.pad_a = must_a;
       L.pad_w = must_w;
-      if (L.pad_a || N > 1) L.a = c.take((size_t)m * L.kp * 2);   // dW's product reads it k x n, in one piece
+      // dW's product reads A k x n: in the shards where they are whole k-tiles,
+      // else in one piece
+      L.groups = N > 1 && !L.pad_a && m_s % 64 == 0;
+      if (L.pad_a || (N > 1 && !L.groups)) L.a = c.take((size_t)m * L.kp * 2);
       if (L.pad_w) L.w = c.take((size_t)cols() * L.kp * 2);
       L.d = c.take((size_t)m * ld_d() * 2);
       L.dt = c.take((size_t)cols() * ld_dt() * 2);
-      L.b_sums = reinterpret_cast<float*>(c.take((size_t)cdiv(m, agmm::kDRows) * cols() * 4));
+      L.d_rows = cdiv(m, 128) * cdiv(n, agmm::kDCols) >= 2 * cu_count ? 128 : 32;
+      L.b_sums = reinterpret_cast<float*>(c.take((size_t)cdiv(m, L.d_rows) * cols() * 4));
       // One launch computes both products; each sum may be cut into ranges.
       // Tile and ranges are those that take the least: the workgroups' time
       // spread over the CUs and half of one for the last round, but no less than
@@ -250,8 +256,8 @@ struct agmm_ff_plan : PlanBase {
     return r;
   }
 
-  // Copies of A and W as rows of whole 16-byte vectors, where the layout has them.
-  int copies(const Layout& L, const void* const* shards, const void* W, hipStream_t s) const {
+  // The copies of A (shards not NULL) and W that the layout has.
+  agmm::FeedCopies copies(const Layout& L, const void* const* shards, const void* W) const {
     const auto copy = [&](const void* const* groups, int count, int64_t rows, int64_t ld, void* out) {
       agmm::PadRows c{};
       for (int g = 0; g < count; ++g) c.group[g] = groups[g];
@@ -261,17 +267,12 @@ struct agmm_ff_plan : PlanBase {
       c.ld = ld;
       c.chunks = L.kp / 8;
       c.out = out;
-      return agmm::launch_loss_prepare(nullptr, &c, dtype, s);
+      return c;
     };
-    if (L.a && shards) {
-      const hipError_t err = copy(shards, N, m_s, ld_a(), L.a);
-      if (err != hipSuccess) return hip_err(err, "row copy launch");
-    }
-    if (L.w && W) {
-      const hipError_t err = copy(&W, 1, cols(), ld_w(), L.w);
-      if (err != hipSuccess) return hip_err(err, "weight copy launch");
-    }
-    return AGMM_OK;
+    agmm::FeedCopies c{};
+    if (L.a && shards) c.a = copy(shards, N, m_s, ld_a(), L.a);
+    if (L.w && W) c.w = copy(&W, 1, cols(), ld_w(), L.w);
+    return c;
   }
 
   agmm::KeptRows kept_rows(const void* values, const void* scales) const {
@@ -281,8 +282,10 @@ struct agmm_ff_plan : PlanBase {
   int forward(const void* const* shards, const void* W, const void* bias, const void* residual, void* Y,
               void* saved, void* saved_scales, hipStream_t s) {
     const Layout& L = forward_layout;
-    const int rc = copies(L, shards, W, s);
-    if (rc != AGMM_OK) return rc;
+    if (L.a || L.w) {
+      const hipError_t err = agmm::launch_feed_copies(copies(L, shards, W), s);
+      if (err != hipSuccess) return hip_err(err, "operand copy launch");
+    }
     agmm::FeedProblem p{};
     if (L.a) {
       p.gemm.rows = dense(L.a, m, L.kp);
@@ -325,9 +328,8 @@ struct agmm_ff_plan : PlanBase {
   int backward(const void* const* shards, const void* W, const void* saved, const void* saved_scales, const void* dY, void* dA,
                void* dW, void* dbias, hipStream_t s) {
     const Layout& L = backward_layout;
-    const int rc = copies(L, dW ? shards : nullptr, dA ? W : nullptr, s);
-    if (rc != AGMM_OK) return rc;
     agmm::FeedDProblem e{};
+    e.block = L.d_rows;
     e.m = m;
     e.n = (int32_t)n;
     e.gated = parts == 2;
@@ -340,9 +342,10 @@ struct agmm_ff_plan : PlanBase {
     e.dt = dW ? L.dt : nullptr;
     e.ldt = ld_dt();
     e.sums = dbias ? L.b_sums : nullptr;
-    hipError_t err = agmm::launch_feed_d(e, dtype, s);
+    hipError_t err = agmm::launch_feed_d(e, copies(L, dW ? shards : nullptr, dA ? W : nullptr), dtype, s);
     if (err != hipSuccess) return hip_err(err, "feed-forward gradient launch");
-    agmm::GemmProblem ga{}, gw{};
+    agmm::FeedGrads g{};
+    agmm::GemmProblem &ga = g.a, &gw = g.w;
     ga.rows = dense(L.d, m, e.ldd);
     ga.order = tiles_of(m, k, L.tile_grads);
     ga.m = (int32_t)m;
@@ -360,33 +363,27 @@ struct agmm_ff_plan : PlanBase {
     gw.m = (int32_t)cols();
     gw.n = (int32_t)k;
     gw.k = (int32_t)m;
-    gw.b = L.a ? L.a : shards[0];
+    gw.b = L.a ? L.a : shards ? shards[0] : nullptr;
     gw.ldb = L.a ? L.kp : ld_a();
     gw.splits = L.w_ranges;
     gw.k_per_split = (int32_t)L.w_per;
     gw.partials = L.w_sums;
     gw.c = dW;
     gw.ldc = lddw ? lddw : k;
-    if (dA || dW) {
-      err = agmm::launch_feed_grads(dA ? &ga : nullptr, dW ? &gw : nullptr, L.tile_grads, dtype, s);
-      if (err != hipSuccess) return hip_err(err, "gradient products launch");
-    }
+    if (L.groups)
+      for (int r = 0; r < N && shards; ++r) g.w_group[r] = shards[r];
+    g.w_rows = L.groups ? (int32_t)m_s : 0;
+    if (!dA) ga.m = 0;
+    if (!dW) gw.m = 0;
+    if (dbias) g.bias = {L.b_sums, cdiv(m, L.d_rows), cols(), dbias};
+    err = agmm::launch_feed_grads(g, L.tile_grads, dtype, s);
+    if (err != hipSuccess) return hip_err(err, "gradient products launch");
     const auto ranges = [&](const agmm::GemmProblem& g) { return agmm::SumRanges{g.partials, g.splits, g.m, g.n, g.c, g.ldc}; };
     const agmm::SumRanges sa = ranges(ga), sw = ranges(gw);
     const bool more_a = dA && L.a_ranges > 1, more_w = dW && L.w_ranges > 1;
     if (more_a || more_w) {
       err = agmm::launch_sum_ranges(more_a ? &sa : nullptr, more_w ? &sw : nullptr, dtype, s);
       if (err != hipSuccess) return hip_err(err, "gradient sums launch");
-    }
-    if (dbias) {
-      agmm::SumColumns b{};
-      b.sums = L.b_sums;
-      b.groups = cdiv(m, agmm::kDRows);
-      b.cols = b.first = cols();
-      b.out = dbias;
-      b.dtype = dtype;
-      err = agmm::launch_sum_columns(b, s);
-      if (err != hipSuccess) return hip_err(err, "bias gradient launch");
     }
     return AGMM_OK;
   }

@@ -50,62 +50,161 @@ __device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
   return u32x4_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
 }
 
-template <int DT, bool GATED>
-__global__ __launch_bounds__(256) void feed_d_kernel(FeedDProblem p) {
+// One thread's share of a copy: every `step`-th 16-byte piece of its output.
+__device__ __forceinline__ void copy_rows(const PadRows& c, int64_t first, int64_t step) {
+  const int64_t all = c.num_groups * c.rows * c.chunks;
+  const auto from = [&](int64_t u, int64_t& row, int& col) {
+    row = u / (uint32_t)c.chunks;
+    col = (int)(u - row * c.chunks) * 8;
+    const int64_t g = row / (uint32_t)c.rows;
+    return static_cast<const uint16_t*>(c.group[g]) + (row - g * c.rows) * c.ld + col;
+  };
+#pragma unroll 1
+  for (int64_t u = first; u < all; u += 4 * step) {
+    u32x4_t v[4];                              // on their way together
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      int64_t row;
+      int col;
+      if (u + q * step < all) {
+        const uint16_t* x = from(u + q * step, row, col);
+        v[q] = load8(x, (int)c.cols - col);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (u + q * step < all) *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(c.out) + (u + q * step) * 8) = v[q];
+  }
+}
+
+// Workgroups of 256 of a copy: 16 KiB each, as many as fill the chip.
+int64_t copy_groups(const PadRows& c) {
+  const int64_t pieces = c.num_groups * c.rows * c.chunks, want = (pieces + 1023) / 1024;
+  return want < 8192 ? want : 8192;
+}
+
+__device__ __forceinline__ void copy_block(const FeedCopies& c, int64_t block, int64_t a_groups, int64_t w_groups) {
+  const bool w = block >= a_groups;
+  const int64_t step = (w ? w_groups : a_groups) * 256;
+  copy_rows(w ? c.w : c.a, (w ? block - a_groups : block) * 256 + threadIdx.x, step);
+}
+
+__global__ __launch_bounds__(256) void feed_copies_kernel(FeedCopies c, int32_t a_groups, int32_t w_groups) {
+  copy_block(c, blockIdx.x, a_groups, w_groups);
+}
+
+// What a thread loads of a row: eight columns of dy and of the parts kept.
+template <bool GATED>
+struct RawRow {
+  u32x4_t dy, p[GATED ? 2 : 1];
+  uint32_t code[GATED ? 2 : 1];
+};
+
+// ROWS rows x 64 columns of y per workgroup: 128, or 32 where that leaves CUs
+// idle.  The loop over a thread's rows is not unrolled: a small launch waits for
+// its instructions (111 x 2051 gated took 12.6 us unrolled), a large one has
+// enough other waves; the next row's loads are on their way meanwhile.
+template <int DT, bool GATED, int ROWS>
+__global__ __launch_bounds__(256) void feed_d_kernel(FeedDProblem p, FeedCopies copies, int32_t blocks, int32_t a_groups, int32_t w_groups) {
+  if ((int)blockIdx.x >= blocks) {
+    copy_block(copies, (int)blockIdx.x - blocks, a_groups, w_groups);
+    return;
+  }
   constexpr int PARTS = GATED ? 2 : 1, RB = kDCols * 2, CH = RB / 16;
-  __shared__ __attribute__((aligned(1024))) char smem[PARTS * kDRows * RB];
+  __shared__ __attribute__((aligned(1024))) char smem[PARTS * ROWS * RB];
   __shared__ float sums[4][PARTS][kDCols];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int ncb = (p.n + kDCols - 1) / kDCols;
   const int64_t rb = blockIdx.x / (unsigned)ncb;
   const int cb = (int)(blockIdx.x - rb * ncb);
-  const int64_t m0 = rb * kDRows;
+  const int64_t m0 = rb * ROWS;
   const int c = tid & 7, col = cb * kDCols + 8 * c, left = p.n - col;
+  const int kind = p.act.kind;
+  const bool need_p = kind != kActLinear || GATED, bytes = p.kept.scales != nullptr;
   const float c1 = p.act.c1, c3 = p.act.c3;
   float total[PARTS][8] = {};
-  with_kind(p.act.kind, [&](auto kind) {
-    constexpr int KIND = decltype(kind)::value;
+  const auto load = [&](int r, RawRow<GATED>& x) {
+    const int64_t row = m0 + r;
+    if (row >= p.m || left <= 0) return;
+    x.dy = load8(static_cast<const uint16_t*>(p.dy) + row * p.lddy + col, left);
+    if (!need_p) return;
 #pragma unroll
-    for (int pass = 0; pass < kDRows / 32; ++pass) {
-      const int r = pass * 32 + (tid >> 3);
-      const int64_t row = m0 + r;
-      float d[PARTS][8] = {};
-      if (row < p.m && left > 0) {
-        float dy[8];
-        unpack8<DT>(load8(static_cast<const uint16_t*>(p.dy) + row * p.lddy + col, left), dy);
-        float x[8], u[8];
-        if (KIND != kActLinear || GATED) kept8<DT>(p.kept, row * PARTS * p.kept.wide + col, x);
-        if constexpr (GATED) kept8<DT>(p.kept, (row * PARTS + 1) * p.kept.wide + col, u);
+    for (int h = 0; h < PARTS; ++h) {
+      const int64_t at = (row * PARTS + h) * p.kept.wide + col;
+      if (bytes) {
+        const u32x2_t q = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(p.kept.values) + at);
+        x.p[h][0] = q[0];
+        x.p[h][1] = q[1];
+        x.code[h] = p.kept.scales[at / kKeptBlock];
+      } else {
+        x.p[h] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p.kept.values) + at);
+      }
+    }
+  };
+  const auto values = [&](const RawRow<GATED>& x, int h, float (&v)[8]) {
+    if (bytes) {
+      const float s = scale_value(x.code[h]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float value, slope;
-          if (KIND == kActLinear && !GATED) {
-            d[0][e] = dy[e];
-          } else {
+      for (int w = 0; w < 2; ++w) {
+        const int q = (int)x.p[h][w];
+        v[4 * w + 0] = __builtin_amdgcn_cvt_f32_fp8(q, 0) * s;
+        v[4 * w + 1] = __builtin_amdgcn_cvt_f32_fp8(q, 1) * s;
+        v[4 * w + 2] = __builtin_amdgcn_cvt_f32_fp8(q, 2) * s;
+        v[4 * w + 3] = __builtin_amdgcn_cvt_f32_fp8(q, 3) * s;
+      }
+    } else {
+      unpack8<DT>(x.p[h], v);
+    }
+  };
+  RawRow<GATED> raw = {}, next = {};
+  load(tid >> 3, raw);
+#pragma unroll 1
+  for (int r = tid >> 3; r < ROWS; r += 32) {
+    if (r + 32 < ROWS) load(r + 32, next);
+    __builtin_amdgcn_sched_barrier(0);
+    const int64_t row = m0 + r;
+    float d[PARTS][8] = {};
+    if (row < p.m && left > 0) {
+      float dy[8], x[8], u[8];
+      unpack8<DT>(raw.dy, dy);
+      values(raw, 0, x);
+      if constexpr (GATED) values(raw, 1, u);
+      if (!need_p) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[0][e] = dy[e];
+      } else {
+        with_kind(kind, [&](auto tag) {
+          constexpr int KIND = decltype(tag)::value;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float value, slope;
             act_both<KIND>(x[e], c1, c3, value, slope);
             d[0][e] = dy[e] * (GATED ? u[e] * slope : slope);
             if constexpr (GATED) d[1][e] = dy[e] * value;
           }
-          if (e >= left)
-#pragma unroll
-            for (int h = 0; h < PARTS; ++h) d[h][e] = 0.0f;
-        }
+        });
       }
 #pragma unroll
-      for (int h = 0; h < PARTS; ++h) {
-        const u32x4_t w = pack8<DT>(d[h]);
+      for (int e = 0; e < 8; ++e)
+        if (e >= left)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) total[h][e] += d[h][e];
-        if (p.dt) *reinterpret_cast<u32x4_t*>(smem + (h * kDRows + r) * RB + ((c ^ (r & (CH - 1))) << 4)) = w;
-        if (p.d && row < p.m && left > 0) {
-          uint16_t* out = static_cast<uint16_t*>(p.d) + row * p.ldd + (int64_t)h * p.n;
-          store8(out + col, w, left);
-          if (h == PARTS - 1 && left <= 8)   // the row's end, up to a whole 16-byte piece
-            for (int64_t e = p.n; (h * (int64_t)p.n + e) % 8 != 0; ++e) out[e] = 0;
-        }
+          for (int h = 0; h < PARTS; ++h) d[h][e] = 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < PARTS; ++h) {
+      const u32x4_t w = pack8<DT>(d[h]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) total[h][e] += d[h][e];
+      if (p.dt) *reinterpret_cast<u32x4_t*>(smem + (h * ROWS + r) * RB + ((c ^ (r & (CH - 1))) << 4)) = w;
+      if (p.d && row < p.m && left > 0) {
+        uint16_t* out = static_cast<uint16_t*>(p.d) + row * p.ldd + (int64_t)h * p.n;
+        store8(out + col, w, left);
+        if (h == PARTS - 1 && left <= 8)       // the row's end, up to a whole 16-byte piece
+          for (int64_t e = p.n; (h * (int64_t)p.n + e) % 8 != 0; ++e) out[e] = 0;
       }
     }
-  });
+    raw = next;
+  }
   if (p.sums) {
     // over the rows of the wave (lanes 8 apart hold the same columns), then the waves
 #pragma unroll
@@ -131,16 +230,16 @@ __global__ __launch_bounds__(256) void feed_d_kernel(FeedDProblem p) {
     // lane of a group giving the address of row i16 / 4, columns 4 (i16 % 4) ..
     // + 3 of the 4 x 16 block), 16 bytes of the column's row.
     const int g4 = lane >> 4, i16 = lane & 15;
-    constexpr int UNITS = PARTS * (kDCols / 16) * (kDRows / 32);
-#pragma unroll
+    constexpr int UNITS = PARTS * (kDCols / 16) * (ROWS / 32);
+#pragma unroll 2
     for (int q = 0; q < UNITS / 4; ++q) {
       const int u = q * 4 + wave, h = u / (UNITS / PARTS), v = u % (UNITS / PARTS);
-      const int nb = (v / (kDRows / 32)) * 16, mb = (v % (kDRows / 32)) * 32 + 8 * g4;
+      const int nb = (v / (ROWS / 32)) * 16, mb = (v % (ROWS / 32)) * 32 + 8 * g4;
       u32x2_t half[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int r = mb + 4 * s + (i16 >> 2), x = nb + 4 * (i16 & 3);
-        half[s] = read_tr(smem + (h * kDRows + r) * RB + (((x >> 3) ^ (r & (CH - 1))) << 4) + (x & 4) * 2);
+        half[s] = read_tr(smem + (h * ROWS + r) * RB + (((x >> 3) ^ (r & (CH - 1))) << 4) + (x & 4) * 2);
       }
       const int x = cb * kDCols + nb + i16;
       if (x < p.n && m0 + mb < p.ldt)
@@ -238,16 +337,42 @@ constexpr int64_t kLoopGrid = 1 << 16;   // workgroups of the kernels that loop 
 
 }  // namespace
 
-hipError_t launch_feed_d(const FeedDProblem& p, int dtype, hipStream_t s) {
+static bool copies_valid(const FeedCopies& c) {
+  for (const PadRows* r : {&c.a, &c.w})
+    if (r->num_groups != 0 && (r->num_groups < 1 || r->num_groups > kMaxGroups || r->rows < 1 || r->rows > INT32_MAX || r->chunks < 1 ||
+                               r->chunks > INT32_MAX || r->cols < 1 || r->cols > r->chunks * 8 || r->cols > INT32_MAX || !r->out))
+      return false;
+  return true;
+}
+
+hipError_t launch_feed_copies(const FeedCopies& c, hipStream_t s) {
+  if (!copies_valid(c)) return hipErrorInvalidValue;
+  const int64_t a = copy_groups(c.a), w = copy_groups(c.w);
+  if (a + w < 1) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(feed_copies_kernel, dim3((unsigned)(a + w)), dim3(256), 0, s, c, (int32_t)a, (int32_t)w);
+  return hipGetLastError();
+}
+
+hipError_t launch_feed_d(const FeedDProblem& p, const FeedCopies& copies, int dtype, hipStream_t s) {
   const int parts = p.gated ? 2 : 1;
-  const int64_t grid = (p.m + kDRows - 1) / kDRows * ((p.n + kDCols - 1) / kDCols);
-  if (p.m < 1 || p.n < 1 || grid >= kFeedGrid || (!p.kept.values && (p.gated || p.act.kind != kActLinear)) ||
+  const int64_t blocks = (p.m + p.block - 1) / p.block * ((p.n + kDCols - 1) / kDCols);
+  const int64_t a = copy_groups(copies.a), w = copy_groups(copies.w);
+  if (p.m < 1 || p.n < 1 || (p.block != 32 && p.block != 128) || blocks >= kFeedGrid - 16384 || !copies_valid(copies) ||
+      (!p.kept.values && (p.gated || p.act.kind != kActLinear)) ||
       (p.kept.values && p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock) ||
-      (p.d && (p.ldd % 8 != 0 || p.ldd < (int64_t)parts * p.n)) || (p.dt && (p.ldt % 8 != 0 || p.ldt < p.m)) || (dtype != kDtypeBf16 && dtype != kDtypeFp16))
+      (p.d && (p.ldd % 8 != 0 || p.ldd < (int64_t)parts * p.n)) || (p.dt && (p.ldt % 8 != 0 || p.ldt < p.m)) ||
+      (dtype != kDtypeBf16 && dtype != kDtypeFp16))
     return hipErrorInvalidValue;
-  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, p); };
-  if (dtype == kDtypeBf16) p.gated ? go(feed_d_kernel<kDtypeBf16, true>) : go(feed_d_kernel<kDtypeBf16, false>);
-  else p.gated ? go(feed_d_kernel<kDtypeFp16, true>) : go(feed_d_kernel<kDtypeFp16, false>);
+  const auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks + a + w)), dim3(256), 0, s, p, copies, (int32_t)blocks, (int32_t)a, (int32_t)w);
+  };
+  const auto rows = [&](auto dt, auto gated) {
+    constexpr int DT = decltype(dt)::value;
+    constexpr bool G = decltype(gated)::value;
+    p.block == 128 ? go(feed_d_kernel<DT, G, 128>) : go(feed_d_kernel<DT, G, 32>);
+  };
+  if (dtype == kDtypeBf16) p.gated ? rows(IntTag<kDtypeBf16>{}, BoolTag<true>{}) : rows(IntTag<kDtypeBf16>{}, BoolTag<false>{});
+  else p.gated ? rows(IntTag<kDtypeFp16>{}, BoolTag<true>{}) : rows(IntTag<kDtypeFp16>{}, BoolTag<false>{});
   return hipGetLastError();
 }
 

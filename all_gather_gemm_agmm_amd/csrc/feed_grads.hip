@@ -2,10 +2,12 @@
 // two products (gfx950), on the 16-bit d that feed_d_kernel leaves:
 //
 //     dA = d W        (rows of d [m][parts * n], W k x n as stored)
-//     dW = d^T A      (d transposed [parts * n][m], A k x n as gathered)
+//     dW = d^T A      (d transposed [parts * n][m], A k x n: gathered, or, where the
+//                      shards' rows are whole k-tiles, in the shards)
+//     db = sums of the column sums that feed_d_kernel leaves
 //
-// Both are the part-ring GEMM (gemm_m16_loop.inc) with B stored k x n and
-// share a launch: with few rows neither fills the CUs alone.  Where few output
+// The products are the part-ring GEMM (gemm_m16_loop.inc) with B stored k x n
+// and share a launch: with few rows neither fills the CUs alone.  Where few output
 // tiles would leave CUs idle, a product's sum is cut into ranges, whose fp32
 // sums a last pass adds in order and rounds; otherwise the tile is rounded and
 // stored here, whole rows through LDS.  Bound: MFMA.
@@ -15,14 +17,32 @@ namespace agmm {
 
 namespace {
 
-struct FeedPair {
-  GemmProblem a, w;        // dA and dW
-  int32_t a_tiles;         // workgroups of dA: the first ones
-};
+// out[c] = sum over groups, in a fixed order, of sums[group][c], rounded.
+template <int DT>
+__device__ __forceinline__ void bias_sums(const FeedBias& b, int64_t block, float (&part)[4][64]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = block * 64 + lane;
+  float t = 0.0f;
+  if (col < b.cols) {
+    int64_t g = wave;
+    for (; g + 28 < b.groups; g += 32) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = b.sums[(g + 4 * q) * b.cols + col];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) t += v[q];
+    }
+    for (; g < b.groups; g += 4) t += b.sums[g * b.cols + col];
+  }
+  part[wave][lane] = t;
+  __syncthreads();
+  if (wave == 0 && col < b.cols)
+    static_cast<uint16_t*>(b.out)[col] = cvt1<DT>((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]));
+}
 
 template <int BM, int BN, int DT, int OCC>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
-void feed_grads_kernel(FeedPair gp) {
+void feed_grads_kernel(FeedGrads gp) {
   constexpr bool BT = false, SPLIT = true;
   constexpr int BK = 64, WAVES = 4;
   using T = GemmTile<BM, BN, BK, DT, BT, 5, WAVES, kLoopParts>;
@@ -30,10 +50,16 @@ void feed_grads_kernel(FeedPair gp) {
   constexpr int FM = T::TM / 16, FN = T::TN / 16;
   constexpr int STEPS = BK / 32;
   __shared__ __attribute__((aligned(1024))) char smem[T::LDS_BYTES];
+  if ((int)blockIdx.x >= gp.tiles) {
+    bias_sums<DT>(gp.bias, (int)blockIdx.x - gp.tiles, *reinterpret_cast<float(*)[4][64]>(smem));
+    return;
+  }
   const bool is_a = (int)blockIdx.x < gp.a_tiles;
   const GemmProblem& p = is_a ? gp.a : gp.w;
 
 #define AGMM_CLAMP
+#define AGMM_B_GROUPS gp.w_group
+#define AGMM_B_GROUP_ROWS (is_a ? 0 : gp.w_rows)
 #define AGMM_TILE_ID (is_a ? (int)blockIdx.x : (int)blockIdx.x - gp.a_tiles)
 #include "gemm_m16_loop.inc"
 
@@ -89,19 +115,16 @@ bool fits(const GemmProblem& p, int tile) {
 
 }  // namespace
 
-hipError_t launch_feed_grads(const GemmProblem* a, const GemmProblem* w, int tile, int dtype, hipStream_t s) {
-  if ((!a && !w) || (a && !fits(*a, tile)) || (w && !fits(*w, tile))) return hipErrorInvalidValue;
-  FeedPair gp{};
-  int64_t grid = 0;
-  if (a) {
-    gp.a = *a;
-    grid += (int64_t)a->order.num_rb * a->order.num_cb * a->splits;
-  }
+hipError_t launch_feed_grads(FeedGrads gp, int tile, int dtype, hipStream_t s) {
+  const bool a = gp.a.m > 0, w = gp.w.m > 0, bias = gp.bias.out != nullptr;
+  if ((!a && !w && !bias) || (a && !fits(gp.a, tile)) || (w && !fits(gp.w, tile)) ||
+      (w && gp.w_rows && (gp.w_rows % 64 != 0 || gp.w.k % gp.w_rows != 0 || gp.w.k / gp.w_rows > kMaxGroups)))
+    return hipErrorInvalidValue;
+  int64_t grid = a ? (int64_t)gp.a.order.num_rb * gp.a.order.num_cb * gp.a.splits : 0;
   gp.a_tiles = (int32_t)grid;
-  if (w) {
-    gp.w = *w;
-    grid += (int64_t)w->order.num_rb * w->order.num_cb * w->splits;
-  }
+  if (w) grid += (int64_t)gp.w.order.num_rb * gp.w.order.num_cb * gp.w.splits;
+  gp.tiles = (int32_t)grid;
+  if (bias) grid += (gp.bias.cols + 63) / 64;
   if (grid >= kFeedGrid) return hipErrorInvalidValue;
   const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, gp); };
   if (dtype == kDtypeBf16) tile == 256 ? go(feed_grads_kernel<256, 256, kDtypeBf16, 1>) : go(feed_grads_kernel<128, 128, kDtypeBf16, 2>);

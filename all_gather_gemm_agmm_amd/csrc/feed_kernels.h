@@ -3,7 +3,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "agmm_kernels.h"
+#include "ops_kernels.h"
 
 namespace agmm {
 
@@ -59,14 +59,22 @@ hipError_t launch_feed_tiles(const FeedProblem& p, int tile, int dtype, hipStrea
 // order.num_cb counts blocks of yc columns.
 hipError_t launch_feed_few(const FeedProblem& p, int fm, int yc, int dtype, hipStream_t stream);
 
+// Copies of A and of W as rows of whole 128-byte lines (PadRows, ops_kernels.h;
+// num_groups 0: none).
+struct FeedCopies {
+  PadRows a, w;
+};
+hipError_t launch_feed_copies(const FeedCopies& c, hipStream_t stream);
+
 // The elementwise part of the way back: d = dy * (derivative of y by p), by
 // rows [m][ldd] (zeros past parts * n up to a multiple of 8) and transposed
 // [parts * n][ldt] (the same past m), each where asked for, and the sums of d
-// over blocks of kDRows rows.
-constexpr int kDRows = 128, kDCols = 64;
+// over blocks of `block` rows, 32 or 128.
+constexpr int kDCols = 64;
 struct FeedDProblem {
   int64_t m;
   int32_t n, gated;
+  int32_t block;
   Activation act;
   KeptRows kept;           // values may be null for a linear product without a gate
   const void* dy;
@@ -77,7 +85,8 @@ struct FeedDProblem {
   int64_t ldt;
   float* sums;             // [blocks of rows][parts * n] or null
 };
-hipError_t launch_feed_d(const FeedDProblem& p, int dtype, hipStream_t stream);
+// ... and, in the same launch, copies of A and W.
+hipError_t launch_feed_d(const FeedDProblem& p, const FeedCopies& c, int dtype, hipStream_t stream);
 
 // y = act(p) [* p of the second part] from the kept pre-activations.
 struct FeedAgainProblem {
@@ -90,10 +99,25 @@ struct FeedAgainProblem {
 };
 hipError_t launch_feed_again(const FeedAgainProblem& p, int dtype, hipStream_t stream);
 
-// The products dA = d W and dW = dt A, B k x n, in one launch: with splits > 1
-// fp32 sums per k range into partials [splits][m][n rounded up to 4], else the
-// result itself, rounded.  Either may be null.
-hipError_t launch_feed_grads(const GemmProblem* a, const GemmProblem* w, int tile, int dtype, hipStream_t stream);
+// The products dA = d W and dW = dt A, B k x n, in one launch (m 0: none): with
+// splits > 1 fp32 sums per k range into partials [splits][m][n rounded up to 4],
+// else the result itself, rounded; and the bias's gradient (out null: none) from
+// the sums over blocks of rows.
+struct FeedBias {
+  const float* sums;       // [groups][cols]
+  int64_t groups, cols;
+  void* out;
+};
+struct FeedGrads {
+  GemmProblem a, w;
+  // dW's B, A's rows: in one piece at w.b (w_rows 0), or w_rows rows, a multiple
+  // of 64, at each of w_group
+  const void* w_group[kMaxGroups];
+  int32_t w_rows;
+  int32_t a_tiles, tiles;  // set by launch_feed_grads: workgroups of dA, of both
+  FeedBias bias;
+};
+hipError_t launch_feed_grads(FeedGrads g, int tile, int dtype, hipStream_t stream);
 
 // out[row][col] = sum over ranges, in order, of sums[range][row][cols rounded
 // up to 4], rounded to `dtype` (a 16-bit type).
