@@ -97,14 +97,15 @@ struct agmm_ff_plan : PlanBase {
 
   // Microseconds of the products' tiles, measured on MI355X: of a launch of
   // `tiles` of them, each over `sum` elements of k.  A 256 x 256 tile has a CU to
-  // itself, 10 and 1.4 per 64 of its sum, 1.1 where half the CUs have none; a
-  // 128 x 128 one shares it, 5 and 0.92, or 0.48 alone.  `lines`: the operands'
+  // itself, 10 and 1.4 per 64 of its sum, 1.1 where half the CUs have none, and
+  // 256 x 224 seven eighths of that; a 128 x 128 one shares it, 5 and 0.92, or 0.48 alone.  `lines`: the operands'
   // rows start on 128-byte lines; where they do not, a tile's loads take twice
   // the lines, which slows the smaller tile (1011 x 4040 -> 2 x 2051: 74 us, 40
   // at 4096).
   double tiles_us(int t, int64_t tiles, int64_t sum, bool lines) const {
     const double steps = (double)cdiv(sum, 64);
-    if (t == 256) return (double)cdiv(tiles, cu_count) * (10.0 + (2 * tiles <= cu_count ? 1.1 : 1.4) * steps * (lines ? 1.0 : 1.05));
+    if (t >= 224)
+      return (double)cdiv(tiles, cu_count) * (10.0 + t / 256.0 * (2 * tiles <= cu_count ? 1.1 : 1.4) * steps * (lines ? 1.0 : 1.05));
     const double by = steps * (lines ? 1.0 : 1.8);
     const int64_t rest = tiles % (2 * cu_count);
     const double shared = std::max(0.0, (double)rest / cu_count - 1.0);   // CUs with two in the last round
@@ -146,7 +147,7 @@ struct agmm_ff_plan : PlanBase {
     for (bool copied : {false, true}) {
       if (!copied && must_copy) continue;
       if (copied && !must_copy && lines) continue;
-      offer(256, copied, 1, tiles_us(256, cdiv(m, 256) * cdiv(nc, 256), k, lines || copied));
+      for (int t : {256, 224}) offer(t, copied, 1, tiles_us(t, cdiv(m, 256) * cdiv(nc, t), k, lines || copied));
       const int64_t tiles = cdiv(m, 128) * cdiv(nc, 128);
       for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
         if (s > 1 && (k < 256 * s || tiles * s > 4 * cu_count)) break;
@@ -203,7 +204,7 @@ struct agmm_ff_plan : PlanBase {
       double best = -1;
       int64_t want_a = 1, want_w = 1;
       for (int t : {256, 128}) {
-        if (tile_key > 64 && t != tile_key) continue;
+        if (tile_key > 64 && t != (tile_key == 224 ? 256 : tile_key)) continue;
         const int64_t a_tiles = cdiv(m, t) * cdiv(k, t), w_tiles = cdiv(cols(), t) * cdiv(k, t);
         const double slots = cu_count * (t == 128 ? 2 : 1);
         const auto one = [&](int64_t sum) { return t == 256 ? 10.0 + 1.4 * (double)cdiv(sum, 64) : 5.0 + 0.92 * (double)cdiv(sum, 64); };
@@ -238,10 +239,10 @@ struct agmm_ff_plan : PlanBase {
     return AGMM_OK;
   }
 
-  agmm::TileOrder tiles_of(int64_t rows, int64_t columns, int tile) const {
+  agmm::TileOrder tiles_of(int64_t rows, int64_t columns, int tile_rows, int tile_columns) const {
     agmm::TileOrder o{};
-    o.num_rb = (int32_t)cdiv(rows, tile);
-    o.num_cb = (int32_t)cdiv(columns, tile);
+    o.num_rb = (int32_t)cdiv(rows, tile_rows);
+    o.num_cb = (int32_t)cdiv(columns, tile_columns);
     o.group_m = group_rows(o.num_rb, o.num_cb);
     o.xcd_remap = 1;
     return o;
@@ -296,13 +297,15 @@ struct agmm_ff_plan : PlanBase {
       p.gemm.rows.num_groups = N;
       p.gemm.rows.c_group_rows = m_s;
     }
+    // 8-bit pre-activations of a gated product come in no tile of 224
+    const int tile = L.tile == 224 && parts == 2 && saved_scales ? 256 : L.tile;
     // kept rows are written in blocks of 32 columns of a part
     const int yc = saved ? most_yc() : L.yc;
     if (L.tile == 64) {
       p.gemm.order.num_rb = (int32_t)cdiv(m, 16 * L.fm);
       p.gemm.order.num_cb = (int32_t)cdiv(n, yc);
     } else {
-      p.gemm.order = tiles_of(m, tile_cols(), L.tile);
+      p.gemm.order = tiles_of(m, tile_cols(), tile == 224 ? 256 : tile, tile);
     }
     p.gemm.m = (int32_t)m;
     p.gemm.n = (int32_t)tile_cols();
@@ -321,7 +324,7 @@ struct agmm_ff_plan : PlanBase {
     p.y = Y;
     p.ldy = ldy ? ldy : n;
     p.kept = kept_rows(saved, saved_scales);
-    const hipError_t err = L.tile == 64 ? agmm::launch_feed_few(p, L.fm, yc, dtype, s) : agmm::launch_feed_tiles(p, L.tile, dtype, s);
+    const hipError_t err = L.tile == 64 ? agmm::launch_feed_few(p, L.fm, yc, dtype, s) : agmm::launch_feed_tiles(p, tile, dtype, s);
     return err == hipSuccess ? AGMM_OK : hip_err(err, "feed-forward launch");
   }
 
@@ -347,7 +350,7 @@ struct agmm_ff_plan : PlanBase {
     agmm::FeedGrads g{};
     agmm::GemmProblem &ga = g.a, &gw = g.w;
     ga.rows = dense(L.d, m, e.ldd);
-    ga.order = tiles_of(m, k, L.tile_grads);
+    ga.order = tiles_of(m, k, L.tile_grads, L.tile_grads);
     ga.m = (int32_t)m;
     ga.n = (int32_t)k;
     ga.k = (int32_t)cols();
@@ -359,7 +362,7 @@ struct agmm_ff_plan : PlanBase {
     ga.c = dA;
     ga.ldc = ldda ? ldda : k;
     gw.rows = dense(L.dt, cols(), ld_dt());
-    gw.order = tiles_of(cols(), k, L.tile_grads);
+    gw.order = tiles_of(cols(), k, L.tile_grads, L.tile_grads);
     gw.m = (int32_t)cols();
     gw.n = (int32_t)k;
     gw.k = (int32_t)m;
@@ -486,7 +489,7 @@ int agmm_ff_plan_set_int(agmm_ff_plan_t p, const char* key, int64_t v) {
     if (v != 0 && (v < p->n || v >= kDimLimit)) return bad();
     field = k == "ldr" ? &p->ldr : k == "ldy" ? &p->ldy : &p->lddy;
   } else if (k == "tile") {
-    if (v != -1 && v != 64 && v != 128 && v != 256) return bad();
+    if (v != -1 && v != 64 && v != 128 && v != 224 && v != 256) return bad();
     if (v == 64 && !p->few_fits()) return set_err(AGMM_ERR_UNSUPPORTED, "too many workgroups for tile 64");
     field = &p->tile_key;
   } else {

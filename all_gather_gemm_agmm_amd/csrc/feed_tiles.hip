@@ -2,8 +2,8 @@
 //
 //     p = A B^T + bias,  y = act(p) + residual      or, gated,  y = act(p_0) * p_1
 //
-// A tile is one of the part-ring GEMM (gemm_m16_loop.inc), 256 x 256 or 128 x
-// 128 tile columns.  Gated, the tile's columns are blocks of 16 rows of the
+// A tile is one of the part-ring GEMM (gemm_m16_loop.inc), 256 x 256, 256 x 224
+// or 128 x 128 tile columns.  Gated, the tile's columns are blocks of 16 rows of the
 // first n rows of B and 16 of the second n in turn, so that both parts of a
 // column of y are in the tile: one launch instead of two products and an
 // elementwise kernel that reads and writes both.
@@ -50,11 +50,12 @@ void feed_tile_kernel(FeedProblem fp) {
 #include "gemm_m16_loop.inc"
 
   constexpr int PARTS = GATED ? 2 : 1;
-  constexpr int ROW = BN * 4;                  // bytes of a row of sums; 16-byte piece c of row r at c ^ (r % 16)
+  constexpr int ROW = BN == 224 ? 1024 : BN * 4;   // bytes of a row of sums; 16-byte piece c of row r at c ^ (r % 16)
   constexpr int HALVES = BM * ROW > T::LDS_BYTES ? 2 : 1, HR = BM / HALVES;
   static_assert(HALVES == 1 || HR == T::TM, "a half is the rows of one wave row");
   constexpr int PIECES = BN / PARTS / 8;       // of eight columns of y, a thread each
-  constexpr int STEP = T::THREADS / PIECES;    // rows at a time
+  constexpr int STEP = T::THREADS / PIECES;    // rows at a time; 224: four threads are left over
+  constexpr bool EVEN = STEP * PIECES == T::THREADS && HR % STEP == 0;
   const int c = tid % PIECES;
   const int col = n0 / PARTS + 8 * c;
   // 16-byte pieces of the thread's columns: pieces at, at + 1 of the first part
@@ -78,9 +79,7 @@ void feed_tile_kernel(FeedProblem fp) {
     __syncthreads();
     with_kind(fp.act.kind, [&](auto kind) {
       constexpr int KIND = decltype(kind)::value;
-#pragma unroll 2
-      for (int it = 0; it < HR / STEP; ++it) {
-        const int r = it * STEP + tid / PIECES;
+      const auto one = [&](int r) {
         const int64_t row = m0 + half * HR + r;
         float v[PARTS][8];
 #pragma unroll
@@ -92,6 +91,13 @@ void feed_tile_kernel(FeedProblem fp) {
             for (int e = 0; e < 4; ++e) v[h][4 * s + e] = x[e] + bias[h][4 * s + e];
           }
         finish8<DT, GATED, KIND>(fp, v, row, row < M, col);
+      };
+      if constexpr (EVEN) {
+#pragma unroll 2
+        for (int it = 0; it < HR / STEP; ++it) one(it * STEP + tid / PIECES);
+      } else if (tid < STEP * PIECES) {
+#pragma unroll 1
+        for (int r = tid / PIECES; r < HR; r += STEP) one(r);
       }
     });
   }
@@ -176,6 +182,8 @@ hipError_t launch_type(const FeedProblem& p, int tile, hipStream_t s) {
     const int64_t pieces = ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * (kKeptBlock / 8);
     const unsigned joins = (unsigned)((p.gemm.m * pieces + 255) / 256);
     p.gated ? go(feed_join_kernel<DT, true>, joins) : go(feed_join_kernel<DT, false>, joins);
+  } else if (tile == 224) {
+    p.gated ? go(feed_tile_kernel<256, 224, DT, 1, true>, grid) : go(feed_tile_kernel<256, 224, DT, 1, false>, grid);
   } else if (tile == 256) {
     p.gated ? go(feed_tile_kernel<256, 256, DT, 1, true>, grid) : go(feed_tile_kernel<256, 256, DT, 1, false>, grid);
   } else {
@@ -188,14 +196,15 @@ hipError_t launch_type(const FeedProblem& p, int tile, hipStream_t s) {
 
 hipError_t launch_feed_tiles(const FeedProblem& p, int tile, int dtype, hipStream_t s) {
   const int64_t cols = p.gated ? 2 * (((int64_t)p.n + 15) / 16 * 16) : p.n;
-  if ((tile != 256 && tile != 128) || p.gemm.n != cols || p.gemm.order.num_rb != (p.gemm.m + tile - 1) / tile ||
+  const int bm = tile == 224 ? 256 : tile;
+  if ((tile != 256 && tile != 224 && tile != 128) || p.gemm.n != cols || p.gemm.order.num_rb != (p.gemm.m + bm - 1) / bm ||
       p.gemm.order.num_cb != (p.gemm.n + tile - 1) / tile ||
       p.gemm.splits < 1 || (int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb * p.gemm.splits >= kFeedGrid || p.gemm.k % 8 != 0 ||
       (p.gemm.splits > 1 && (tile != 128 || !p.gemm.partials || p.gemm.k_per_split % 64 != 0 ||
                              (int64_t)p.gemm.splits * p.gemm.k_per_split < p.gemm.k ||
                              (int64_t)(p.gemm.splits - 1) * p.gemm.k_per_split >= p.gemm.k ||
                              p.gemm.m * (((int64_t)p.n + 31) / 32 * 4) >= kFeedGrid * 256)) ||
-      (p.gated && p.residual) || (p.kept.values && p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock))
+      (p.gated && p.residual) || (tile == 224 && p.gated && p.kept.scales) || (p.kept.values && p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock))
     return hipErrorInvalidValue;
   return dtype == kDtypeBf16 ? launch_type<kDtypeBf16>(p, tile, s)
        : dtype == kDtypeFp16 ? launch_type<kDtypeFp16>(p, tile, s) : hipErrorInvalidValue;

@@ -48,10 +48,11 @@ def kept_matches(saved, p, e, n, parts, dtype):
 
 SHAPES = [  # N, m_per_shard, k, n
     (1, 1, 1, 1), (1, 1, 64, 16), (2, 3, 100, 33), (8, 1, 512, 96), (1, 16, 130, 48), (3, 7, 71, 65), (2, 40, 256, 160),
-    (5, 13, 257, 31), (1, 64, 1024, 256), (3, 100, 192, 200), (2, 129, 320, 130), (1, 257, 72, 257), (4, 128, 256, 384)]
+    (5, 13, 257, 31), (1, 64, 1024, 256), (3, 100, 192, 200), (2, 129, 320, 130), (1, 257, 72, 257), (4, 128, 256, 384),
+    (3, 64, 128, 224), (1, 300, 4040, 240), (7, 20, 1100, 500)]
 
 
-@pytest.mark.parametrize("tile", [-1, 64, 128, 256])
+@pytest.mark.parametrize("tile", [-1, 64, 128, 224, 256])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
 @pytest.mark.parametrize("gated", [False, True])
 def test_forward(shape, gated, tile):
@@ -340,7 +341,7 @@ def test_tiles_agree_at_scale():
         shards, w, b, _ = make(N, ms, k, n, BF16, parts)
         dy = (torch.randn((N * ms, n), device="cuda") / 8).bfloat16()
         want = None
-        for tile in (128, 256):
+        for tile in (128, 224, 256):
             with agmm.FeedForwardPlan(N, ms, k, n, BF16, activation="gelu_tanh", gated=gated, tile=tile) as plan:
                 y, saved = plan.forward(shards, w, b, keep=8)
                 grads = plan.backward(shards, w, saved, dy, need_dbias=True)
