@@ -867,16 +867,25 @@ class FeedForwardPlan(_OpPlan):
         self._ldw = self._like((parts * n, k), t, self.get("lddw"))
         # kept pre-activations, seen as matrices of their rows
         self._kept_shape, self._scales_shape = torch.Size((m, parts, wide)), torch.Size((m, parts, wide // KEPT_BLOCK))
+        # a tensor like another is made faster than from its description: for y of
+        # up to 1 MiB, where that counts, the plan keeps one
+        small = m * n <= 1 << 19 and self._ly[3] == (n, 1)
+        self._proto, self._same = self._new(self._ly) if small else None, torch.empty_like
         self._kept_types = {16: t, 8: torch.float8_e4m3fn}
         self._scale_types = {t: None, torch.float8_e4m3fn: torch.float8_e8m0fnu}
 
     def _shards(self, shards):
         if len(shards) != self.num_shards:
             raise ValueError(f"expected {self.num_shards} shards, got {len(shards)}")
-        la, on, pa = self._la, self._on, self._table()
-        for r, s in enumerate(shards):
-            # the common case in one comparison
-            pa[r] = s.data_ptr() if (s.dtype, s.device, s.shape, s.stride()) == la else on(s, la, "shards")
+        la, on, pa, device, r = self._la, self._on, self._table(), self.device, 0
+        dtype, _, shape, stride = la
+        for s in shards:
+            try:   # the common case
+                same = s.dtype is dtype and s.shape == shape and s.stride() == stride and s.get_device() == device
+            except AttributeError:
+                same = False
+            pa[r] = s.data_ptr() if same else on(s, la, "shards")
+            r += 1
         return pa
 
     def _kept(self, saved):
@@ -917,7 +926,7 @@ class FeedForwardPlan(_OpPlan):
         saved = v = s = None
         with _device_and_stream(self.device, stream):
             if out is None:
-                out = self._new(self._ly)
+                out = self._new(self._ly) if self._proto is None else self._same(self._proto)
                 y = out.data_ptr()
             if keep:
                 empty, device, t = self._empty, self._la[1], self._kept_types[keep]
@@ -989,6 +998,8 @@ class NormPlan(_OpPlan):
         self._ldy, self._ldx = self._like(shape, t, self.get("lddy")), self._like(shape, t, self.get("lddx"))
         self._lw = self._like((self.cols,), _torch_dtype(self.weight_dtype))
         self._ls = self._like((self.rows,), torch.float32)
+        # a tensor like another is made faster than from its description
+        self._stats, self._same = torch.empty(self.rows, dtype=torch.float32, device=self._ls[1]), torch.empty_like
 
     @property
     def m(self) -> int:
@@ -996,16 +1007,16 @@ class NormPlan(_OpPlan):
 
     def forward(self, x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
         """(y, mean, rstd): y [rows, cols] and the rows' fp32 statistics."""
-        on, new = self._on, self._new
+        on, same = self._on, self._same
         px = on(x, self._lx, "x")
         w = None if weight is None else on(weight, self._lw, "weight")
         b = None if bias is None else on(bias, self._lw, "bias")
         y = None if out is None else on(out, self._ly, "out")
         with _device_and_stream(self.device, stream):
             if out is None:
-                out = new(self._ly)
+                out = same(x) if x.stride() == self._ly[3] else self._new(self._ly)
                 y = out.data_ptr()
-            mean, rstd = new(self._ls), new(self._ls)
+            mean, rstd = same(self._stats), same(self._stats)
             _check(self._fwd(self.handle, px, w, b, eps, y, mean.data_ptr(), rstd.data_ptr(), _stream_handle(stream, self.device)))
         return out, mean, rstd
 
@@ -1021,7 +1032,7 @@ class NormPlan(_OpPlan):
         d = None if dx is None else on(dx, self._ldx, "dx")
         with _device_and_stream(self.device, stream):
             if dx is None and need_dx:
-                dx = new(self._ldx)
+                dx = self._same(x) if x.stride() == self._ldx[3] else new(self._ldx)
                 d = dx.data_ptr()
             dw = new(self._lw) if need_dweight else None
             db = new(self._lw) if need_dbias else None
