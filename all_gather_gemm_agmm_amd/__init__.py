@@ -998,8 +998,9 @@ class NormPlan(_OpPlan):
         self._ldy, self._ldx = self._like(shape, t, self.get("lddy")), self._like(shape, t, self.get("lddx"))
         self._lw = self._like((self.cols,), _torch_dtype(self.weight_dtype))
         self._ls = self._like((self.rows,), torch.float32)
-        # a tensor like another is made faster than from its description
-        self._stats, self._same = torch.empty(self.rows, dtype=torch.float32, device=self._ls[1]), torch.empty_like
+        # a tensor like another is made faster than from its description: for
+        # statistics of up to 1 MiB, where that counts, the plan keeps one
+        self._stats, self._same = self._new(self._ls) if self.rows <= 1 << 18 else None, torch.empty_like
 
     @property
     def m(self) -> int:
@@ -1016,7 +1017,10 @@ class NormPlan(_OpPlan):
             if out is None:
                 out = same(x) if x.stride() == self._ly[3] else self._new(self._ly)
                 y = out.data_ptr()
-            mean, rstd = same(self._stats), same(self._stats)
+            if self._stats is None:
+                mean, rstd = self._new(self._ls), self._new(self._ls)
+            else:
+                mean, rstd = same(self._stats), same(self._stats)
             _check(self._fwd(self.handle, px, w, b, eps, y, mean.data_ptr(), rstd.data_ptr(), _stream_handle(stream, self.device)))
         return out, mean, rstd
 
