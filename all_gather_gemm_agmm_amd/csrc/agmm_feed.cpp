@@ -51,7 +51,7 @@ agmm::Activation activation_of(int act) {
     case AGMM_ACT_RELU: return {agmm::kActRelu, 0.0f, 0.0f};
     case AGMM_ACT_GELU: return {agmm::kActNormal, 0.0f, 0.0f};
     case AGMM_ACT_GELU_TANH: return {agmm::kActLogistic, c, c * 0.044715f};   // x (1 + tanh u) / 2 = x / (1 + exp(-2 u))
-    case AGMM_ACT_SILU: return {agmm::kActLogistic, 1.0f, 0.0f};
+    case AGMM_ACT_SILU: return {agmm::kActSilu, 0.0f, 0.0f};
     default: return {agmm::kActLinear, 0.0f, 0.0f};
   }
 }

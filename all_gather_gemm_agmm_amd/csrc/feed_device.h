@@ -22,37 +22,37 @@ __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f
 
 // The normal distribution function.  With z = |x| / sqrt 2 the smaller tail is
 // erfc(z) / 2 = exp(-z^2) erfcx(z) / 2; erfcx, which is smooth and between 1
-// and 1 / (z sqrt pi), is fitted as t * polynomial(t), t = 1 / (1 + 0.3 z)
-// (least relative error over 0 <= z <= 10: 2.0e-8; in fp32 5e-7).  So both
-// tails keep their relative precision, which 1 + erf does not.  Beyond |x| =
-// 13.2 exp(-z^2) is 0.
+// and 1 / (z sqrt pi), is fitted as t * polynomial(t), t = 1 / (1 + 0.38 z)
+// (least relative error over 0 <= z <= 10: 1.0e-6, in fp32 1.3e-6; the results
+// are rounded to 16 bits, 2^-11 at best).  So both tails keep their relative
+// precision, which 1 + erf does not.  Beyond |x| = 13.2 exp(-z^2) is 0.
 __device__ __forceinline__ float normal_share(float x) {
-  const float z = fminf(__builtin_fabsf(x), 32.0f);
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(z, 0.21213203435596426f, 1.0f));
-  float q = -0.1295236349105835f;
-  q = __builtin_fmaf(q, t, 0.4855668544769287f);
-  q = __builtin_fmaf(q, t, -0.5122858285903931f);
-  q = __builtin_fmaf(q, t, 0.5477291941642761f);
-  q = __builtin_fmaf(q, t, -0.09465726464986801f);
-  q = __builtin_fmaf(q, t, 0.21492893993854523f);
-  q = __builtin_fmaf(q, t, 0.1483384072780609f);
-  q = __builtin_fmaf(q, t, 0.17071533203125f);
-  q = __builtin_fmaf(q, t, 0.169187992811203f);
-  q = 0.5f * q * t * exp_of(-0.5f * z * z);
+  const float z = __builtin_fabsf(x);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(z, 0.26870057685088806f, 1.0f));
+  float q = -0.5f * 0.12520186603069305f;
+  q = __builtin_fmaf(q, t, 0.5f * 0.33520618081092834f);
+  q = __builtin_fmaf(q, t, 0.5f * -0.0686253011226654f);
+  q = __builtin_fmaf(q, t, 0.5f * 0.2468075305223465f);
+  q = __builtin_fmaf(q, t, 0.5f * 0.1810360699892044f);
+  q = __builtin_fmaf(q, t, 0.5f * 0.21648065745830536f);
+  q = __builtin_fmaf(q, t, 0.5f * 0.21429570019245148f);
+  q = q * t * __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
   return x >= 0.0f ? 1.0f - q : q;
 }
 
-// x is cut in the cubic term, where c3 may be 0 and x infinite.
+// x is cut in the cubic term, where it may be infinite.
 __device__ __forceinline__ float logistic_share(float x, float c1, float c3) {
   const float q = fminf(__builtin_fabsf(x), 1e9f);
-  return __builtin_amdgcn_rcpf(1.0f + exp_of(-x * __builtin_fmaf(c3 * q, q, c1)));
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x * __builtin_fmaf(c3 * kLog2e * q, q, c1 * kLog2e)));
 }
+__device__ __forceinline__ float silu_share(float x) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e)); }
 
 // act(x).  A NaN stays one in every kind; the limits at -infinity are those of
 // the arithmetic (x times a share of 0: NaN), as for the formula in IEEE numbers.
 template <int KIND>
 __device__ __forceinline__ float act_value(float x, float c1, float c3) {
-  if constexpr (KIND == kActLogistic) return x * logistic_share(x, c1, c3);
+  if constexpr (KIND == kActSilu) return x * silu_share(x);
+  else if constexpr (KIND == kActLogistic) return x * logistic_share(x, c1, c3);
   else if constexpr (KIND == kActNormal) return x * normal_share(x);
   else if constexpr (KIND == kActRelu) return x < 0.0f ? 0.0f : x;
   else return x;
@@ -63,7 +63,11 @@ __device__ __forceinline__ float act_value(float x, float c1, float c3) {
 template <int KIND>
 __device__ __forceinline__ void act_both(float x, float c1, float c3, float& value, float& slope) {
   const float near = fminf(fmaxf(x, -128.0f), 128.0f);
-  if constexpr (KIND == kActLogistic) {
+  if constexpr (KIND == kActSilu) {
+    const float s = silu_share(x);
+    value = x * s;
+    slope = __builtin_fmaf(near * s, 1.0f - s, s);
+  } else if constexpr (KIND == kActLogistic) {
     const float s = logistic_share(x, c1, c3);
     value = x * s;
     slope = __builtin_fmaf(near * s, (1.0f - s) * __builtin_fmaf(3.0f * c3 * near, near, c1), s);
@@ -168,7 +172,8 @@ __device__ __forceinline__ f32x4_t load4(const uint16_t* x, int left) {
 // Calls f with the activation's kind as a constant.
 template <class F>
 __device__ __forceinline__ void with_kind(int kind, F&& f) {
-  if (kind == kActLogistic) f(IntTag<kActLogistic>{});
+  if (kind == kActSilu) f(IntTag<kActSilu>{});
+  else if (kind == kActLogistic) f(IntTag<kActLogistic>{});
   else if (kind == kActNormal) f(IntTag<kActNormal>{});
   else if (kind == kActRelu) f(IntTag<kActRelu>{});
   else f(IntTag<kActLinear>{});
@@ -187,16 +192,26 @@ __device__ __forceinline__ void finish8(const FeedProblem& fp, const float (&v)[
     for (int h = 0; h < PARTS; ++h) {
       float w[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = e < left ? v[h][e] : 0.0f;
+      for (int e = 0; e < 8; ++e) w[e] = v[h][e];
+      if (left < 8)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e >= left) w[e] = 0.0f;
       const int64_t out = (row * PARTS + h) * wide + col;
       if (!fp.kept.scales) {
         if (in)
           *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(fp.kept.values) + out) =
               u32x4_t{pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3]), pack2<DT>(w[4], w[5]), pack2<DT>(w[6], w[7])};
       } else {
+        // the maximum passes over NaN; an infinite one is taken anew
         float size = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) size = larger_finite(size, w[e]);
+        for (int e = 0; e < 8; ++e) size = fmaxf(size, __builtin_fabsf(w[e]));
+        if (size == __builtin_inff()) {
+          size = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) size = larger_finite(size, w[e]);
+        }
         size = fmaxf(size, __shfl_xor(size, 1));
         size = fmaxf(size, __shfl_xor(size, 2));
         const uint32_t code = scale_code(size);

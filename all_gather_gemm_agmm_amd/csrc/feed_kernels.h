@@ -11,8 +11,9 @@ namespace agmm {
 enum ActKind : int {
   kActLinear = 0,      // 1
   kActRelu = 1,        // 1 for x > 0, else 0
-  kActLogistic = 2,    // 1 / (1 + exp(-x (c1 + c3 x^2))): silu, and gelu's tanh form
+  kActLogistic = 2,    // 1 / (1 + exp(-x (c1 + c3 x^2))): gelu's tanh form
   kActNormal = 3,      // the normal distribution function: gelu
+  kActSilu = 4,        // 1 / (1 + exp(-x))
 };
 struct Activation {
   int32_t kind;

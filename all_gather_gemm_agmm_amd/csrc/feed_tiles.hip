@@ -88,8 +88,13 @@ void feed_tile_kernel(FeedProblem fp) {
           for (int s = 0; s < 2; ++s) {
             const f32x4_t x = *reinterpret_cast<const f32x4_t*>(smem + r * ROW + ((at + 4 * h + s) ^ (r & 15)) * 16);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[h][4 * s + e] = x[e] + bias[h][4 * s + e];
+            for (int e = 0; e < 4; ++e) v[h][4 * s + e] = x[e];
           }
+        if (fp.bias)
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[h][e] += bias[h][e];
         finish8<DT, GATED, KIND>(fp, v, row, row < M, col);
       };
       if constexpr (EVEN) {
