@@ -646,6 +646,20 @@ class _OpPlan:
             return self._empty(shape, dtype=dtype, device=device)
         return self._empty((shape[0], stride[0]), dtype=dtype, device=device)[:, :shape[1]]
 
+    def _maker(self, like):
+        """A function that makes new tensors as `like` describes them.  A tensor
+        like another is made faster than from its description: for dense ones of
+        up to 1 MiB, where that counts, the plan keeps one."""
+        import functools
+
+        import torch
+        dtype, device, shape, stride = like
+        if len(shape) > 1 and stride[0] != shape[1]:
+            return functools.partial(self._new, like)
+        if shape.numel() * dtype.itemsize <= 1 << 20:
+            return functools.partial(torch.empty_like, torch.empty(shape, dtype=dtype, device=device))
+        return functools.partial(torch.empty, shape, dtype=dtype, device=device)
+
     @property
     def m(self) -> int:
         return self.num_shards * self.m_per_shard
@@ -867,10 +881,7 @@ class FeedForwardPlan(_OpPlan):
         self._ldw = self._like((parts * n, k), t, self.get("lddw"))
         # kept pre-activations, seen as matrices of their rows
         self._kept_shape, self._scales_shape = torch.Size((m, parts, wide)), torch.Size((m, parts, wide // KEPT_BLOCK))
-        # a tensor like another is made faster than from its description: for y of
-        # up to 1 MiB, where that counts, the plan keeps one
-        small = m * n <= 1 << 19 and self._ly[3] == (n, 1)
-        self._proto, self._same = self._new(self._ly) if small else None, torch.empty_like
+        self._new_y, self._new_da, self._new_dw, self._new_db = (self._maker(x) for x in (self._ly, self._lda, self._ldw, self._lb))
         self._kept_types = {16: t, 8: torch.float8_e4m3fn}
         self._scale_types = {t: None, torch.float8_e4m3fn: torch.float8_e8m0fnu}
 
@@ -926,7 +937,7 @@ class FeedForwardPlan(_OpPlan):
         saved = v = s = None
         with _device_and_stream(self.device, stream):
             if out is None:
-                out = self._new(self._ly) if self._proto is None else self._same(self._proto)
+                out = self._new_y()
                 y = out.data_ptr()
             if keep:
                 empty, device, t = self._empty, self._la[1], self._kept_types[keep]
@@ -951,13 +962,13 @@ class FeedForwardPlan(_OpPlan):
         pb = None if dbias is None else on(dbias, self._lb, "dbias")
         with _device_and_stream(self.device, stream):
             if dA is None and need_dA:
-                dA = self._new(self._lda)
+                dA = self._new_da()
                 pa = dA.data_ptr()
             if dW is None and need_dW:
-                dW = self._new(self._ldw)
+                dW = self._new_dw()
                 pw = dW.data_ptr()
             if dbias is None and need_dbias:
-                dbias = self._new(self._lb)
+                dbias = self._new_db()
                 pb = dbias.data_ptr()
             _check(self._bwd(self.handle, a, w, v, s, g, pa, pw, pb, _stream_handle(stream, self.device)))
         return dA, dW, dbias
@@ -969,7 +980,7 @@ class FeedForwardPlan(_OpPlan):
         v, s = self._kept(saved)
         with _device_and_stream(self.device, stream):
             if out is None:
-                out = self._new(self._ly)
+                out = self._new_y()
             _check(self._again(self.handle, v, s, self._on(out, self._ly, "out"), _stream_handle(stream, self.device)))
         return out
 
@@ -998,9 +1009,7 @@ class NormPlan(_OpPlan):
         self._ldy, self._ldx = self._like(shape, t, self.get("lddy")), self._like(shape, t, self.get("lddx"))
         self._lw = self._like((self.cols,), _torch_dtype(self.weight_dtype))
         self._ls = self._like((self.rows,), torch.float32)
-        # a tensor like another is made faster than from its description: for
-        # statistics of up to 1 MiB, where that counts, the plan keeps one
-        self._stats, self._same = self._new(self._ls) if self.rows <= 1 << 18 else None, torch.empty_like
+        self._new_y, self._new_dx, self._new_w, self._new_s = (self._maker(x) for x in (self._ly, self._ldx, self._lw, self._ls))
 
     @property
     def m(self) -> int:
@@ -1008,19 +1017,16 @@ class NormPlan(_OpPlan):
 
     def forward(self, x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
         """(y, mean, rstd): y [rows, cols] and the rows' fp32 statistics."""
-        on, same = self._on, self._same
+        on = self._on
         px = on(x, self._lx, "x")
         w = None if weight is None else on(weight, self._lw, "weight")
         b = None if bias is None else on(bias, self._lw, "bias")
         y = None if out is None else on(out, self._ly, "out")
         with _device_and_stream(self.device, stream):
             if out is None:
-                out = same(x) if x.stride() == self._ly[3] else self._new(self._ly)
+                out = self._new_y()
                 y = out.data_ptr()
-            if self._stats is None:
-                mean, rstd = self._new(self._ls), self._new(self._ls)
-            else:
-                mean, rstd = same(self._stats), same(self._stats)
+            mean, rstd = self._new_s(), self._new_s()
             _check(self._fwd(self.handle, px, w, b, eps, y, mean.data_ptr(), rstd.data_ptr(), _stream_handle(stream, self.device)))
         return out, mean, rstd
 
@@ -1029,17 +1035,17 @@ class NormPlan(_OpPlan):
         """(dx, dweight, dbias) for the upstream gradient dy of y and the
         statistics that forward returned; None in the place of one that is not
         needed."""
-        on, new = self._on, self._new
+        on = self._on
         px, g = on(x, self._lx, "x"), on(dy, self._ldy, "dy")
         w = None if weight is None else on(weight, self._lw, "weight")
         mu, rs = on(mean, self._ls, "mean"), on(rstd, self._ls, "rstd")
         d = None if dx is None else on(dx, self._ldx, "dx")
         with _device_and_stream(self.device, stream):
             if dx is None and need_dx:
-                dx = self._same(x) if x.stride() == self._ldx[3] else new(self._ldx)
+                dx = self._new_dx()
                 d = dx.data_ptr()
-            dw = new(self._lw) if need_dweight else None
-            db = new(self._lw) if need_dbias else None
+            dw = self._new_w() if need_dweight else None
+            db = self._new_w() if need_dbias else None
             _check(self._bwd(self.handle, px, g, w, mu, rs, d, None if dw is None else dw.data_ptr(),
                              None if db is None else db.data_ptr(), _stream_handle(stream, self.device)))
         return dx, dw, db

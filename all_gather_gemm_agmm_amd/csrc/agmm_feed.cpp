@@ -616,7 +616,7 @@ agmm_norm_plan_t agmm_norm_plan_create(int64_t rows, int64_t cols, int dtype, in
   int rc = p->init();
   if (rc == AGMM_OK) {
     p->groups = agmm::norm_groups(rows, cols, dtype, p->cu_count);
-    rc = p->reserve((size_t)p->groups * 2 * cols * sizeof(float));
+    if (!agmm::norm_direct(cols, dtype, p->groups)) rc = p->reserve((size_t)p->groups * 2 * cols * sizeof(float));
   }
   if (rc != AGMM_OK) {
     const int st = agmm::g_status;
@@ -702,7 +702,7 @@ int agmm_norm_backward(agmm_norm_plan_t p, const void* x, const void* dy, const 
   if (rc != AGMM_OK) return rc;
   std::lock_guard<std::mutex> lk(p->mu);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool sums = dweight || dbias;
+  const bool direct = agmm::norm_direct(p->cols, p->dtype, p->groups), sums = !direct && (dweight || dbias);
   agmm::NormProblem n = p->problem(x, weight);
   n.dy = dy;
   n.lddy = p->lddy ? p->lddy : p->cols;
@@ -711,6 +711,8 @@ int agmm_norm_backward(agmm_norm_plan_t p, const void* x, const void* dy, const 
   n.dx = dx;
   n.lddx = p->lddx ? p->lddx : p->cols;
   n.sums = sums ? reinterpret_cast<float*>(p->ws) : nullptr;
+  n.dweight = direct ? dweight : nullptr;
+  n.dbias = direct ? dbias : nullptr;
   return p->run(s, sums, [&]() -> int {
     hipError_t err = agmm::launch_norm_backward(n, s);
     if (err != hipSuccess) return hip_err(err, "norm gradient launch");

@@ -54,13 +54,13 @@ void feed_grads_kernel(FeedGrads gp) {
     bias_sums<DT>(gp.bias, (int)blockIdx.x - gp.tiles, *reinterpret_cast<float(*)[4][64]>(smem));
     return;
   }
-  const bool is_a = (int)blockIdx.x < gp.a_tiles;
+  const bool is_a = (int)blockIdx.x >= gp.a_first && (int)blockIdx.x < gp.a_first + gp.a_tiles;
   const GemmProblem& p = is_a ? gp.a : gp.w;
 
 #define AGMM_CLAMP
 #define AGMM_B_GROUPS gp.w_group
 #define AGMM_B_GROUP_ROWS (is_a ? 0 : gp.w_rows)
-#define AGMM_TILE_ID (is_a ? (int)blockIdx.x : (int)blockIdx.x - gp.a_tiles)
+#define AGMM_TILE_ID ((int)blockIdx.x - (is_a ? gp.a_first : gp.a_first ? 0 : gp.a_tiles))
 #include "gemm_m16_loop.inc"
 
   if (p.splits > 1) {
@@ -120,9 +120,12 @@ hipError_t launch_feed_grads(FeedGrads gp, int tile, int dtype, hipStream_t s) {
   if ((!a && !w && !bias) || (a && !fits(gp.a, tile)) || (w && !fits(gp.w, tile)) ||
       (w && gp.w_rows && (gp.w_rows % 64 != 0 || gp.w.k % gp.w_rows != 0 || gp.w.k / gp.w_rows > kMaxGroups)))
     return hipErrorInvalidValue;
-  int64_t grid = a ? (int64_t)gp.a.order.num_rb * gp.a.order.num_cb * gp.a.splits : 0;
-  gp.a_tiles = (int32_t)grid;
-  if (w) grid += (int64_t)gp.w.order.num_rb * gp.w.order.num_cb * gp.w.splits;
+  const int64_t a_tiles = a ? (int64_t)gp.a.order.num_rb * gp.a.order.num_cb * gp.a.splits : 0;
+  const int64_t w_tiles = w ? (int64_t)gp.w.order.num_rb * gp.w.order.num_cb * gp.w.splits : 0;
+  int64_t grid = a_tiles + w_tiles;
+  gp.a_tiles = (int32_t)a_tiles;
+  // the longer sums begin first, the others fill what they leave
+  gp.a_first = a && w && gp.w.k_per_split > gp.a.k_per_split ? (int32_t)w_tiles : 0;
   gp.tiles = (int32_t)grid;
   if (bias) grid += (gp.bias.cols + 63) / 64;
   if (grid >= kFeedGrid) return hipErrorInvalidValue;

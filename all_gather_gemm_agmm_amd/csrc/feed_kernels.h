@@ -117,7 +117,7 @@ struct FeedGrads {
   // of 64, at each of w_group
   const void* w_group[kMaxGroups];
   int32_t w_rows;
-  int32_t a_tiles, tiles;  // set by launch_feed_grads: workgroups of dA, of both
+  int32_t a_tiles, a_first, tiles;   // set by launch_feed_grads: workgroups of dA, the first of them, of both
   FeedBias bias;
 };
 hipError_t launch_feed_grads(FeedGrads g, int tile, int dtype, hipStream_t stream);
@@ -166,9 +166,12 @@ struct NormProblem {
   int64_t lddx;
   float* sums;             // [groups][2][cols]: sums of dy * xhat and of dy; or null
   int32_t groups;
+  void *dweight, *dbias;   // one group: the sums themselves, rounded to wtype (sums null); or null
 };
 hipError_t launch_norm_forward(const NormProblem& p, hipStream_t stream);
 hipError_t launch_norm_backward(const NormProblem& p, hipStream_t stream);
+// Whether the backward pass writes dweight and dbias itself.
+bool norm_direct(int64_t cols, int dtype, int groups);
 // Workgroups (and groups of sums) of the backward pass.
 int norm_groups(int64_t rows, int64_t cols, int dtype, int cus);
 

@@ -349,7 +349,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p) {
       }
     }
   }
-  if (!p.sums) return;
+  if (!p.sums && !p.dweight && !p.dbias) return;
   if constexpr (ROWS > 1)
 #pragma unroll 1
     for (int r = 1; r < ROWS; ++r) {
@@ -373,6 +373,20 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p) {
       __syncthreads();
     }
   if (sub) return;
+  if (!p.sums) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int64_t col = col_of(c);
+      if (col >= p.cols) continue;
+      constexpr int U = Elem<WT>::V < V ? Elem<WT>::V : V;
+#pragma unroll
+      for (int s = 0; s < V / U; ++s) {
+        if (p.dweight) store_piece<WT>(p.dweight, col + U * s, p.cols - col - U * s, dw[c] + U * s);
+        if (p.dbias) store_piece<WT>(p.dbias, col + U * s, p.cols - col - U * s, db[c] + U * s);
+      }
+    }
+    return;
+  }
   float* out = p.sums + (int64_t)blockIdx.x * 2 * p.cols;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -458,6 +472,9 @@ __global__ __launch_bounds__(256) void norm_sums_long_kernel(NormProblem p) {
 
 int64_t pieces_of(int64_t cols, int dtype) { return (cols + (dtype == kDtypeFp32 ? 3 : 7)) / (dtype == kDtypeFp32 ? 4 : 8); }
 
+// Pieces of the longest rows that the backward kernel holds in registers.
+int64_t held_pieces(int dtype) { return dtype == kDtypeFp32 ? 2048 : 1024; }
+
 template <int DT, int WT>
 hipError_t forward_type(const NormProblem& p, hipStream_t s) {
   const int64_t pieces = pieces_of(p.cols, DT);
@@ -514,6 +531,8 @@ hipError_t by_type(const NormProblem& p, F&& f) {
 
 }  // namespace
 
+bool norm_direct(int64_t cols, int dtype, int groups) { return groups == 1 && pieces_of(cols, dtype) <= held_pieces(dtype); }
+
 int norm_groups(int64_t rows, int64_t cols, int dtype, int cus) {
   const int64_t pieces = pieces_of(cols, dtype);
   int64_t at_once = 1;                         // rows that a workgroup takes at a time
@@ -521,8 +540,11 @@ int norm_groups(int64_t rows, int64_t cols, int dtype, int cus) {
   // one workgroup a CU, whose sums are one row of [groups]; long rows: so many
   // strips that they fill the CUs four times
   int64_t groups = cus;
-  if (pieces > (dtype == kDtypeFp32 ? 2048 : 1024)) groups = 4 * cus / ((pieces + 255) / 256);
+  if (pieces > held_pieces(dtype)) groups = 4 * cus / ((pieces + 255) / 256);
   else rows = (rows + at_once - 1) / at_once;
+  // few rows: one workgroup writes the sums itself, which saves the launch that
+  // adds groups (about 4 us, as long as four turns of a workgroup)
+  if (pieces <= held_pieces(dtype) && rows <= 4) return 1;
   if (groups > rows) groups = rows;
   return (int)(groups < 1 ? 1 : groups);
 }
@@ -533,7 +555,8 @@ hipError_t launch_norm_forward(const NormProblem& p, hipStream_t s) {
 }
 
 hipError_t launch_norm_backward(const NormProblem& p, hipStream_t s) {
-  if (!valid(p) || !p.dy || !p.mean || !p.rstd || (!p.dx && !p.sums) || p.groups < 1 || p.groups > p.rows)
+  if (!valid(p) || !p.dy || !p.mean || !p.rstd || (!p.dx && !p.sums && !p.dweight && !p.dbias) || p.groups < 1 ||
+      ((p.dweight || p.dbias) && (p.sums || p.groups != 1 || pieces_of(p.cols, p.dtype) > held_pieces(p.dtype))) || p.groups > p.rows)
     return hipErrorInvalidValue;
   return by_type(p, [&](auto t, auto w) { return backward_type<decltype(t)::value, decltype(w)::value>(p, s); });
 }
