@@ -97,23 +97,23 @@ struct agmm_ff_plan : PlanBase {
 
   // Microseconds of the products' tiles, measured on MI355X: of a launch of
   // `tiles` of them, each over `sum` elements of k.  A 256 x 256 tile has a CU to
-  // itself, 10 and 1.4 per 64 of its sum, 1.1 where half the CUs have none, and
-  // 256 x 224 seven eighths of that; a 128 x 128 one shares it, 5 and 0.92, or 0.48 alone.  `lines`: the operands'
-  // rows start on 128-byte lines; where they do not, a tile's loads take twice
-  // the lines, which slows the smaller tile (1011 x 4040 -> 2 x 2051: 74 us, 40
-  // at 4096).
+  // itself, 17 and 1.1 per 64 of its sum, 0.93 where half the CUs have none, and
+  // 256 x 224 seven eighths of that; a 128 x 128 one shares it, 5 and 0.92, in the
+  // last round less, or has it alone, 0.48.  `lines`: the operands' rows start on
+  // 128-byte lines; where they do not, a tile's loads take twice the lines
+  // (1011 x 4040 -> 2 x 2051: 64 us, 40 at 4096).
   double tiles_us(int t, int64_t tiles, int64_t sum, bool lines) const {
     const double steps = (double)cdiv(sum, 64);
     if (t >= 224)
-      return (double)cdiv(tiles, cu_count) * (10.0 + t / 256.0 * (2 * tiles <= cu_count ? 1.1 : 1.4) * steps * (lines ? 1.0 : 1.05));
-    const double by = steps * (lines ? 1.0 : 1.8);
+      return (double)cdiv(tiles, cu_count) * (17.0 + t / 256.0 * (2 * tiles <= cu_count ? 0.93 : 1.1) * steps * (lines ? 1.0 : 1.25));
     const int64_t rest = tiles % (2 * cu_count);
-    const double shared = std::max(0.0, (double)rest / cu_count - 1.0);   // CUs with two in the last round
-    return (double)(tiles / (2 * cu_count)) * (5.0 + 0.92 * by) + (rest == 0 ? 0.0 : 5.0 + (0.48 + 0.44 * shared) * by);
+    const double by = steps * (lines ? 1.0 : tiles <= cu_count ? 1.55 : 1.4);
+    const double last = rest <= cu_count ? 0.48 : 0.78 + 0.14 * ((double)rest / cu_count - 1.0);
+    return (double)(tiles / (2 * cu_count)) * (5.0 + 0.92 * by) + (rest == 0 ? 0.0 : 5.0 + last * by);
   }
 
   // Microseconds of copies of A and W as rows of whole lines.
-  double copy_us() const { return 5.0 + (double)(m + cols()) * (double)k * 4 / 4.8e6; }
+  double copy_us() const { return 5.0 + (double)(m + cols()) * (double)k * 4 / 6.5e6; }
 
   // The few-row form in blocks of yc columns of y: 4.5 and 21 per MB of a CU's
   // rows and columns (27 where four waves share out k, 1.7 times that for odd
