@@ -6,11 +6,15 @@
 // from the kept pre-activations, as 16-bit operands of the two gradient
 // products, by rows [m][parts * n] for dA = d W and transposed [parts * n][m]
 // for dW = d^T A, and the column sums of d for the bias.  A workgroup takes 128
-// rows x 64 columns of y: 16-byte pieces of rows in, d by rows out of the same
+// (few: 32) rows x 64 columns of y: 16-byte pieces of rows in, d by rows out of the same
 // registers, and through LDS and transposing reads out again by columns.  Bound:
 // HBM, every value read once and d written twice (that the matrix cores can
 // read both operands along k).  d is rounded to the operands' type, as every
 // other operand of these products is; its sums are taken before that, in fp32.
+//
+// Measured: 8192 x 2 x 3584 bf16 from 8 bits 76-80 us, 355 MB at 4.5 TB/s; 2048 x
+// 1024 bf16, tanh's gelu 6.4, in blocks of 32 rows, so that there are enough; 111 x
+// 2 x 2051 fp16, with the copies that the products need, 6.3.
 //
 // What is read again as fp32 sums over ranges of k, or over blocks of rows, is
 // added in a fixed order.

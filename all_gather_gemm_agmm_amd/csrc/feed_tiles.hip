@@ -20,6 +20,14 @@
 // the operands' type or to 8 bits: a power of two for 32 columns of a row, four
 // neighbouring threads', so their largest takes two exchanges, and multiplying
 // by its inverse is exact: e4m3's rounding is the only one.
+//
+// Bound: MFMA, in practice power.  Measured, rows x k -> columns: 8192 x 8192 ->
+// 2 x 7168 bf16, silu, 8 bits kept, 1360-1450 us, 1330-1410 TFLOP/s (a library
+// product of that size alone reaches 1480); 8192 x 8192 -> 3584 fp16, gelu, 372-
+// 416 us by 256 x 224 (two even rounds of the CUs, where 448 tiles of 256 x 256
+// are one and three quarters: 380), 10 of them gelu's exponentials, which no
+// MFMA of the same wave runs beside.  1011 x 4040 -> 2 x 2051 fp16: 57 us on 264
+// tiles, more than the CUs at one each, and 16 for the copies.
 #include "feed_device.h"
 
 namespace agmm {

@@ -10,12 +10,17 @@
 // would lose the variance of rows far from 0).
 // Rows longer than 1024 threads hold are read again for each sum.
 //
-// Backward, a workgroup takes every `groups`-th row; a lane's columns stay the
-// same, so the two column sums are registers too, and leave once at the end as
-// [groups][2][columns], which sum_columns_kernel adds in order.  The next row's
-// loads are on their way while a row is reduced.
+// Backward, a workgroup takes as many rows at a time as 1024 threads hold, and
+// every `groups`-th such set; a lane's columns stay the same, so the two column
+// sums are registers too, and leave once at the end as [groups][2][columns],
+// which sum_columns_kernel adds in order (one group: as dw and db at once).  The
+// next row's loads are on their way while a row is reduced.
 //
-// Bound: HBM.  Statistics and sums are fp32; results are rounded once.
+// Bound: HBM; few rows: a launch.  Statistics and sums are fp32; results are
+// rounded once.  Measured: forward 8192 x 8192 bf16, fp32 weights 53-55 us, 4.9
+// TB/s (weights are loaded once per workgroup of three a CU, not per row: 80 us);
+// 128 x 4096 4; backward 8192 x 8192 77-80 us, 5.1 TB/s, and 4 for the sums; 1011
+// x 4035 fp16 11 and 3.
 #include "feed_device.h"
 
 namespace agmm {

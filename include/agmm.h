@@ -693,8 +693,9 @@ agmm_ff_plan_t agmm_ff_plan_create(int num_shards, int64_t m_per_shard, int64_t 
  *   saved, saved_scales  as above, or NULL (no scales: 16 bits)
  * Shards, W and saved are 16-byte aligned, the others to their elements.
  * Outputs must not overlap inputs, but for residual = Y with equal strides.
- * Stream, capture and ordering rules are agmm_run's (a call that copies nothing
- * shares no workspace with others and is not ordered with them).
+ * Stream, capture and ordering rules are agmm_run's (where the settings in use
+ * need neither copies nor ranges of k, calls share no workspace and are not
+ * ordered).
  */
 int agmm_ff_forward(agmm_ff_plan_t plan, const void *const *shard_ptrs, const void *W,
                     const void *bias, const void *residual, void *Y, void *saved,
@@ -768,8 +769,9 @@ int agmm_norm_forward(agmm_norm_plan_t plan, const void *x, const void *weight, 
 
 /* Enqueue the backward pass from the forward pass's mean and rstd: dx, rows
  * "lddx" apart, dweight and dbias [cols], each or NULL (not all); dy rows "lddy"
- * apart; dx may be dy itself with equal strides.  Calls with dweight or dbias
- * share the plan's workspace and are ordered as agmm_run's are. */
+ * apart; dx may be dy itself with equal strides, and outputs overlap nothing
+ * else.  Calls with dweight or dbias share the plan's workspace and are ordered
+ * as agmm_run's are; few rows need none and are not. */
 int agmm_norm_backward(agmm_norm_plan_t plan, const void *x, const void *dy, const void *weight,
                        const float *mean, const float *rstd, void *dx, void *dweight, void *dbias,
                        void *stream);
