@@ -120,10 +120,10 @@ struct agmm_ff_plan : PlanBase {
   // strides), or W at 4.5 TB/s, and a tenth of the other.  E.g. (us) 8 x 4096 -> 1792: 7.8 by 8 columns, 8.7
   // by 16, 21 by 64; 128 x 4096 -> 7168: 73 by 16, 35 by 64; 8 x 8192 -> 3584: 24
   // by 8, 16 by 16.
-  double few_us(int fm, int yc) const {
-    const double mb = 2e-6 * (double)k * (double)(std::min<int64_t>(m, 16 * fm) + parts * yc);
+  double few_us(int fm, int yc, int splits) const {
+    const double mb = 2e-6 * (double)cdiv(k, splits) * (double)(std::min<int64_t>(m, 16 * fm) + parts * yc);
     const double each = (fm == 1 && yc <= 16 ? 21.0 : 27.0) * (ld_a() % 2 != 0 || ld_w() % 2 != 0 ? 1.7 : 1.0);
-    const int64_t wgs = cdiv(m, 16 * fm) * cdiv(n, yc);
+    const int64_t wgs = cdiv(m, 16 * fm) * cdiv(n, yc) * splits;
     const double in = 4.5 + (double)cdiv(wgs, cu_count) * each * mb, read = 2.0 + (double)cols() * (double)k * 2 / 4.5e6;
     return std::max(in, read) + 0.1 * std::min(in, read);
   }
@@ -151,21 +151,28 @@ struct agmm_ff_plan : PlanBase {
       const int64_t tiles = cdiv(m, 128) * cdiv(nc, 128);
       for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
         if (s > 1 && (k < 256 * s || tiles * s > 4 * cu_count)) break;
-        // the ranges' sums are written and read at 4 TB/s
-        const double join = s > 1 ? 4.0 + (double)(s * m) * (double)nc * 8 / 4e6 : 0.0;
-        offer(128, copied, s, tiles_us(128, tiles * s, cdiv(k, s), lines || copied) + join);
+        offer(128, copied, s, tiles_us(128, tiles * s, cdiv(k, s), lines || copied) + (s > 1 ? join_us(s, 4.0) : 0.0));
       }
     }
     L.fm = m <= 16 ? 1 : 4;
     if (!few_fits()) return;
     double few = -1;
+    int ranges = 1;
     for (int yc : {8, 16, most_yc()}) {
       if (yc == 8 && L.fm > 1) continue;
-      const double us = few_us(L.fm, yc);
-      if (few < 0 || us < few) few = us, L.yc = yc;
+      const int64_t blocks = cdiv(m, 16 * L.fm) * cdiv(n, yc);
+      for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        if (s > 1 && (yc == 8 || k < 256 * s || blocks * s > 2 * cu_count)) break;
+        const double us = few_us(L.fm, yc, s) + (s > 1 ? join_us(s, 5.0) : 0.0);
+        if (few < 0 || us < few) few = us, L.yc = yc, ranges = s;
+      }
     }
-    offer(64, false, 1, few);
+    offer(64, false, ranges, few);
   }
+
+  // Microseconds of adding ranges of k: the launch (5 behind the few-row form, whose
+  // own is short), and the sums written and read at 4 TB/s.
+  double join_us(int splits, double launch) const { return launch + (double)(splits * m) * (double)tile_cols() * 8 / 4e6; }
 
   int most_yc() const { return parts == 2 ? 32 : 64; }
 
@@ -299,8 +306,9 @@ struct agmm_ff_plan : PlanBase {
     }
     // 8-bit pre-activations of a gated product come in no tile of 224
     const int tile = L.tile == 224 && parts == 2 && saved_scales ? 256 : L.tile;
-    // kept rows are written in blocks of 32 columns of a part
-    const int yc = saved ? most_yc() : L.yc;
+    // kept rows are written in blocks of 32 columns of a part, by one workgroup
+    // or by the launch that joins ranges
+    const int yc = saved && L.splits == 1 ? most_yc() : L.yc;
     if (L.tile == 64) {
       p.gemm.order.num_rb = (int32_t)cdiv(m, 16 * L.fm);
       p.gemm.order.num_cb = (int32_t)cdiv(n, yc);

@@ -6,7 +6,10 @@
 // so k and the strides may be anything and nothing is copied first.  The waves' sums are added in LDS in a fixed order, wave w
 // taking row block w, and bias, activation, product, residual and rounding
 // follow there (feed_tiles.hip says how).  Gated, blocks of 16 rows of the
-// first n rows of B and of the second n take turns.
+// first n rows of B and of the second n take turns.  Where the blocks leave CUs
+// idle and k is long, it is cut into ranges as well, whose fp32 sums a second
+// launch adds in order and finishes (63 x 3814 -> 2 x 381: 20 us in one launch,
+// 13 so; 128 x 2834 -> 2 x 252: 15 and 11.5; 8 x 1001 -> 700 is faster in one, 8).
 //
 // ODD (a stride is odd): rows that start in the middle of a word are read from
 // that word on, with one word more, and shifted; accesses that start there take
@@ -34,8 +37,11 @@ __global__ __launch_bounds__(64 * WAVES) void feed_few_kernel(FeedProblem fp) {
   __shared__ float part[WAVES][FM][FN][4][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g4 = lane >> 4, i16 = lane & 15;
-  const int M = p.m, NC = fp.n, K = p.k;
-  const int cb = (int)blockIdx.x / p.order.num_rb, rb = (int)blockIdx.x - cb * p.order.num_rb;
+  const int blocks = p.order.num_rb * p.order.num_cb, range = (int)blockIdx.x / blocks, id = (int)blockIdx.x - range * blocks;
+  const int cb = id / p.order.num_rb, rb = id - cb * p.order.num_rb;
+  const bool whole = p.splits == 1;            // not one of several ranges of k
+  const int k0 = range * p.k_per_split;
+  const int M = p.m, NC = fp.n, K = min(p.k - k0, p.k_per_split);
   const int m0 = rb * 16 * FM, y0 = cb * YC;
   // rows and columns past the end read the last one and are never used
   const uint16_t *a[FM], *b[FN];
@@ -50,18 +56,18 @@ __global__ __launch_bounds__(64 * WAVES) void feed_few_kernel(FeedProblem fp) {
       const void* other = p.rows.a_group[min(first + q, p.rows.num_groups - 1)];
       if (g == first + q) base = other;
     }
-    a[0] = static_cast<const uint16_t*>(base) + (int64_t)(i - g * rpg) * p.rows.a_ld + 8 * g4;
+    a[0] = static_cast<const uint16_t*>(base) + (int64_t)(i - g * rpg) * p.rows.a_ld + k0 + 8 * g4;
   } else {
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
       const int i = min(m0 + 16 * f + i16, M - 1), g = i / p.rows.rows_per_group;
-      a[f] = static_cast<const uint16_t*>(p.rows.a_group[g]) + (int64_t)(i - g * p.rows.rows_per_group) * p.rows.a_ld + 8 * g4;
+      a[f] = static_cast<const uint16_t*>(p.rows.a_group[g]) + (int64_t)(i - g * p.rows.rows_per_group) * p.rows.a_ld + k0 + 8 * g4;
     }
   }
 #pragma unroll
   for (int f = 0; f < FN; ++f) {
     const int h = HALF ? (GATED ? i16 >> 3 : 0) : f % PARTS, c = HALF ? i16 & 7 : 16 * (f / PARTS) + i16;
-    b[f] = static_cast<const uint16_t*>(p.b) + 8 * g4 + ((int64_t)h * NC + min(y0 + c, NC - 1)) * p.ldb;
+    b[f] = static_cast<const uint16_t*>(p.b) + k0 + 8 * g4 + ((int64_t)h * NC + min(y0 + c, NC - 1)) * p.ldb;
   }
 
   // what the epilogue adds, on its way early
@@ -71,13 +77,13 @@ __global__ __launch_bounds__(64 * WAVES) void feed_few_kernel(FeedProblem fp) {
   for (int j = 0; j < FN; ++j) {
     const int h = HALF ? (GATED ? g4 >> 1 : 0) : j % PARTS, c = y0 + (HALF ? 4 * (g4 & 1) : 16 * (j / PARTS) + 4 * g4);
     bias[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if (fp.bias && wave < FM) bias[j] = load4<DT>(static_cast<const uint16_t*>(fp.bias) + (int64_t)h * NC + c, NC - c);
+    if (fp.bias && whole && wave < FM) bias[j] = load4<DT>(static_cast<const uint16_t*>(fp.bias) + (int64_t)h * NC + c, NC - c);
   }
 #pragma unroll
   for (int q = 0; q < FQ; ++q) {
     const int c = y0 + (HALF ? 4 * (g4 & 1) : 16 * q + 4 * g4);
     res[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if (!GATED && fp.residual && wave < FM && row < M)
+    if (!GATED && fp.residual && whole && wave < FM && row < M)
       res[q] = load4<DT>(static_cast<const uint16_t*>(fp.residual) + (int64_t)row * fp.ldr + c, NC - c);
   }
 
@@ -190,6 +196,16 @@ __global__ __launch_bounds__(64 * WAVES) void feed_few_kernel(FeedProblem fp) {
       x[j][e] = t + bias[j][e];
     }
   }
+  if (!HALF && !whole) {
+    // fp32 sums [range][m][tile columns rounded up to 16] for launch_feed_join
+    const int64_t ld = (p.n + 15) & ~15;
+    float* out = p.partials + ((int64_t)range * M + row) * ld + PARTS * y0 + 4 * g4;
+    if (in)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        if (PARTS * y0 + 16 * j < ld) *reinterpret_cast<f32x4_t*>(out + 16 * j) = f32x4_t{x[j][0], x[j][1], x[j][2], x[j][3]};
+    return;
+  }
   if (YC >= kKeptBlock && fp.kept.values) {
     const int64_t wide = fp.kept.wide;
     // blocks of 32 columns of a part: two accumulator blocks 
@@ -277,15 +293,21 @@ hipError_t launch_type(const FeedProblem& p, int fm, int yc, unsigned grid, hipS
 }  // namespace
 
 hipError_t launch_feed_few(const FeedProblem& p, int fm, int yc, int dtype, hipStream_t stream) {
-  const int64_t grid = (int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb;
+  const GemmProblem& g = p.gemm;
+  const int64_t grid = (int64_t)g.order.num_rb * g.order.num_cb * g.splits;
   const int most = p.gated ? 32 : 64;
   if ((fm != 1 && fm != 4) || (yc != 8 && yc != 16 && yc != most) || (yc == 8 && fm != 1) || (p.gated && p.residual) ||
       p.gemm.order.num_rb != (p.gemm.m + 16 * fm - 1) / (16 * fm) || p.gemm.order.num_cb != (p.n + (int64_t)yc - 1) / yc ||
       grid < 1 || grid >= kFeedGrid || (int64_t)p.gemm.rows.num_groups * p.gemm.rows.rows_per_group != p.gemm.m ||
-      (p.kept.values && (yc != most || p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock)))
+      g.splits < 1 || (g.splits == 1 && g.k_per_split < g.k) ||
+      (g.splits > 1 && (yc == 8 || !g.partials || g.k_per_split % 64 != 0 || (int64_t)g.splits * g.k_per_split < g.k ||
+                        (int64_t)(g.splits - 1) * g.k_per_split >= g.k ||
+                        g.n != (p.gated ? 2 * (((int64_t)p.n + 15) / 16 * 16) : p.n))) ||
+      (p.kept.values && ((g.splits == 1 && yc != most) || p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock)))
     return hipErrorInvalidValue;
-  return dtype == kDtypeBf16 ? launch_type<kDtypeBf16>(p, fm, yc, (unsigned)grid, stream)
-       : dtype == kDtypeFp16 ? launch_type<kDtypeFp16>(p, fm, yc, (unsigned)grid, stream) : hipErrorInvalidValue;
+  const hipError_t err = dtype == kDtypeBf16 ? launch_type<kDtypeBf16>(p, fm, yc, (unsigned)grid, stream)
+                       : dtype == kDtypeFp16 ? launch_type<kDtypeFp16>(p, fm, yc, (unsigned)grid, stream) : hipErrorInvalidValue;
+  return err == hipSuccess && g.splits > 1 ? launch_feed_join(p, dtype, stream) : err;
 }
 
 }  // namespace agmm

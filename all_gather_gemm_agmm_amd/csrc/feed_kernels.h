@@ -56,10 +56,13 @@ constexpr int64_t kFeedGrid = int64_t(1) << 24;
 // gemm.splits > 1 (tile 128): ranges of k to gemm.partials [splits][m][tile
 // columns rounded up to 16], and a second launch that finishes.
 hipError_t launch_feed_tiles(const FeedProblem& p, int tile, int dtype, hipStream_t stream);
+// The sums of gemm.splits ranges in gemm.partials, added in order and finished.
+hipError_t launch_feed_join(const FeedProblem& p, int dtype, hipStream_t stream);
 // Few rows: blocks of 16 fm rows x yc columns of y (fm 1 or 4; yc 8 with fm 1,
 // 16, or 64, gated 32: that where pre-activations are kept, whose blocks of 32
 // columns of a part lie in one workgroup); any k and strides, operands in place.
-// order.num_cb counts blocks of yc columns.
+// order.num_cb counts blocks of yc columns.  gemm.splits > 1 (not yc 8): ranges of
+// k, as above, and launch_feed_join; kept pre-activations then at any yc.
 hipError_t launch_feed_few(const FeedProblem& p, int fm, int yc, int dtype, hipStream_t stream);
 
 // Copies of A and of W as rows of whole 128-byte lines (PadRows, ops_kernels.h;

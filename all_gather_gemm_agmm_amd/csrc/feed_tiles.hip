@@ -192,9 +192,7 @@ hipError_t launch_type(const FeedProblem& p, int tile, hipStream_t s) {
     p.gated ? go(feed_part_kernel<DT, true>, grid) : go(feed_part_kernel<DT, false>, grid);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const int64_t pieces = ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * (kKeptBlock / 8);
-    const unsigned joins = (unsigned)((p.gemm.m * pieces + 255) / 256);
-    p.gated ? go(feed_join_kernel<DT, true>, joins) : go(feed_join_kernel<DT, false>, joins);
+    return launch_feed_join(p, DT, s);
   } else if (tile == 224) {
     p.gated ? go(feed_tile_kernel<256, 224, DT, 1, true>, grid) : go(feed_tile_kernel<256, 224, DT, 1, false>, grid);
   } else if (tile == 256) {
@@ -207,6 +205,15 @@ hipError_t launch_type(const FeedProblem& p, int tile, hipStream_t s) {
 
 }  // namespace
 
+hipError_t launch_feed_join(const FeedProblem& p, int dtype, hipStream_t s) {
+  const int64_t pieces = ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * (kKeptBlock / 8), all = p.gemm.m * pieces;
+  if (all >= kFeedGrid * 256 || !p.gemm.partials || (dtype != kDtypeBf16 && dtype != kDtypeFp16)) return hipErrorInvalidValue;
+  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)((all + 255) / 256)), dim3(256), 0, s, p); };
+  if (dtype == kDtypeBf16) p.gated ? go(feed_join_kernel<kDtypeBf16, true>) : go(feed_join_kernel<kDtypeBf16, false>);
+  else p.gated ? go(feed_join_kernel<kDtypeFp16, true>) : go(feed_join_kernel<kDtypeFp16, false>);
+  return hipGetLastError();
+}
+
 hipError_t launch_feed_tiles(const FeedProblem& p, int tile, int dtype, hipStream_t s) {
   const int64_t cols = p.gated ? 2 * (((int64_t)p.n + 15) / 16 * 16) : p.n;
   const int bm = tile == 224 ? 256 : tile;
@@ -215,8 +222,7 @@ hipError_t launch_feed_tiles(const FeedProblem& p, int tile, int dtype, hipStrea
       p.gemm.splits < 1 || (int64_t)p.gemm.order.num_rb * p.gemm.order.num_cb * p.gemm.splits >= kFeedGrid || p.gemm.k % 8 != 0 ||
       (p.gemm.splits > 1 && (tile != 128 || !p.gemm.partials || p.gemm.k_per_split % 64 != 0 ||
                              (int64_t)p.gemm.splits * p.gemm.k_per_split < p.gemm.k ||
-                             (int64_t)(p.gemm.splits - 1) * p.gemm.k_per_split >= p.gemm.k ||
-                             p.gemm.m * (((int64_t)p.n + 31) / 32 * 4) >= kFeedGrid * 256)) ||
+                             (int64_t)(p.gemm.splits - 1) * p.gemm.k_per_split >= p.gemm.k)) ||
       (p.gated && p.residual) || (tile == 224 && p.gated && p.kept.scales) || (p.kept.values && p.kept.wide != ((int64_t)p.n + kKeptBlock - 1) / kKeptBlock * kKeptBlock))
     return hipErrorInvalidValue;
   return dtype == kDtypeBf16 ? launch_type<kDtypeBf16>(p, tile, s)

@@ -727,7 +727,7 @@ int agmm_ff_recompute(agmm_ff_plan_t plan, const void *saved, const void *saved_
  *   "tile"          -1 automatic, 128 or 256: rows and columns of the products' tiles (128: k may
  *                   be cut into ranges); 224: 256 x 224 (the gradient's products, and a gated
  *                   product that keeps 8 bits, by 256); 64: blocks of up to 64 x 64 whose waves
- *                   share out k, for few rows (the gradient's products keep their automatic tiles)
+ *                   share out k (or a range of it), for few rows (the gradient's products keep their automatic tiles)
  * A change that needs more workspace reallocates it; the plan keeps its
  * previous settings when that fails.  Settings are fixed once a call was
  * captured into a graph.  get reads the values in use, "saved_cols" (ns), and

@@ -333,6 +333,31 @@ def test_every_gradient_range_count():
                 assert torch.equal(x, z)           # fixed order: the same bits
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("shape", [(3, 21, 3814, 381), (1, 32, 2231, 36), (1, 63, 2050, 16), (4, 16, 4096, 17), (2, 100, 1537, 50),
+                                   (1, 40, 1024, 100)], ids=str)
+def test_few_rows_in_ranges_of_k(shape, gated):
+    """Short y, long k: the few-row form adds ranges of k in a second launch, with everything that is done there."""
+    N, ms, k, n = shape
+    parts = 2 if gated else 1
+    for i, (name, dtype, keep, pad) in enumerate([("silu", BF16, 8, 0), ("gelu", FP16, 16, 1), ("relu", BF16, 0, 3)]):
+        shards, w, b, r = make(N, ms, k, n, dtype, parts, bias=i != 1, residual=not gated, seed=i)
+        wide = torch.full((parts * n, k + pad), float("nan"), dtype=TYPE[dtype], device="cuda")
+        wide[:, :k] = w
+        want, bound, p, e = R.forward(name, gated, torch.cat(shards), w, b, r, TYPE[dtype])
+        with agmm.FeedForwardPlan(N, ms, k, n, dtype, activation=name, gated=gated, with_gradient=False, tile=64, ldw=k + pad) as plan:
+            assert plan.workspace_bytes() > 0 or k < 1500   # the ranges' sums: this form copies nothing
+            first = plan.forward(shards, wide[:, :k], b, r, keep=keep)
+            out = torch.full((N * ms, n), float("nan"), dtype=TYPE[dtype], device="cuda") if gated else r.clone()
+            again = plan.forward(shards, wide[:, :k], b, None if gated else out, out=out, keep=keep)
+            y, saved = first if keep else (first, None)
+            R.check(y, want, bound, f"{name} y")
+            assert torch.equal(y, out)               # in place and fixed order: the same bits
+            if keep:
+                kept_matches(saved, p, e, n, parts, TYPE[dtype])
+                assert torch.equal(saved.values.view(torch.uint8), again[1].values.view(torch.uint8))
+
+
 def test_tiles_agree_at_scale():
     """A training step's shapes: tiles of 256 with interior and edge tiles, XCD order and several shards per tile."""
     N, ms, k, n = 3, 700, 1024, 1100
