@@ -83,7 +83,9 @@ struct agmm_ff_plan : PlanBase {
     float *parts = nullptr, *a_sums = nullptr, *w_sums = nullptr, *b_sums = nullptr;
     size_t bytes = 0;
   };
-  Layout forward_layout, backward_layout;   // those of the settings and the workspace
+  // those of the settings and the workspace: forward, forward with pre-activations
+  // kept, backward
+  Layout layouts[3];
 
   int64_t ld_a() const { return lda ? lda : k; }
   int64_t ld_w() const { return ldw ? ldw : k; }
@@ -131,7 +133,7 @@ struct agmm_ff_plan : PlanBase {
   // Form of the forward product: the one that takes the least, with the copies
   // it needs.  Copies have rows of whole lines; rows that are whole 16-byte
   // vectors already are copied where that pays.
-  void pick_tile(Layout& L, bool must_copy) const {
+  void pick_tile(Layout& L, bool must_copy, bool kept) const {
     const int64_t nc = tile_cols();
     const bool lines = ld_a() % 64 == 0 && ld_w() % 64 == 0;
     double best = -1;
@@ -162,6 +164,7 @@ struct agmm_ff_plan : PlanBase {
       if (yc == 8 && L.fm > 1) continue;
       const int64_t blocks = cdiv(m, 16 * L.fm) * cdiv(n, yc);
       for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        if (s == 1 && kept && yc != most_yc()) continue;   // blocks of 32 kept columns lie in one workgroup
         if (s > 1 && (yc == 8 || k < 256 * s || blocks * s > 2 * cu_count)) break;
         const double us = few_us(L.fm, yc, s) + (s > 1 ? join_us(s, 5.0) : 0.0);
         if (few < 0 || us < few) few = us, L.yc = yc, ranges = s;
@@ -179,13 +182,13 @@ struct agmm_ff_plan : PlanBase {
   // Whether every form of the few-row kernel stays within a launch.
   bool few_fits() const { return cdiv(m, m <= 16 ? 16 : 64) * cdiv(n, m <= 16 ? 8 : 16) < agmm::kFeedGrid; }
 
-  Layout layout(bool grad, char* base) const {
+  Layout layout(int which, char* base) const {
     Layout L;
     L.kp = round_up(k, 64);
     const bool must_a = k % 8 != 0 || ld_a() % 8 != 0, must_w = k % 8 != 0 || ld_w() % 8 != 0;   // not whole 16-byte vectors
     Cut c{base};
-    if (!grad) {
-      pick_tile(L, must_a || must_w);
+    if (which < 2) {
+      pick_tile(L, must_a || must_w, which == 1);
       if (L.pad_a) L.a = c.take((size_t)m * L.kp * 2);
       if (L.pad_w) L.w = c.take((size_t)cols() * L.kp * 2);
       L.per = round_up(cdiv(L.pad_a ? L.kp : k, L.splits), 64);
@@ -237,12 +240,10 @@ struct agmm_ff_plan : PlanBase {
 
   int apply() {
     size_t bytes = 0;
-    for (bool grad : {false, true})
-      if (!grad || with_gradient) bytes = std::max(bytes, layout(grad, nullptr).bytes);
+    for (int which = 0; which < 2 + with_gradient; ++which) bytes = std::max(bytes, layout(which, nullptr).bytes);
     const int rc = reserve(bytes);
     if (rc != AGMM_OK) return rc;
-    forward_layout = layout(false, ws);
-    if (with_gradient) backward_layout = layout(true, ws);
+    for (int which = 0; which < 2 + with_gradient; ++which) layouts[which] = layout(which, ws);
     return AGMM_OK;
   }
 
@@ -289,7 +290,7 @@ struct agmm_ff_plan : PlanBase {
 
   int forward(const void* const* shards, const void* W, const void* bias, const void* residual, void* Y,
               void* saved, void* saved_scales, hipStream_t s) {
-    const Layout& L = forward_layout;
+    const Layout& L = layouts[saved != nullptr];
     if (L.a || L.w) {
       const hipError_t err = agmm::launch_feed_copies(copies(L, shards, W), s);
       if (err != hipSuccess) return hip_err(err, "operand copy launch");
@@ -306,12 +307,9 @@ struct agmm_ff_plan : PlanBase {
     }
     // 8-bit pre-activations of a gated product come in no tile of 224
     const int tile = L.tile == 224 && parts == 2 && saved_scales ? 256 : L.tile;
-    // kept rows are written in blocks of 32 columns of a part, by one workgroup
-    // or by the launch that joins ranges
-    const int yc = saved && L.splits == 1 ? most_yc() : L.yc;
     if (L.tile == 64) {
       p.gemm.order.num_rb = (int32_t)cdiv(m, 16 * L.fm);
-      p.gemm.order.num_cb = (int32_t)cdiv(n, yc);
+      p.gemm.order.num_cb = (int32_t)cdiv(n, L.yc);
     } else {
       p.gemm.order = tiles_of(m, tile_cols(), tile == 224 ? 256 : tile, tile);
     }
@@ -332,13 +330,13 @@ struct agmm_ff_plan : PlanBase {
     p.y = Y;
     p.ldy = ldy ? ldy : n;
     p.kept = kept_rows(saved, saved_scales);
-    const hipError_t err = L.tile == 64 ? agmm::launch_feed_few(p, L.fm, yc, dtype, s) : agmm::launch_feed_tiles(p, tile, dtype, s);
+    const hipError_t err = L.tile == 64 ? agmm::launch_feed_few(p, L.fm, L.yc, dtype, s) : agmm::launch_feed_tiles(p, tile, dtype, s);
     return err == hipSuccess ? AGMM_OK : hip_err(err, "feed-forward launch");
   }
 
   int backward(const void* const* shards, const void* W, const void* saved, const void* saved_scales, const void* dY, void* dA,
                void* dW, void* dbias, hipStream_t s) {
-    const Layout& L = backward_layout;
+    const Layout& L = layouts[2];
     agmm::FeedDProblem e{};
     e.block = L.d_rows;
     e.m = m;
@@ -525,7 +523,7 @@ int agmm_ff_plan_get_int(agmm_ff_plan_t p, const char* key, int64_t* value) {
   else if (k == "ldy") *value = p->ldy ? p->ldy : p->n;
   else if (k == "lddy") *value = p->lddy ? p->lddy : p->n;
   else if (k == "saved_cols") *value = p->wide();
-  else if (k == "tile") *value = p->forward_layout.tile;
+  else if (k == "tile") *value = p->layouts[0].tile;
   else if (k == "captured") *value = p->captured;
   else return set_err(AGMM_ERR_INVALID_ARG, "unknown key '%s'", key);
   return ok();
@@ -549,7 +547,7 @@ int agmm_ff_forward(agmm_ff_plan_t p, const void* const* shard_ptrs, const void*
   if (saved_scales && !saved) return set_err(AGMM_ERR_INVALID_ARG, "saved_scales without saved");
   std::lock_guard<std::mutex> lk(p->mu);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool ordered = p->forward_layout.bytes > 0;
+  const bool ordered = p->layouts[saved != nullptr].bytes > 0;
   return p->run(s, ordered, [&] { return p->forward(shard_ptrs, W, bias, residual, Y, saved, saved_scales, s); });
 }
 
