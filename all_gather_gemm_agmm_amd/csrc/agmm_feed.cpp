@@ -1,6 +1,7 @@
 // C ABI of the feed-forward block's operators (host side): the product with an
 // epilogue and the gated product, their way back, and layer norm.  Their plans
 // are used as those of agmm_ops.cpp are.
+#include <initializer_list>
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -534,6 +535,16 @@ int agmm_ff_plan_get_int(agmm_ff_plan_t p, const char* key, int64_t* value) {
 
 size_t agmm_ff_plan_workspace_bytes(agmm_ff_plan_t p) { return p ? p->ws_bytes : 0; }
 
+// An output at the address of an input, or of another output (a partial overlap
+// is the caller's to avoid).
+static int check_apart(const void* out, const char* name, std::initializer_list<const void*> others, const void* const* shards = nullptr,
+                       int N = 0) {
+  if (!out) return AGMM_OK;
+  bool same = std::find(others.begin(), others.end(), out) != others.end();
+  for (int r = 0; r < N && shards; ++r) same = same || shards[r] == out;
+  return same ? set_err(AGMM_ERR_INVALID_ARG, "%s overlaps an operand of the call", name) : AGMM_OK;
+}
+
 int agmm_ff_forward(agmm_ff_plan_t p, const void* const* shard_ptrs, const void* W, const void* bias, const void* residual, void* Y,
                     void* saved, void* saved_scales, void* stream) {
   if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
@@ -548,7 +559,11 @@ int agmm_ff_forward(agmm_ff_plan_t p, const void* const* shard_ptrs, const void*
   if (rc != AGMM_OK) return rc;
   if (residual && p->parts == 2) return set_err(AGMM_ERR_UNSUPPORTED, "a gated product takes no residual");
   if (saved_scales && !saved) return set_err(AGMM_ERR_INVALID_ARG, "saved_scales without saved");
+  rc = check_apart(Y, "Y", {W, bias, saved}, shard_ptrs, p->N);
+  if (rc != AGMM_OK) return rc;
   std::lock_guard<std::mutex> lk(p->mu);
+  if (residual == Y && (p->ldr ? p->ldr : p->n) != (p->ldy ? p->ldy : p->n))
+    return set_err(AGMM_ERR_INVALID_ARG, "Y over residual needs equal strides");
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool ordered = p->layouts[saved != nullptr].bytes > 0;
   return p->run(s, ordered, [&] { return p->forward(shard_ptrs, W, bias, residual, Y, saved, saved_scales, s); });
@@ -578,6 +593,9 @@ int agmm_ff_backward(agmm_ff_plan_t p, const void* const* shard_ptrs, const void
   if (rc == AGMM_OK && dA) rc = check_ptr(dA, "dA", -1, 2);
   if (rc == AGMM_OK && dW) rc = check_ptr(dW, "dW", -1, 2);
   if (rc == AGMM_OK && dbias) rc = check_ptr(dbias, "dbias", -1, 2);
+  if (rc == AGMM_OK) rc = check_apart(dA, "dA", {W, saved, dY, dW, dbias}, shard_ptrs, p->N);
+  if (rc == AGMM_OK) rc = check_apart(dW, "dW", {W, saved, dY, dbias}, shard_ptrs, p->N);
+  if (rc == AGMM_OK) rc = check_apart(dbias, "dbias", {W, saved, dY}, shard_ptrs, p->N);
   if (rc != AGMM_OK) return rc;
   std::lock_guard<std::mutex> lk(p->mu);
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -588,6 +606,7 @@ int agmm_ff_recompute(agmm_ff_plan_t p, const void* saved, const void* saved_sca
   if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
   int rc = check_ptr(saved, "saved", -1, 16);
   if (rc == AGMM_OK) rc = check_ptr(Y, "Y", -1, 2);
+  if (rc == AGMM_OK) rc = check_apart(Y, "Y", {saved});
   if (rc != AGMM_OK) return rc;
   std::lock_guard<std::mutex> lk(p->mu);
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -679,11 +698,13 @@ int agmm_norm_forward(agmm_norm_plan_t p, const void* x, const void* weight, con
   if (rc == AGMM_OK) rc = check_ptr(y, "y", -1, p->elem());
   if (rc == AGMM_OK && mean) rc = check_ptr(mean, "mean", -1, 4);
   if (rc == AGMM_OK && rstd) rc = check_ptr(rstd, "rstd", -1, 4);
+  if (rc == AGMM_OK) rc = check_apart(y, "y", {weight, bias});
   if (rc != AGMM_OK) return rc;
   if (!(eps >= 0.0f) || std::isinf(eps)) return set_err(AGMM_ERR_INVALID_ARG, "eps must be a finite number >= 0 (got %g)", (double)eps);
   std::lock_guard<std::mutex> lk(p->mu);
   hipStream_t s = static_cast<hipStream_t>(stream);
   agmm::NormProblem n = p->problem(x, weight);
+  if (y == x && n.ldx != (p->ldy ? p->ldy : p->cols)) return set_err(AGMM_ERR_INVALID_ARG, "y over x needs equal strides");
   n.bias = bias;
   n.eps = eps;
   n.y = y;
@@ -708,6 +729,9 @@ int agmm_norm_backward(agmm_norm_plan_t p, const void* x, const void* dy, const 
   if (rc == AGMM_OK && dx) rc = check_ptr(dx, "dx", -1, p->elem());
   if (rc == AGMM_OK && dweight) rc = check_ptr(dweight, "dweight", -1, p->weight_elem());
   if (rc == AGMM_OK && dbias) rc = check_ptr(dbias, "dbias", -1, p->weight_elem());
+  if (rc == AGMM_OK) rc = check_apart(dx, "dx", {x, weight});
+  if (rc == AGMM_OK) rc = check_apart(dweight, "dweight", {x, dy, weight, dx, dbias});
+  if (rc == AGMM_OK) rc = check_apart(dbias, "dbias", {x, dy, weight, dx});
   if (rc != AGMM_OK) return rc;
   std::lock_guard<std::mutex> lk(p->mu);
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -719,6 +743,7 @@ int agmm_norm_backward(agmm_norm_plan_t p, const void* x, const void* dy, const 
   n.rstd = const_cast<float*>(rstd);
   n.dx = dx;
   n.lddx = p->lddx ? p->lddx : p->cols;
+  if (dx == dy && n.lddx != n.lddy) return set_err(AGMM_ERR_INVALID_ARG, "dx over dy needs equal strides");
   n.sums = sums ? reinterpret_cast<float*>(p->ws) : nullptr;
   n.dweight = direct ? dweight : nullptr;
   n.dbias = direct ? dbias : nullptr;

@@ -692,7 +692,8 @@ agmm_ff_plan_t agmm_ff_plan_create(int num_shards, int64_t m_per_shard, int64_t 
  *   Y           device [m, n_local], rows "ldy" apart
  *   saved, saved_scales  as above, or NULL (no scales: 16 bits)
  * Shards, W and saved are 16-byte aligned, the others to their elements.
- * Outputs must not overlap inputs, but for residual = Y with equal strides.
+ * Outputs must not overlap inputs, but for residual = Y with equal strides (one at
+ * another operand's address is refused).
  * Stream, capture and ordering rules are agmm_run's (where the settings in use
  * need neither copies nor ranges of k, calls share no workspace and are not
  * ordered).
@@ -708,7 +709,7 @@ int agmm_ff_forward(agmm_ff_plan_t plan, const void *const *shard_ptrs, const vo
  *   dA          device [m, k] of the plan's dtype, rows "ldda" apart, or NULL
  *   dW          device [parts * n_local, k], rows "lddw" apart, or NULL
  *   dbias       device [parts * n_local] of the plan's dtype, or NULL (not all three)
- * shard_ptrs may be NULL without dW, and W without dA.
+ * shard_ptrs may be NULL without dW, and W without dA.  Outputs overlap nothing.
  */
 int agmm_ff_backward(agmm_ff_plan_t plan, const void *const *shard_ptrs, const void *W,
                      const void *saved, const void *saved_scales, const void *dY, void *dA,

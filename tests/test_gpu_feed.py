@@ -408,6 +408,68 @@ def test_captured_into_a_graph():
         del graph
 
 
+def test_ranges_of_k_captured_into_a_graph():
+    """Few rows whose ranges of k use the workspace, with and without kept pre-activations, replayed with eager calls between."""
+    N, ms, k, n = 2, 20, 3001, 100
+    shards, w, b, _ = make(N, ms, k, n, FP16, 2)
+    dy = torch.randn((N * ms, n), device="cuda").half()
+    with agmm.FeedForwardPlan(N, ms, k, n, FP16, activation="gelu", gated=True) as plan:
+        want = [plan.forward(shards, w, b), *plan.forward(shards, w, b, keep=16)]
+        da, dw, _ = plan.backward(shards, w, want[2], dy)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            y0 = plan.forward(shards, w, b)
+            y1, saved = plan.forward(shards, w, b, keep=16)
+            da1, dw1, _ = plan.backward(shards, w, saved, dy)
+        for _ in range(4):
+            for t in (y0, y1, saved.values, da1, dw1):
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            for t, z in ((y0, want[0]), (y1, want[1]), (saved.values, want[2].values), (da1, da), (dw1, dw)):
+                assert torch.equal(t, z)
+            other = plan.forward([s * 2 for s in shards], w, b)
+            torch.cuda.synchronize()
+            assert not torch.equal(other, want[0])
+        del graph
+
+
+def test_ranges_of_k_on_two_streams():
+    """Calls that share the ranges' sums are ordered across streams."""
+    N, ms, k, n = 1, 48, 4096, 60
+    shards, w, b, _ = make(N, ms, k, n, BF16, 1)
+    twice = [s * 2 for s in shards]
+    with agmm.FeedForwardPlan(N, ms, k, n, BF16, activation="silu", with_gradient=False) as plan:
+        assert plan.workspace_bytes() > 0
+        want = [plan.forward(shards, w, b), plan.forward(twice, w, b)]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        for _ in range(8):
+            got = [plan.forward(a, w, b, stream=s) for a, s in zip((shards, twice), streams)]
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_outputs_over_operands_are_refused():
+    m, k = 8, 32
+    shards, w, b, r = make(1, m, k, k, BF16, 1, residual=True)
+    with agmm.FeedForwardPlan(1, m, k, k, BF16) as plan:
+        with pytest.raises(agmm.AgmmError, match="overlaps"):
+            plan.forward(shards, w, b, out=shards[0])
+        with pytest.raises(agmm.AgmmError, match="dA overlaps"):
+            plan.backward(shards, w, None, r, dA=shards[0])
+        with pytest.raises(agmm.AgmmError, match="dA overlaps"):
+            plan.backward(shards, w, None, r, dA=r)
+        with pytest.raises(agmm.AgmmError, match="dW overlaps"):
+            plan.backward(shards, w, None, r, dW=w)
+        plan.set("ldy", k + 8)
+        wide = torch.zeros((m, k + 8), dtype=torch.bfloat16, device="cuda")
+        dense = wide.view(-1)[:m * k].view(m, k)
+        with pytest.raises(agmm.AgmmError, match="strides"):
+            plan.forward(shards, w, b, dense, out=wide[:, :k])
+
+
 def test_two_streams_share_a_plan():
     """Calls on two streams are ordered where they share the workspace."""
     N, ms, k, n = 2, 300, 500, 300

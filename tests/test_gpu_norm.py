@@ -215,3 +215,19 @@ def test_refusals():
             plan.set("ldx", 31)
     with pytest.raises(agmm.AgmmError, match="weights have"):
         agmm.NormPlan(4, 32, agmm.AGMM_BF16, agmm.AGMM_FP16)
+
+
+def test_outputs_over_operands_are_refused():
+    x, dy, w, b = make(4, 32, agmm.AGMM_BF16, agmm.AGMM_BF16)
+    with agmm.NormPlan(4, 32, agmm.AGMM_BF16) as plan:
+        _, mean, rstd = plan.forward(x, w, b)
+        with pytest.raises(agmm.AgmmError, match="dx overlaps"):
+            plan.backward(x, dy, w, mean, rstd, dx=x)
+        wide = torch.zeros((4, 40), dtype=torch.bfloat16, device="cuda")
+        dense = wide.view(-1)[:128].view(4, 32)
+        plan.set("ldy", 40)
+        with pytest.raises(agmm.AgmmError, match="strides"):
+            plan.forward(dense, w, b, out=wide[:, :32])
+        plan.set("lddx", 40)
+        with pytest.raises(agmm.AgmmError, match="strides"):
+            plan.backward(x, dense, w, mean, rstd, dx=wide[:, :32])
