@@ -51,8 +51,10 @@ struct FeedProblem {
 };
 constexpr int64_t kFeedGrid = int64_t(1) << 24;
 // Tiles of 256 x 256 (tile 256), 256 x 224 (224; not for 8-bit pre-activations of
-// a gated product, whose blocks of 32 columns its 112 columns of y would cut) or
-// 128 x 128 tile columns (128); rows of whole 16-byte vectors.
+// a gated product, whose blocks of 32 columns its 112 columns of y would cut; 16-bit
+// ones need no block in one tile, and the last tile column writes the zeros of the
+// block that it ends in) or 128 x 128 tile columns (128); rows of whole 16-byte
+// vectors.
 // gemm.splits > 1 (tile 128): ranges of k to gemm.partials [splits][m][tile
 // columns rounded up to 16], and a second launch that finishes.
 hipError_t launch_feed_tiles(const FeedProblem& p, int tile, int dtype, hipStream_t stream);

@@ -69,6 +69,10 @@ void feed_tile_kernel(FeedProblem fp) {
   // 16-byte pieces of the thread's columns: pieces at, at + 1 of the first part
   // and, gated, at + 4, at + 5 of the second
   const int at = GATED ? 8 * (c >> 1) + 2 * (c & 1) : 2 * c;
+  // A gated tile of 224 ends in the middle of a block of 32 kept columns (112 of y):
+  // where it is the last one, the block's other 16, all past n, are zeros from
+  // the two threads whose own columns are 16 before them.
+  const bool tail = GATED && BN == 224 && fp.kept.values && n0 + BN >= N && c >= PIECES - 2 && col + 16 < fp.kept.wide;
   float bias[PARTS][8];
   bias8<DT, GATED>(fp, col, bias);
 
@@ -104,6 +108,11 @@ void feed_tile_kernel(FeedProblem fp) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[h][e] += bias[h][e];
         finish8<DT, GATED, KIND>(fp, v, row, row < M, col);
+        if (GATED && BN == 224 && tail && row < M)
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h)
+            *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(fp.kept.values) + (row * PARTS + h) * fp.kept.wide + col + 16) =
+                u32x4_t{0u, 0u, 0u, 0u};
       };
       if constexpr (EVEN) {
 #pragma unroll 2
