@@ -85,8 +85,11 @@ struct agmm_ff_plan : PlanBase {
     size_t bytes = 0;
   };
   // those of the settings and the workspace: forward, forward with pre-activations
-  // kept, backward
-  Layout layouts[3];
+  // kept in 16 bits, in 8 bits, backward
+  enum Pass { kForward, kKeep16, kKeep8, kBackward };
+  Layout layouts[4];
+  static Pass forward_pass(const void* saved, const void* scales) { return !saved ? kForward : scales ? kKeep8 : kKeep16; }
+  int passes() const { return with_gradient ? kBackward + 1 : kBackward; }
 
   int64_t ld_a() const { return lda ? lda : k; }
   int64_t ld_w() const { return ldw ? ldw : k; }
@@ -136,13 +139,16 @@ struct agmm_ff_plan : PlanBase {
 
   // Form of the forward product: the one that takes the least, with the copies
   // it needs.  Copies have rows of whole lines; rows that are whole 16-byte
-  // vectors already are copied where that pays.
-  void pick_tile(Layout& L, bool must_copy, bool kept) const {
+  // vectors already are copied where that pays.  8-bit pre-activations of a gated
+  // product come in no tile of 224 (feed_kernels.h): asked for, it is 256.
+  void pick_tile(Layout& L, bool must_copy, Pass pass) const {
     const int64_t nc = tile_cols();
+    const bool kept = pass != kForward, no_224 = pass == kKeep8 && parts == 2;
+    const int64_t want = tile_key == 224 && no_224 ? 256 : tile_key;
     const bool lines = ld_a() % 64 == 0 && ld_w() % 64 == 0;
     double best = -1;
     const auto offer = [&](int tile, bool copied, int splits, double us) {
-      if (tile_key > 0 && tile != tile_key) return;
+      if ((want > 0 && tile != want) || (tile == 224 && no_224)) return;
       us += copied ? copy_us() : 0.0;
       if (best >= 0 && us >= best) return;
       best = us;
@@ -186,13 +192,13 @@ struct agmm_ff_plan : PlanBase {
   // Whether every form of the few-row kernel stays within a launch.
   bool few_fits() const { return cdiv(m, m <= 16 ? 16 : 64) * cdiv(n, m <= 16 ? 8 : 16) < agmm::kFeedGrid; }
 
-  Layout layout(int which, char* base) const {
+  Layout layout(Pass pass, char* base) const {
     Layout L;
     L.kp = round_up(k, 64);
     const bool must_a = k % 8 != 0 || ld_a() % 8 != 0, must_w = k % 8 != 0 || ld_w() % 8 != 0;   // not whole 16-byte vectors
     Cut c{base};
-    if (which < 2) {
-      pick_tile(L, must_a || must_w, which == 1);
+    if (pass != kBackward) {
+      pick_tile(L, must_a || must_w, pass);
       if (L.pad_a) L.a = c.take((size_t)m * L.kp * 2);
       if (L.pad_w) L.w = c.take((size_t)cols() * L.kp * 2);
       L.per = round_up(cdiv(L.pad_a ? L.kp : k, L.splits), 64);
@@ -244,10 +250,10 @@ struct agmm_ff_plan : PlanBase {
 
   int apply() {
     size_t bytes = 0;
-    for (int which = 0; which < 2 + with_gradient; ++which) bytes = std::max(bytes, layout(which, nullptr).bytes);
+    for (int pass = 0; pass < passes(); ++pass) bytes = std::max(bytes, layout((Pass)pass, nullptr).bytes);
     const int rc = reserve(bytes);
     if (rc != AGMM_OK) return rc;
-    for (int which = 0; which < 2 + with_gradient; ++which) layouts[which] = layout(which, ws);
+    for (int pass = 0; pass < passes(); ++pass) layouts[pass] = layout((Pass)pass, ws);
     return AGMM_OK;
   }
 
@@ -294,7 +300,7 @@ struct agmm_ff_plan : PlanBase {
 
   int forward(const void* const* shards, const void* W, const void* bias, const void* residual, void* Y,
               void* saved, void* saved_scales, hipStream_t s) {
-    const Layout& L = layouts[saved != nullptr];
+    const Layout& L = layouts[forward_pass(saved, saved_scales)];
     if (L.a || L.w) {
       const hipError_t err = agmm::launch_feed_copies(copies(L, shards, W), s);
       if (err != hipSuccess) return hip_err(err, "operand copy launch");
@@ -309,13 +315,11 @@ struct agmm_ff_plan : PlanBase {
       p.gemm.rows.num_groups = N;
       p.gemm.rows.c_group_rows = m_s;
     }
-    // 8-bit pre-activations of a gated product come in no tile of 224
-    const int tile = L.tile == 224 && parts == 2 && saved_scales ? 256 : L.tile;
     if (L.tile == 64) {
       p.gemm.order.num_rb = (int32_t)cdiv(m, 16 * L.fm);
       p.gemm.order.num_cb = (int32_t)cdiv(n, L.yc);
     } else {
-      p.gemm.order = tiles_of(m, tile_cols(), tile == 224 ? 256 : tile, tile);
+      p.gemm.order = tiles_of(m, tile_cols(), L.tile == 224 ? 256 : L.tile, L.tile);
     }
     p.gemm.m = (int32_t)m;
     p.gemm.n = (int32_t)tile_cols();
@@ -334,13 +338,13 @@ struct agmm_ff_plan : PlanBase {
     p.y = Y;
     p.ldy = ldy ? ldy : n;
     p.kept = kept_rows(saved, saved_scales);
-    const hipError_t err = L.tile == 64 ? agmm::launch_feed_few(p, L.fm, L.yc, dtype, s) : agmm::launch_feed_tiles(p, tile, dtype, s);
+    const hipError_t err = L.tile == 64 ? agmm::launch_feed_few(p, L.fm, L.yc, dtype, s) : agmm::launch_feed_tiles(p, L.tile, dtype, s);
     return err == hipSuccess ? AGMM_OK : hip_err(err, "feed-forward launch");
   }
 
   int backward(const void* const* shards, const void* W, const void* saved, const void* saved_scales, const void* dY, void* dA,
                void* dW, void* dbias, hipStream_t s) {
-    const Layout& L = layouts[2];
+    const Layout& L = layouts[kBackward];
     agmm::FeedDProblem e{};
     e.block = L.d_rows;
     e.m = m;
@@ -527,7 +531,7 @@ int agmm_ff_plan_get_int(agmm_ff_plan_t p, const char* key, int64_t* value) {
   else if (k == "ldy") *value = p->ldy ? p->ldy : p->n;
   else if (k == "lddy") *value = p->lddy ? p->lddy : p->n;
   else if (k == "saved_cols") *value = p->wide();
-  else if (k == "tile") *value = p->layouts[0].tile;
+  else if (k == "tile") *value = p->layouts[agmm_ff_plan::kForward].tile;
   else if (k == "captured") *value = p->captured;
   else return set_err(AGMM_ERR_INVALID_ARG, "unknown key '%s'", key);
   return ok();
@@ -565,7 +569,7 @@ int agmm_ff_forward(agmm_ff_plan_t p, const void* const* shard_ptrs, const void*
   if (residual == Y && (p->ldr ? p->ldr : p->n) != (p->ldy ? p->ldy : p->n))
     return set_err(AGMM_ERR_INVALID_ARG, "Y over residual needs equal strides");
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool ordered = p->layouts[saved != nullptr].bytes > 0;
+  const bool ordered = p->layouts[agmm_ff_plan::forward_pass(saved, saved_scales)].bytes > 0;
   return p->run(s, ordered, [&] { return p->forward(shard_ptrs, W, bias, residual, Y, saved, saved_scales, s); });
 }
 
