@@ -563,7 +563,9 @@ int agmm_ff_forward(agmm_ff_plan_t p, const void* const* shard_ptrs, const void*
   if (rc != AGMM_OK) return rc;
   if (residual && p->parts == 2) return set_err(AGMM_ERR_UNSUPPORTED, "a gated product takes no residual");
   if (saved_scales && !saved) return set_err(AGMM_ERR_INVALID_ARG, "saved_scales without saved");
-  rc = check_apart(Y, "Y", {W, bias, saved}, shard_ptrs, p->N);
+  rc = check_apart(Y, "Y", {W, bias, saved, saved_scales}, shard_ptrs, p->N);
+  if (rc == AGMM_OK) rc = check_apart(saved, "saved", {W, bias, residual, saved_scales}, shard_ptrs, p->N);
+  if (rc == AGMM_OK) rc = check_apart(saved_scales, "saved_scales", {W, bias, residual}, shard_ptrs, p->N);
   if (rc != AGMM_OK) return rc;
   std::lock_guard<std::mutex> lk(p->mu);
   if (residual == Y && (p->ldr ? p->ldr : p->n) != (p->ldy ? p->ldy : p->n))
@@ -597,9 +599,9 @@ int agmm_ff_backward(agmm_ff_plan_t p, const void* const* shard_ptrs, const void
   if (rc == AGMM_OK && dA) rc = check_ptr(dA, "dA", -1, 2);
   if (rc == AGMM_OK && dW) rc = check_ptr(dW, "dW", -1, 2);
   if (rc == AGMM_OK && dbias) rc = check_ptr(dbias, "dbias", -1, 2);
-  if (rc == AGMM_OK) rc = check_apart(dA, "dA", {W, saved, dY, dW, dbias}, shard_ptrs, p->N);
-  if (rc == AGMM_OK) rc = check_apart(dW, "dW", {W, saved, dY, dbias}, shard_ptrs, p->N);
-  if (rc == AGMM_OK) rc = check_apart(dbias, "dbias", {W, saved, dY}, shard_ptrs, p->N);
+  if (rc == AGMM_OK) rc = check_apart(dA, "dA", {W, saved, saved_scales, dY, dW, dbias}, shard_ptrs, p->N);
+  if (rc == AGMM_OK) rc = check_apart(dW, "dW", {W, saved, saved_scales, dY, dbias}, shard_ptrs, p->N);
+  if (rc == AGMM_OK) rc = check_apart(dbias, "dbias", {W, saved, saved_scales, dY}, shard_ptrs, p->N);
   if (rc != AGMM_OK) return rc;
   std::lock_guard<std::mutex> lk(p->mu);
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -610,7 +612,7 @@ int agmm_ff_recompute(agmm_ff_plan_t p, const void* saved, const void* saved_sca
   if (!p) return set_err(AGMM_ERR_INVALID_ARG, "plan is NULL");
   int rc = check_ptr(saved, "saved", -1, 16);
   if (rc == AGMM_OK) rc = check_ptr(Y, "Y", -1, 2);
-  if (rc == AGMM_OK) rc = check_apart(Y, "Y", {saved});
+  if (rc == AGMM_OK) rc = check_apart(Y, "Y", {saved, saved_scales});
   if (rc != AGMM_OK) return rc;
   std::lock_guard<std::mutex> lk(p->mu);
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -702,7 +704,9 @@ int agmm_norm_forward(agmm_norm_plan_t p, const void* x, const void* weight, con
   if (rc == AGMM_OK) rc = check_ptr(y, "y", -1, p->elem());
   if (rc == AGMM_OK && mean) rc = check_ptr(mean, "mean", -1, 4);
   if (rc == AGMM_OK && rstd) rc = check_ptr(rstd, "rstd", -1, 4);
-  if (rc == AGMM_OK) rc = check_apart(y, "y", {weight, bias});
+  if (rc == AGMM_OK) rc = check_apart(y, "y", {weight, bias, mean, rstd});
+  if (rc == AGMM_OK) rc = check_apart(mean, "mean", {x, weight, bias, rstd});
+  if (rc == AGMM_OK) rc = check_apart(rstd, "rstd", {x, weight, bias});
   if (rc != AGMM_OK) return rc;
   if (!(eps >= 0.0f) || std::isinf(eps)) return set_err(AGMM_ERR_INVALID_ARG, "eps must be a finite number >= 0 (got %g)", (double)eps);
   std::lock_guard<std::mutex> lk(p->mu);
@@ -733,9 +737,9 @@ int agmm_norm_backward(agmm_norm_plan_t p, const void* x, const void* dy, const 
   if (rc == AGMM_OK && dx) rc = check_ptr(dx, "dx", -1, p->elem());
   if (rc == AGMM_OK && dweight) rc = check_ptr(dweight, "dweight", -1, p->weight_elem());
   if (rc == AGMM_OK && dbias) rc = check_ptr(dbias, "dbias", -1, p->weight_elem());
-  if (rc == AGMM_OK) rc = check_apart(dx, "dx", {x, weight});
-  if (rc == AGMM_OK) rc = check_apart(dweight, "dweight", {x, dy, weight, dx, dbias});
-  if (rc == AGMM_OK) rc = check_apart(dbias, "dbias", {x, dy, weight, dx});
+  if (rc == AGMM_OK) rc = check_apart(dx, "dx", {x, weight, mean, rstd});
+  if (rc == AGMM_OK) rc = check_apart(dweight, "dweight", {x, dy, weight, mean, rstd, dx, dbias});
+  if (rc == AGMM_OK) rc = check_apart(dbias, "dbias", {x, dy, weight, mean, rstd, dx});
   if (rc != AGMM_OK) return rc;
   std::lock_guard<std::mutex> lk(p->mu);
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -692,8 +692,9 @@ agmm_ff_plan_t agmm_ff_plan_create(int num_shards, int64_t m_per_shard, int64_t 
  *   Y           device [m, n_local], rows "ldy" apart
  *   saved, saved_scales  as above, or NULL (no scales: 16 bits)
  * Shards, W and saved are 16-byte aligned, the others to their elements.
- * Outputs must not overlap inputs, but for residual = Y with equal strides (one at
- * another operand's address is refused).
+ * Outputs (Y, saved, saved_scales) overlap no other operand, but for residual = Y
+ * with equal strides; an output at another operand's address is refused, here and
+ * in the calls below.
  * Stream, capture and ordering rules are agmm_run's (where the settings in use
  * need neither copies nor ranges of k, calls share no workspace and are not
  * ordered).
@@ -717,7 +718,7 @@ int agmm_ff_backward(agmm_ff_plan_t plan, const void *const *shard_ptrs, const v
 
 /* Enqueue Y = act(p), or act(p_0) * p_1, again from what the forward pass kept:
  * for callers who keep 8 bits of p instead of y for the next layer's weight
- * gradient.  Uses no workspace. */
+ * gradient.  Y overlaps neither.  Uses no workspace. */
 int agmm_ff_recompute(agmm_ff_plan_t plan, const void *saved, const void *saved_scales, void *Y,
                       void *stream);
 
@@ -763,8 +764,9 @@ agmm_norm_plan_t agmm_norm_plan_create(int64_t rows, int64_t cols, int dtype, in
 /* Enqueue the forward pass: x, y [rows, cols], rows "ldx" and "ldy" elements
  * apart; weight, bias [cols] or NULL (1, 0); mean, rstd fp32 [rows], written, or
  * NULL; eps finite and >= 0.  Pointers are aligned to their elements (rows of
- * whole 16-byte vectors are read faster); y may be x itself with equal strides.
- * Uses no workspace. */
+ * whole 16-byte vectors are read faster); y may be x itself with equal strides,
+ * and outputs overlap nothing else (one at another operand's address is refused,
+ * in the backward pass too).  Uses no workspace. */
 int agmm_norm_forward(agmm_norm_plan_t plan, const void *x, const void *weight, const void *bias,
                       float eps, void *y, float *mean, float *rstd, void *stream);
 

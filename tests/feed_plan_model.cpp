@@ -7,7 +7,9 @@
 #include <cstdlib>
 #include <cstring>
 #include <random>
+#include <set>
 #include <string>
+#include <vector>
 
 struct ihipStream_t {};
 struct ihipEvent_t {};
@@ -136,11 +138,76 @@ void forms() {
   expect(by[64] > 100 && by[128] > 100 && by[224] > 100 && by[256] > 100, "every form is chosen");
 }
 
+// Two operands of a call at one address: refused where either is an output, with
+// nothing launched, but for the pairs that may be in place.
+struct Operand {
+  std::string name;
+  void** where;
+  bool output;
+};
+template <class F>
+void pairs(const std::string& entry, const std::vector<Operand>& operands, const std::set<std::string>& in_place, F&& call) {
+  launched = Launched{};
+  expect(call() == AGMM_OK && launched.count > 0, entry + ": " + agmm::g_msg);
+  for (const Operand& out : operands) {
+    if (!out.output) continue;
+    for (const Operand& other : operands) {
+      if (&out == &other) continue;
+      void* const kept = *out.where;
+      *out.where = *other.where;
+      launched = Launched{};
+      const int rc = call();
+      const std::string what = entry + ": " + out.name + " at " + other.name;
+      if (in_place.count(out.name + " " + other.name)) {
+        expect(rc == AGMM_OK && launched.count > 0, what + ": " + agmm::g_msg);
+      } else {
+        expect(rc == AGMM_ERR_INVALID_ARG && agmm::g_msg.find("overlaps") != std::string::npos, what + " is not refused");
+        expect(launched.count == 0, what + ": launched");
+      }
+      *out.where = kept;
+    }
+  }
+}
+
+void overlaps() {
+  for (int gated : {0, 1})
+    for (int scaled : {0, 1}) {
+      void *A[3] = {at(0), at(1), at(2)}, *W = at(3), *b = at(4), *r = gated ? nullptr : at(5), *y = at(6), *v = at(7), *s = scaled ? at(8) : nullptr;
+      void *dy = at(9), *da = at(10), *dw = at(11), *db = at(12);
+      agmm_ff_plan_t p = agmm_ff_plan_create(3, 4, 64, 64, AGMM_BF16, AGMM_ACT_SILU, gated, 1);
+      std::vector<Operand> all = {{"shard 0", &A[0], false}, {"shard 2", &A[2], false}, {"W", &W, false}, {"bias", &b, false},
+                                  {"Y", &y, true}, {"saved", &v, true}};
+      if (!gated) all.push_back({"residual", &r, false});
+      if (scaled) all.push_back({"saved_scales", &s, true});
+      pairs("forward", all, {"Y residual"}, [&] { return agmm_ff_forward(p, A, W, b, r, y, v, s, nullptr); });
+      all = {{"shard 0", &A[0], false}, {"shard 2", &A[2], false}, {"W", &W, false}, {"saved", &v, false}, {"dY", &dy, false},
+             {"dA", &da, true}, {"dW", &dw, true}, {"dbias", &db, true}};
+      if (scaled) all.push_back({"saved_scales", &s, false});
+      pairs("backward", all, {}, [&] { return agmm_ff_backward(p, A, W, v, s, dy, da, dw, db, nullptr); });
+      all = {{"saved", &v, false}, {"Y", &y, true}};
+      if (scaled) all.push_back({"saved_scales", &s, false});
+      pairs("recompute", all, {}, [&] { return agmm_ff_recompute(p, v, s, y, nullptr); });
+      agmm_ff_plan_destroy(p);
+    }
+  for (int64_t rows : {2, 100}) {               // the weights' gradients in one launch, and in two
+    void *x = at(0), *dy = at(1), *w = at(2), *b = at(3), *y = at(4), *mean = at(5), *rstd = at(6), *dx = at(7), *dw = at(8), *db = at(9);
+    agmm_norm_plan_t p = agmm_norm_plan_create(rows, 64, AGMM_FP32, AGMM_FP32);
+    const auto f = [](void*& q) { return static_cast<float*>(q); };
+    pairs("norm", {{"x", &x, false}, {"weight", &w, false}, {"bias", &b, false}, {"y", &y, true}, {"mean", &mean, true}, {"rstd", &rstd, true}},
+          {"y x"}, [&] { return agmm_norm_forward(p, x, w, b, 1e-5f, y, f(mean), f(rstd), nullptr); });
+    pairs("norm backward", {{"x", &x, false}, {"dy", &dy, false}, {"weight", &w, false}, {"mean", &mean, false}, {"rstd", &rstd, false},
+                            {"dx", &dx, true}, {"dweight", &dw, true}, {"dbias", &db, true}},
+          {"dx dy"}, [&] { return agmm_norm_backward(p, x, dy, w, f(mean), f(rstd), dx, dw, db, nullptr); });
+    agmm_norm_plan_destroy(p);
+  }
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
   const std::string part = argc > 1 ? argv[1] : "forms";
   if (part == "forms") forms();
+  else if (part == "overlaps") overlaps();
   else expect(false, "unknown part");
   if (!failures) std::printf("all as expected\n");
   return failures ? 1 : 0;

@@ -32,3 +32,9 @@ def test_calls_run_the_form_they_can_use(model):
     """Whatever is kept, a call launches the form that was priced for it, no
     tiles of 224 where 8 bits of a gated product are kept."""
     run_model(model, "forms")
+
+
+def test_outputs_at_other_operands_are_refused(model):
+    """Every output of every entry point at the address of every other operand,
+    but for the pairs that may be in place: refused before anything is launched."""
+    run_model(model, "overlaps")
