@@ -538,8 +538,7 @@ __device__ __forceinline__ void loss_rows(const LossRows& c) {
 }
 
 // Rows of 16-bit elements, `cols` of each, as rows of whole 16-byte vectors:
-// out[(g * rows + t) * chunks * 8 + c] = group[g][t * ld + c], zeros past cols
-// (chunks may pass them by any number).
+// out[(g * rows + t) * chunks * 8 + c] = group[g][t * ld + c], zeros past cols.
 // A source row may start at any element (16-byte accesses to global memory
 // need no alignment); its last chunk is read element by element.
 __device__ __forceinline__ void pad_chunk(const PadRows& c, int64_t u) {
@@ -643,7 +642,8 @@ constexpr int64_t kCopyGroups = 1 << 14;
 hipError_t launch_loss_prepare(const LossRows* r, const PadRows* c, int dtype, hipStream_t stream) {
   int64_t copies = 0;
   if (c) {
-    if (c->rows < 1 || c->rows > INT32_MAX || c->chunks < 1 || c->chunks > INT32_MAX || c->cols > c->chunks * 8 || c->num_groups < 1 || c->num_groups > kMaxGroups)
+    if (c->rows < 1 || c->rows > INT32_MAX || c->chunks < 1 || c->chunks > INT32_MAX || c->cols <= (c->chunks - 1) * 8 ||
+        c->cols > c->chunks * 8 || c->num_groups < 1 || c->num_groups > kMaxGroups)
       return hipErrorInvalidValue;
     // beyond 2^14 workgroups (256 MiB) each copies several pieces: any size fits a launch
     copies = (c->num_groups * c->rows * c->chunks + 1023) / 1024;

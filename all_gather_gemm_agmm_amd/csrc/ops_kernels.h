@@ -144,8 +144,8 @@ struct LossRows {
 };
 
 // Copy of 16-bit rows as rows of whole 16-byte vectors (zeros past cols):
-// out [num_groups][rows][8 * chunks], chunks >= ceil(cols / 8).  Sources need
-// element alignment only.
+// out [num_groups][rows][8 * chunks], chunks = ceil(cols / 8) (launch_feed_copies:
+// or more).  Sources need element alignment only.
 struct PadRows {
   const void* group[kMaxGroups];
   int64_t num_groups, rows, cols, ld, chunks;
