@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdio>
+#include <initializer_list>
 
 #include "ops_kernels.h"
 
