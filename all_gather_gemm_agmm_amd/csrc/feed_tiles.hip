@@ -34,6 +34,17 @@ namespace agmm {
 
 namespace {
 
+// The main loop's B for both kernels here, GATED, BN and NC, the columns of y,
+// being the kernel's own.  Tile column r of a gated tile: block r / 32 of y's
+// columns, part (r / 16) % 2.
+#define AGMM_CLAMP
+#define AGMM_B_ROW(r) \
+  (GATED ? min((n0 >> 1) + (((r) >> 5) << 4) + ((r) & 15), NC - 1) + (((r) >> 4) & 1) * NC : min(n0 + (r), N - 1))
+#define AGMM_B_IN(r) true
+#define AGMM_B_FIRST (GATED ? n0 >> 1 : n0)
+#define AGMM_B_LAST (GATED ? (n0 >> 1) + BN / 2 - 1 + NC : n0 + BN - 1)
+#define AGMM_B_WHOLE (GATED ? (n0 + BN) >> 1 <= NC : n0 + BN <= N)
+
 template <int BM, int BN, int DT, int OCC, bool GATED>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 void feed_tile_kernel(FeedProblem fp) {
@@ -47,14 +58,6 @@ void feed_tile_kernel(FeedProblem fp) {
   const GemmProblem& p = fp.gemm;
   const int NC = fp.n;                         // columns of y
 
-// Tile column r of a gated tile: block r / 32 of y's columns, part (r / 16) % 2.
-#define AGMM_CLAMP
-#define AGMM_B_ROW(r) \
-  (GATED ? min((n0 >> 1) + (((r) >> 5) << 4) + ((r) & 15), NC - 1) + (((r) >> 4) & 1) * NC : min(n0 + (r), N - 1))
-#define AGMM_B_IN(r) true
-#define AGMM_B_FIRST (GATED ? n0 >> 1 : n0)
-#define AGMM_B_LAST (GATED ? (n0 >> 1) + BN / 2 - 1 + NC : n0 + BN - 1)
-#define AGMM_B_WHOLE (GATED ? (n0 + BN) >> 1 <= NC : n0 + BN <= N)
 #include "gemm_m16_loop.inc"
 
   constexpr int PARTS = GATED ? 2 : 1;
