@@ -126,8 +126,8 @@ struct agmm_ff_plan : PlanBase {
   // strides), with 2.7 for every further workgroup of 64 rows on a CU, 4.9 where k
   // ends inside 64, or W at 4.5 TB/s, and a tenth of the other.  E.g. (us) 8 x 4096
   // -> 1792: 7.8 by 8 columns, 8.7 by 16, 21 by 64; 128 x 4096 -> 7168: 73 by 16,
-  // 35 by 64; 8 x 8192 -> 3584: 24 by 8, 16 by 16; 3000 x 130 -> 6307: 115 by 64,
-  // 33 in tiles of 128.
+  // 35 by 64, 22 in tiles of 128; 8 x 8192 -> 3584: 24 by 8, 16 by 16; 3000 x 130 ->
+  // 6307: 114 by 64, 30 in tiles of 128.  (Calls back to back in a graph.)
   double few_us(int fm, int yc, int splits) const {
     const double mb = 2e-6 * (double)cdiv(k, splits) * (double)(std::min<int64_t>(m, 16 * fm) + parts * yc);
     const double each = (fm == 1 && yc <= 16 ? 21.0 : 27.0) * (ld_a() % 2 != 0 || ld_w() % 2 != 0 ? 1.7 : 1.0);

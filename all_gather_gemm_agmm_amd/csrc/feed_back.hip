@@ -14,7 +14,8 @@
 //
 // Measured: 8192 x 2 x 3584 bf16 from 8 bits 76-80 us, 355 MB at 4.5 TB/s; 2048 x
 // 1024 bf16, tanh's gelu 6.4, in blocks of 32 rows, so that there are enough; 111 x
-// 2 x 2051 fp16, with the copies that the products need, 6.3.
+// 2 x 2051 fp16, with the copies that the products need, 6.3.  y again (recompute),
+// 8192 x 2 x 3584 bf16: 22 us from 8 bits, 30 from 16, 119 and 176 MB.
 //
 // What is read again as fp32 sums over ranges of k, or over blocks of rows, is
 // added in a fixed order.

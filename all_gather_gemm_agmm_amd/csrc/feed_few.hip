@@ -9,7 +9,7 @@
 // first n rows of B and of the second n take turns.  Where the blocks leave CUs
 // idle and k is long, it is cut into ranges as well, whose fp32 sums a second
 // launch adds in order and finishes (63 x 3814 -> 2 x 381: 20 us in one launch,
-// 13 so; 128 x 2834 -> 2 x 252: 15 and 11.5; 8 x 1001 -> 700 is faster in one, 8).
+// 12 so; 128 x 2834 -> 2 x 252: 15 and 11; 8 x 1001 -> 700 is faster in one, 5).
 //
 // ODD (a stride is odd): rows that start in the middle of a word are read from
 // that word on, with one word more, and shifted; accesses that start there take
@@ -17,8 +17,10 @@
 //
 // Bound: what a CU streams in, 22 bytes a cycle, its columns of W and the rows
 // of A again per workgroup, and a launch.  Blocks of 8 columns fill the CUs of a
-// short y.  Measured (us): 8 x 4096 -> 1792 bf16 8.5, of which W at 4.5 TB/s is
-// 3.3; gated, twice the W, 10.0; 8 x 8192 -> 3584 16; 128 x 4096 -> 7168 35.
+// short y.  Measured (us, calls back to back in a graph): 8 x 4096 -> 1792 bf16 7.8
+// (8.4 under a profiler), of which W at 4.5 TB/s is 3.3; gated, twice the W, 9.4;
+// 8 x 8192 -> 3584 16; 128 x 4096 -> 7168 35, where tiles of 128 take 22 and are
+// chosen.
 #include "feed_device.h"
 
 namespace agmm {

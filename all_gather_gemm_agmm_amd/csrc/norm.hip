@@ -20,7 +20,9 @@
 // rounded once.  Measured: forward 8192 x 8192 bf16, fp32 weights 53-55 us, 4.9
 // TB/s (weights are loaded once per workgroup of three a CU, not per row: 80 us);
 // 128 x 4096 4; backward 8192 x 8192 77-80 us, 5.1 TB/s, and 4 for the sums; 1011
-// x 4035 fp16 11 and 3.
+// x 4035 fp16 11 and 3 (1011 x 4096: 10.6; rows at odd addresses cost little).
+// Backward past 8192 16-bit columns x and dy are read three times: 4096 x 16384
+// bf16 59, 119 and 5.
 #include "feed_device.h"
 
 namespace agmm {
